@@ -27,7 +27,7 @@ LIB = os.path.join(PKG, "libep.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "layout.hip", "dispatch.hip", "hier.hip", "combine.hip", "combine2.hip",
-           "source.hip"]
+           "source.hip", "experts.hip", "swiglu.hip", "few.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [

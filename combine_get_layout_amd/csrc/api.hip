@@ -443,6 +443,110 @@ int ep_source_dispatch_fused(const ep_shape* shape, const ep_sources* sources, c
                                           static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
 
+// Checks shared by the expert products over expand-mode rows.
+static int check_expert_rows(const ep_shape* shape, const ep_layout* layout, int64_t rows, int64_t a, int64_t b,
+                             void* ws, size_t ws_bytes) {
+    int rc = check_shape(shape);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_ws(shape, ws, ws_bytes)) != EP_OK) return rc;
+    if (!layout || rows < 0 || a < 8 || b < 8 || a % 8 != 0 || b % 8 != 0) return EP_ERR_ARG;
+    if (rows > INT32_MAX || a > EP_MAX_DIM || b > EP_MAX_DIM) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+int ep_expert_matmul(const ep_shape* shape, const ep_layout* layout, const uint16_t* x, int64_t rows,
+                     int32_t k_dim, const uint16_t* w, int32_t n_dim, int w_order, uint16_t* y,
+                     void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_expert_rows(shape, layout, rows, k_dim, n_dim, ws, ws_bytes);
+    if (rc != EP_OK) return rc;
+    if (w_order != EP_WEIGHT_NK && w_order != EP_WEIGHT_KN) return EP_ERR_ARG;
+    if (!layout->expert_offsets || !w || (rows > 0 && (!x || !y))) return EP_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(layout->expert_offsets, 4))
+        return EP_ERR_ARG;
+    if (expert_matmul_grid(rows, shape->E, n_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    return hip_status(launch_expert_matmul(*shape, *layout, x, rows, k_dim, w, n_dim, w_order, y,
+                                           static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_swiglu(const ep_shape* shape, const ep_layout* layout, const uint16_t* x, int64_t rows,
+                     const uint16_t* w13, int32_t F, uint16_t* act, uint8_t* gu_fp8, float* gu_scales,
+                     void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_shape(shape);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_expert_rows(shape, layout, rows, shape->H, F, ws, ws_bytes)) != EP_OK) return rc;
+    if (!layout->expert_offsets || !w13 || (rows > 0 && (!x || !act))) return EP_ERR_ARG;
+    if (!gu_fp8 != !gu_scales || (gu_fp8 && F % 128 != 0)) return EP_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(act, 16) || !aligned(gu_fp8, 16) ||
+        !aligned(gu_scales, 16) || !aligned(layout->expert_offsets, 4))
+        return EP_ERR_ARG;
+    // 32-bit offsets inside one expert's matrix.
+    if (4 * (int64_t)F * shape->H >= INT32_MAX - 15) return EP_ERR_UNSUPPORTED;
+    if (expert_swiglu_grid(rows, shape->E, F) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    return hip_status(launch_expert_swiglu(*shape, *layout, x, rows, w13, F, act, gu_fp8, gu_scales,
+                                           static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+int ep_swiglu_grad(const ep_shape* shape, const ep_layout* layout, int32_t F, const uint8_t* gu_fp8,
+                   const float* gu_scales, const uint16_t* d_act, int64_t rows,
+                   const float* topk_weights, uint16_t* d_gu, uint16_t* act_w, float* d_topk_weights,
+                   void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_expert_rows(shape, layout, rows, F, F, ws, ws_bytes);
+    if (rc != EP_OK) return rc;
+    if (F % 128 != 0) return EP_ERR_ARG;
+    if (shape->T > 0 && (!layout->expert_slot || !topk_weights)) return EP_ERR_ARG;
+    if (rows > 0 && (!gu_fp8 || !gu_scales || !d_act || !d_gu)) return EP_ERR_ARG;
+    if (!aligned(gu_fp8, 16) || !aligned(gu_scales, 16) || !aligned(d_act, 16) || !aligned(d_gu, 16) ||
+        !aligned(act_w, 16) || !aligned(topk_weights, 4) || !aligned(d_topk_weights, 4) ||
+        !aligned(layout->expert_slot, 4))
+        return EP_ERR_ARG;
+    return hip_status(launch_swiglu_grad(*shape, *layout, F, gu_fp8, gu_scales, d_act, rows, topk_weights, d_gu,
+                                         act_w, d_topk_weights, static_cast<char*>(ws),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int ep_expert_wgrad(const ep_shape* shape, const ep_layout* layout, const uint16_t* dy, int64_t rows,
+                    int32_t n_dim, const ep_rows* x, int32_t k_dim, void* dw, int dtype, void* ws,
+                    size_t ws_bytes, void* stream) {
+    int rc = check_expert_rows(shape, layout, rows, n_dim, k_dim, ws, ws_bytes);
+    if (rc != EP_OK) return rc;
+    if (!layout->expert_offsets || !x || !dw || (dtype != EP_GRAD_BF16 && dtype != EP_GRAD_F32)) return EP_ERR_ARG;
+    if (x->x && (x->x_fp8 || x->x_scales)) return EP_ERR_ARG;
+    if (!x->x_fp8 != !x->x_scales || (x->x_fp8 && k_dim % 128 != 0)) return EP_ERR_ARG;
+    if (rows > 0 && (!dy || (!x->x && !x->x_fp8))) return EP_ERR_ARG;
+    if (!aligned(dy, 16) || !aligned(x->x, 16) || !aligned(x->x_fp8, 16) || !aligned(x->x_scales, 16) ||
+        !aligned(dw, 16) || !aligned(layout->expert_offsets, 4))
+        return EP_ERR_ARG;
+    if (expert_wgrad_grid(shape->E, n_dim, k_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    return hip_status(launch_expert_wgrad(*shape, *layout, dy, rows, n_dim, x->x, x->x_fp8, x->x_scales, k_dim, dw,
+                                          dtype, static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_few_workspace_bytes(const ep_shape* shape, int32_t F) {
+    if (check_shape(shape) != EP_OK || shape->T > EP_FEW_MAX_TOKENS || F < 8 || F % 8 != 0 || F > EP_MAX_DIM) return 0;
+    return ws_few(*shape, F).total;
+}
+
+int ep_moe_few(const ep_shape* shape, const ep_tokens* tokens, const ep_experts* experts,
+               uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_shape(shape);
+    if (rc != EP_OK) return rc;
+    if (!tokens || !experts || experts->F < 8 || experts->F % 8 != 0) return EP_ERR_ARG;
+    if (shape->T > EP_FEW_MAX_TOKENS || experts->F > EP_MAX_DIM || shape->H > EP_MAX_DIM) return EP_ERR_UNSUPPORTED;
+    if (!ws || !aligned(ws, 256) || ws_bytes < ws_few(*shape, experts->F).total) return EP_ERR_ARG;
+    const ep_experts& x = *experts;
+    const bool bf16 = x.w13 && x.w2 && !x.w13_fp8 && !x.w2_fp8 && !x.w13_scales && !x.w2_scales;
+    const bool fp8 = x.w13_fp8 && x.w2_fp8 && x.w13_scales && x.w2_scales && !x.w13 && !x.w2;
+    if (!bf16 && !fp8) return EP_ERR_ARG;
+    if (fp8 && (x.F % 128 != 0 || shape->H % 128 != 0)) return EP_ERR_ARG;
+    if (shape->T > 0 && (!tokens->x || !tokens->topk_idx || !tokens->topk_weights || !out)) return EP_ERR_ARG;
+    if (!aligned(tokens->x, 16) || !aligned(tokens->topk_idx, 8) || !aligned(tokens->topk_weights, 4) ||
+        !aligned(out, 16) || !aligned(x.w13, 16) || !aligned(x.w2, 16) || !aligned(x.w13_fp8, 16) ||
+        !aligned(x.w2_fp8, 16) || !aligned(x.w13_scales, 16) || !aligned(x.w2_scales, 16))
+        return EP_ERR_ARG;
+    return hip_status(launch_moe_few(*shape, *tokens, x, out, static_cast<char*>(ws),
+                                     static_cast<hipStream_t>(stream)));
+}
+
 int ep_clear_errors(void* ws, void* stream) {
     if (!ws || !aligned(ws, 256)) return EP_ERR_ARG;
     hipLaunchKernelGGL(clear_error_kernel, dim3(1), dim3(1), 0, static_cast<hipStream_t>(stream),

@@ -107,6 +107,31 @@ hipError_t launch_copy_epilogue(const ep_shape& s, const ep_sources& src, const 
 // Send and copy epilogue in one launch (records' pieces as in tokens).
 hipError_t launch_source_fused(const ep_shape& s, const ep_sources& src, const ep_tokens& tk,
                                uint32_t epoch, void* staging, const ep_recv& rv, char* ws, hipStream_t st);
+
+// Expert products (rows already fits 31 bits).
+int64_t expert_matmul_grid(int64_t rows, int E, int n_dim);
+int64_t expert_swiglu_grid(int64_t rows, int E, int F);
+int64_t expert_wgrad_grid(int E, int n_dim, int k_dim);
+hipError_t launch_expert_matmul(const ep_shape& s, const ep_layout& L, const uint16_t* x, int64_t rows, int k_dim,
+                                const uint16_t* w, int n_dim, int order, uint16_t* y, char* ws, hipStream_t st);
+hipError_t launch_expert_swiglu(const ep_shape& s, const ep_layout& L, const uint16_t* x, int64_t rows,
+                                const uint16_t* w13, int F, uint16_t* act, uint8_t* gu, float* scales, char* ws,
+                                hipStream_t st);
+hipError_t launch_swiglu_grad(const ep_shape& s, const ep_layout& L, int F, const uint8_t* gu, const float* scales,
+                              const uint16_t* d_act, int64_t rows, const float* w, uint16_t* d_gu, uint16_t* act_w,
+                              float* d_w, char* ws, hipStream_t st);
+hipError_t launch_expert_wgrad(const ep_shape& s, const ep_layout& L, const uint16_t* dy, int64_t rows, int n_dim,
+                               const uint16_t* x, const uint8_t* x8, const float* x_scales, int k_dim, void* dw,
+                               int dtype, char* ws, hipStream_t st);
+
+// Workspace of the few-token layer: error words, the number of used experts
+// and their ids, (expert, token) routes, the inner activations [T*K][F] bf16.
+struct WsFew {
+    size_t used, routes, act, total;
+};
+WsFew ws_few(const ep_shape& s, int F);
+hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_experts& x, uint16_t* out, char* ws,
+                          hipStream_t st);
 constexpr uint32_t kSourceFusedTimeoutUs = 100000;  // longest wait for one batch flag of that launch
 
 }  // namespace ep

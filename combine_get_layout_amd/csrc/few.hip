@@ -1,0 +1,411 @@
+// few.hip -- ep_moe_few on gfx950: the whole expert layer for a few tokens in
+// two launches.
+//
+//   act[t][e] = silu(W13g[e] x[t]) * (W13u[e] x[t])          (first launch)
+//   out[t]    = sum over the experts e of t of w[t][e] * W2[e] act[t][e]
+//
+// Bound: the used experts' weights are read once from HBM; every other array
+// is small and stays in L2.
+#include <algorithm>
+
+#include "ep_internal.h"
+#include "ep_mfma.h"
+
+namespace ep {
+namespace {
+
+constexpr int kFewThreads = 512;
+constexpr int kFewWaves = kFewThreads / kWave;
+constexpr int kUpCols = 32;    // values of f per workgroup of the first launch
+constexpr int kDownCols = 16;  // values of h per workgroup of the second
+constexpr int kDownSpan = 256; // contracted values per unit of work of the second launch
+
+// One (used expert, token) pair: the token's first lane with that expert (-1:
+// none) and the sum of its lanes' weights.
+struct Route {
+    int lane;
+    float w;
+};
+
+struct FewArgs {
+    int T, H, K, E, F;
+    const uint16_t* x;
+    const int64_t* topk;
+    const float* topk_w;
+    const char* w13;
+    const float* s13;
+    const char* w2;
+    const float* s2;
+    uint16_t* out;
+    uint32_t* err;
+    int* used;        // number of used experts, then their ids
+    Route* routes;    // [used][T]
+    uint16_t* act;    // [T*K][F], row = first lane of (token, expert)
+};
+
+__device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// Eight e4m3 bytes to bf16, exactly.
+__device__ __forceinline__ bf16x8 e4m3_to_bf16(uint32_t lo, uint32_t hi) {
+    bf16x8 r;
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1];
+    r[4] = c[0], r[5] = c[1], r[6] = d[0], r[7] = d[1];
+    return r;
+}
+
+// The blockIdx.y-th used expert in ascending order (-1 if there are fewer)
+// and its tokens in ascending order. Each workgroup finds them for itself:
+// the ids are a few KB in L2.
+struct Found {
+    int expert, used, tokens;
+};
+__device__ __forceinline__ Found find_expert(const FewArgs& a, uint32_t* bits, short* token, int* scratch) {
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+    if (tid < EP_MAX_EXPERTS / 32) bits[tid] = 0u;
+    __syncthreads();
+    for (int i = tid; i < a.T * a.K; i += kFewThreads) {
+        const int64_t e = a.topk[i];
+        if (expert_ok(e, a.E)) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    const uint64_t word = (uint64_t)bits[2 * lane] | (uint64_t)bits[2 * lane + 1] << 32;
+    const int n = __popcll(word);
+    int sum = n;
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int v = __shfl_up(sum, d);
+        if (lane >= d) sum += v;
+    }
+    Found f;
+    f.used = readlane(sum, kWave - 1);
+    f.expert = -1;
+    f.tokens = 0;
+    const int want = blockIdx.y;
+    const uint64_t in = __ballot(want >= sum - n && want < sum);
+    if (!in) return f;
+    const int src = __ffsll((unsigned long long)in) - 1;
+    uint64_t w = (uint64_t)(uint32_t)readlane((int)word, src) | (uint64_t)(uint32_t)readlane((int)(word >> 32), src) << 32;
+    for (int skip = want - readlane(sum - n, src); skip > 0; --skip) w &= w - 1;
+    f.expert = src * 64 + __ffsll((unsigned long long)w) - 1;
+
+    bool mine = false;
+    if (wave < 2) {
+        Route r = {-1, 0.f};
+        if (tid < a.T) {
+            for (int k = 0; k < a.K; ++k) {
+                if (a.topk[tid * a.K + k] != f.expert) continue;
+                if (r.lane < 0) r.lane = k;
+                r.w += a.topk_w[tid * a.K + k];
+            }
+            if (blockIdx.x == 0) a.routes[(int64_t)want * a.T + tid] = r;
+        }
+        mine = r.lane >= 0;
+        const uint64_t m = __ballot(mine);
+        if (wave == 0 && lane == 0) scratch[0] = __popcll(m);
+        if (wave == 1 && lane == 0) scratch[1] = __popcll(m);
+        scratch[2 + tid] = mine ? r.lane : -1;
+    }
+    __syncthreads();
+    if (wave < 2 && mine) {
+        const uint64_t m = __ballot(true);
+        const int at = (wave ? scratch[0] : 0) + __popcll(m & ((1ull << lane) - 1));
+        token[at] = (short)tid;
+    }
+    f.tokens = scratch[0] + scratch[1];
+    __syncthreads();
+    return f;
+}
+
+// First launch: workgroup (x, y) computes 32 values of f for the tokens of the
+// y-th used expert: 64 weight rows (32 gate, 32 up) in four 16-row tiles, the
+// contracted axis H cut into steps that the 8 waves take in turn. Weights go
+// straight from memory into the registers of the matrix instruction (each is
+// used once, so LDS would only add a trip); the tokens' values come from L2.
+struct UpShared {
+    uint32_t bits[EP_MAX_EXPERTS / 32];
+    short token[128];
+    int scratch[2 + 128];
+    float part[kFewWaves][4][16][17];
+};
+
+// Tokens [t0, t0 + 16 * NT) of the expert's list, all NT tiles in use.
+template <bool FP8, int NT>
+__device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, UpShared& sh, int t0) {
+    constexpr int kStep = FP8 ? 128 : 64, kX = FP8 ? 4 : 2, kBytes = FP8 ? 1 : 2;
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+    const int i = lane & 15, q = lane >> 4;
+    const int f0 = blockIdx.x * kUpCols, cols = min(kUpCols, a.F - f0);
+    const uint32_t ld = (uint32_t)a.H * kBytes;
+    const char* w = a.w13 + ((int64_t)found.expert * 2 * a.F + f0) * ld;
+    // Gate rows, up rows and the tokens' rows; rows past F read as zeros.
+    const auto d_gate = buf_resource(w, cols * ld), d_up = buf_resource(w + (int64_t)a.F * ld, cols * ld);
+    const auto d_x = buf_resource(a.x, (uint32_t)a.T * a.H * 2);
+    const uint32_t row0 = i * ld + q * 16, row1 = row0 + 16 * ld;
+    const int blocks = a.H / 128;
+    const float* sc = FP8 ? a.s13 + ((int64_t)found.expert * 2 * a.F + min(f0 + i, a.F - 1)) * blocks : nullptr;
+    const int64_t sc1 = (int64_t)(min(f0 + 16 + i, a.F - 1) - min(f0 + i, a.F - 1)) * blocks;
+    const int64_t sc_up = (int64_t)a.F * blocks;
+    const int steps = (a.H + kStep - 1) / kStep;
+    uint32_t xr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        xr[n] = (uint32_t)sh.token[min(t0 + n * 16 + i, found.tokens - 1)] * a.H * 2 + q * (FP8 ? 32 : 16);
+    f32x4 acc[4][NT] = {};
+    // One step's loads at a time: the other waves' loads (three or more to a
+    // SIMD) cover the wait.
+    for (int s = wave; s < steps; s += kFewWaves) {
+        u32x4 wv[4][2], xv[NT][kX];
+        float sv[4];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t at = s * 128 + p * 64;  // bytes of a weight row
+            // Values past H (the last step of a bf16 row): past the end.
+            const uint32_t far = !FP8 && s * kStep + (p * 4 + q) * 8 >= a.H ? kBufFar : 0u;
+            wv[0][p] = buf_load16(d_gate, row0 + far, at);
+            wv[1][p] = buf_load16(d_gate, row1 + far, at);
+            wv[2][p] = buf_load16(d_up, row0 + far, at);
+            wv[3][p] = buf_load16(d_up, row1 + far, at);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < kX / 2; ++h)
+                    xv[n][p * (kX / 2) + h] = buf_load16(d_x, xr[n] + far, at * (FP8 ? 2 : 1) + h * 16);
+        }
+        if constexpr (FP8) {
+            sv[0] = sc[s];
+            sv[1] = sc[sc1 + s];
+            sv[2] = sc[sc_up + s];
+            sv[3] = sc[sc_up + sc1 + s];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            bf16x8 wf[kX];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                if constexpr (FP8) {
+                    wf[2 * p] = e4m3_to_bf16(wv[r][p][0], wv[r][p][1]);
+                    wf[2 * p + 1] = e4m3_to_bf16(wv[r][p][2], wv[r][p][3]);
+                } else {
+                    wf[p] = as_bf16(wv[r][p]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                f32x4 c = {};
+                if constexpr (!FP8) c = acc[r][n];
+#pragma unroll
+                for (int p = 0; p < kX; ++p) c = mfma_bf16(as_bf16(xv[n][p]), wf[p], c);
+                if constexpr (FP8) {
+                    // The block's scale on the 32-bit sum: the products of
+                    // e4m3 values themselves are not rounded.
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(sv[r], c[j], acc[r][n][j]);
+                } else {
+                    acc[r][n] = c;
+                }
+            }
+        }
+    }
+    settle(acc);
+    // Sum the waves' parts: thread -> (token of 16, f of 32).
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sh.part[wave][r][q * 4 + j][i] = acc[r][n][j];
+        __syncthreads();
+        const int tk = tid >> 5, c = tid & 31;
+        const int at = t0 + n * 16 + tk, f = f0 + c;
+        if (at < found.tokens && f < a.F) {
+            float g = 0.f, u = 0.f;
+#pragma unroll
+            for (int v = 0; v < kFewWaves; ++v) {
+                g += sh.part[v][c >> 4][tk][c & 15];
+                u += sh.part[v][2 + (c >> 4)][tk][c & 15];
+            }
+            const float r = g / (1.0f + __expf(-g)) * u;
+            const int t = sh.token[at];
+            // Rounded to bf16 for the second product's matrix instruction.
+            a.act[((int64_t)t * a.K + sh.scratch[2 + t]) * a.F + f] = (uint16_t)f32_to_bf16(r);
+        }
+        __syncthreads();
+    }
+}
+
+template <bool FP8, int NT>
+__global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_up_kernel(FewArgs a) {
+    __shared__ UpShared sh;
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.err[0] = 0u;
+    const Found found = find_expert(a, sh.bits, sh.token, sh.scratch);
+    if (blockIdx.x == 0 && tid == 0) {
+        if (blockIdx.y == 0) a.used[0] = found.used;
+        if (found.expert >= 0) a.used[1 + blockIdx.y] = found.expert;
+    }
+    if (found.expert < 0) return;
+    if constexpr (NT == 1) {
+        up_tokens<FP8, 1>(a, found, sh, 0);
+    } else {
+        for (int t0 = 0; t0 < found.tokens; t0 += 64) {
+            const int left = found.tokens - t0;
+            if (left > 48)
+                up_tokens<FP8, 4>(a, found, sh, t0);
+            else if (left > 32)
+                up_tokens<FP8, 3>(a, found, sh, t0);
+            else if (left > 16)
+                up_tokens<FP8, 2>(a, found, sh, t0);
+            else
+                up_tokens<FP8, 1>(a, found, sh, t0);
+        }
+    }
+}
+
+// Second launch: workgroup x computes 16 values of h for every token. Unit u =
+// (used expert, span of 256 values of f); the 8 waves take the units in turn. A
+// unit's product goes into a temporary and is then added, weighted, to the
+// tokens routed to its expert alone, so that an expert's infinities or NaN
+// stay with its own tokens.
+template <bool FP8, int NT>
+__global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_down_kernel(FewArgs a) {
+    constexpr int kLoads = FP8 ? 4 : 8, kBytes = FP8 ? 1 : 2;
+    __shared__ float part[kFewWaves][NT][16][17];
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+    if (blockIdx.x == 0) {
+        bool bad = false;
+        for (int n = tid; n < a.T * a.K; n += kFewThreads) bad |= expert_bad(a.topk[n], a.E);
+        if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_EXPERT_ID);
+    }
+    const int i = lane & 15, q = lane >> 4;
+    const int h0 = blockIdx.x * kDownCols;
+    const int hr = min(h0 + i, a.H - 1);
+    const int spans = (a.F + kDownSpan - 1) / kDownSpan;
+    const int units = a.used[0] * spans;
+    const int nt = (a.T + 15) / 16;
+    f32x4 acc[NT] = {};
+    struct Buf {
+        u32x4 w[kLoads];
+        float s[2];
+    };
+    auto load = [&](Buf& b, int u) {
+        const int rank = u / spans, span = u % spans;
+        const int64_t e = a.used[1 + rank];
+        const char* p = a.w2 + (e * a.H + hr) * a.F * kBytes;
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+            const int k = span * kDownSpan + (n * 4 + q) * (16 / kBytes);
+            const bool in = k < a.F;
+            b.w[n] = ld16(p + (in ? k : 0) * kBytes);
+            if (!in) b.w[n] = zero;
+        }
+        if constexpr (FP8) {
+            const float* s = a.s2 + (e * a.H + hr) * (a.F / 128) + span * 2;
+            b.s[0] = s[0];
+            b.s[1] = span * kDownSpan + 128 < a.F ? s[1] : 0.f;
+        }
+    };
+    auto compute = [&](const Buf& b, int u) {
+        const int rank = u / spans, span = u % spans;
+        const Route* routes = a.routes + (int64_t)rank * a.T;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (NT > 1 && n >= nt) continue;
+            const int t = n * 16 + i;
+            const int k1 = t < a.T ? routes[t].lane : -1;
+            if (!__ballot(k1 >= 0)) continue;
+            const uint16_t* p = a.act + ((int64_t)min(t, a.T - 1) * a.K + max(k1, 0)) * a.F;
+            f32x4 c[1][2] = {};
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                int k;
+                if constexpr (FP8)
+                    k = span * kDownSpan + ((m >> 1) * 4 + q) * 16 + (m & 1) * 8;
+                else
+                    k = span * kDownSpan + (m * 4 + q) * 8;
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (k1 >= 0 && k < a.F) v = ld16(p + k);
+                bf16x8 wf;
+                if constexpr (FP8)
+                    wf = e4m3_to_bf16(b.w[m >> 1][(m & 1) * 2], b.w[m >> 1][(m & 1) * 2 + 1]);
+                else
+                    wf = as_bf16(b.w[m]);
+                // FP8: the first four fragments are the span's first block of 128.
+                c[0][FP8 ? m >> 2 : 0] = mfma_bf16(as_bf16(v), wf, c[0][FP8 ? m >> 2 : 0]);
+            }
+            settle(c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int tj = n * 16 + q * 4 + j;
+                const Route r = tj < a.T ? routes[tj] : Route{-1, 0.f};
+                const float v = FP8 ? fmaf(b.s[1], c[0][1][j], b.s[0] * c[0][0][j]) : c[0][0][j];
+                if (r.lane >= 0) acc[n][j] = fmaf(r.w, v, acc[n][j]);
+            }
+        }
+    };
+    for (int u = wave; u < units; u += kFewWaves) {
+        Buf b;
+        load(b, u);
+        compute(b, u);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if (NT > 1 && n >= nt) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[wave][n][q * 4 + j][i] = acc[n][j];
+    }
+    __syncthreads();
+    for (int n = tid; n < nt * 256; n += kFewThreads) {
+        const int t = n >> 4, h = h0 + (n & 15);
+        if (t >= a.T || h >= a.H) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) v += part[w][t >> 4][t & 15][n & 15];
+        a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
+    }
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+WsFew ws_few(const ep_shape& s, int F) {
+    WsFew w;
+    const size_t lanes = (size_t)s.T * s.K, used = std::min<size_t>(s.E, lanes);
+    w.used = 256;
+    w.routes = w.used + align256(4 * (1 + used));
+    w.act = w.routes + align256(sizeof(Route) * used * s.T);
+    w.total = w.act + align256(2 * lanes * F);
+    return w;
+}
+
+hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_experts& x, uint16_t* out, char* ws,
+                          hipStream_t st) {
+    uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+    if (s.T == 0) {
+        hipError_t e = launch_zero_words(err, 1, st);
+        return e != hipSuccess ? e : hipGetLastError();
+    }
+    const WsFew l = ws_few(s, x.F);
+    const bool fp8 = x.w13_fp8 != nullptr;
+    const FewArgs a = {s.T, s.H, s.K, s.E, x.F, tk.x, tk.topk_idx, tk.topk_weights,
+                       fp8 ? (const char*)x.w13_fp8 : (const char*)x.w13, x.w13_scales,
+                       fp8 ? (const char*)x.w2_fp8 : (const char*)x.w2, x.w2_scales, out, err,
+                       reinterpret_cast<int*>(ws + l.used), reinterpret_cast<Route*>(ws + l.routes),
+                       reinterpret_cast<uint16_t*>(ws + l.act)};
+    const dim3 up((x.F + kUpCols - 1) / kUpCols, (unsigned)std::min<int64_t>(s.E, (int64_t)s.T * s.K));
+    const dim3 down((s.H + kDownCols - 1) / kDownCols);
+    void (*const ups[2][2])(FewArgs) = {{few_up_kernel<false, 1>, few_up_kernel<false, 4>},
+                                        {few_up_kernel<true, 1>, few_up_kernel<true, 4>}};
+    void (*const downs[2][2])(FewArgs) = {{few_down_kernel<false, 1>, few_down_kernel<false, 8>},
+                                          {few_down_kernel<true, 1>, few_down_kernel<true, 8>}};
+    const int many = s.T > 16;
+    hipLaunchKernelGGL(ups[fp8][many], up, dim3(kFewThreads), 0, st, a);
+    hipLaunchKernelGGL(downs[fp8][many], down, dim3(kFewThreads), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -25,6 +25,9 @@ EP_FUSED_WITHHOLD = 1
 EP_SEG_BF16, EP_SEG_FP8, EP_SEG_SCALES = 1, 2, 4
 EP_FMT_PLAIN, EP_FMT_CHUNKED = 0, 1
 EP_HIER_SCALEOUT, EP_HIER_FORWARD = 1, 2
+EP_WEIGHT_NK, EP_WEIGHT_KN = 0, 1
+EP_GRAD_BF16, EP_GRAD_F32 = 0, 1
+EP_FEW_MAX_TOKENS = 128
 
 _P = ctypes.c_void_p
 
@@ -62,14 +65,24 @@ class ep_sources(ctypes.Structure):
                 ("recv_offsets", _P), ("src_slot", _P)]
 
 
+class ep_rows(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("x", "x_fp8", "x_scales")]
+
+
+class ep_experts(ctypes.Structure):
+    _fields_ = [("F", ctypes.c_int32)] + [(n, _P) for n in ("w13", "w2", "w13_fp8", "w13_scales",
+                                                            "w2_fp8", "w2_scales")]
+
+
 EXPORTS = ("ep_workspace_bytes", "ep_record_bytes", "ep_chunked_record_bytes", "ep_get_layout",
            "ep_get_layout_noalloc",
            "ep_dispatch", "ep_dispatch_expand", "ep_hierarchical_dispatch",
            "ep_hierarchical_dispatch_fused", "ep_combine",
            "ep_combine_expand", "ep_partial_row_bytes", "ep_combine_two_level",
            "ep_source_workspace_bytes", "ep_source_layout", "ep_source_dispatch",
-           "ep_copy_epilogue", "ep_source_dispatch_fused", "ep_clear_errors", "ep_check_errors",
-           "ep_check_sticky_errors",
+           "ep_copy_epilogue", "ep_source_dispatch_fused", "ep_expert_matmul", "ep_expert_swiglu",
+           "ep_swiglu_grad", "ep_expert_wgrad", "ep_few_workspace_bytes", "ep_moe_few",
+           "ep_clear_errors", "ep_check_errors", "ep_check_sticky_errors",
            "ep_status_string")
 
 _lib = None
@@ -115,6 +128,14 @@ def lib() -> ctypes.CDLL:
                                    _P]
     L.ep_source_dispatch_fused.argtypes = [sp, xp, ctypes.POINTER(ep_tokens), u32, _P,
                                            ctypes.POINTER(ep_recv), _P, sz, _P]
+    i32, ci = ctypes.c_int32, ctypes.c_int
+    L.ep_expert_matmul.argtypes = [sp, lp, _P, i64, i32, _P, i32, ci, _P, _P, sz, _P]
+    L.ep_expert_swiglu.argtypes = [sp, lp, _P, i64, _P, i32, _P, _P, _P, _P, sz, _P]
+    L.ep_swiglu_grad.argtypes = [sp, lp, i32, _P, _P, _P, i64, _P, _P, _P, _P, _P, sz, _P]
+    L.ep_expert_wgrad.argtypes = [sp, lp, _P, i64, i32, ctypes.POINTER(ep_rows), i32, _P, ci, _P, sz, _P]
+    L.ep_few_workspace_bytes.argtypes = [sp, i32]
+    L.ep_few_workspace_bytes.restype = sz
+    L.ep_moe_few.argtypes = [sp, ctypes.POINTER(ep_tokens), ctypes.POINTER(ep_experts), _P, _P, sz, _P]
     L.ep_clear_errors.argtypes = [_P, _P]
     L.ep_check_errors.argtypes = [_P, _P, ctypes.POINTER(u32)]
     L.ep_check_sticky_errors.argtypes = [_P, _P, ctypes.POINTER(u32)]
@@ -123,7 +144,9 @@ def lib() -> ctypes.CDLL:
     for f in ("ep_get_layout", "ep_get_layout_noalloc", "ep_dispatch", "ep_dispatch_expand",
               "ep_hierarchical_dispatch", "ep_hierarchical_dispatch_fused",
               "ep_combine", "ep_combine_expand", "ep_combine_two_level", "ep_source_layout",
-              "ep_source_dispatch", "ep_copy_epilogue", "ep_source_dispatch_fused", "ep_clear_errors",
+              "ep_source_dispatch", "ep_copy_epilogue", "ep_source_dispatch_fused",
+              "ep_expert_matmul", "ep_expert_swiglu", "ep_swiglu_grad", "ep_expert_wgrad",
+              "ep_moe_few", "ep_clear_errors",
               "ep_check_errors",
               "ep_check_sticky_errors"):
         getattr(L, f).restype = ctypes.c_int
@@ -376,6 +399,71 @@ def ep_source_dispatch_fused(shape, sources: dict, tokens: dict, epoch: int, sta
         *_ws(ws), _stream(stream)), "ep_source_dispatch_fused")
 
 
+def ep_expert_matmul(shape, layout: dict, x, rows: int, k_dim: int, w, n_dim: int, w_order: int, y, ws,
+                     stream=None):
+    L = _layout_struct(shape, layout)
+    n = max(int(rows), 0)
+    _check(lib().ep_expert_matmul(ctypes.byref(shape), ctypes.byref(L), _ptr(x, "x", 2 * n * k_dim),
+                                  int(rows), int(k_dim), _ptr(w, "w", 2 * shape.E * n_dim * k_dim),
+                                  int(n_dim), int(w_order), _ptr(y, "y", 2 * n * n_dim), *_ws(ws),
+                                  _stream(stream)), "ep_expert_matmul")
+
+
+def ep_expert_swiglu(shape, layout: dict, x, rows: int, w13, F: int, act, gu_fp8, gu_scales, ws,
+                     stream=None):
+    L = _layout_struct(shape, layout)
+    n = max(int(rows), 0)
+    _check(lib().ep_expert_swiglu(ctypes.byref(shape), ctypes.byref(L), _ptr(x, "x", 2 * n * shape.H),
+                                  int(rows), _ptr(w13, "w13", 4 * shape.E * F * shape.H), int(F),
+                                  _ptr(act, "act", 2 * n * F), _ptr(gu_fp8, "gu_fp8", 2 * n * F),
+                                  _ptr(gu_scales, "gu_scales", 8 * n * (F // 128)), *_ws(ws),
+                                  _stream(stream)), "ep_expert_swiglu")
+
+
+def ep_swiglu_grad(shape, layout: dict, F: int, gu_fp8, gu_scales, d_act, rows: int, topk_weights, d_gu,
+                   act_w, d_topk_weights, ws, stream=None):
+    L = _layout_struct(shape, layout)
+    n, lanes = max(int(rows), 0), shape.T * shape.K
+    _check(lib().ep_swiglu_grad(ctypes.byref(shape), ctypes.byref(L), int(F),
+                                _ptr(gu_fp8, "gu_fp8", 2 * n * F),
+                                _ptr(gu_scales, "gu_scales", 8 * n * (F // 128)),
+                                _ptr(d_act, "d_act", 2 * n * F), int(rows),
+                                _ptr(topk_weights, "topk_weights", 4 * lanes),
+                                _ptr(d_gu, "d_gu", 4 * n * F), _ptr(act_w, "act_w", 2 * n * F),
+                                _ptr(d_topk_weights, "d_topk_weights", 4 * lanes), *_ws(ws),
+                                _stream(stream)), "ep_swiglu_grad")
+
+
+def ep_expert_wgrad(shape, layout: dict, dy, rows: int, n_dim: int, x: dict, k_dim: int, dw, dtype: int,
+                    ws, stream=None):
+    """x: {"x": bf16 rows} or {"x_fp8": e4m3 rows, "x_scales": scales}."""
+    L = _layout_struct(shape, layout)
+    n = max(int(rows), 0)
+    X = ep_rows(_ptr(x.get("x"), "x", 2 * n * k_dim), _ptr(x.get("x_fp8"), "x_fp8", n * k_dim),
+                _ptr(x.get("x_scales"), "x_scales", 4 * n * (k_dim // 128)))
+    size = 4 if int(dtype) == EP_GRAD_F32 else 2
+    _check(lib().ep_expert_wgrad(ctypes.byref(shape), ctypes.byref(L), _ptr(dy, "dy", 2 * n * n_dim),
+                                 int(rows), int(n_dim), ctypes.byref(X), int(k_dim),
+                                 _ptr(dw, "dw", size * shape.E * n_dim * k_dim), int(dtype), *_ws(ws),
+                                 _stream(stream)), "ep_expert_wgrad")
+
+
+def ep_few_workspace_bytes(shape: ep_shape, F: int) -> int:
+    return int(lib().ep_few_workspace_bytes(ctypes.byref(shape), int(F)))
+
+
+def ep_moe_few(shape, tokens: dict, experts: dict, out, ws, stream=None):
+    """experts: {"F", "w13", "w2"} (bf16) or {"F", "w13_fp8", "w13_scales",
+    "w2_fp8", "w2_scales"}."""
+    tk = _tokens_struct(shape, tokens)
+    E, H, F = shape.E, shape.H, int(experts["F"])
+    need = dict(w13=4 * E * F * H, w2=2 * E * H * F, w13_fp8=2 * E * F * H,
+                w13_scales=8 * E * F * (H // 128), w2_fp8=E * H * F, w2_scales=4 * E * H * (F // 128))
+    X = ep_experts(F, *[_ptr(experts.get(n), n, need[n]) for n in need])
+    _check(lib().ep_moe_few(ctypes.byref(shape), ctypes.byref(tk), ctypes.byref(X),
+                            _ptr(out, "out", 2 * shape.T * H), *_ws(ws), _stream(stream)), "ep_moe_few")
+
+
 def ep_clear_errors(ws, stream=None):
     _check(lib().ep_clear_errors(_ptr(ws, "workspace"), _stream(stream)), "ep_clear_errors")
 
@@ -420,6 +508,14 @@ def alloc_source_workspace(shape: ep_shape, S: int, device="cuda") -> torch.Tens
     n = ep_source_workspace_bytes(shape, S)
     if n == 0:
         raise RuntimeError("ep_source_workspace_bytes: unsupported shape or source count")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_few_workspace(shape: ep_shape, F: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of ep_moe_few."""
+    n = ep_few_workspace_bytes(shape, F)
+    if n == 0:
+        raise RuntimeError("ep_few_workspace_bytes: unsupported shape or inner size")
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 

@@ -76,7 +76,18 @@ extern "C" {
 #define EP_HIER_SCALEOUT 1 /* step 1: one write per (token, destination group) */
 #define EP_HIER_FORWARD 2  /* step 2: forward group rows to scale-up peers */
 
+/* Order of an expert's weight matrix (ep_expert_matmul): rows of the
+ * contracted index, or rows of the produced one. */
+#define EP_WEIGHT_NK 0 /* w[e][n][k]: y = x * w[e]^T (forward) */
+#define EP_WEIGHT_KN 1 /* w[e][k][n]: y = x * w[e]   (gradient of the rows) */
+
+/* Element type of a weight gradient (ep_expert_wgrad). */
+#define EP_GRAD_BF16 0
+#define EP_GRAD_F32 1
+
 /* Supported limits (EP_ERR_UNSUPPORTED beyond them). */
+#define EP_FEW_MAX_TOKENS 128 /* tokens of ep_moe_few */
+#define EP_MAX_DIM (1 << 20)  /* columns of the expert products' matrices */
 #define EP_MAX_TOPK 64
 #define EP_MAX_RANKS 1024
 #define EP_MAX_GROUPS 256
@@ -424,6 +435,121 @@ int ep_copy_epilogue(const ep_shape *shape, const ep_sources *sources, const voi
 int ep_source_dispatch_fused(const ep_shape *shape, const ep_sources *sources, const ep_tokens *tokens,
                              uint32_t epoch, void *staging, const ep_recv *recv, void *ws,
                              size_t ws_bytes, void *stream);
+
+/* ---- Expert products -------------------------------------------------------
+ * What runs between dispatch and combine: the experts' two-layer network with
+ * a SwiGLU gate,
+ *   expert(x) = W2 (silu(G) * U),  [G; U] = W13 x,  silu(v) = v / (1 + exp(-v)),
+ * on the expand-mode rows that ep_dispatch_expand writes ([V2] §3.3 阶段3: rows
+ * grouped by expert for the expert GEMMs), its gradients, and for a few
+ * tokens the whole layer in two launches without dispatch and combine.
+ *
+ * Rows of expert e are [expert_offsets[e], expert_offsets[e+1]) of the given
+ * arrays, which hold `rows` rows; rows at and past expert_offsets[E] are
+ * neither read nor written, rows >= `rows` are left out and set
+ * EP_DEVERR_CAPACITY. An expert may have no rows. Sums are held in 32 bits and
+ * rounded once to the output's type (round to nearest even). Matrix
+ * dimensions are multiples of 8 up to EP_MAX_DIM; all arrays here need 16 B
+ * aligned base pointers, except topk_weights and its gradient (4 B). Outputs
+ * must not overlap inputs. Calls that only use the workspace for its error
+ * words (all but ep_moe_few) may overlap on one workspace.
+ *
+ * A whole training step of a layer, from these calls:
+ *   forward   ep_get_layout, ep_dispatch_expand, ep_expert_swiglu (act and the
+ *             8-bit checkpoint), ep_expert_matmul (W2, NK), ep_combine_expand
+ *   backward  ep_dispatch_expand of the output's gradient (rows d_y),
+ *             ep_expert_matmul (d_y, W2, KN -> d_act), ep_swiglu_grad (-> d_gu,
+ *             w * act, d_topk_weights), ep_expert_wgrad (d_y, w * act -> dW2),
+ *             ep_expert_wgrad (d_gu, x -> dW13; x the dispatched bf16 or FP8
+ *             rows), ep_expert_matmul (d_gu, W13, KN -> d_x rows),
+ *             ep_combine_expand of those with weights of 1. */
+
+/* Rows times the experts' matrices: for each row i of expert e,
+ *   y[i][n] = bf16_rne(sum_k x[i][k] * w[e][n][k])   (EP_WEIGHT_NK)
+ *   y[i][n] = bf16_rne(sum_k x[i][k] * w[e][k][n])   (EP_WEIGHT_KN)
+ * x: [rows][k_dim] bf16, y: [rows][n_dim] bf16. Needs layout->expert_offsets. */
+int ep_expert_matmul(const ep_shape *shape, const ep_layout *layout, const uint16_t *x, int64_t rows,
+                     int32_t k_dim, const uint16_t *w, int32_t n_dim, int w_order, uint16_t *y,
+                     void *ws, size_t ws_bytes, void *stream);
+
+/* Gate/up product with SwiGLU in one pass, and the 8-bit checkpoint that its
+ * gradient reads: for each row i of expert e, in 32 bits,
+ *   g = x[i] * w13[e][0:F]^T, u = x[i] * w13[e][F:2F]^T,
+ *   act[i] = bf16_rne(silu(g) * u);
+ * and, when gu_fp8 is non-NULL, for every block of 128 values of [g, u]:
+ *   gu_scales = m / 448, m the block's largest magnitude (1 if m < 1e-33)
+ *   gu_fp8 = e4m3_rne(v * (1 / gu_scales)).
+ * A block that holds an infinity or NaN keeps no finite meaning: its infinite
+ * values (with an infinity, all its values) read back as NaN.
+ * x: [rows][H], w13: [E][2F][H] (gate rows, then up rows), act: [rows][F] bf16;
+ * gu_fp8: [rows][2F], gu_scales: [rows][2F/128], both or neither (F % 128 ==
+ * 0 with them). 4 * F * H must stay below 2^31 - 16 (EP_ERR_UNSUPPORTED). */
+int ep_expert_swiglu(const ep_shape *shape, const ep_layout *layout, const uint16_t *x, int64_t rows,
+                     const uint16_t *w13, int32_t F, uint16_t *act, uint8_t *gu_fp8, float *gu_scales,
+                     void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of the SwiGLU from the checkpoint. For each lane (t, k) with row i
+ * = layout->expert_slot[t*K+k] >= 0 and weight w = topk_weights[t*K+k], with g
+ * and u the values that the checkpoint stands for, s = 1 / (1 + exp(-g)) and d
+ * = d_act[i] (the gradient of the row's expert output, without w, times W2):
+ *   d_gu[i]  = bf16_rne([w d u s (1 + g (1 - s)), w d g s])
+ *   act_w[i] = bf16_rne(w g s u)         (the rows that W2's gradient takes)
+ *   d_topk_weights[t*K+k] = sum_f d g s u  (0 for a lane without a row)
+ * gu_fp8, gu_scales as written by ep_expert_swiglu; d_act, act_w: [rows][F];
+ * d_gu: [rows][2F]; d_topk_weights: [T*K] fp32. act_w and d_topk_weights may
+ * be NULL. F % 128 == 0. A slot >= rows is left out (EP_DEVERR_CAPACITY) and
+ * its d_topk_weights is 0. */
+int ep_swiglu_grad(const ep_shape *shape, const ep_layout *layout, int32_t F, const uint8_t *gu_fp8,
+                   const float *gu_scales, const uint16_t *d_act, int64_t rows,
+                   const float *topk_weights, uint16_t *d_gu, uint16_t *act_w, float *d_topk_weights,
+                   void *ws, size_t ws_bytes, void *stream);
+
+/* Rows of ep_expert_wgrad's second operand: x, or x_fp8 with x_scales. */
+typedef struct ep_rows {
+    const uint16_t *x;      /* [rows][k_dim] bf16, or NULL */
+    const uint8_t *x_fp8;   /* [rows][k_dim] e4m3, or NULL */
+    const float *x_scales;  /* [rows][k_dim/128] fp32, with x_fp8 */
+} ep_rows;
+
+/* Weight gradient: for every expert e (0 for one without rows)
+ *   dw[e][n][k] = sum over rows i of e of dy[i][n] * x[i][k]
+ * dy: [rows][n_dim] bf16; x: bf16 rows, or the FP8 rows with their scales
+ * that dispatch delivers (k_dim % 128 == 0; each value q * scale is rounded
+ * to bf16 for the matrix instruction). dw: [E][n_dim][k_dim], bf16 or fp32
+ * (dtype EP_GRAD_*), overwritten. */
+int ep_expert_wgrad(const ep_shape *shape, const ep_layout *layout, const uint16_t *dy, int64_t rows,
+                    int32_t n_dim, const ep_rows *x, int32_t k_dim, void *dw, int dtype, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* Weights of the experts: bf16 matrices, or e4m3 ones with one fp32 scale for
+ * each row and 128 columns (the same form for both matrices). */
+typedef struct ep_experts {
+    int32_t F;                 /* inner size, F % 8 == 0 (F % 128 == 0 and H % 128 == 0 for FP8) */
+    const uint16_t *w13;       /* [E][2F][H] bf16: gate rows, then up rows; or NULL */
+    const uint16_t *w2;        /* [E][H][F] bf16, or NULL */
+    const uint8_t *w13_fp8;    /* [E][2F][H] e4m3, or NULL */
+    const float *w13_scales;   /* [E][2F][H/128] */
+    const uint8_t *w2_fp8;     /* [E][H][F] e4m3, or NULL */
+    const float *w2_scales;    /* [E][H][F/128] */
+} ep_experts;
+
+/* Bytes of workspace of ep_moe_few (>= 256; error words at offset 0 as in
+ * ep_workspace_bytes). Host only; 0 on bad args (T > EP_FEW_MAX_TOKENS too). */
+size_t ep_few_workspace_bytes(const ep_shape *shape, int32_t F);
+
+/* The whole expert layer for at most EP_FEW_MAX_TOKENS tokens (decoding),
+ * without layout, dispatch and combine:
+ *   out[t] = bf16_rne(sum over the distinct experts e of t's lanes of
+ *            w * W2[e] bf16_rne(silu(g) * u)),  w = the sum of the weights of
+ *            t's lanes with expert e, [g; u] = W13[e] x[t]
+ * tokens: x, topk_idx and topk_weights required. A token without a valid lane
+ * gets zeros. An expert's non-finite results reach only its own tokens. Starts
+ * a pass: clears error word 0, then sets EP_DEVERR_EXPERT_ID for ids < -1 or
+ * >= E (treated as -1). out: [T*H] bf16. ws: ep_few_workspace_bytes, 256 B
+ * aligned, needs no initialisation besides ep_clear_errors; calls on one
+ * workspace must not overlap. */
+int ep_moe_few(const ep_shape *shape, const ep_tokens *tokens, const ep_experts *experts,
+               uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
 /* Clear both workspace error words (a stream-ordered kernel, no memset
  * node). */

@@ -1,0 +1,676 @@
+"""The expert products (ep_expert_matmul, ep_expert_swiglu, ep_swiglu_grad,
+ep_expert_wgrad) and the few-token layer (ep_moe_few) against plain 64-bit
+arithmetic on the CPU.
+
+Tolerances are bounds by arithmetic, computed per element beside each
+reference:
+  - a sum of n products held in 32 bits is off by at most n * 2^-23 * sum|a b|
+    (one unit in the last place a step, which covers either rounding of the
+    matrix instruction's adder);
+  - one rounding to bf16 is off by at most 2^-8 of the value, to e4m3 by 2^-4
+    of it, or by half its smallest step, 2^-10, near zero;
+  - 1 / (1 + exp(-g)) in 32 bits is off by (|g| + 16) * 2^-23 of its value
+    (the argument's scaling to base 2 loses |g| * 2^-24, the rest is a few
+    units in the last place).
+"""
+import numpy as np
+import pytest
+import torch
+
+from combine_get_layout_amd import ep
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, F64, U8, F8 = torch.bfloat16, torch.float32, torch.float64, torch.uint8, torch.float8_e4m3fn
+U23, HALF_BF16, HALF_E4M3 = 2.0 ** -23, 2.0 ** -8, 2.0 ** -4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ep.lib()
+
+
+def randn(g, *shape, scale=1.0):
+    return (torch.randn(shape, generator=g, dtype=F32) * scale).to(BF16)
+
+
+def routing(T, K, E, seed, skip=0.0, skew=0.0, repeat=False):
+    """Expert ids [T, K] (distinct unless `repeat`), and weights."""
+    r = np.random.default_rng(seed)
+    if repeat:
+        idx = r.integers(0, E, size=(T, K))
+    else:
+        keys = r.gumbel(size=(T, E)) - skew * np.log(np.arange(1, E + 1))
+        idx = np.argsort(-keys, axis=1)[:, :K]
+    idx = np.where(r.random((T, K)) < skip, -1, idx).astype(np.int64)
+    w = r.random((T, K)).astype(np.float32) - 0.3  # weights of either sign
+    return torch.from_numpy(idx), torch.from_numpy(w)
+
+
+def grouped(idx, E):
+    """Expand rows of idx in plain Python: offsets, slot, expert of each row."""
+    T, K = idx.shape
+    rows = sorted((int(idx[t, k]), t, k) for t in range(T) for k in range(K) if idx[t, k] >= 0)
+    slot = torch.full((T, K), -1, dtype=torch.int32)
+    for i, (_, t, k) in enumerate(rows):
+        slot[t, k] = i
+    experts = torch.tensor([e for e, _, _ in rows], dtype=torch.int64)
+    counts = torch.bincount(experts, minlength=E) if rows else torch.zeros(E, dtype=torch.int64)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = counts.cumsum(0)
+    return off, slot, experts
+
+
+def per_expert(off, f, like):
+    """Rows [off[e], off[e+1]) of f(e, slice), one after the other."""
+    parts = [f(e, slice(int(off[e]), int(off[e + 1]))) for e in range(len(off) - 1)]
+    return torch.cat(parts) if parts else like
+
+
+def check(got, ref, bound, what):
+    got = got.double().cpu()
+    assert got.shape == ref.shape, what
+    over = (got - ref).abs() - bound
+    worst = over.max().item() if over.numel() else 0.0
+    assert not torch.isnan(got).any(), f"{what}: NaN"
+    assert worst <= 0, f"{what}: {worst:.3g} over its bound at {np.unravel_index(int(over.argmax()), over.shape)}"
+
+
+def gpu(*ts):
+    return [t.cuda() for t in ts]
+
+
+# (tokens, K, E, k_dim, n_dim, options): one row, no row, sizes that fill no
+# tile, tails of every kind of a 256-row tile, skewed and empty experts.
+PRODUCTS = [
+    (1, 1, 1, 8, 8, {}),
+    (1, 2, 4, 64, 256, {}),
+    (5, 3, 7, 72, 264, dict(skip=0.3)),
+    (64, 2, 1 + 1, 136, 520, {}),
+    (129, 2, 3, 200, 96, {}),
+    (300, 2, 2, 320, 512, {}),
+    (700, 4, 5, 128, 248, dict(skew=1.5)),
+    (40, 4, 600, 64, 128, {}),      # more experts than threads in a workgroup
+    (257, 1, 1, 1032, 24, {}),
+    (33, 64, 64, 48, 40, dict(repeat=True)),
+]
+
+
+def product_case(case, seed):
+    T, K, E, k, n, opt = case
+    g = torch.Generator().manual_seed(seed)
+    idx, w = routing(T, K, E, seed, **opt)
+    off, slot, experts = grouped(idx, E)
+    N = len(experts)
+    shape = ep.make_shape(T, 128, K, E, 1)
+    return g, idx, w, off, slot, N, shape, ep.alloc_workspace(shape)
+
+
+@pytest.mark.parametrize("back", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("case", PRODUCTS, ids=str)
+def test_matmul(case, back):
+    g, idx, w, off, slot, N, shape, ws = product_case(case, 11)
+    E, k, n = case[2], case[3], case[4]
+    spare = 3  # rows behind the last expert's stay as they were
+    x = randn(g, N + spare, k)
+    wt = randn(g, *((E, k, n) if back else (E, n, k)), scale=k ** -0.5)
+    y = torch.full((N + spare, n), 7.0, dtype=BF16, device="cuda")
+    xd, wd, od = gpu(x, wt, off)
+    ep.ep_expert_matmul(shape, dict(expert_offsets=od), xd, N + spare, k, wd, n,
+                        ep.EP_WEIGHT_KN if back else ep.EP_WEIGHT_NK, y, ws)
+    assert ep.ep_check_errors(ws) == 0
+    m = wt.double() if back else wt.double().transpose(1, 2)
+    ref = per_expert(off, lambda e, s: x[s].double() @ m[e], None)
+    mag = per_expert(off, lambda e, s: x[s].double().abs() @ m[e].abs(), None)
+    acc = k * U23 * mag
+    check(y[:N], ref, acc + HALF_BF16 * (ref.abs() + acc), "y")
+    assert (y[N:] == 7.0).all()
+
+
+def silu_parts(gu, F):
+    gate, up = gu[:, :F], gu[:, F:]
+    s = torch.sigmoid(gate)
+    return gate, up, s, gate * s * up
+
+
+def act_bound(gate, up, s, act, dg, du):
+    """How far silu(g) u in 32 bits is off for g, u off by dg, du (|silu'| <= 1.1)."""
+    return 1.1 * dg * (up.abs() + du) + (gate * s).abs() * du + (gate.abs() + 20) * U23 * act.abs()
+
+
+SWIGLU = [
+    (1, 1, 1, 8, 128, {}),
+    (3, 2, 5, 72, 128, {}),
+    (65, 2, 3, 200, 256, dict(skip=0.2)),
+    (300, 3, 4, 264, 384, dict(skew=1.0)),
+    (140, 8, 9, 512, 640, {}),
+    (512, 1, 1, 64, 128, {}),
+]
+
+
+@pytest.mark.parametrize("case", SWIGLU, ids=str)
+def test_swiglu_with_checkpoint(case):
+    T, K, E, H, F, opt = case
+    g, idx, w, off, slot, N, _, _ = product_case(case, 23)
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_workspace(shape)
+    spare = 2
+    x, w13 = randn(g, N + spare, H), randn(g, E, 2 * F, H, scale=H ** -0.5)
+    act = torch.full((N + spare, F), 7.0, dtype=BF16, device="cuda")
+    q = torch.full((N + spare, 2 * F), 0x55, dtype=U8, device="cuda")
+    sc = torch.full((N + spare, 2 * F // 128), 7.0, device="cuda")
+    xd, wd, od = gpu(x, w13, off)
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=od), xd, N + spare, wd, F, act, q, sc, ws)
+    alone = torch.full_like(act, 7.0)
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=od), xd, N + spare, wd, F, alone, None, None, ws)
+    assert ep.ep_check_errors(ws) == 0
+    assert torch.equal(alone, act)
+    assert (act[N:] == 7.0).all() and (q[N:] == 0x55).all() and (sc[N:] == 7.0).all()
+
+    gu = per_expert(off, lambda e, s: x[s].double() @ w13[e].double().T, None)
+    acc = H * U23 * per_expert(off, lambda e, s: x[s].double().abs() @ w13[e].double().abs().T, None)
+    gate, up, s, ref = silu_parts(gu, F)
+    b = act_bound(gate, up, s, ref, acc[:, :F], acc[:, F:])
+    check(act[:N], ref, b + HALF_BF16 * (ref.abs() + b), "act")
+    # Scales: amax / 448; the largest magnitude is off by the sums' error.
+    blocks = gu.reshape(N, -1, 128).abs().amax(2)
+    dacc = acc.reshape(N, -1, 128).amax(2)
+    check(sc[:N], blocks / 448, dacc / 448 + 4 * U23 * blocks / 448, "scales")
+    # Values: v * (1 / scale) rounded to e4m3, for the scale as written.
+    rep = sc[:N].double().cpu().repeat_interleave(128, 1)
+    val = q[:N].cpu().view(F8).double() * rep
+    off_by = acc + 4 * U23 * gu.abs()
+    check(val, gu, off_by + HALF_E4M3 * (gu.abs() + off_by) + 2.0 ** -10 * rep, "checkpoint")
+    assert (q[:N].cpu().view(F8).float().abs().reshape(N, -1, 128).amax(2) == 448).all()
+
+
+@pytest.mark.parametrize("F", [8, 72, 136, 1000])
+def test_swiglu_without_checkpoint_takes_odd_sizes(F):
+    T, K, E, H = 90, 2, 4, 104
+    g, idx, w, off, slot, N, _, _ = product_case((T, K, E, H, F, {}), 5)
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_workspace(shape)
+    x, w13 = randn(g, N, H), randn(g, E, 2 * F, H, scale=H ** -0.5)
+    act = torch.empty((N, F), dtype=BF16, device="cuda")
+    xd, wd, od = gpu(x, w13, off)
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=od), xd, N, wd, F, act, None, None, ws)
+    gu = per_expert(off, lambda e, s: x[s].double() @ w13[e].double().T, None)
+    acc = H * U23 * per_expert(off, lambda e, s: x[s].double().abs() @ w13[e].double().abs().T, None)
+    gate, up, s, ref = silu_parts(gu, F)
+    b = act_bound(gate, up, s, ref, acc[:, :F], acc[:, F:])
+    check(act, ref, b + HALF_BF16 * (ref.abs() + b), "act")
+
+
+def test_swiglu_zero_and_nonfinite_rows():
+    """An all-zero row stores scales of 1 and zeros; a row with an infinity
+    reads back as NaN where it matters and leaves its neighbours alone."""
+    H, F, N = 64, 128, 5
+    g = torch.Generator().manual_seed(1)
+    x, w13 = randn(g, N, H), randn(g, 1, 2 * F, H)
+    x[1] = 0
+    x[3, 7] = float("inf")
+    shape = ep.make_shape(N, H, 1, 1, 1)
+    ws = ep.alloc_workspace(shape)
+    off = torch.tensor([0, N], dtype=torch.int32)
+    act = torch.empty((N, F), dtype=BF16, device="cuda")
+    q = torch.empty((N, 2 * F), dtype=U8, device="cuda")
+    sc = torch.empty((N, 2), device="cuda")
+    xd, wd, od = gpu(x, w13, off)
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=od), xd, N, wd, F, act, q, sc, ws)
+    assert (sc[1] == 1).all() and (q[1].view(F8).float() == 0).all() and (act[1] == 0).all()
+    val = q.view(F8).float() * sc.repeat_interleave(128, 1)
+    assert torch.isnan(val[3]).all()
+    for i in (0, 2, 4):
+        assert torch.isfinite(val[i]).all() and torch.isfinite(act[i]).all() and (sc[i] != 1).all()
+
+
+def checkpoint(g, N, F, scale=1.0):
+    v = torch.randn((N, 2 * F), generator=g) * scale
+    s = v.reshape(N, -1, 128).abs().amax(2) / 448
+    return (v / s.repeat_interleave(128, 1)).to(F8), s
+
+
+GRAD = [(1, 1, 1, 128, {}), (7, 3, 5, 256, dict(skip=0.3)), (50, 8, 16, 640, {}), (33, 2, 4, 1152, {}),
+        (20, 4, 4, 2176, dict(repeat=True))]
+
+
+def grad_reference(idx, w, slot, q, sc, d, F):
+    N = len(q)
+    gu = q.double() * sc.double().repeat_interleave(128, 1)
+    row_w = torch.zeros((N, 1), dtype=F64)
+    has = slot >= 0
+    row_w[slot[has].long(), 0] = w[has].double()
+    return gu, row_w, has
+
+
+@pytest.mark.parametrize("scale", [1.0, 12.0], ids=["", "wide"])
+@pytest.mark.parametrize("case", GRAD, ids=str)
+def test_swiglu_grad(case, scale):
+    T, K, E, F, opt = case
+    g = torch.Generator().manual_seed(31)
+    idx, w = routing(T, K, E, 3, **opt)
+    off, slot, experts = grouped(idx, E)
+    N = len(experts)
+    q, sc = checkpoint(g, N, F, scale)
+    d = randn(g, N, F)
+    shape = ep.make_shape(T, 128, K, E, 1)
+    ws = ep.alloc_workspace(shape)
+    spare = 2
+    d_gu = torch.full((N + spare, 2 * F), 7.0, dtype=BF16, device="cuda")
+    act_w = torch.full((N + spare, F), 7.0, dtype=BF16, device="cuda")
+    d_w = torch.full((T, K), 7.0, device="cuda")
+    pad = lambda t: torch.cat([t.cuda(), torch.zeros((spare, t.shape[1]), device="cuda").to(t.dtype)])
+    L = dict(expert_slot=slot.cuda())
+    ep.ep_swiglu_grad(shape, L, F, pad(q), pad(sc), pad(d), N + spare, w.cuda(), d_gu, act_w, d_w, ws)
+    assert ep.ep_check_errors(ws) == 0
+    assert (d_gu[N:] == 7.0).all() and (act_w[N:] == 7.0).all()
+
+    gu, row_w, has = grad_reference(idx, w, slot, q, sc, d, F)
+    gate, up, s, act = silu_parts(gu, F)
+    dd = d.double()
+    rel = (gate.abs() + 24) * U23
+    ref_g = row_w * dd * up * s * (1 + gate * (1 - s))
+    ref_u = row_w * dd * gate * s
+    # 1 + g (1 - s) may cancel: its error goes by the size of its terms.
+    bg = (row_w * dd * up * s).abs() * (1 + gate.abs()) * rel
+    bu = ref_u.abs() * rel
+    check(d_gu[:N, :F], ref_g, bg + HALF_BF16 * (ref_g.abs() + bg), "d_gate")
+    check(d_gu[:N, F:], ref_u, bu + HALF_BF16 * (ref_u.abs() + bu), "d_up")
+    ref_a = row_w * act
+    ba = ref_a.abs() * rel
+    check(act_w[:N], ref_a, ba + HALF_BF16 * (ref_a.abs() + ba), "act_w")
+    ref_w = torch.zeros((T, K), dtype=F64)
+    bw = torch.zeros((T, K), dtype=F64)
+    ref_w[has] = (dd * act).sum(1)[slot[has].long()]
+    bw[has] = ((dd * act).abs() * (rel + F * U23)).sum(1)[slot[has].long()]
+    check(d_w, ref_w, bw, "d_topk_weights")
+    # Optional outputs left out: the others stay the same.
+    again = torch.empty_like(d_gu)
+    ep.ep_swiglu_grad(shape, L, F, pad(q), pad(sc), pad(d), N + spare, w.cuda(), again, None, None, ws)
+    assert torch.equal(again[:N], d_gu[:N])
+
+
+def test_swiglu_grad_against_differences():
+    """The gradient against central differences, in 64 bits, of
+    sum w d silu(g) u at the checkpoint's values: steps of 1e-4 leave errors of
+    about 1e-8 |w d| (1 + |u|), far under the result's bf16 rounding."""
+    T, K, E, F = 6, 2, 3, 128
+    g = torch.Generator().manual_seed(77)
+    idx, w = routing(T, K, E, 8)
+    off, slot, experts = grouped(idx, E)
+    N = len(experts)
+    q, sc = checkpoint(g, N, F)
+    d = randn(g, N, F)
+    shape = ep.make_shape(T, 128, K, E, 1)
+    ws = ep.alloc_workspace(shape)
+    d_gu = torch.empty((N, 2 * F), dtype=BF16, device="cuda")
+    ep.ep_swiglu_grad(shape, dict(expert_slot=slot.cuda()), F, q.cuda(), sc.cuda(), d.cuda(), N, w.cuda(), d_gu,
+                      None, None, ws)
+    gu, row_w, _ = grad_reference(idx, w, slot, q, sc, d, F)
+    f = lambda a, b: row_w * d.double() * a * torch.sigmoid(a) * b
+    gate, up, h = gu[:, :F], gu[:, F:], 1e-4
+    num = torch.cat([(f(gate + h, up) - f(gate - h, up)), (f(gate, up + h) - f(gate, up - h))], 1) / (2 * h)
+    small = 1e-7 * (row_w * d.double()).abs().repeat(1, 2) * (1 + up.abs().repeat(1, 2)) * (8 + gate.abs().repeat(1, 2))
+    check(d_gu, num, small + HALF_BF16 * (num.abs() + small), "d_gu against differences")
+
+
+WGRAD = [
+    (1, 1, 1, 8, 128, {}),
+    (5, 3, 9, 72, 128, dict(skip=0.3)),
+    (100, 2, 3, 264, 384, {}),
+    (300, 2, 2, 520, 256, dict(skew=1.0)),
+    (64, 1, 1, 256, 256, {}),
+    (65, 1, 1, 24, 640, {}),
+]
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["rows", "fp8rows"])
+@pytest.mark.parametrize("case", WGRAD, ids=str)
+def test_wgrad(case, fp8, wide):
+    T, K, E, n, k, opt = case
+    g, idx, w, off, slot, N, shape, ws = product_case((T, K, E, k, n, opt), 41)
+    dy = randn(g, N + 1, n)
+    if fp8:
+        q, sc = checkpoint(g, N + 1, k // 2)
+        x = q.double() * sc.double().repeat_interleave(128, 1)
+        rows = dict(x_fp8=q.cuda(), x_scales=sc.cuda())
+    else:
+        xb = randn(g, N + 1, k)
+        x, rows = xb.double(), dict(x=xb.cuda())
+    dw = torch.full((E, n, k), 7.0, dtype=F32 if wide else BF16, device="cuda")
+    dyd, od = gpu(dy, off)
+    ep.ep_expert_wgrad(shape, dict(expert_offsets=od), dyd, N + 1, n, rows, k, dw,
+                       ep.EP_GRAD_F32 if wide else ep.EP_GRAD_BF16, ws)
+    assert ep.ep_check_errors(ws) == 0
+    parts = [slice(int(off[e]), int(off[e + 1])) for e in range(E)]
+    ref = torch.stack([dy[p].double().T @ x[p] for p in parts])
+    mag = torch.stack([dy[p].double().abs().T @ x[p].abs() for p in parts])
+    most = max(p.stop - p.start for p in parts)
+    acc = most * U23 * mag + (HALF_BF16 * mag * (1 + most * U23) + U23 * mag if fp8 else 0)
+    check(dw, ref, acc if wide else acc + HALF_BF16 * (ref.abs() + acc), "dw")
+    # The sum over one row more is the old one plus that row's product: the
+    # gradient is linear in the rows (a difference, exact up to roundings).
+    if wide and not fp8 and E == 1:
+        od2 = torch.tensor([0, N + 1], dtype=torch.int32, device="cuda")
+        more = torch.empty_like(dw)
+        ep.ep_expert_wgrad(shape, dict(expert_offsets=od2), dyd, N + 1, n, rows, k, more, ep.EP_GRAD_F32, ws)
+        outer = dy[N].double().unsqueeze(1) * x[N].unsqueeze(0)
+        both = mag[0] + outer.abs()
+        check((more.double() - dw.double())[0], outer, 2 * (N + 1) * U23 * both, "difference by one row")
+
+
+FEW = [
+    # (T, H, F, E, K, options)
+    (1, 256, 512, 16, 2, {}),
+    (1, 8, 8, 1, 1, {}),
+    (2, 72, 40, 3, 2, {}),
+    (13, 264, 136, 40, 3, dict(skip=0.2)),
+    (16, 640, 384, 8, 8, {}),
+    (17, 128, 256, 5, 4, dict(repeat=True)),
+    (40, 200, 264, 4, 2, {}),
+    (128, 136, 72, 2, 1, {}),            # 64 tokens and more to one expert
+    (36, 128, 128, 1, 1, {}),            # three token tiles of one expert
+    (128, 128, 128, 4096, 4, {}),        # the largest number of experts
+    (100, 64, 48, 3, 64, dict(repeat=True)),
+    (5, 1032, 712, 6, 6, {}),
+]
+
+
+def few_reference(x, w13, w2, idx, w, F):
+    """out and its bound in 64 bits."""
+    T, H = x.shape
+    out, bound = torch.zeros((T, H), dtype=F64), torch.zeros((T, H), dtype=F64)
+    xd = x.double()
+    lanes = 0
+    for e in range(len(w13)):
+        hit = (idx == e)
+        ts = hit.any(1).nonzero()[:, 0]
+        if not len(ts):
+            continue
+        lanes += 1
+        a, b2 = w13[e].double(), w2[e].double()
+        gu = xd[ts] @ a.T
+        acc = H * U23 * (xd[ts].abs() @ a.abs().T)
+        gate, up, s, act = silu_parts(gu, F)
+        da = act_bound(gate, up, s, act, acc[:, :F], acc[:, F:])
+        da = da + HALF_BF16 * (act.abs() + da)
+        we = (w.double() * hit).sum(1)[ts].unsqueeze(1)
+        wabs = (w.double().abs() * hit).sum(1)[ts].unsqueeze(1)
+        out[ts] += we * (act @ b2.T)
+        mag = (act.abs() + da) @ b2.abs().T
+        bound[ts] += wabs * (da @ b2.abs().T + F * U23 * mag) + 80 * U23 * wabs * mag
+    bound = bound + 8 * U23 * out.abs()
+    return out, bound + HALF_BF16 * (out.abs() + bound)
+
+
+def eight(w):
+    """e4m3 weights, scales and the values they stand for."""
+    E, n, k = w.shape
+    s = w.float().reshape(E, n, -1, 128).abs().amax(3).clamp(min=1e-20) / 448
+    q = (w.float() / s.repeat_interleave(128, 2)).to(F8)
+    return q, s, q.double() * s.double().repeat_interleave(128, 2)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("case", FEW, ids=str)
+def test_few(case, fp8):
+    T, H, F, E, K, opt = case
+    if fp8:  # the same cases at the next sizes that FP8 takes
+        H, F = -(-H // 128) * 128, -(-F // 128) * 128
+        if E == 4096:
+            E = 1024
+    g = torch.Generator().manual_seed(9)
+    idx, w = routing(T, K, E, 17, **opt)
+    x, w13, w2 = randn(g, T, H), randn(g, E, 2 * F, H, scale=H ** -0.5), randn(g, E, H, F, scale=F ** -0.5)
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_few_workspace(shape, F).fill_(0xAB)
+    ep.ep_clear_errors(ws)
+    if fp8:
+        (q13, s13, w13), (q2, s2, w2) = eight(w13), eight(w2)
+        experts = dict(F=F, w13_fp8=q13.cuda(), w13_scales=s13.cuda(), w2_fp8=q2.cuda(), w2_scales=s2.cuda())
+    else:
+        experts = dict(F=F, w13=w13.cuda(), w2=w2.cuda())
+    out = torch.full((T, H), 7.0, dtype=BF16, device="cuda")
+    tokens = dict(x=x.cuda(), topk_idx=idx.cuda(), topk_weights=w.cuda())
+    ep.ep_moe_few(shape, tokens, experts, out, ws)
+    assert ep.ep_check_errors(ws) == 0
+    ref, bound = few_reference(x, w13, w2, idx, w, F)
+    check(out, ref, bound, "out")
+    again = torch.empty_like(out)
+    ep.ep_moe_few(shape, tokens, experts, again, ws)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+
+
+def test_few_keeps_nonfinite_values_with_their_tokens():
+    """NaN and infinite weights of one expert reach only its tokens; a token of
+    NaN only itself; a token without a lane gets zeros; bad ids are reported
+    and skipped."""
+    T, H, F, E, K = 6, 128, 256, 4, 2
+    g = torch.Generator().manual_seed(2)
+    x, w13, w2 = randn(g, T, H), randn(g, E, 2 * F, H, scale=H ** -0.5), randn(g, E, H, F, scale=F ** -0.5)
+    idx = torch.tensor([[0, 1], [1, 2], [-1, -1], [3, 0], [0, 99], [-7, 1]])
+    w = torch.full((T, K), 0.5)
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_few_workspace(shape, F)
+    clean = torch.where((idx < 0) | (idx >= E), -1, idx)
+    ref, bound = few_reference(x, w13, w2, clean, w, F)
+    bad13, bad2, badx = w13.clone(), w2.clone(), x.clone()
+    bad13[2, 3, :] = float("inf")     # expert 2: token 1 only
+    bad2[2, 5, 9] = float("nan")
+    bad2[3] = float("nan")            # expert 3: token 3 only
+    badx[4] = float("nan")            # token 4 only
+    out = torch.empty((T, H), dtype=BF16, device="cuda")
+    ep.ep_moe_few(shape, dict(x=badx.cuda(), topk_idx=idx.cuda(), topk_weights=w.cuda()),
+                  dict(F=F, w13=bad13.cuda(), w2=bad2.cuda()), out, ws)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_EXPERT_ID
+    for t in (0, 2, 5):
+        check(out[t], ref[t], bound[t], f"token {t}")
+    assert (out[2] == 0).all()
+    assert torch.isnan(out[3]).all() and torch.isnan(out[4]).all() and not torch.isfinite(out[1]).all()
+
+
+def test_rows_past_the_capacity_are_left_out():
+    E, k, n, N = 3, 64, 72, 50
+    g = torch.Generator().manual_seed(4)
+    off = torch.tensor([0, 20, 40, N], dtype=torch.int32)
+    have = 33
+    x, wt = randn(g, have, k), randn(g, E, n, k, scale=k ** -0.5)
+    shape = ep.make_shape(N, 128, 1, E, 1)
+    ws = ep.alloc_workspace(shape)
+    ep.ep_clear_errors(ws)
+    y = torch.empty((have, n), dtype=BF16, device="cuda")
+    xd, wd, od = gpu(x, wt, off)
+    ep.ep_expert_matmul(shape, dict(expert_offsets=od), xd, have, k, wd, n, ep.EP_WEIGHT_NK, y, ws)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY
+    cut = off.clamp(max=have)
+    ref = per_expert(cut, lambda e, s: x[s].double() @ wt[e].double().T, None)
+    mag = per_expert(cut, lambda e, s: x[s].double().abs() @ wt[e].double().abs().T, None)
+    check(y, ref, k * U23 * mag + HALF_BF16 * (ref.abs() + k * U23 * mag), "y")
+    # A lane whose row lies past the capacity: reported, gradient 0.
+    F = 128
+    slot = torch.tensor([[0], [33]], dtype=torch.int32, device="cuda")
+    s2 = ep.make_shape(2, 128, 1, E, 1)
+    ep.ep_clear_errors(ws)
+    q, sc = checkpoint(g, have, F)
+    d_w = torch.full((2, 1), 7.0, device="cuda")
+    d_gu = torch.full((have, 2 * F), 7.0, dtype=BF16, device="cuda")
+    ep.ep_swiglu_grad(s2, dict(expert_slot=slot), F, q.cuda(), sc.cuda(), randn(g, have, F).cuda(), have,
+                      torch.ones((2, 1), device="cuda"), d_gu, None, d_w, ws)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY
+    assert d_w[1, 0] == 0 and d_w[0, 0] != 7.0 and (d_gu[1:] == 7.0).all()
+
+
+def test_no_rows_and_no_tokens():
+    E, k, n = 5, 64, 128
+    shape = ep.make_shape(4, 128, 2, E, 1)
+    ws = ep.alloc_workspace(shape)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    wt = torch.zeros((E, n, k), dtype=BF16, device="cuda")
+    y = torch.full((8, n), 7.0, dtype=BF16, device="cuda")
+    x = torch.zeros((8, n), dtype=BF16, device="cuda")
+    L = dict(expert_offsets=off)
+    ep.ep_expert_matmul(shape, L, x, 8, k, wt, n, ep.EP_WEIGHT_NK, y, ws)
+    ep.ep_expert_matmul(shape, L, None, 0, k, wt, n, ep.EP_WEIGHT_NK, None, ws)
+    assert (y == 7.0).all()
+    for rows, dy, xs in ((8, y, dict(x=x)), (0, None, {})):
+        dw = torch.full((E, n, k), 7.0, device="cuda")
+        ep.ep_expert_wgrad(shape, L, dy, rows, n, xs, k, dw, ep.EP_GRAD_F32, ws)
+        assert (dw == 0).all()
+    s0 = ep.make_shape(0, 128, 2, E, 1)
+    w0 = ep.alloc_few_workspace(s0, 8).fill_(0xAB)
+    ep.ep_moe_few(s0, {}, dict(F=8, w13=wt, w2=wt), None, w0)
+    assert ep.ep_check_errors(w0) == 0
+
+
+def layer_case(T=150, H=256, F=256, E=8, K=3, skip=0.1):
+    g = torch.Generator().manual_seed(6)
+    idx, w = routing(T, K, E, 21, skip=skip)
+    x, dout = randn(g, T, H), randn(g, T, H)
+    w13, w2 = randn(g, E, 2 * F, H, scale=H ** -0.5), randn(g, E, H, F, scale=F ** -0.5)
+    return idx, w, x, dout, w13, w2
+
+
+def layer_step(shape, F, idx, w, x, dout, w13, w2, bufs=None):
+    """Forward and backward of a whole layer by the entry points; every
+    intermediate in a dict."""
+    T, H, K, E = shape.T, shape.H, shape.K, shape.E
+    b = bufs if bufs is not None else {}
+    N = T * K
+
+    def buf(name, *size, dtype=BF16):
+        if name not in b:
+            b[name] = torch.zeros(size, dtype=dtype, device="cuda")
+        return b[name]
+
+    if "L" not in b:
+        b["L"], b["ws"] = ep.alloc_layout(shape, expand=True), ep.alloc_workspace(shape)
+        b["recv"] = ep.alloc_recv(shape, N)
+        b["d_recv"] = ep.alloc_recv(shape, N, meta=False)
+        b["ones"] = torch.ones((T, K), device="cuda")
+    L, ws = b["L"], b["ws"]
+    ep.ep_get_layout(shape, idx, L, ws)
+    ep.ep_dispatch_expand(shape, L, dict(x=x, topk_idx=idx, topk_weights=w), b["recv"], N, ws)
+    xr = b["recv"]["x"]
+    act, q = buf("act", N, F), buf("q", N, 2 * F, dtype=U8)
+    sc = buf("sc", N, 2 * F // 128, dtype=F32)
+    ep.ep_expert_swiglu(shape, L, xr, N, w13, F, act, q, sc, ws)
+    y, out = buf("y", N, H), buf("out", T, H)
+    ep.ep_expert_matmul(shape, L, act, N, F, w2, H, ep.EP_WEIGHT_NK, y, ws)
+    ep.ep_combine_expand(shape, L, y, N, 2 * H, ep.EP_FMT_PLAIN, 0, w, out, ws)
+
+    ep.ep_dispatch_expand(shape, L, dict(x=dout, topk_idx=idx), b["d_recv"], N, ws)
+    dy = b["d_recv"]["x"]
+    d_act, d_gu, act_w = buf("d_act", N, F), buf("d_gu", N, 2 * F), buf("act_w", N, F)
+    d_w = buf("d_w", T, K, dtype=F32)
+    ep.ep_expert_matmul(shape, L, dy, N, H, w2, F, ep.EP_WEIGHT_KN, d_act, ws)
+    ep.ep_swiglu_grad(shape, L, F, q, sc, d_act, N, w, d_gu, act_w, d_w, ws)
+    dw2, dw13 = buf("dw2", E, H, F, dtype=F32), buf("dw13", E, 2 * F, H, dtype=F32)
+    ep.ep_expert_wgrad(shape, L, dy, N, H, dict(x=act_w), F, dw2, ep.EP_GRAD_F32, ws)
+    ep.ep_expert_wgrad(shape, L, d_gu, N, 2 * F, dict(x=xr), H, dw13, ep.EP_GRAD_F32, ws)
+    dxr, dx = buf("dxr", N, H), buf("dx", T, H)
+    ep.ep_expert_matmul(shape, L, d_gu, N, 2 * F, w13, H, ep.EP_WEIGHT_KN, dxr, ws)
+    ep.ep_combine_expand(shape, L, dxr, N, 2 * H, ep.EP_FMT_PLAIN, 0, b["ones"], dx, ws)
+    return b
+
+
+def test_whole_layer_forward_and_backward():
+    """A layer's training step against automatic differentiation in 64 bits.
+
+    The forward output passes three roundings to bf16 (act, y, out): each
+    2^-8 at most, so the 2-norm is off by at most 3 * 2^-8 of itself for values
+    of random sign. The backward also uses g and u from 8 bits (2^-4 at most
+    of each value, uniformly spread: 2^-4 / sqrt(3) in 2-norm for the largest
+    mantissa step, less on average), which enters the gradients through
+    products of g and u: twice that, and the bf16 roundings, bound them by
+    2 * 2^-4 + 4 * 2^-8 of their norm."""
+    T, H, F, E, K = 150, 256, 256, 8, 3
+    idx, w, x, dout, w13, w2 = layer_case(T, H, F, E, K)
+    shape = ep.make_shape(T, H, K, E, 1)
+    b = layer_step(shape, F, *gpu(idx, w, x, dout, w13, w2))
+    assert ep.ep_check_errors(b["ws"]) == 0
+    X, W13, W2, W = (t.double().requires_grad_() for t in (x, w13, w2, w))
+    out = torch.zeros((T, H), dtype=F64)
+    for e in range(E):
+        t, k = (idx == e).nonzero(as_tuple=True)
+        gu = X[t] @ W13[e].T
+        a = gu[:, :F] * torch.sigmoid(gu[:, :F]) * gu[:, F:]
+        out = out.index_add(0, t, W[t, k].unsqueeze(1) * (a @ W2[e].T))
+    out.backward(dout.double())
+    rel = lambda a, r: ((a.double().cpu() - r).norm() / r.norm()).item()
+    assert rel(b["out"], out.detach()) <= 3 * HALF_BF16
+    for name, ref in (("dx", X.grad), ("dw13", W13.grad), ("dw2", W2.grad), ("d_w", W.grad)):
+        assert rel(b[name], ref) <= 2 * HALF_E4M3 + 4 * HALF_BF16, name
+    # The few-token layer computes the same output.
+    s2 = ep.make_shape(128, H, K, E, 1)
+    ws = ep.alloc_few_workspace(s2, F)
+    few = torch.empty((128, H), dtype=BF16, device="cuda")
+    ep.ep_moe_few(s2, dict(x=x[:128].cuda(), topk_idx=idx[:128].cuda().contiguous(),
+                           topk_weights=w[:128].cuda().contiguous()), dict(F=F, w13=w13.cuda(), w2=w2.cuda()), few, ws)
+    assert rel(few, out.detach()[:128]) <= 3 * HALF_BF16
+
+
+def test_whole_layer_in_a_graph():
+    """The training step and the few-token layer captured once and replayed
+    with new inputs, other work and waits between the replays; every replay
+    equals the eager result bit for bit."""
+    T, H, F, E, K = 100, 128, 128, 6, 2
+    shape = ep.make_shape(T, H, K, E, 1)
+    inputs = [gpu(*layer_case(T, H, F, E, K)), None, None]
+    for i in (1, 2):
+        idx, w = routing(T, K, E, 50 + i, skip=0.2)
+        g = torch.Generator().manual_seed(60 + i)
+        inputs[i] = [idx.cuda(), w.cuda(), randn(g, T, H).cuda(), randn(g, T, H).cuda(), inputs[0][4], inputs[0][5]]
+    names = ("out", "dx", "dw13", "dw2", "d_w", "few")
+
+    def step(args, b):
+        layer_step(shape, F, *args, bufs=b)
+        if "few" not in b:
+            b["few"], b["few_ws"] = torch.zeros((T, H), dtype=BF16, device="cuda"), ep.alloc_few_workspace(shape, F)
+        ep.ep_moe_few(shape, dict(x=args[2], topk_idx=args[0], topk_weights=args[1]),
+                      dict(F=F, w13=args[4], w2=args[5]), b["few"], b["few_ws"])
+
+    eager = []
+    for args in inputs:
+        b = {}
+        step(args, b)
+        torch.cuda.synchronize()
+        eager.append({n: b[n].clone() for n in names})
+    static, b = [t.clone() for t in inputs[0]], {}
+    step(static, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(static, b)
+    for i in (0, 1, 2, 1, 0):
+        for s, t in zip(static, inputs[i]):
+            s.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(b[n].view(U8), eager[i][n].view(U8)), (i, n)
+        torch.randn(1000, device="cuda").sum().item()
+        step(inputs[i], {})  # eager work on buffers of its own between replays
+
+
+def test_calls_run_on_the_given_stream():
+    """Each call on a stream of its own, ordered behind work queued there."""
+    T, H, F, E, K = 16, 128, 128, 4, 2
+    idx, w, x, dout, w13, w2 = gpu(*layer_case(T, H, F, E, K))
+    shape = ep.make_shape(T, H, K, E, 1)
+    ref = layer_step(shape, F, idx, w, x, dout, w13, w2)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    x2, b = torch.zeros_like(x), {}
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        big = torch.randn(2048, 2048, device="cuda")
+        for _ in range(20):
+            big = big @ big * 1e-3
+        x2.copy_(x)
+        layer_step(shape, F, idx, w, x2, dout, w13, w2, bufs=b)
+    st.synchronize()
+    for n in ("out", "dx", "dw13", "dw2", "d_w"):
+        assert torch.equal(b[n], ref[n]), n
