@@ -15,11 +15,11 @@ namespace {
 
 constexpr int kThreads = 512;   // 8 waves, two per SIMD
 constexpr int kTileN = 256;     // columns of a tile
-constexpr int kTileK = 64;      // contracted indices per step
+constexpr int kStep = 64;       // contracted indices per step
 constexpr int kFullRows = 256;  // rows of a full tile
-constexpr int kHalf = 32768;    // LDS bytes of one operand's stage (256 x 64 bf16)
-constexpr int kStage = 2 * kHalf;
-constexpr int kLdsBytes = 2 * kStage;
+constexpr int kPart = 32768;    // LDS bytes of one operand's step (256 x 64 bf16)
+constexpr int kRingB = 2 * kPart;  // two steps of the first operand, then three of the second
+constexpr int kLdsBytes = 5 * kPart;
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(EP_LDS_PTR(const char))p;
@@ -28,22 +28,33 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // ---- Operand tiles in LDS ---------------------------------------------------
 //
 // "Rows" layout: ROWS rows of 64 contracted values (128 bytes, eight 16-byte
-// chunks). Chunk c of row r lies at chunk c ^ ((r >> 1) & 7): the 16 rows that
-// the 16 lanes of a quarter wave read at one chunk then cover all 64 banks.
+// chunks). Chunk c of row r lies at chunk c ^ ((r >> 1) & 7), which a wave's
+// 16-byte reads pass without bank conflicts.
 //
 // "Columns" layout: 64 contracted rows of 256 values (512 bytes, sixteen
 // 32-byte blocks). Block b of row k lies at block b ^ f(k), f(k) = (k & 3) |
 // ((k >> 3) & 3) << 2: the 16 rows that a wave's transposing read touches then
 // cover the banks evenly.
+//
+// Steps of 64 rather than 32 indices, so that every copy takes whole 128-byte
+// lines: with 64-byte pieces a tile's copies alone filled the L2's requests
+// (1060 against TFLOP/s at 32 experts of 1,024 x 7168 x 4096).
+
+// An operand that needs no work between its copy and its reads.
+struct NoStaging {
+    __device__ __forceinline__ void stage(char*) {}
+};
 
 // A tile operand whose contracted index is contiguous in memory.
 template <int ROWS>
-struct RowsLoader {
+struct RowsLoader : NoStaging {
     static constexpr int kLoads = ROWS / 64;
     const char* p;
     uint32_t bytes;
     uint32_t off[kLoads];
-    int k;  // this lane's first contracted index within a step
+    int k;         // this lane's first contracted index within a step
+    u32x4 d;       // descriptor of the step under way
+    uint32_t far;  // added to the offsets: kBufFar where the step is past the end
 
     // row(r): byte offset of tile row r from p.
     template <class RowOff>
@@ -51,33 +62,35 @@ struct RowsLoader {
         p = static_cast<const char*>(base);
         bytes = n_bytes;
         const int lane = lane_id(), wave = wave_in_block();
-        const int chunk = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
+        const int r = wave * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ ((r >> 1) & 7);
         k = chunk * 8;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const uint32_t o = row(j * 64 + wave * 8 + (lane >> 3));
+            const uint32_t o = row(j * 64 + r);
             off[j] = o == kBufOutside ? o : o + chunk * 16;
         }
     }
-    // Requests the step whose first index is k0 of k_dim into LDS.
-    __device__ __forceinline__ void load(int k0, int k_dim, uint32_t lds) {
-        const int wave = uniform_wave();
-        const u32x4 d = buf_desc(p + (int64_t)k0 * 2, bytes - (uint32_t)k0 * 2);
-        const bool in = k0 + k < k_dim;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-            copy16_to_lds(d, in ? off[j] : kBufOutside, lds + (j * 64 + wave * 8) * 128);
+    // Turns to the step whose first index is k0 of k_dim (zeros past k_dim).
+    __device__ __forceinline__ void begin(int k0, int k_dim) {
+        d = buf_desc(p + (int64_t)k0 * 2, k0 < k_dim ? bytes - (uint32_t)k0 * 2 : 0u);
+        far = k0 + k < k_dim ? 0u : kBufFar;
+    }
+    // Requests part j of kLoads of that step into LDS.
+    __device__ __forceinline__ void copy(int j, uint32_t lds) {
+        copy16_to_lds(d, off[j] + far, lds + (j * 64 + uniform_wave() * 8) * 128);
     }
 };
 
 // A tile operand whose 256 columns are contiguous in memory (one contracted
 // index per memory row of ld values).
-struct ColsLoader {
+struct ColsLoader : NoStaging {
     static constexpr int kLoads = 4;
     const char* p;
     int64_t ld_bytes;
     uint32_t col_bytes;  // bytes of a row before the tile's first column
     uint32_t off[kLoads];
+    u32x4 d;
 
     __device__ __forceinline__ void init(const void* base, int64_t ld, int col0) {
         p = static_cast<const char*>(base) + (int64_t)col0 * 2;
@@ -92,17 +105,19 @@ struct ColsLoader {
             off[j] = (uint32_t)(r * ld_bytes) + block * 32 + (lane & 1) * 16;
         }
     }
-    __device__ __forceinline__ void load(int k0, int k_dim, uint32_t lds) {
-        const int wave = uniform_wave();
-        const int rows = min(k_dim - k0, kTileK);
-        const u32x4 d = buf_desc(p + (int64_t)k0 * ld_bytes, (uint32_t)(rows * ld_bytes) - col_bytes);
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) copy16_to_lds(d, off[j], lds + (j * 16 + wave * 2) * 512);
+    __device__ __forceinline__ void begin(int k0, int k_dim) {
+        const int rows = min(k_dim - k0, kStep);
+        d = buf_desc(p + (int64_t)k0 * ld_bytes, rows > 0 ? (uint32_t)(rows * ld_bytes) - col_bytes : 0u);
+    }
+    __device__ __forceinline__ void copy(int j, uint32_t lds) {
+        copy16_to_lds(d, off[j], lds + (j * 16 + uniform_wave() * 2) * 512);
     }
 };
 
-// 16 x 32 fragments: sub-tile s (16 rows or columns) and half kk of the step.
+// 16 x 32 fragments of the step at lds: sub-tile s (16 rows or columns), half
+// `half` of the contracted indices.
 struct RowsReader {
+    static constexpr int kReads = 1;  // LDS instructions per fragment
     uint32_t base[2];
     __device__ __forceinline__ void init(int first_sub) {
         const int i = lane_id() & 15, q = lane_id() >> 4;
@@ -110,12 +125,13 @@ struct RowsReader {
         base[0] = row + ((q ^ (i >> 1)) * 16);
         base[1] = row + (((q + 4) ^ (i >> 1)) * 16);
     }
-    __device__ __forceinline__ bf16x8 read(const char* lds, int s, int kk) const {
-        return *reinterpret_cast<const bf16x8*>(lds + base[kk] + s * 2048);
+    __device__ __forceinline__ bf16x8 read(const char* lds, int s, int half) const {
+        return *reinterpret_cast<const bf16x8*>(lds + base[half] + s * 2048);
     }
 };
 template <int SUBS>
 struct ColsReader {
+    static constexpr int kReads = 2;
     uint32_t base[SUBS];
     __device__ __forceinline__ void init(int first_sub) {
         const int i = lane_id() & 15, q = lane_id() >> 4;
@@ -126,8 +142,8 @@ struct ColsReader {
     }
     // Each 16-lane group reads 4 contracted rows of 16 values and receives
     // them transposed: lane i gets the 4 rows' values of column i.
-    __device__ __forceinline__ bf16x8 read(const char* lds, int s, int kk) const {
-        const char* p = lds + base[s] + kk * 16384;
+    __device__ __forceinline__ bf16x8 read(const char* lds, int s, int half) const {
+        const char* p = lds + base[s] + half * 16384;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS_PTR(s16x4))p);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS_PTR(s16x4))(p + 2048));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -136,43 +152,105 @@ struct ColsReader {
     }
 };
 
+template <int MS, int NS>
+struct Fragments {
+    bf16x8 a[MS], b[NS];
+};
+// The fragments are wanted on the loop's way out too: without this the
+// compiler moves their reads past the exit test, behind the matrix instructions
+// that they should run beside.
+template <int MS, int NS>
+__device__ __forceinline__ void keep(const Fragments<MS, NS>& f) {
+#pragma unroll
+    for (int i = 0; i < MS; ++i) asm volatile("" ::"v"(f.a[i]));
+#pragma unroll
+    for (int i = 0; i < NS; ++i) asm volatile("" ::"v"(f.b[i]));
+}
+
+// One half step: multiplies the fragments `cur` while the fragments `next` are
+// read from (la_lds, lb_lds, half), in MS groups of NS matrix instructions, each
+// behind its share of the reads (all within the first GROUPS groups) and one
+// of the copies: copies issued in one go would stand in the waves' way until
+// the memory pipeline has taken them all (16 clocks each).
+template <int MS, int NS, int GROUPS, class RA, class RB, class Copies>
+__device__ __forceinline__ void half_step(const RA& ra, const RB& rb, const char* a_lds, const char* b_lds, int half,
+                                          const Fragments<MS, NS>& cur, Fragments<MS, NS>& next,
+                                          f32x4 (&acc)[MS][NS], Copies copies) {
+    constexpr int R = MS + NS;
+#pragma unroll
+    for (int g = 0; g < MS; ++g) {
+#pragma unroll
+        for (int r = g * R / GROUPS; r < (g + 1) * R / GROUPS && r < R; ++r) {
+            if (r < NS)
+                next.b[r] = rb.read(b_lds, r, half);
+            else
+                next.a[r - NS] = ra.read(a_lds, r - NS, half);
+        }
+        copies(g);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) acc[g][n] = mfma_bf16(cur.b[n], cur.a[g], acc[g][n]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // One workgroup's product: acc[mi][ni] += rows sub-tile mi times columns
-// sub-tile ni over k_dim contracted indices, two LDS stages: step s + 1 is
-// copied in while step s is multiplied.
+// sub-tile ni over k_dim contracted indices. Each half of a step is multiplied
+// from registers while the fragments of the next half are read from LDS, with
+// one barrier per step. All of the LDS holds steps: two of the first operand,
+// three of the second. In the first half of step s the copies of the second
+// operand's step s + 2 are issued (into the slot of step s - 1), in the second
+// half those of the first operand's (into the slot of step s, whose last
+// fragments have then been read), so copies are spread over the whole step
+// and have between one and two steps' time to arrive.
 template <int MS, int NS, class LA, class LB, class RA, class RB>
 __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB& rb, int k_dim, char* lds,
                                          f32x4 (&acc)[MS][NS]) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
-    const int steps = (k_dim + kTileK - 1) / kTileK;
+    const int steps = (k_dim + kStep - 1) / kStep;
     if (steps > 0) {
-        la.load(0, k_dim, at);
-        lb.load(0, k_dim, at + kHalf);
-    }
-    for (int s = 0; s < steps; ++s) {
-        wait_copies<0>();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            la.begin(s * kStep, k_dim);
+            lb.begin(s * kStep, k_dim);
+            for (int c = 0; c < LA::kLoads; ++c) la.copy(c, at + s * kPart);
+            for (int c = 0; c < LB::kLoads; ++c) lb.copy(c, at + kRingB + s * kPart);
+            lb.stage(lds + kRingB + s * kPart);
+        }
+        Fragments<MS, NS> f[2];
+        wait_copies<LA::kLoads + LB::kLoads>();
         barrier_only();
-        const int cur = (s & 1) * kStage;
-        if (s + 1 < steps) {
-            la.load((s + 1) * kTileK, k_dim, at + (cur ^ kStage));
-            lb.load((s + 1) * kTileK, k_dim, at + (cur ^ kStage) + kHalf);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) f[0].b[i] = rb.read(lds + kRingB, i, 0);
+#pragma unroll
+        for (int i = 0; i < MS; ++i) f[0].a[i] = ra.read(lds, i, 0);
+        int b_now = kRingB, b_next = kRingB + kPart, b_free = kRingB + 2 * kPart;
+        for (int s = 0; s < steps; s += 2) {
+#pragma unroll
+            for (int slot = 0; slot < 2; ++slot) {
+                if (slot && s + 1 >= steps) break;
+                lb.begin((s + slot + 2) * kStep, k_dim);
+                half_step<MS, NS, MS>(ra, rb, lds + slot * kPart, lds + b_now, 1, f[0], f[1], acc, [&](int g) {
+#pragma unroll
+                    for (int c = g * LB::kLoads / MS; c < (g + 1) * LB::kLoads / MS; ++c) lb.copy(c, at + b_free);
+                });
+                wait_copies<LB::kLoads>();
+                barrier_only();
+                la.begin((s + slot + 2) * kStep, k_dim);
+                half_step<MS, NS, MS>(ra, rb, lds + (slot ^ 1) * kPart, lds + b_next, 0, f[1], f[0], acc, [&](int g) {
+#pragma unroll
+                    for (int c = g * LA::kLoads / MS; c < (g + 1) * LA::kLoads / MS; ++c)
+                        la.copy(c, at + slot * kPart);
+                });
+                lb.stage(lds + b_free);
+                const int b = b_now;
+                b_now = b_next, b_next = b_free, b_free = b;
+            }
         }
-        const char* pa = lds + cur;
-        const char* pb = pa + kHalf;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            bf16x8 a[MS], b[NS];
-#pragma unroll
-            for (int i = 0; i < NS; ++i) b[i] = rb.read(pb, i, kk);
-#pragma unroll
-            for (int i = 0; i < MS; ++i) a[i] = ra.read(pa, i, kk);
-#pragma unroll
-            for (int i = 0; i < MS; ++i)
-#pragma unroll
-                for (int j = 0; j < NS; ++j) acc[i][j] = mfma_bf16(b[j], a[i], acc[i][j]);
-        }
+        keep(f[0]);
+        wait_copies<0>();  // none may land after the workgroup has left its LDS
     }
     settle(acc);
-    barrier_only();  // the caller may use the stages again
+    barrier_only();  // the caller may use the slots again
 }
 
 // ---- Tiles of ragged experts ------------------------------------------------
@@ -228,8 +306,12 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int row
         const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
         const int m = hi - lo, nf = m / kFullRows, nt = m % kFullRows != 0;
         if (!is_tail && item >= pf * n_tiles && item < (pf + nf) * n_tiles) {
+            // Groups of up to 8 row tiles, the column tiles of a group one after
+            // the other: the 32 tiles that an XCD works on at a time are then
+            // about 8 x 4 and share their operands, also in an expert of many rows.
             const int local = item - pf * n_tiles;
-            *found = {e, lo + (local % nf) * kFullRows, kFullRows, local / nf, kFullRows};
+            const int group = local / (8 * n_tiles), in = local % (8 * n_tiles), high = min(8, nf - group * 8);
+            *found = {e, lo + (group * 8 + in % high) * kFullRows, kFullRows, in / high, kFullRows};
         }
         if (is_tail && nt && item >= pt * n_tiles && item < (pt + 1) * n_tiles) {
             const int r = m % kFullRows;
@@ -458,39 +540,41 @@ struct WgradArgs {
     uint32_t* err;
 };
 
-// The FP8 rows of a step: each thread reads 32 values (two 16-byte vectors) of
-// one memory row with their block's scale, and writes them to LDS as bf16 in
-// the columns layout. The value is rounded to bf16 once (2^-9 of it, against
-// e4m3's own 2^-4) because the matrix instruction multiplies bf16.
+// The FP8 rows of a step: each thread fetches 32 values (two 16-byte vectors) of
+// one memory row with their block's scale into registers, and half a step
+// later writes them to LDS as bf16 in the columns layout. The value is rounded
+// to bf16 once (2^-8 of it, against e4m3's own 2^-4) because the matrix
+// instruction multiplies bf16.
 struct Fp8Loader {
+    static constexpr int kLoads = 0;  // copies to LDS
     const uint8_t* p;
     const float* s;
     int64_t ld;
-    int col, cols, row;
+    int row, col;
+    bool in_cols;
     u32x4 v[2];
     float scale;
 
     __device__ __forceinline__ void init(const uint8_t* x8, const float* scales, int64_t k_dim, int col0) {
         row = threadIdx.x >> 3;
         col = (threadIdx.x & 7) * 32;
-        cols = (int)k_dim - col0;
         ld = k_dim;
-        p = x8 + col0 + col;
-        s = scales + (col0 + col) / 128;
+        in_cols = col0 + col < k_dim;
+        p = x8 + row * ld + col0 + col;
+        s = scales + row * (ld / 128) + (col0 + col) / 128;
     }
-    __device__ __forceinline__ void fetch(int k0, int k_dim) {
-        const bool in = k0 + row < k_dim && col < cols;
-        const int64_t r = in ? k0 + row : 0;
+    __device__ __forceinline__ void copy(int, uint32_t) {}
+    __device__ __forceinline__ void begin(int k0, int k_dim) {
         const u32x4 zero = {0u, 0u, 0u, 0u};
         v[0] = v[1] = zero;
         scale = 0.f;
-        if (in) {
-            v[0] = ld16(p + r * ld);
-            v[1] = ld16(p + r * ld + 16);
-            scale = s[r * (ld / 128)];
+        if (k0 + row < k_dim && in_cols) {
+            v[0] = ld16(p + k0 * ld);
+            v[1] = ld16(p + k0 * ld + 16);
+            scale = s[k0 * (ld / 128)];
         }
     }
-    __device__ __forceinline__ void store(char* lds) const {
+    __device__ __forceinline__ void stage(char* lds) const {
         const int f = (row & 3) | (((row >> 3) & 3) << 2);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -539,36 +623,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     } else {
         Fp8Loader lb;
         lb.init(a.x8 + (int64_t)row0 * a.k_dim, a.x_scales + (int64_t)row0 * (a.k_dim / 128), a.k_dim, k0);
-        const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
-        const int steps = (rows + kTileK - 1) / kTileK;
-        if (steps > 0) {
-            la.load(0, rows, at);
-            lb.fetch(0, rows);
-            lb.store(lds + kHalf);
-        }
-        for (int s = 0; s < steps; ++s) {
-            wait_copies<0>();
-            barrier_only();
-            const int cur = (s & 1) * kStage;
-            if (s + 1 < steps) {
-                la.load((s + 1) * kTileK, rows, at + (cur ^ kStage));
-                lb.fetch((s + 1) * kTileK, rows);
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8 fa[MS], fb[NS];
-#pragma unroll
-                for (int i = 0; i < NS; ++i) fb[i] = rb.read(lds + cur + kHalf, i, kk);
-#pragma unroll
-                for (int i = 0; i < MS; ++i) fa[i] = ra.read(lds + cur, i, kk);
-#pragma unroll
-                for (int i = 0; i < MS; ++i)
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
-            }
-            if (s + 1 < steps) lb.store(lds + (cur ^ kStage) + kHalf);
-        }
-        settle(acc);
+        multiply<MS, NS>(la, lb, ra, rb, rows, lds, acc);
     }
     const int i = lane_id() & 15, q = lane_id() >> 4;
 #pragma unroll
