@@ -463,7 +463,7 @@ int ep_expert_matmul(const ep_shape* shape, const ep_layout* layout, const uint1
     if (!layout->expert_offsets || !w || (rows > 0 && (!x || !y))) return EP_ERR_ARG;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(layout->expert_offsets, 4))
         return EP_ERR_ARG;
-    if (expert_matmul_grid(rows, shape->E, n_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (expert_matmul_tiles(rows, shape->E, n_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
     return hip_status(launch_expert_matmul(*shape, *layout, x, rows, k_dim, w, n_dim, w_order, y,
                                            static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
@@ -481,7 +481,7 @@ int ep_expert_swiglu(const ep_shape* shape, const ep_layout* layout, const uint1
         return EP_ERR_ARG;
     // 32-bit offsets inside one expert's matrix.
     if (4 * (int64_t)F * shape->H >= INT32_MAX - 15) return EP_ERR_UNSUPPORTED;
-    if (expert_swiglu_grid(rows, shape->E, F) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (expert_swiglu_tiles(rows, shape->E, F) > INT32_MAX) return EP_ERR_UNSUPPORTED;
     return hip_status(launch_expert_swiglu(*shape, *layout, x, rows, w13, F, act, gu_fp8, gu_scales,
                                            static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
@@ -516,7 +516,7 @@ int ep_expert_wgrad(const ep_shape* shape, const ep_layout* layout, const uint16
     if (!aligned(dy, 16) || !aligned(x->x, 16) || !aligned(x->x_fp8, 16) || !aligned(x->x_scales, 16) ||
         !aligned(dw, 16) || !aligned(layout->expert_offsets, 4))
         return EP_ERR_ARG;
-    if (expert_wgrad_grid(shape->E, n_dim, k_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (expert_wgrad_tiles(shape->E, n_dim, k_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
     return hip_status(launch_expert_wgrad(*shape, *layout, dy, rows, n_dim, x->x, x->x_fp8, x->x_scales, k_dim, dw,
                                           dtype, static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }

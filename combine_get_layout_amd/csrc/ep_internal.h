@@ -108,10 +108,11 @@ hipError_t launch_copy_epilogue(const ep_shape& s, const ep_sources& src, const 
 hipError_t launch_source_fused(const ep_shape& s, const ep_sources& src, const ep_tokens& tk,
                                uint32_t epoch, void* staging, const ep_recv& rv, char* ws, hipStream_t st);
 
-// Expert products (rows already fits 31 bits).
-int64_t expert_matmul_grid(int64_t rows, int E, int n_dim);
-int64_t expert_swiglu_grid(int64_t rows, int E, int F);
-int64_t expert_wgrad_grid(int E, int n_dim, int k_dim);
+// Expert products (rows already fits 31 bits). Tiles: the most a call may have,
+// which must fit 31 bits.
+int64_t expert_matmul_tiles(int64_t rows, int E, int n_dim);
+int64_t expert_swiglu_tiles(int64_t rows, int E, int F);
+int64_t expert_wgrad_tiles(int E, int n_dim, int k_dim);
 hipError_t launch_expert_matmul(const ep_shape& s, const ep_layout& L, const uint16_t* x, int64_t rows, int k_dim,
                                 const uint16_t* w, int n_dim, int order, uint16_t* y, char* ws, hipStream_t st);
 hipError_t launch_expert_swiglu(const ep_shape& s, const ep_layout& L, const uint16_t* x, int64_t rows,

@@ -6,6 +6,7 @@
 //   swiglu  g = x W13[e][0:F]^T, u = x W13[e][F:2F]^T, act = silu(g) u
 //   wgrad   dW[e][n][k] = sum_{i of e} dy[i][n] x[i][k]
 #include <algorithm>
+#include <type_traits>
 
 #include "ep_internal.h"
 #include "ep_mfma.h"
@@ -27,27 +28,27 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 
 // ---- Operand tiles in LDS ---------------------------------------------------
 //
-// "Rows" layout: ROWS rows of 64 contracted values (128 bytes, eight 16-byte
-// chunks). Chunk c of row r lies at chunk c ^ ((r >> 1) & 7), which a wave's
-// 16-byte reads pass without bank conflicts.
+// "Rows" layout: rows of 64 contracted values (128 bytes, eight 16-byte
+// chunks). Chunk c of row r lies at chunk c ^ f(r). A wave's 16-byte reads go
+// through the banks (64 x 4 bytes) in groups of 16 lanes such as {0-3, 12-15,
+// 20-27}; f(r) = (r >> 1) & 7 serves lanes that read 16 rows in a run,
+// pairs_swizzle those that read rows 8 a + b (a, b = 0..3), both without
+// conflicts.
 //
 // "Columns" layout: 64 contracted rows of 256 values (512 bytes, sixteen
-// 32-byte blocks). Block b of row k lies at block b ^ f(k), f(k) = (k & 3) |
-// ((k >> 3) & 3) << 2: the 16 rows that a wave's transposing read touches then
-// cover the banks evenly.
+// 32-byte blocks). Block b of row k lies at block b ^ cols_swizzle(k): the 16
+// rows that a wave's transposing read touches then cover the banks evenly.
 //
 // Steps of 64 rather than 32 indices, so that every copy takes whole 128-byte
-// lines: with 64-byte pieces a tile's copies alone filled the L2's requests
-// (1060 against TFLOP/s at 32 experts of 1,024 x 7168 x 4096).
+// lines: with 64-byte pieces the copies filled the L2's requests (1,060
+// against 1,120 TFLOP/s at 32 experts of 1,024 x 7168 x 4096, else alike).
+__device__ __forceinline__ int pairs_swizzle(int r) { return ((r >> 1) & 1) | ((r >> 3) & 3) << 1; }
+__device__ __forceinline__ int cols_swizzle(int k) { return (k & 3) | ((k >> 3) & 3) << 2; }
 
-// An operand that needs no work between its copy and its reads.
-struct NoStaging {
-    __device__ __forceinline__ void stage(char*) {}
-};
-
-// A tile operand whose contracted index is contiguous in memory.
-template <int ROWS>
-struct RowsLoader : NoStaging {
+// A tile operand whose contracted index is contiguous in memory: ROWS rows,
+// first (BY_PAIRS false) or second operand.
+template <int ROWS, bool BY_PAIRS>
+struct RowsLoader {
     static constexpr int kLoads = ROWS / 64;
     const char* p;
     uint32_t bytes;
@@ -61,9 +62,8 @@ struct RowsLoader : NoStaging {
     __device__ __forceinline__ void init(const void* base, uint32_t n_bytes, RowOff row) {
         p = static_cast<const char*>(base);
         bytes = n_bytes;
-        const int lane = lane_id(), wave = wave_in_block();
-        const int r = wave * 8 + (lane >> 3);
-        const int chunk = (lane & 7) ^ ((r >> 1) & 7);
+        const int lane = lane_id(), r = wave_in_block() * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ (BY_PAIRS ? pairs_swizzle(r) : (r >> 1) & 7);
         k = chunk * 8;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
@@ -80,11 +80,12 @@ struct RowsLoader : NoStaging {
     __device__ __forceinline__ void copy(int j, uint32_t lds) {
         copy16_to_lds(d, off[j] + far, lds + (j * 64 + uniform_wave() * 8) * 128);
     }
+    __device__ __forceinline__ void stage(char*) {}
 };
 
 // A tile operand whose 256 columns are contiguous in memory (one contracted
 // index per memory row of ld values).
-struct ColsLoader : NoStaging {
+struct ColsLoader {
     static constexpr int kLoads = 4;
     const char* p;
     int64_t ld_bytes;
@@ -100,8 +101,7 @@ struct ColsLoader : NoStaging {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int r = j * 16 + wave * 2 + (lane >> 5);
-            const int f = (r & 3) | (((r >> 3) & 3) << 2);
-            const int block = ((lane & 31) >> 1) ^ f;
+            const int block = ((lane & 31) >> 1) ^ cols_swizzle(r);
             off[j] = (uint32_t)(r * ld_bytes) + block * 32 + (lane & 1) * 16;
         }
     }
@@ -112,16 +112,71 @@ struct ColsLoader : NoStaging {
     __device__ __forceinline__ void copy(int j, uint32_t lds) {
         copy16_to_lds(d, off[j], lds + (j * 16 + uniform_wave() * 2) * 512);
     }
+    __device__ __forceinline__ void stage(char*) {}
 };
 
-// 16 x 32 fragments of the step at lds: sub-tile s (16 rows or columns), half
-// `half` of the contracted indices.
+// The FP8 rows of a step as second operand: each thread fetches 32 values (two
+// 16-byte vectors) of one memory row with their block's scale into registers,
+// and a step later writes them to LDS as bf16 in the columns layout. The value
+// is rounded to bf16 once (2^-8 of it, against e4m3's own 2^-4) because the
+// matrix instruction multiplies bf16.
+struct Fp8Loader {
+    static constexpr int kLoads = 0;  // copies to LDS
+    const uint8_t* p;
+    const float* s;
+    int64_t ld;
+    int row, col;
+    bool in_cols;
+    u32x4 v[2];
+    float scale;
+
+    __device__ __forceinline__ void init(const uint8_t* x8, const float* scales, int64_t k_dim, int col0) {
+        row = threadIdx.x >> 3;
+        col = (threadIdx.x & 7) * 32;
+        ld = k_dim;
+        in_cols = col0 + col < k_dim;
+        p = x8 + row * ld + col0 + col;
+        s = scales + row * (ld / 128) + (col0 + col) / 128;
+    }
+    __device__ __forceinline__ void copy(int, uint32_t) {}
+    __device__ __forceinline__ void begin(int k0, int k_dim) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        v[0] = v[1] = zero;
+        scale = 0.f;
+        if (k0 + row < k_dim && in_cols) {
+            v[0] = ld16(p + k0 * ld);
+            v[1] = ld16(p + k0 * ld + 16);
+            scale = s[k0 * (ld / 128)];
+        }
+    }
+    __device__ __forceinline__ void stage(char* lds) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t o[8];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[h][w], false);
+                const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[h][w], true);
+                o[2 * w] = pack_bf16(lo[0] * scale, lo[1] * scale);
+                o[2 * w + 1] = pack_bf16(hi[0] * scale, hi[1] * scale);
+            }
+            char* d = lds + row * 512 + (((col / 16 + h) ^ cols_swizzle(row)) << 5);
+            *reinterpret_cast<u32x4*>(d) = {o[0], o[1], o[2], o[3]};
+            *reinterpret_cast<u32x4*>(d + 16) = {o[4], o[5], o[6], o[7]};
+        }
+    }
+};
+
+// 16 x 32 fragments of the step at lds: sub-tile s, half `half` of the
+// contracted indices. First operand: sub-tile s is rows (or columns) 16 s .. +
+// 15. Second operand ("pairs"): sub-tiles 2 p + u, u = 0, 1, share 32 columns,
+// u holding columns 8 a + 4 u + b (a, b = 0..3) as its 16, so that a lane's
+// results of both are 8 consecutive columns: 16-byte stores of bf16.
 struct RowsReader {
-    static constexpr int kReads = 1;  // LDS instructions per fragment
     uint32_t base[2];
-    __device__ __forceinline__ void init(int first_sub) {
+    __device__ __forceinline__ void init(int first_row) {
         const int i = lane_id() & 15, q = lane_id() >> 4;
-        const uint32_t row = (first_sub * 16 + i) * 128;
+        const uint32_t row = (first_row + i) * 128;
         base[0] = row + ((q ^ (i >> 1)) * 16);
         base[1] = row + (((q + 4) ^ (i >> 1)) * 16);
     }
@@ -129,21 +184,37 @@ struct RowsReader {
         return *reinterpret_cast<const bf16x8*>(lds + base[half] + s * 2048);
     }
 };
-template <int SUBS>
-struct ColsReader {
-    static constexpr int kReads = 2;
-    uint32_t base[SUBS];
-    __device__ __forceinline__ void init(int first_sub) {
+struct RowsPairReader {
+    uint32_t base[2];
+    int step;  // LDS bytes from one sub-tile of a pair to the other
+    __device__ __forceinline__ void init(int first_col, int from_u_to_u = 4) {
         const int i = lane_id() & 15, q = lane_id() >> 4;
-        const int f = (i >> 2) | (q << 2);
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s)
-            base[s] = (q * 8 + (i >> 2)) * 512 + (((first_sub + s) ^ f) << 5) + (i & 3) * 8;
+        const int r = (i >> 2) * 8 + (i & 3);
+        const uint32_t row = (first_col + r) * 128;
+        base[0] = row + ((q ^ pairs_swizzle(r)) * 16);
+        base[1] = row + (((q + 4) ^ pairs_swizzle(r)) * 16);
+        step = from_u_to_u * 128;
     }
-    // Each 16-lane group reads 4 contracted rows of 16 values and receives
-    // them transposed: lane i gets the 4 rows' values of column i.
     __device__ __forceinline__ bf16x8 read(const char* lds, int s, int half) const {
-        const char* p = lds + base[s] + half * 16384;
+        return *reinterpret_cast<const bf16x8*>(lds + base[half] + (s >> 1) * 4096 + (s & 1) * step);
+    }
+};
+// The columns layout is read by the transposing instruction: each 16-lane
+// group reads 4 contracted rows of 4 pieces of 4 values and receives them
+// transposed: lane i gets the 4 rows' values of column i % 4 of piece i / 4.
+template <int SUBS, bool PAIRS>
+struct ColsReader {
+    uint32_t base[PAIRS ? SUBS / 2 : SUBS];
+    __device__ __forceinline__ void init(int first_col) {
+        const int i = lane_id() & 15, q = lane_id() >> 4, piece = i & 3;
+        const int k = q * 8 + (i >> 2), b0 = first_col / 16;
+#pragma unroll
+        for (int s = 0; s < (PAIRS ? SUBS / 2 : SUBS); ++s)
+            base[s] = PAIRS ? k * 512 + (((b0 + 2 * s + (piece >> 1)) ^ cols_swizzle(k)) << 5) + (piece & 1) * 16
+                            : k * 512 + (((b0 + s) ^ cols_swizzle(k)) << 5) + piece * 8;
+    }
+    __device__ __forceinline__ bf16x8 read(const char* lds, int s, int half) const {
+        const char* p = lds + (PAIRS ? base[s >> 1] + (s & 1) * 8 : base[s]) + half * 16384;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS_PTR(s16x4))p);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS_PTR(s16x4))(p + 2048));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -200,140 +271,162 @@ __device__ __forceinline__ void half_step(const RA& ra, const RB& rb, const char
 // three of the second. In the first half of step s the copies of the second
 // operand's step s + 2 are issued (into the slot of step s - 1), in the second
 // half those of the first operand's (into the slot of step s, whose last
-// fragments have then been read), so copies are spread over the whole step
-// and have between one and two steps' time to arrive.
+// fragments have then been read), one for each four
+// matrix instructions from the start, so copies are spread over the step and
+// still have nearly one step (a step is 1.1 us) and one and a half to arrive.
+template <class LA, class LB>
+__device__ __forceinline__ void first_steps(LA& la, LB& lb, int k_dim, char* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
+    LB lb1 = lb;
+    lb.begin(0, k_dim);
+    lb1.begin(kStep, k_dim);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        la.begin(s * kStep, k_dim);
+#pragma unroll
+        for (int c = 0; c < LA::kLoads; ++c) la.copy(c, at + s * kPart);
+#pragma unroll
+        for (int c = 0; c < LB::kLoads; ++c) (s ? lb1 : lb).copy(c, at + kRingB + s * kPart);
+    }
+    lb.stage(lds + kRingB);
+    lb1.stage(lds + kRingB + kPart);
+}
+// After first_steps (which may be long before: the copies of a tile's first
+// steps run beside the results of the tile before it).
 template <int MS, int NS, class LA, class LB, class RA, class RB>
 __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB& rb, int k_dim, char* lds,
                                          f32x4 (&acc)[MS][NS]) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
     const int steps = (k_dim + kStep - 1) / kStep;
-    if (steps > 0) {
+    wait_copies<0>();
+    barrier_only();
+    Fragments<MS, NS> f[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            la.begin(s * kStep, k_dim);
-            lb.begin(s * kStep, k_dim);
-            for (int c = 0; c < LA::kLoads; ++c) la.copy(c, at + s * kPart);
-            for (int c = 0; c < LB::kLoads; ++c) lb.copy(c, at + kRingB + s * kPart);
-            lb.stage(lds + kRingB + s * kPart);
+    for (int i = 0; i < NS; ++i) f[0].b[i] = rb.read(lds + kRingB, i, 0);
+#pragma unroll
+    for (int i = 0; i < MS; ++i) f[0].a[i] = ra.read(lds, i, 0);
+    int b_now = kRingB, b_next = kRingB + kPart, b_free = kRingB + 2 * kPart;
+    for (int s = 0; s < steps; s += 2) {
+#pragma unroll
+        for (int slot = 0; slot < 2; ++slot) {
+            if (slot && s + 1 >= steps) break;
+            lb.begin((s + slot + 2) * kStep, k_dim);
+            half_step<MS, NS, MS>(ra, rb, lds + slot * kPart, lds + b_now, 1, f[0], f[1], acc, [&](int g) {
+#pragma unroll
+                for (int c = g; c < LB::kLoads && c == g; ++c) lb.copy(c, at + b_free);
+            });
+            wait_copies<LB::kLoads>();
+            barrier_only();
+            la.begin((s + slot + 2) * kStep, k_dim);
+            half_step<MS, NS, MS>(ra, rb, lds + (slot ^ 1) * kPart, lds + b_next, 0, f[1], f[0], acc, [&](int g) {
+#pragma unroll
+                for (int c = g; c < LA::kLoads && c == g; ++c) la.copy(c, at + slot * kPart);
+            });
+            lb.stage(lds + b_free);
+            const int b = b_now;
+            b_now = b_next, b_next = b_free, b_free = b;
         }
-        Fragments<MS, NS> f[2];
-        wait_copies<LA::kLoads + LB::kLoads>();
-        barrier_only();
-#pragma unroll
-        for (int i = 0; i < NS; ++i) f[0].b[i] = rb.read(lds + kRingB, i, 0);
-#pragma unroll
-        for (int i = 0; i < MS; ++i) f[0].a[i] = ra.read(lds, i, 0);
-        int b_now = kRingB, b_next = kRingB + kPart, b_free = kRingB + 2 * kPart;
-        for (int s = 0; s < steps; s += 2) {
-#pragma unroll
-            for (int slot = 0; slot < 2; ++slot) {
-                if (slot && s + 1 >= steps) break;
-                lb.begin((s + slot + 2) * kStep, k_dim);
-                half_step<MS, NS, MS>(ra, rb, lds + slot * kPart, lds + b_now, 1, f[0], f[1], acc, [&](int g) {
-#pragma unroll
-                    for (int c = g * LB::kLoads / MS; c < (g + 1) * LB::kLoads / MS; ++c) lb.copy(c, at + b_free);
-                });
-                wait_copies<LB::kLoads>();
-                barrier_only();
-                la.begin((s + slot + 2) * kStep, k_dim);
-                half_step<MS, NS, MS>(ra, rb, lds + (slot ^ 1) * kPart, lds + b_next, 0, f[1], f[0], acc, [&](int g) {
-#pragma unroll
-                    for (int c = g * LA::kLoads / MS; c < (g + 1) * LA::kLoads / MS; ++c)
-                        la.copy(c, at + slot * kPart);
-                });
-                lb.stage(lds + b_free);
-                const int b = b_now;
-                b_now = b_next, b_next = b_free, b_free = b;
-            }
-        }
-        keep(f[0]);
-        wait_copies<0>();  // none may land after the workgroup has left its LDS
     }
+    keep(f[0]);
+    wait_copies<0>();  // none may land after the slots have been handed on
     settle(acc);
-    barrier_only();  // the caller may use the slots again
+    barrier_only();
 }
 
 // ---- Tiles of ragged experts ------------------------------------------------
 
 struct Tile {
     int expert;
-    int row0;   // first row of the tile
-    int rows;   // rows of the tile that exist
-    int n;      // column tile
-    int shape;  // row capacity of the tile: 256 (full), else the tail's
+    int row0;  // first row of the tile
+    int rows;  // rows of the tile that exist
+    int n;     // column tile
 };
 
-// Finds this workgroup's tile; false if there is none. Every expert has
-// floor(m / 256) full tiles and one tail of m % 256 rows, each times `n_tiles`.
-// Full tiles come first (tails fill the gaps at the end). Workgroups go to the
-// 8 XCDs in turn, so each XCD takes a contiguous run of tiles: within an
-// expert the row tiles of one column tile follow each other, and the tiles that
-// an XCD holds at a time share their operands through its L2.
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int rows, int n_tiles, char* lds, Tile& t) {
-    int* wave_sum = reinterpret_cast<int*>(lds);       // [8][2]
-    Tile* found = reinterpret_cast<Tile*>(lds + 256);
-    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
-    const int per = (E + kThreads - 1) / kThreads;
-    const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
-    int full = 0, tail = 0;
-    for (int e = e0; e < e1; ++e) {
-        const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
-        full += (hi - lo) / kFullRows;
-        tail += (hi - lo) % kFullRows != 0;
-    }
-    int sf = full, st = tail;
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int a = __shfl_up(sf, d), b = __shfl_up(st, d);
-        if (lane >= d) sf += a, st += b;
-    }
-    if (lane == kWave - 1) wave_sum[wave * 2] = sf, wave_sum[wave * 2 + 1] = st;
-    if (tid == 0) found->expert = -1;
-    __syncthreads();
-    int total_f = 0, total_t = 0, before_f = 0, before_t = 0;
-    for (int w = 0; w < kThreads / kWave; ++w) {
-        if (w == wave) before_f = total_f, before_t = total_t;
-        total_f += wave_sum[w * 2], total_t += wave_sum[w * 2 + 1];
-    }
-    // Exclusive prefix of this thread's experts.
-    int pf = before_f + sf - full, pt = before_t + st - tail;
-    const int per_f = (total_f * n_tiles + 7) / 8, per_t = (total_t * n_tiles + 7) / 8;
-    const int xcd = blockIdx.x % 8, seq = blockIdx.x / 8;
-    const bool is_tail = seq >= per_f;
-    const int item = is_tail ? xcd * per_t + seq - per_f : xcd * per_f + seq;
-    const bool none = is_tail ? (seq - per_f >= per_t || item >= total_t * n_tiles) : item >= total_f * n_tiles;
-    if (none) return false;
-    for (int e = e0; e < e1; ++e) {
-        const int lo = min(max(offsets[e], 0), rows), hi = min(max(offsets[e + 1], lo), rows);
-        const int m = hi - lo, nf = m / kFullRows, nt = m % kFullRows != 0;
-        if (!is_tail && item >= pf * n_tiles && item < (pf + nf) * n_tiles) {
-            // Groups of up to 8 row tiles, the column tiles of a group one after
-            // the other: the 32 tiles that an XCD works on at a time are then
-            // about 8 x 4 and share their operands, also in an expert of many rows.
-            const int local = item - pf * n_tiles;
-            const int group = local / (8 * n_tiles), in = local % (8 * n_tiles), high = min(8, nf - group * 8);
-            *found = {e, lo + (group * 8 + in % high) * kFullRows, kFullRows, in / high, kFullRows};
-        }
-        if (is_tail && nt && item >= pt * n_tiles && item < (pt + 1) * n_tiles) {
-            const int r = m % kFullRows;
-            *found = {e, hi - r, r, item - pt * n_tiles, r > 128 ? 256 : r > 64 ? 128 : 64};
-        }
-        pf += nf, pt += nt;
-    }
-    __syncthreads();
-    t = *found;
-    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
-    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    t.n = __builtin_amdgcn_readfirstlane(t.n);
-    t.shape = __builtin_amdgcn_readfirstlane(t.shape);
-    __syncthreads();
-    return t.expert >= 0;
-}
+// The tiles of a launch. Every expert has floor(m / 256) full tiles and one
+// tail of m % 256 rows, each times `n_tiles`; full tiles come first (tails fill
+// the gaps at the end). Workgroups go to the 8 XCDs in turn, so each XCD takes
+// a contiguous run of tiles, and its workgroups take them in turn: within an
+// expert groups of up to 8 row tiles, the column tiles of a group one after the
+// other, so that the 32 tiles that an XCD works on at a time are about 8 x 4 (4
+// x 8 at 1,024 rows) and share their operands through its L2.
+struct Tiles {
+    const int32_t* offsets;
+    int rows, n_tiles;
+    int e0, e1;            // this thread's experts
+    int pf, pt;            // full and tail row tiles of the experts before e0
+    int total_f, total_t;
+    Tile* found;
 
-// Workgroups that cover every tile of `rows` rows over E experts.
-int64_t tile_grid(int64_t rows, int E, int64_t n_tiles) {
-    const int64_t full = rows / kFullRows * n_tiles, tails = std::min<int64_t>(E, rows) * n_tiles;
-    return (full + 7) / 8 * 8 + (tails + 7) / 8 * 8;
+    __device__ __forceinline__ void bounds(int e, int& lo, int& hi) const {
+        lo = min(max(offsets[e], 0), rows);
+        hi = min(max(offsets[e + 1], lo), rows);
+    }
+    __device__ __forceinline__ void init(const int32_t* offs, int E, int n_rows, int n, char* lds) {
+        offsets = offs, rows = n_rows, n_tiles = n;
+        found = reinterpret_cast<Tile*>(lds + kLdsBytes - 64);  // in the slot that first_steps leaves free
+        int* wave_sum = reinterpret_cast<int*>(lds);
+        const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+        const int per = (E + kThreads - 1) / kThreads;
+        e0 = min(E, tid * per), e1 = min(E, e0 + per);
+        int full = 0, tail = 0;
+        for (int e = e0; e < e1; ++e) {
+            int lo, hi;
+            bounds(e, lo, hi);
+            full += (hi - lo) / kFullRows;
+            tail += (hi - lo) % kFullRows != 0;
+        }
+        int sf = full, st = tail;
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int a = __shfl_up(sf, d), b = __shfl_up(st, d);
+            if (lane >= d) sf += a, st += b;
+        }
+        if (lane == kWave - 1) wave_sum[wave * 2] = sf, wave_sum[wave * 2 + 1] = st;
+        __syncthreads();
+        total_f = total_t = 0;
+        pf = sf - full, pt = st - tail;
+        for (int w = 0; w < kThreads / kWave; ++w) {
+            if (w < wave) pf += wave_sum[w * 2], pt += wave_sum[w * 2 + 1];
+            total_f += wave_sum[w * 2], total_t += wave_sum[w * 2 + 1];
+        }
+        total_f = __builtin_amdgcn_readfirstlane(total_f);
+        total_t = __builtin_amdgcn_readfirstlane(total_t);
+        __syncthreads();
+    }
+    // The seq-th tile of this workgroup's XCD; false if there is none.
+    __device__ __forceinline__ bool find(int seq, Tile& t) const {
+        const int xcd = blockIdx.x % 8;
+        const int all_f = total_f * n_tiles, all_t = total_t * n_tiles;
+        const int per_f = (all_f + 7) / 8, per_t = (all_t + 7) / 8;
+        const int mine_f = min(max(all_f - xcd * per_f, 0), per_f), mine_t = min(max(all_t - xcd * per_t, 0), per_t);
+        const bool is_tail = seq >= mine_f;
+        if (is_tail && seq - mine_f >= mine_t) return false;
+        const int item = is_tail ? xcd * per_t + seq - mine_f : xcd * per_f + seq;
+        const int target = item / n_tiles;  // lies in its expert's range of row tiles
+        int f = pf, l = pt;
+        for (int e = e0; e < e1; ++e) {
+            int lo, hi;
+            bounds(e, lo, hi);
+            const int m = hi - lo, nf = m / kFullRows, nt = m % kFullRows != 0;
+            if (!is_tail && target >= f && target < f + nf) {
+                const int local = item - f * n_tiles;
+                const int group = local / (8 * n_tiles), in = local % (8 * n_tiles), high = min(8, nf - group * 8);
+                *found = {e, lo + (group * 8 + in % high) * kFullRows, kFullRows, in / high};
+            }
+            if (is_tail && nt && target == l) *found = {e, hi - m % kFullRows, m % kFullRows, item - l * n_tiles};
+            f += nf, l += nt;
+        }
+        __syncthreads();
+        t.expert = __builtin_amdgcn_readfirstlane(found->expert);
+        t.row0 = __builtin_amdgcn_readfirstlane(found->row0);
+        t.rows = __builtin_amdgcn_readfirstlane(found->rows);
+        t.n = __builtin_amdgcn_readfirstlane(found->n);
+        return true;
+    }
+};
+
+// Most tiles of `rows` rows over E experts.
+int64_t most_tiles(int64_t rows, int E, int64_t n_tiles) {
+    return (rows / kFullRows + std::min<int64_t>(E, rows)) * n_tiles;
 }
 
 struct MatmulArgs {
@@ -349,65 +442,90 @@ __device__ __forceinline__ void check_rows(const int32_t* offsets, int E, int ro
     if (blockIdx.x == 0 && threadIdx.x == 0 && offsets[E] > rows) report(err, EP_DEVERR_CAPACITY);
 }
 
-// Waves: WM over rows, 8 / WM over columns; a wave's block is MS x NS sub-tiles
-// of 16 x 16.
-template <int WM, int MS, bool KN>
-__device__ __forceinline__ void matmul_tile(const MatmulArgs& a, const Tile& t, char* lds) {
-    constexpr int WN = 8 / WM, NS = 16 / WN, ROWS = WM * MS * 16;
-    const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
-    const int64_t K = a.k_dim, N = a.n_dim;
-    const int n0 = t.n * kTileN;
-    RowsLoader<ROWS> la;
-    const uint32_t x_ld = (uint32_t)K * 2;
-    la.init(a.x + (int64_t)t.row0 * K, (uint32_t)t.rows * x_ld,
-            [&](int r) { return r < t.rows ? r * x_ld : kBufOutside; });
-    RowsReader ra;
-    ra.init(wm * MS);
-    f32x4 acc[MS][NS] = {};
-    const uint16_t* w = a.w + (int64_t)t.expert * N * K;
-    if constexpr (KN) {
-        ColsLoader lb;
-        lb.init(w, N, n0);
-        ColsReader<NS> rb;
-        rb.init(wn * NS);
-        multiply<MS, NS>(la, lb, ra, rb, a.k_dim, lds, acc);
-    } else {
-        RowsLoader<kTileN> lb;
-        const int cols = min((int)N - n0, kTileN);
-        lb.init(w + (int64_t)n0 * K, (uint32_t)cols * x_ld,
-                [&](int r) { return r < cols ? r * x_ld : kBufOutside; });
-        RowsReader rb;
-        rb.init(wn * NS);
-        multiply<MS, NS>(la, lb, ra, rb, a.k_dim, lds, acc);
+template <bool KN>
+struct MatmulLoaders;
+template <>
+struct MatmulLoaders<false> {
+    RowsLoader<kFullRows, false> a;
+    RowsLoader<kTileN, true> b;
+    __device__ __forceinline__ void init_b(const MatmulArgs& m, const uint16_t* w, int n0) {
+        const uint32_t ld = (uint32_t)m.k_dim * 2;
+        const int cols = min(m.n_dim - n0, kTileN);
+        b.init(w + (int64_t)n0 * m.k_dim, (uint32_t)cols * ld, [&](int r) { return r < cols ? r * ld : kBufOutside; });
     }
+};
+template <>
+struct MatmulLoaders<true> {
+    RowsLoader<kFullRows, false> a;
+    ColsLoader b;
+    __device__ __forceinline__ void init_b(const MatmulArgs& m, const uint16_t* w, int n0) { b.init(w, m.n_dim, n0); }
+};
+
+// Waves: WM over rows, 8 / WM over columns; a wave's block is MS x NS sub-tiles
+// of 16 x 16. `after_product` runs between the product and its results.
+template <int WM, int MS, bool KN, class After>
+__device__ __forceinline__ void matmul_tile(const MatmulArgs& a, const Tile& t, MatmulLoaders<KN>& l, char* lds,
+                                            After after_product) {
+    constexpr int WN = 8 / WM, NS = 16 / WN;
+    const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
+    const int N = a.n_dim;
+    RowsReader ra;
+    ra.init(wm * MS * 16);
+    std::conditional_t<KN, ColsReader<NS, true>, RowsPairReader> rb;
+    rb.init(wn * NS * 16);
+    f32x4 acc[MS][NS] = {};
+    multiply<MS, NS>(l.a, l.b, ra, rb, a.k_dim, lds, acc);
+    after_product();
     const int i = lane_id() & 15, q = lane_id() >> 4;
+    const int n0 = t.n * kTileN + wn * NS * 16 + q * 8;
+    uint16_t* base = a.y + (int64_t)t.row0 * N;
 #pragma unroll
     for (int mi = 0; mi < MS; ++mi) {
         const int m = (wm * MS + mi) * 16 + i;
         if (m >= t.rows) continue;
-        uint16_t* row = a.y + (int64_t)(t.row0 + m) * N;
 #pragma unroll
-        for (int ni = 0; ni < NS; ++ni) {
-            const int n = n0 + (wn * NS + ni) * 16 + q * 4;
-            const f32x4 v = acc[mi][ni];
-            const u32x2 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            if (n < N) *reinterpret_cast<u32x2*>(row + n) = o;
+        for (int p = 0; p < NS / 2; ++p) {
+            const f32x4 v = acc[mi][2 * p], w = acc[mi][2 * p + 1];
+            const u32x4 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]),
+                             pack_bf16(w[2], w[3])};
+            if (n0 + p * 32 < N) st16(base + (int64_t)m * N + n0 + p * 32, o);
         }
     }
 }
 
+// One workgroup per CU takes tiles until there are none. The first two steps
+// of the next tile are requested before the results of this one are stored, so
+// that a tile's start and end run beside each other.
 template <bool KN>
 __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(MatmulArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
     check_rows(a.offsets, a.E, a.rows, a.err);
+    Tiles tiles;
+    tiles.init(a.offsets, a.E, a.rows, (a.n_dim + kTileN - 1) / kTileN, lds);
+    MatmulLoaders<KN> l;
     Tile t;
-    if (!find_tile(a.offsets, a.E, a.rows, (a.n_dim + kTileN - 1) / kTileN, lds, t)) return;
-    if (t.shape == 256)
-        matmul_tile<2, 8, KN>(a, t, lds);
-    else if (t.shape == 128)
-        matmul_tile<2, 4, KN>(a, t, lds);
-    else
-        matmul_tile<1, 4, KN>(a, t, lds);
+    auto start = [&](int seq) {
+        if (!tiles.find(seq, t)) return false;
+        const uint32_t ld = (uint32_t)a.k_dim * 2;
+        const int rows = t.rows;
+        l.a.init(a.x + (int64_t)t.row0 * a.k_dim, (uint32_t)rows * ld,
+                 [&](int r) { return r < rows ? r * ld : kBufOutside; });
+        l.init_b(a, a.w + (int64_t)t.expert * a.n_dim * a.k_dim, t.n * kTileN);
+        first_steps(l.a, l.b, a.k_dim, lds);
+        return true;
+    };
+    int seq = blockIdx.x / 8;
+    bool more = start(seq);
+    while (more) {
+        const Tile now = t;
+        auto next = [&] { more = start(seq += gridDim.x / 8); };
+        if (now.rows > 128)
+            matmul_tile<2, 8, KN>(a, now, l, lds, next);
+        else if (now.rows > 64)
+            matmul_tile<2, 4, KN>(a, now, l, lds, next);
+        else
+            matmul_tile<1, 4, KN>(a, now, l, lds, next);
+    }
 }
 
 // ---- Gate/up product with SwiGLU and the 8-bit checkpoint -------------------
@@ -423,37 +541,45 @@ struct SwigluArgs {
     uint32_t* err;
 };
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
 
 // Scale of a block of 128 values with the largest magnitude amax: amax / 448,
 // so that the largest value is e4m3's largest; 1 where amax / 448 would be
 // too small to invert (all values then round to 0).
 __device__ __forceinline__ float block_scale(float amax) { return amax < 1e-33f ? 1.0f : amax / 448.0f; }
 
-// A column tile is 128 values of f: wave wn's columns are gate values of NS / 2
-// sub-tiles, then the up values of the same f, so one lane holds both.
-template <int WM, int MS, bool SAVE>
-__device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, char* lds) {
-    constexpr int WN = 8 / WM, NS = 16 / WN, HS = NS / 2, ROWS = WM * MS * 16;
-    const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
-    const int f0 = t.n * (kTileN / 2);
-    RowsLoader<ROWS> la;
-    RowsLoader<kTileN> lb;
-    const uint32_t ld = (uint32_t)a.H * 2;
-    la.init(a.x + (int64_t)t.row0 * a.H, (uint32_t)t.rows * ld, [&](int r) { return r < t.rows ? r * ld : kBufOutside; });
-    lb.init(a.w13 + (int64_t)t.expert * 2 * a.F * a.H, (uint32_t)(2 * a.F) * ld, [&](int r) {
-        const int in = r % (NS * 16), f = f0 + r / (NS * 16) * (HS * 16) + in % (HS * 16);
-        return f < a.F ? (uint32_t)(f + (in < HS * 16 ? 0 : a.F)) * ld : kBufOutside;
-    });
-    RowsReader ra, rb;
-    ra.init(wm * MS);
-    rb.init(wn * NS);
-    f32x4 acc[MS][NS] = {};
-    multiply<MS, NS>(la, lb, ra, rb, a.H, lds, acc);
+struct SwigluLoaders {
+    RowsLoader<kFullRows, false> a;
+    RowsLoader<kTileN, true> b;
+};
 
+// A column tile is 128 values of f: of each 64 LDS rows of the second operand
+// the first 32 are gate rows, the last 32 the up rows of the same f, so that
+// one lane holds both. V: consecutive values of f that a lane holds.
+template <int WM, int MS, bool SAVE, class After>
+__device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, SwigluLoaders& l, char* lds,
+                                            After after_product) {
+    constexpr int WN = 8 / WM, NS = 16 / WN, HS = NS / 2, ROWS = WM * MS * 16, V = 4 * HS;
+    const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
     const int i = lane_id() & 15, q = lane_id() >> 4;
-    const int fw = f0 + wn * HS * 16 + q * 4;
-    float* amax = reinterpret_cast<float*>(lds);  // [WN][ROWS][2]
+    RowsReader ra;
+    RowsPairReader rb;
+    ra.init(wm * MS * 16);
+    int f;
+    if constexpr (NS == 4) {
+        rb.init(wn * 64);
+        f = t.n * 128 + wn * 32 + q * 8;
+    } else {  // two waves share 64 LDS rows: u tells them apart, sub-tile 0 is gate, 1 up
+        rb.init((wn >> 1) * 64 + (wn & 1) * 4, 32);
+        f = t.n * 128 + (wn >> 1) * 32 + q * 8 + (wn & 1) * 4;
+    }
+    f32x4 acc[MS][NS] = {};
+    multiply<MS, NS>(l.a, l.b, ra, rb, a.H, lds, acc);
+    after_product();
+
+    float* amax = reinterpret_cast<float*>(lds + kRingB + 2 * kPart);  // [WN][ROWS][2], in the free slot
     if constexpr (SAVE) {
 #pragma unroll
         for (int mi = 0; mi < MS; ++mi) {
@@ -472,7 +598,7 @@ __device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, 
                 p[0] = g, p[1] = u;
             }
         }
-        __syncthreads();
+        barrier_only();
     }
 #pragma unroll
     for (int mi = 0; mi < MS; ++mi) {
@@ -494,21 +620,23 @@ __device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, 
             }
             gi = 1.0f / g, ui = 1.0f / u;
         }
+        if (f >= a.F) continue;
+        uint32_t o[V / 2], cg[HS], cu[HS];
 #pragma unroll
         for (int ni = 0; ni < HS; ++ni) {
-            const int f = fw + ni * 16;
-            if (f >= a.F) continue;
             const f32x4 g = acc[mi][ni], u = acc[mi][ni + HS];
-            float v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = g[j] * sigmoid(g[j]) * u[j];
-            const u32x2 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            *reinterpret_cast<u32x2*>(a.act + row * a.F + f) = o;
+            o[2 * ni] = pack_bf16(silu_mul(g[0], u[0]), silu_mul(g[1], u[1]));
+            o[2 * ni + 1] = pack_bf16(silu_mul(g[2], u[2]), silu_mul(g[3], u[3]));
             if constexpr (SAVE) {
-                uint8_t* c = a.gu + row * 2 * a.F + f;
-                *reinterpret_cast<uint32_t*>(c) = pack_e4m3(g[0] * gi, g[1] * gi, g[2] * gi, g[3] * gi);
-                *reinterpret_cast<uint32_t*>(c + a.F) = pack_e4m3(u[0] * ui, u[1] * ui, u[2] * ui, u[3] * ui);
+                cg[ni] = pack_e4m3(g[0] * gi, g[1] * gi, g[2] * gi, g[3] * gi);
+                cu[ni] = pack_e4m3(u[0] * ui, u[1] * ui, u[2] * ui, u[3] * ui);
             }
+        }
+        __builtin_memcpy(__builtin_assume_aligned(a.act + row * a.F + f, V * 2), o, V * 2);
+        if constexpr (SAVE) {
+            uint8_t* c = a.gu + row * 2 * a.F + f;
+            __builtin_memcpy(__builtin_assume_aligned(c, V), cg, V);
+            __builtin_memcpy(__builtin_assume_aligned(c + a.F, V), cu, V);
         }
     }
 }
@@ -517,14 +645,35 @@ template <bool SAVE>
 __global__ __launch_bounds__(kThreads, 2) void swiglu_kernel(SwigluArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
     check_rows(a.offsets, a.E, a.rows, a.err);
+    Tiles tiles;
+    tiles.init(a.offsets, a.E, a.rows, (a.F + 127) / 128, lds);
+    SwigluLoaders l;
     Tile t;
-    if (!find_tile(a.offsets, a.E, a.rows, (a.F + kTileN / 2 - 1) / (kTileN / 2), lds, t)) return;
-    if (t.shape == 256)
-        swiglu_tile<2, 8, SAVE>(a, t, lds);
-    else if (t.shape == 128)
-        swiglu_tile<2, 4, SAVE>(a, t, lds);
-    else
-        swiglu_tile<1, 4, SAVE>(a, t, lds);
+    auto start = [&](int seq) {
+        if (!tiles.find(seq, t)) return false;
+        const uint32_t ld = (uint32_t)a.H * 2;
+        const int rows = t.rows, f0 = t.n * 128;
+        l.a.init(a.x + (int64_t)t.row0 * a.H, (uint32_t)rows * ld,
+                 [&](int r) { return r < rows ? r * ld : kBufOutside; });
+        l.b.init(a.w13 + (int64_t)t.expert * 2 * a.F * a.H, (uint32_t)(2 * a.F) * ld, [&](int r) {
+            const int f = f0 + r / 64 * 32 + r % 32;
+            return f < a.F ? (uint32_t)(f + (r % 64 < 32 ? 0 : a.F)) * ld : kBufOutside;
+        });
+        first_steps(l.a, l.b, a.H, lds);
+        return true;
+    };
+    int seq = blockIdx.x / 8;
+    bool more = start(seq);
+    while (more) {
+        const Tile now = t;
+        auto next = [&] { more = start(seq += gridDim.x / 8); };
+        if (now.rows > 128)
+            swiglu_tile<2, 8, SAVE>(a, now, l, lds, next);
+        else if (now.rows > 64)
+            swiglu_tile<2, 4, SAVE>(a, now, l, lds, next);
+        else
+            swiglu_tile<1, 4, SAVE>(a, now, l, lds, next);
+    }
 }
 
 // ---- Weight gradient ----------------------------------------------------------
@@ -540,59 +689,9 @@ struct WgradArgs {
     uint32_t* err;
 };
 
-// The FP8 rows of a step: each thread fetches 32 values (two 16-byte vectors) of
-// one memory row with their block's scale into registers, and half a step
-// later writes them to LDS as bf16 in the columns layout. The value is rounded
-// to bf16 once (2^-8 of it, against e4m3's own 2^-4) because the matrix
-// instruction multiplies bf16.
-struct Fp8Loader {
-    static constexpr int kLoads = 0;  // copies to LDS
-    const uint8_t* p;
-    const float* s;
-    int64_t ld;
-    int row, col;
-    bool in_cols;
-    u32x4 v[2];
-    float scale;
-
-    __device__ __forceinline__ void init(const uint8_t* x8, const float* scales, int64_t k_dim, int col0) {
-        row = threadIdx.x >> 3;
-        col = (threadIdx.x & 7) * 32;
-        ld = k_dim;
-        in_cols = col0 + col < k_dim;
-        p = x8 + row * ld + col0 + col;
-        s = scales + row * (ld / 128) + (col0 + col) / 128;
-    }
-    __device__ __forceinline__ void copy(int, uint32_t) {}
-    __device__ __forceinline__ void begin(int k0, int k_dim) {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-        v[0] = v[1] = zero;
-        scale = 0.f;
-        if (k0 + row < k_dim && in_cols) {
-            v[0] = ld16(p + k0 * ld);
-            v[1] = ld16(p + k0 * ld + 16);
-            scale = s[k0 * (ld / 128)];
-        }
-    }
-    __device__ __forceinline__ void stage(char* lds) const {
-        const int f = (row & 3) | (((row >> 3) & 3) << 2);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t o[8];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[h][w], false);
-                const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[h][w], true);
-                o[2 * w] = pack_bf16(lo[0] * scale, lo[1] * scale);
-                o[2 * w + 1] = pack_bf16(hi[0] * scale, hi[1] * scale);
-            }
-            char* d = lds + row * 512 + (((col / 16 + h) ^ f) << 5);
-            *reinterpret_cast<u32x4*>(d) = {o[0], o[1], o[2], o[3]};
-            *reinterpret_cast<u32x4*>(d + 16) = {o[4], o[5], o[6], o[7]};
-        }
-    }
-};
-
+// Tiles of 256 x 256 of each expert's matrix, all of an expert after the
+// other, contracted over the expert's rows; the workgroups of an XCD take a
+// contiguous run of them, in groups of up to 8 tiles along n.
 template <bool FP8, bool F32>
 __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
@@ -600,56 +699,80 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     check_rows(a.offsets, a.E, a.rows, a.err);
     const int tiles_k = (a.k_dim + kTileN - 1) / kTileN, tiles_n = (a.n_dim + kFullRows - 1) / kFullRows;
     const int total = a.E * tiles_k * tiles_n, per = (total + 7) / 8;
-    const int item = (blockIdx.x % 8) * per + blockIdx.x / 8;
-    if ((int)blockIdx.x / 8 >= per || item >= total) return;
-    const int e = item / (tiles_k * tiles_n), local = item % (tiles_k * tiles_n);
-    const int n0 = local % tiles_n * kFullRows, k0 = local / tiles_n * kTileN;
-    const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], lo), a.rows);
-    const int rows = __builtin_amdgcn_readfirstlane(hi - lo);
-    const int row0 = __builtin_amdgcn_readfirstlane(lo);
-
+    const int first = (blockIdx.x % 8) * per, mine = min(max(total - first, 0), per);
     const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
-    f32x4 acc[MS][NS] = {};
-    ColsLoader la;
-    la.init(a.dy + (int64_t)row0 * a.n_dim, a.n_dim, n0);
-    ColsReader<MS> ra;
-    ra.init(wm * MS);
-    ColsReader<NS> rb;
-    rb.init(wn * NS);
-    if constexpr (!FP8) {
-        ColsLoader lb;
-        lb.init(a.x + (int64_t)row0 * a.k_dim, a.k_dim, k0);
-        multiply<MS, NS>(la, lb, ra, rb, rows, lds, acc);
-    } else {
-        Fp8Loader lb;
-        lb.init(a.x8 + (int64_t)row0 * a.k_dim, a.x_scales + (int64_t)row0 * (a.k_dim / 128), a.k_dim, k0);
-        multiply<MS, NS>(la, lb, ra, rb, rows, lds, acc);
-    }
     const int i = lane_id() & 15, q = lane_id() >> 4;
+    ColsReader<MS, false> ra;
+    ra.init(wm * MS * 16);
+    ColsReader<NS, true> rb;
+    rb.init(wn * NS * 16);
+    ColsLoader la;
+    std::conditional_t<FP8, Fp8Loader, ColsLoader> lb;
+    struct Place {
+        int e, n0, k0, rows;
+    } t;
+    auto start = [&](int seq) {
+        if (seq >= mine) return false;
+        const int item = first + seq;
+        t.e = item / (tiles_k * tiles_n);
+        const int local = item % (tiles_k * tiles_n);
+        const int group = local / (8 * tiles_k), in = local % (8 * tiles_k), high = min(8, tiles_n - group * 8);
+        t.n0 = (group * 8 + in % high) * kFullRows;
+        t.k0 = in / high * kTileN;
+        const int lo = min(max(a.offsets[t.e], 0), a.rows), hi = min(max(a.offsets[t.e + 1], lo), a.rows);
+        t.rows = __builtin_amdgcn_readfirstlane(hi - lo);
+        const int64_t row0 = __builtin_amdgcn_readfirstlane(lo);
+        la.init(a.dy + row0 * a.n_dim, a.n_dim, t.n0);
+        if constexpr (FP8)
+            lb.init(a.x8 + row0 * a.k_dim, a.x_scales + row0 * (a.k_dim / 128), a.k_dim, t.k0);
+        else
+            lb.init(a.x + row0 * a.k_dim, a.k_dim, t.k0);
+        first_steps(la, lb, t.rows, lds);
+        return true;
+    };
+    int seq = blockIdx.x / 8;
+    bool more = start(seq);
+    while (more) {
+        const Place now = t;
+        f32x4 acc[MS][NS] = {};
+        multiply<MS, NS>(la, lb, ra, rb, now.rows, lds, acc);
+        more = start(seq += gridDim.x / 8);
+        const int k0 = now.k0 + wn * NS * 16 + q * 8;
 #pragma unroll
-    for (int mi = 0; mi < MS; ++mi) {
-        const int n = n0 + (wm * MS + mi) * 16 + i;
-        if (n >= a.n_dim) continue;
-        const int64_t row = ((int64_t)e * a.n_dim + n) * a.k_dim;
+        for (int mi = 0; mi < MS; ++mi) {
+            const int n = now.n0 + (wm * MS + mi) * 16 + i;
+            if (n >= a.n_dim) continue;
+            const int64_t row = ((int64_t)now.e * a.n_dim + n) * a.k_dim;
 #pragma unroll
-        for (int ni = 0; ni < NS; ++ni) {
-            const int k = k0 + (wn * NS + ni) * 16 + q * 4;
-            if (k >= a.k_dim) continue;
-            const f32x4 v = acc[mi][ni];
-            if constexpr (F32) {
-                *reinterpret_cast<f32x4*>(static_cast<float*>(a.dw) + row + k) = v;
-            } else {
-                const u32x2 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dw) + row + k) = o;
+            for (int p = 0; p < NS / 2; ++p) {
+                const int k = k0 + p * 32;
+                if (k >= a.k_dim) continue;
+                const f32x4 v = acc[mi][2 * p], w = acc[mi][2 * p + 1];
+                if constexpr (F32) {
+                    float* o = static_cast<float*>(a.dw) + row + k;
+                    *reinterpret_cast<f32x4*>(o) = v;
+                    *reinterpret_cast<f32x4*>(o + 4) = w;
+                } else {
+                    const u32x4 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]),
+                                     pack_bf16(w[2], w[3])};
+                    st16(static_cast<uint16_t*>(a.dw) + row + k, o);
+                }
             }
         }
     }
 }
 
+// One workgroup per CU at most (it takes all of the CU's LDS), in multiples of
+// the 8 XCDs.
 template <class Args>
-hipError_t launch_tiles(void (*kernel)(Args), int64_t grid, const Args& a, hipStream_t st) {
-    if (grid <= 0) return hipSuccess;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, a);
+hipError_t launch_tiles(void (*kernel)(Args), int64_t tiles, const Args& a, hipStream_t st) {
+    if (tiles <= 0) return hipSuccess;
+    LaunchInfo info;
+    hipError_t e = launch_info(st, reinterpret_cast<const void*>(kernel), kThreads, &info);
+    if (e != hipSuccess) return e;
+    const int64_t most = std::max(info.cus / 8 * 8, 8);
+    const unsigned grid = (unsigned)std::min(most, (tiles + 7) / 8 * 8);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -657,29 +780,28 @@ uint32_t* err_words(char* ws) { return reinterpret_cast<uint32_t*>(ws); }
 
 }  // namespace
 
-int64_t expert_matmul_grid(int64_t rows, int E, int n_dim) {
-    return tile_grid(rows, E, (n_dim + kTileN - 1) / kTileN);
+int64_t expert_matmul_tiles(int64_t rows, int E, int n_dim) {
+    return most_tiles(rows, E, (n_dim + kTileN - 1) / kTileN);
 }
-int64_t expert_swiglu_grid(int64_t rows, int E, int F) {
-    return tile_grid(rows, E, (F + kTileN / 2 - 1) / (kTileN / 2));
+int64_t expert_swiglu_tiles(int64_t rows, int E, int F) {
+    return most_tiles(rows, E, (F + 127) / 128);
 }
-int64_t expert_wgrad_grid(int E, int n_dim, int k_dim) {
-    const int64_t total = (int64_t)E * ((n_dim + kFullRows - 1) / kFullRows) * ((k_dim + kTileN - 1) / kTileN);
-    return (total + 7) / 8 * 8;
+int64_t expert_wgrad_tiles(int E, int n_dim, int k_dim) {
+    return (int64_t)E * ((n_dim + kFullRows - 1) / kFullRows) * ((k_dim + kTileN - 1) / kTileN);
 }
 
 hipError_t launch_expert_matmul(const ep_shape& s, const ep_layout& L, const uint16_t* x, int64_t rows, int k_dim,
                                 const uint16_t* w, int n_dim, int order, uint16_t* y, char* ws, hipStream_t st) {
     const MatmulArgs a = {L.expert_offsets, x, w, y, s.E, (int)rows, k_dim, n_dim, err_words(ws)};
     return launch_tiles(order == EP_WEIGHT_KN ? matmul_kernel<true> : matmul_kernel<false>,
-                        expert_matmul_grid(rows, s.E, n_dim), a, st);
+                        expert_matmul_tiles(rows, s.E, n_dim), a, st);
 }
 
 hipError_t launch_expert_swiglu(const ep_shape& s, const ep_layout& L, const uint16_t* x, int64_t rows,
                                 const uint16_t* w13, int F, uint16_t* act, uint8_t* gu, float* scales, char* ws,
                                 hipStream_t st) {
     const SwigluArgs a = {L.expert_offsets, x, w13, act, gu, scales, s.E, (int)rows, s.H, F, err_words(ws)};
-    return launch_tiles(gu ? swiglu_kernel<true> : swiglu_kernel<false>, expert_swiglu_grid(rows, s.E, F), a, st);
+    return launch_tiles(gu ? swiglu_kernel<true> : swiglu_kernel<false>, expert_swiglu_tiles(rows, s.E, F), a, st);
 }
 
 hipError_t launch_expert_wgrad(const ep_shape& s, const ep_layout& L, const uint16_t* dy, int64_t rows, int n_dim,
@@ -688,7 +810,7 @@ hipError_t launch_expert_wgrad(const ep_shape& s, const ep_layout& L, const uint
     const WgradArgs a = {L.expert_offsets, dy, x, x8, x_scales, dw, s.E, (int)rows, n_dim, k_dim, err_words(ws)};
     void (*const kernels[2][2])(WgradArgs) = {{wgrad_kernel<false, false>, wgrad_kernel<false, true>},
                                               {wgrad_kernel<true, false>, wgrad_kernel<true, true>}};
-    return launch_tiles(kernels[x8 != nullptr][dtype == EP_GRAD_F32], expert_wgrad_grid(s.E, n_dim, k_dim), a, st);
+    return launch_tiles(kernels[x8 != nullptr][dtype == EP_GRAD_F32], expert_wgrad_tiles(s.E, n_dim, k_dim), a, st);
 }
 
 }  // namespace ep
