@@ -25,8 +25,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 #define EP_LDS_PTR(T) __attribute__((address_space(3))) T*
 
-constexpr uint32_t kBufOutside = 0x7FFFFFF0u;  // an offset past every descriptor's end: reads give zero
-constexpr uint32_t kBufFar = 0x40000000u;      // added to an offset below 2^29: also past the end
+constexpr uint32_t kBufFar = 0x80000000u;  // added to an offset: past the end of every descriptor (all end below 2^31)
 
 // This wave's index, in a scalar register.
 __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_in_block()); }

@@ -45,125 +45,142 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 __device__ __forceinline__ int pairs_swizzle(int r) { return ((r >> 1) & 1) | ((r >> 3) & 3) << 1; }
 __device__ __forceinline__ int cols_swizzle(int k) { return (k & 3) | ((k >> 3) & 3) << 2; }
 
-// A tile operand whose contracted index is contiguous in memory: ROWS rows,
-// first (BY_PAIRS false) or second operand.
-template <int ROWS, bool BY_PAIRS>
-struct RowsLoader {
-    static constexpr int kLoads = ROWS / 64;
-    const char* p;
-    uint32_t bytes;
-    uint32_t off[kLoads];
-    int k;         // this lane's first contracted index within a step
-    u32x4 d;       // descriptor of the step under way
-    uint32_t far;  // added to the offsets: kBufFar where the step is past the end
+// The loaders keep their place in scalar registers; a lane's offsets depend on
+// the launch alone, so turning to another tile costs no vector register.
 
-    // row(r): byte offset of tile row r from p.
-    template <class RowOff>
-    __device__ __forceinline__ void init(const void* base, uint32_t n_bytes, RowOff row) {
-        p = static_cast<const char*>(base);
-        bytes = n_bytes;
+// A tile operand whose contracted index is contiguous in memory: 256 rows,
+// first (PAIRS false) or second operand.
+template <bool PAIRS>
+struct RowsLoader {
+    static constexpr int kLoads = 4;         // copies of a step, 64 rows each
+    static constexpr int kYounger = kLoads;  // loads of later steps at the wait for a step
+    static constexpr bool kStaged = false;   // copies go to LDS as they are
+    uint32_t off[kLoads];  // of this lane's 16 bytes in each copy
+    int k;                 // their first contracted index within a step
+    uint32_t lds_wave;     // LDS bytes before this wave's part of a copy
+    const char* p;
+    uint32_t bytes;  // of the tile's rows that exist; the rest read as zero
+    int k_dim;       // contracted indices; 0: every step is past the end
+    u32x4 d;         // the step under way
+    uint32_t far;
+
+    // row: memory row of LDS row r < 256 of the tile.
+    template <class Row>
+    __device__ __forceinline__ void init(uint32_t ld_bytes, Row row) {
         const int lane = lane_id(), r = wave_in_block() * 8 + (lane >> 3);
-        const int chunk = (lane & 7) ^ (BY_PAIRS ? pairs_swizzle(r) : (r >> 1) & 7);
+        const int chunk = (lane & 7) ^ (PAIRS ? pairs_swizzle(r) : (r >> 1) & 7);
         k = chunk * 8;
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const uint32_t o = row(j * 64 + r);
-            off[j] = o == kBufOutside ? o : o + chunk * 16;
-        }
+        for (int j = 0; j < kLoads; ++j) off[j] = row(j * 64 + r) * ld_bytes + chunk * 16;
+        lds_wave = uniform_wave() * 8 * 128;
     }
-    // Turns to the step whose first index is k0 of k_dim (zeros past k_dim).
-    __device__ __forceinline__ void begin(int k0, int k_dim) {
+    __device__ __forceinline__ void start(const void* base, uint32_t n_bytes, int contracted) {
+        p = static_cast<const char*>(base);
+        bytes = n_bytes;
+        k_dim = contracted;
+    }
+    // Turns to the step whose first index is k0 (zeros past k_dim).
+    __device__ __forceinline__ void begin(int k0) {
         d = buf_desc(p + (int64_t)k0 * 2, k0 < k_dim ? bytes - (uint32_t)k0 * 2 : 0u);
         far = k0 + k < k_dim ? 0u : kBufFar;
     }
     // Requests part j of kLoads of that step into LDS.
     __device__ __forceinline__ void copy(int j, uint32_t lds) {
-        copy16_to_lds(d, off[j] + far, lds + (j * 64 + uniform_wave() * 8) * 128);
+        copy16_to_lds(d, off[j] + far, lds + lds_wave + j * 8192);
     }
-    __device__ __forceinline__ void stage(char*) {}
+    __device__ __forceinline__ void stage(int, char*) {}
+    __device__ __forceinline__ void fetch(int) {}
 };
 
 // A tile operand whose 256 columns are contiguous in memory (one contracted
 // index per memory row of ld values).
 struct ColsLoader {
-    static constexpr int kLoads = 4;
-    const char* p;
-    int64_t ld_bytes;
-    uint32_t col_bytes;  // bytes of a row before the tile's first column
+    static constexpr int kLoads = 4;  // copies of a step, 16 contracted rows each
+    static constexpr int kYounger = kLoads;
+    static constexpr bool kStaged = false;
     uint32_t off[kLoads];
+    uint32_t lds_wave;
+    int64_t ld_bytes;
+    const char* p;
+    uint32_t col_bytes;  // bytes of a row before the tile's first column
+    int k_dim;
     u32x4 d;
 
-    __device__ __forceinline__ void init(const void* base, int64_t ld, int col0) {
-        p = static_cast<const char*>(base) + (int64_t)col0 * 2;
+    __device__ __forceinline__ void init(int64_t ld) {
         ld_bytes = ld * 2;
-        col_bytes = col0 * 2;
-        const int lane = lane_id(), wave = wave_in_block();
+        const int lane = lane_id();
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int r = j * 16 + wave * 2 + (lane >> 5);
+            const int r = j * 16 + wave_in_block() * 2 + (lane >> 5);
             const int block = ((lane & 31) >> 1) ^ cols_swizzle(r);
             off[j] = (uint32_t)(r * ld_bytes) + block * 32 + (lane & 1) * 16;
         }
+        lds_wave = uniform_wave() * 2 * 512;
     }
-    __device__ __forceinline__ void begin(int k0, int k_dim) {
+    __device__ __forceinline__ void start(const void* base, int contracted, int col0) {
+        p = static_cast<const char*>(base) + (int64_t)col0 * 2;
+        col_bytes = col0 * 2;
+        k_dim = contracted;
+    }
+    __device__ __forceinline__ void begin(int k0) {
         const int rows = min(k_dim - k0, kStep);
-        d = buf_desc(p + (int64_t)k0 * ld_bytes, rows > 0 ? (uint32_t)(rows * ld_bytes) - col_bytes : 0u);
+        d = buf_desc(p + (int64_t)k0 * ld_bytes, rows > 0 ? (uint32_t)(rows * (int)ld_bytes) - col_bytes : 0u);
     }
-    __device__ __forceinline__ void copy(int j, uint32_t lds) {
-        copy16_to_lds(d, off[j], lds + (j * 16 + uniform_wave() * 2) * 512);
-    }
-    __device__ __forceinline__ void stage(char*) {}
+    __device__ __forceinline__ void copy(int j, uint32_t lds) { copy16_to_lds(d, off[j], lds + lds_wave + j * 8192); }
+    __device__ __forceinline__ void stage(int, char*) {}
+    __device__ __forceinline__ void fetch(int) {}
 };
 
 // The FP8 rows of a step as second operand: each thread fetches 32 values (two
 // 16-byte vectors) of one memory row with their block's scale into registers,
-// and a step later writes them to LDS as bf16 in the columns layout. The value
-// is rounded to bf16 once (2^-8 of it, against e4m3's own 2^-4) because the
-// matrix instruction multiplies bf16.
+// and a step later writes them to LDS as bf16 in the columns layout, a quarter
+// at a time between the matrix instructions. The value is rounded to bf16
+// once (2^-8 of it, against e4m3's own 2^-4) because the matrix instruction
+// multiplies bf16.
 struct Fp8Loader {
-    static constexpr int kLoads = 0;  // copies to LDS
+    static constexpr int kLoads = 0;    // copies to LDS
+    static constexpr int kYounger = 3;  // the next step's fetch
+    static constexpr bool kStaged = true;
     const uint8_t* p;
     const float* s;
     int64_t ld;
-    int row, col;
-    bool in_cols;
+    int row0, k_dim, col0;
+    bool outside;
     u32x4 v[2];
     float scale;
 
-    __device__ __forceinline__ void init(const uint8_t* x8, const float* scales, int64_t k_dim, int col0) {
-        row = threadIdx.x >> 3;
-        col = (threadIdx.x & 7) * 32;
-        ld = k_dim;
-        in_cols = col0 + col < k_dim;
-        p = x8 + row * ld + col0 + col;
-        s = scales + row * (ld / 128) + (col0 + col) / 128;
+    __device__ __forceinline__ void init(const uint8_t* x8, const float* scales, int64_t ld_) {
+        p = x8, s = scales, ld = ld_;
     }
+    __device__ __forceinline__ void start(int first, int contracted, int col) { row0 = first, k_dim = contracted, col0 = col; }
     __device__ __forceinline__ void copy(int, uint32_t) {}
-    __device__ __forceinline__ void begin(int k0, int k_dim) {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-        v[0] = v[1] = zero;
-        scale = 0.f;
-        if (k0 + row < k_dim && in_cols) {
-            v[0] = ld16(p + k0 * ld);
-            v[1] = ld16(p + k0 * ld + 16);
-            scale = s[k0 * (ld / 128)];
-        }
+    __device__ __forceinline__ void begin(int) {}
+    // Always three loads (wait counts rely on it); outside the expert's rows and
+    // the columns they read the array's first values and count as zero.
+    __device__ __forceinline__ void fetch(int k0) {
+        const int row = k0 + (threadIdx.x >> 3), col = col0 + (threadIdx.x & 7) * 32;
+        const bool in = row < k_dim && col < ld;
+        const int64_t r = in ? row0 + row : 0;
+        const int c = in ? col : 0;
+        v[0] = ld16(p + r * ld + c);
+        v[1] = ld16(p + r * ld + c + 16);
+        scale = s[r * (ld / 128) + c / 128];
+        outside = !in;
     }
-    __device__ __forceinline__ void stage(char* lds) const {
+    __device__ __forceinline__ void stage(int part, char* lds) const {
+        const int row = threadIdx.x >> 3, block = (threadIdx.x & 7) * 2 + (part >> 1);
+        uint32_t o[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t o[8];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[h][w], false);
-                const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[h][w], true);
-                o[2 * w] = pack_bf16(lo[0] * scale, lo[1] * scale);
-                o[2 * w + 1] = pack_bf16(hi[0] * scale, hi[1] * scale);
-            }
-            char* d = lds + row * 512 + (((col / 16 + h) ^ cols_swizzle(row)) << 5);
-            *reinterpret_cast<u32x4*>(d) = {o[0], o[1], o[2], o[3]};
-            *reinterpret_cast<u32x4*>(d + 16) = {o[4], o[5], o[6], o[7]};
+        for (int w = 0; w < 2; ++w) {
+            const int q = outside ? 0 : (int)v[part >> 1][(part & 1) * 2 + w];
+            const float f = outside ? 0.f : scale;
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(q, false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(q, true);
+            o[2 * w] = pack_bf16(lo[0] * f, lo[1] * f);
+            o[2 * w + 1] = pack_bf16(hi[0] * f, hi[1] * f);
         }
+        char* d = lds + row * 512 + ((block ^ cols_swizzle(row)) << 5) + (part & 1) * 16;
+        *reinterpret_cast<u32x4*>(d) = {o[0], o[1], o[2], o[3]};
     }
 };
 
@@ -184,37 +201,37 @@ struct RowsReader {
         return *reinterpret_cast<const bf16x8*>(lds + base[half] + s * 2048);
     }
 };
+// STEP: LDS rows from one sub-tile of a pair to the other.
+template <int STEP>
 struct RowsPairReader {
     uint32_t base[2];
-    int step;  // LDS bytes from one sub-tile of a pair to the other
-    __device__ __forceinline__ void init(int first_col, int from_u_to_u = 4) {
+    __device__ __forceinline__ void init(int first_col) {
         const int i = lane_id() & 15, q = lane_id() >> 4;
         const int r = (i >> 2) * 8 + (i & 3);
         const uint32_t row = (first_col + r) * 128;
         base[0] = row + ((q ^ pairs_swizzle(r)) * 16);
         base[1] = row + (((q + 4) ^ pairs_swizzle(r)) * 16);
-        step = from_u_to_u * 128;
     }
     __device__ __forceinline__ bf16x8 read(const char* lds, int s, int half) const {
-        return *reinterpret_cast<const bf16x8*>(lds + base[half] + (s >> 1) * 4096 + (s & 1) * step);
+        return *reinterpret_cast<const bf16x8*>(lds + base[half] + (s >> 1) * 4096 + (s & 1) * STEP * 128);
     }
 };
 // The columns layout is read by the transposing instruction: each 16-lane
 // group reads 4 contracted rows of 4 pieces of 4 values and receives them
 // transposed: lane i gets the 4 rows' values of column i % 4 of piece i / 4.
-template <int SUBS, bool PAIRS>
+template <bool PAIRS>
 struct ColsReader {
-    uint32_t base[PAIRS ? SUBS / 2 : SUBS];
-    __device__ __forceinline__ void init(int first_col) {
+    uint32_t base;
+    __device__ __forceinline__ void init(int first_col) {  // a multiple of 128, with PAIRS of 32
         const int i = lane_id() & 15, q = lane_id() >> 4, piece = i & 3;
         const int k = q * 8 + (i >> 2), b0 = first_col / 16;
-#pragma unroll
-        for (int s = 0; s < (PAIRS ? SUBS / 2 : SUBS); ++s)
-            base[s] = PAIRS ? k * 512 + (((b0 + 2 * s + (piece >> 1)) ^ cols_swizzle(k)) << 5) + (piece & 1) * 16
-                            : k * 512 + (((b0 + s) ^ cols_swizzle(k)) << 5) + piece * 8;
+        base = PAIRS ? k * 512 + (((b0 + (piece >> 1)) ^ cols_swizzle(k)) << 5) + (piece & 1) * 16
+                     : k * 512 + ((b0 ^ cols_swizzle(k)) << 5) + piece * 8;
     }
+    // Sub-tiles (PAIRS: pairs of them) differ in address bits that are clear in
+    // b0, so that the swizzled address is reached by an exclusive or.
     __device__ __forceinline__ bf16x8 read(const char* lds, int s, int half) const {
-        const char* p = lds + (PAIRS ? base[s >> 1] + (s & 1) * 8 : base[s]) + half * 16384;
+        const char* p = lds + ((PAIRS ? base ^ ((s >> 1) << 6) : base ^ (s << 5)) + (PAIRS ? (s & 1) * 8 : 0) + half * 16384);
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS_PTR(s16x4))p);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EP_LDS_PTR(s16x4))(p + 2048));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -239,11 +256,11 @@ __device__ __forceinline__ void keep(const Fragments<MS, NS>& f) {
 }
 
 // One half step: multiplies the fragments `cur` while the fragments `next` are
-// read from (la_lds, lb_lds, half), in MS groups of NS matrix instructions, each
-// behind its share of the reads (all within the first GROUPS groups) and one
-// of the copies: copies issued in one go would stand in the waves' way until
-// the memory pipeline has taken them all (16 clocks each).
-template <int MS, int NS, int GROUPS, class RA, class RB, class Copies>
+// read from (a_lds, b_lds, half), in MS groups of NS matrix instructions, each
+// behind its share of the reads and of the copies: copies issued in one go
+// would stand in the waves' way until the memory pipeline has taken them all
+// (16 clocks each).
+template <int MS, int NS, class RA, class RB, class Copies>
 __device__ __forceinline__ void half_step(const RA& ra, const RB& rb, const char* a_lds, const char* b_lds, int half,
                                           const Fragments<MS, NS>& cur, Fragments<MS, NS>& next,
                                           f32x4 (&acc)[MS][NS], Copies copies) {
@@ -251,7 +268,7 @@ __device__ __forceinline__ void half_step(const RA& ra, const RB& rb, const char
 #pragma unroll
     for (int g = 0; g < MS; ++g) {
 #pragma unroll
-        for (int r = g * R / GROUPS; r < (g + 1) * R / GROUPS && r < R; ++r) {
+        for (int r = g * R / MS; r < (g + 1) * R / MS; ++r) {
             if (r < NS)
                 next.b[r] = rb.read(b_lds, r, half);
             else
@@ -264,35 +281,47 @@ __device__ __forceinline__ void half_step(const RA& ra, const RB& rb, const char
     }
 }
 
-// One workgroup's product: acc[mi][ni] += rows sub-tile mi times columns
-// sub-tile ni over k_dim contracted indices. Each half of a step is multiplied
-// from registers while the fragments of the next half are read from LDS, with
-// one barrier per step. All of the LDS holds steps: two of the first operand,
-// three of the second. In the first half of step s the copies of the second
-// operand's step s + 2 are issued (into the slot of step s - 1), in the second
-// half those of the first operand's (into the slot of step s, whose last
-// fragments have then been read), one for each four
-// matrix instructions from the start, so copies are spread over the step and
-// still have nearly one step (a step is 1.1 us) and one and a half to arrive.
+// The slots of the steps s and s + 1 and (second operand) the free one.
+struct Ring {
+    int a_now, a_next, b_now, b_next, b_free;
+};
+__device__ __forceinline__ Ring first_ring() { return {0, kPart, kRingB, kRingB + kPart, kRingB + 2 * kPart}; }
+
+// Requests the first two steps of a tile (three of FP8 rows, which it converts).
 template <class LA, class LB>
-__device__ __forceinline__ void first_steps(LA& la, LB& lb, int k_dim, char* lds) {
+__device__ __forceinline__ void first_steps(LA& la, LB& lb, char* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
-    LB lb1 = lb;
-    lb.begin(0, k_dim);
-    lb1.begin(kStep, k_dim);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        la.begin(s * kStep, k_dim);
+        la.begin(s * kStep);
+        lb.begin(s * kStep);
+        lb.fetch(s * kStep);
 #pragma unroll
         for (int c = 0; c < LA::kLoads; ++c) la.copy(c, at + s * kPart);
 #pragma unroll
-        for (int c = 0; c < LB::kLoads; ++c) (s ? lb1 : lb).copy(c, at + kRingB + s * kPart);
+        for (int c = 0; c < LB::kLoads; ++c) lb.copy(c, at + kRingB + s * kPart);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) lb.stage(c, lds + kRingB + s * kPart);
     }
-    lb.stage(lds + kRingB);
-    lb1.stage(lds + kRingB + kPart);
+    lb.fetch(2 * kStep);
 }
-// After first_steps (which may be long before: the copies of a tile's first
-// steps run beside the results of the tile before it).
+
+// One tile's product: acc[mi][ni] += rows sub-tile mi times columns sub-tile
+// ni. Each half of a step is multiplied from registers while the fragments of
+// the next half are read from LDS, with one barrier per step. All of the LDS
+// holds steps: two of the first operand, three of the second. In the first half
+// of step s the copies of the second operand's step s + 2 are issued (into the
+// slot of step s - 1), in the second half those of the first operand's (into
+// the slot of step s, whose last fragments have then been read): one for each
+// four matrix instructions from the half's start, so that they have nearly one
+// and nearly one and a half step's time (a step is 1.1 us) to arrive.
+//
+// Two forms, by what measured better. `multiply`, a tile of its own: from
+// first_steps, which the caller issues beside the results of the tile before,
+// two steps to a turn of the loop, so that the slots are constants.
+// `multiply_stream`: steps past the tile's last are the next tile's first, to which
+// `next` turns the loaders, so that the copies have no gap between short
+// tiles; the slots go round in registers.
 template <int MS, int NS, class LA, class LB, class RA, class RB>
 __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB& rb, int k_dim, char* lds,
                                          f32x4 (&acc)[MS][NS]) {
@@ -301,36 +330,88 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB&
     wait_copies<0>();
     barrier_only();
     Fragments<MS, NS> f[2];
+    Ring r = first_ring();
 #pragma unroll
-    for (int i = 0; i < NS; ++i) f[0].b[i] = rb.read(lds + kRingB, i, 0);
+    for (int i = 0; i < NS; ++i) f[0].b[i] = rb.read(lds + r.b_now, i, 0);
 #pragma unroll
     for (int i = 0; i < MS; ++i) f[0].a[i] = ra.read(lds, i, 0);
-    int b_now = kRingB, b_next = kRingB + kPart, b_free = kRingB + 2 * kPart;
     for (int s = 0; s < steps; s += 2) {
 #pragma unroll
         for (int slot = 0; slot < 2; ++slot) {
             if (slot && s + 1 >= steps) break;
-            lb.begin((s + slot + 2) * kStep, k_dim);
-            half_step<MS, NS, MS>(ra, rb, lds + slot * kPart, lds + b_now, 1, f[0], f[1], acc, [&](int g) {
-#pragma unroll
-                for (int c = g; c < LB::kLoads && c == g; ++c) lb.copy(c, at + b_free);
+            lb.begin((s + slot + 2) * kStep);
+            half_step<MS, NS>(ra, rb, lds + slot * kPart, lds + r.b_now, 1, f[0], f[1], acc, [&](int g) {
+                if (g < LB::kLoads) lb.copy(g, at + r.b_free);
             });
-            wait_copies<LB::kLoads>();
+            wait_copies<LB::kYounger>();
             barrier_only();
-            la.begin((s + slot + 2) * kStep, k_dim);
-            half_step<MS, NS, MS>(ra, rb, lds + (slot ^ 1) * kPart, lds + b_next, 0, f[1], f[0], acc, [&](int g) {
-#pragma unroll
-                for (int c = g; c < LA::kLoads && c == g; ++c) la.copy(c, at + slot * kPart);
+            la.begin((s + slot + 2) * kStep);
+            half_step<MS, NS>(ra, rb, lds + (slot ^ 1) * kPart, lds + r.b_next, 0, f[1], f[0], acc, [&](int g) {
+                if (g < LA::kLoads) la.copy(g, at + slot * kPart);
             });
-            lb.stage(lds + b_free);
-            const int b = b_now;
-            b_now = b_next, b_next = b_free, b_free = b;
+            r = {r.a_next, r.a_now, r.b_next, r.b_free, r.b_now};
         }
     }
     keep(f[0]);
     wait_copies<0>();  // none may land after the slots have been handed on
     settle(acc);
     barrier_only();
+}
+
+// Steps of a streamed tile: as many at least as are requested ahead (three of
+// FP8 rows), so that these never reach past the next tile.
+template <class LB>
+__device__ __forceinline__ int stream_steps(int k_dim) {
+    return max(LB::kStaged ? 3 : 2, (k_dim + kStep - 1) / kStep);
+}
+
+// The streamed form. STORES: at least so many stores of the tile before were
+// issued behind its last copies (if `behind`); they need not have finished in
+// the first step.
+template <int MS, int NS, int STORES, class LA, class LB, class RA, class RB, class Next>
+__device__ __forceinline__ void multiply_stream(LA& la, LB& lb, const RA& ra, const RB& rb, int steps, char* lds,
+                                                Ring& r, bool behind, f32x4 (&acc)[MS][NS], Next next) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
+    Fragments<MS, NS> f[2];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) f[0].b[i] = rb.read(lds + r.b_now, i, 0);
+#pragma unroll
+    for (int i = 0; i < MS; ++i) f[0].a[i] = ra.read(lds + r.a_now, i, 0);
+    auto ahead = [&](int s) { return (s < steps ? s : s - steps) * kStep; };
+    if (!LB::kStaged) {
+        if (steps == 2) next.b();
+        lb.begin(ahead(2));
+    }
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+        half_step<MS, NS>(ra, rb, lds + r.a_now, lds + r.b_now, 1, f[0], f[1], acc, [&](int g) {
+            if (g < LB::kLoads) lb.copy(g, at + r.b_free);
+            if (g == MS - 1) {
+                if (s + 2 == steps) next.a();
+                la.begin(ahead(s + 2));
+            }
+        });
+        if (behind)
+            wait_copies<LB::kYounger + STORES>();
+        else
+            wait_copies<LB::kYounger>();
+        behind = false;
+        barrier_only();
+        half_step<MS, NS>(ra, rb, lds + r.a_next, lds + r.b_next, 0, f[1], f[0], acc, [&](int g) {
+            if (LB::kStaged && g < 4) lb.stage(g, lds + r.b_free);
+            if (g < LA::kLoads) la.copy(g, at + r.a_now);
+            if (g == (LB::kStaged ? 4 : MS - 1)) {
+                if (s + 3 == steps) next.b();
+                if (LB::kStaged)
+                    lb.fetch(ahead(s + 3));
+                else
+                    lb.begin(ahead(s + 3));
+            }
+        });
+        r = {r.a_next, r.a_now, r.b_next, r.b_free, r.b_now};
+    }
+    keep(f[0]);
+    settle(acc);
 }
 
 // ---- Tiles of ragged experts ------------------------------------------------
@@ -352,22 +433,19 @@ struct Tile {
 struct Tiles {
     const int32_t* offsets;
     int rows, n_tiles;
-    int e0, e1;            // this thread's experts
-    int pf, pt;            // full and tail row tiles of the experts before e0
+    int per;     // experts of a lane (each wave covers all and searches for itself)
+    int E;
+    int pf, pt;  // full and tail row tiles of the experts before this lane's
     int total_f, total_t;
-    Tile* found;
 
     __device__ __forceinline__ void bounds(int e, int& lo, int& hi) const {
         lo = min(max(offsets[e], 0), rows);
         hi = min(max(offsets[e + 1], lo), rows);
     }
-    __device__ __forceinline__ void init(const int32_t* offs, int E, int n_rows, int n, char* lds) {
-        offsets = offs, rows = n_rows, n_tiles = n;
-        found = reinterpret_cast<Tile*>(lds + kLdsBytes - 64);  // in the slot that first_steps leaves free
-        int* wave_sum = reinterpret_cast<int*>(lds);
-        const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
-        const int per = (E + kThreads - 1) / kThreads;
-        e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    __device__ __forceinline__ void init(const int32_t* offs, int experts, int n_rows, int n) {
+        offsets = offs, rows = n_rows, n_tiles = n, E = experts;
+        per = (E + kWave - 1) / kWave;
+        const int lane = lane_id(), e0 = min(E, lane * per), e1 = min(E, e0 + per);
         int full = 0, tail = 0;
         for (int e = e0; e < e1; ++e) {
             int lo, hi;
@@ -380,17 +458,9 @@ struct Tiles {
             const int a = __shfl_up(sf, d), b = __shfl_up(st, d);
             if (lane >= d) sf += a, st += b;
         }
-        if (lane == kWave - 1) wave_sum[wave * 2] = sf, wave_sum[wave * 2 + 1] = st;
-        __syncthreads();
-        total_f = total_t = 0;
         pf = sf - full, pt = st - tail;
-        for (int w = 0; w < kThreads / kWave; ++w) {
-            if (w < wave) pf += wave_sum[w * 2], pt += wave_sum[w * 2 + 1];
-            total_f += wave_sum[w * 2], total_t += wave_sum[w * 2 + 1];
-        }
-        total_f = __builtin_amdgcn_readfirstlane(total_f);
-        total_t = __builtin_amdgcn_readfirstlane(total_t);
-        __syncthreads();
+        total_f = readlane(sf, kWave - 1);
+        total_t = readlane(st, kWave - 1);
     }
     // The seq-th tile of this workgroup's XCD; false if there is none.
     __device__ __forceinline__ bool find(int seq, Tile& t) const {
@@ -402,24 +472,29 @@ struct Tiles {
         if (is_tail && seq - mine_f >= mine_t) return false;
         const int item = is_tail ? xcd * per_t + seq - mine_f : xcd * per_f + seq;
         const int target = item / n_tiles;  // lies in its expert's range of row tiles
-        int f = pf, l = pt;
+        const int e0 = min(E, lane_id() * per), e1 = min(E, e0 + per);
+        int f = pf, l = pt, at = -1, lo0 = 0, m0 = 0, before = 0;
         for (int e = e0; e < e1; ++e) {
             int lo, hi;
             bounds(e, lo, hi);
             const int m = hi - lo, nf = m / kFullRows, nt = m % kFullRows != 0;
-            if (!is_tail && target >= f && target < f + nf) {
-                const int local = item - f * n_tiles;
-                const int group = local / (8 * n_tiles), in = local % (8 * n_tiles), high = min(8, nf - group * 8);
-                *found = {e, lo + (group * 8 + in % high) * kFullRows, kFullRows, in / high};
-            }
-            if (is_tail && nt && target == l) *found = {e, hi - m % kFullRows, m % kFullRows, item - l * n_tiles};
+            if (is_tail ? nt && target == l : target >= f && target < f + nf) at = e, lo0 = lo, m0 = m, before = f;
             f += nf, l += nt;
         }
-        __syncthreads();
-        t.expert = __builtin_amdgcn_readfirstlane(found->expert);
-        t.row0 = __builtin_amdgcn_readfirstlane(found->row0);
-        t.rows = __builtin_amdgcn_readfirstlane(found->rows);
-        t.n = __builtin_amdgcn_readfirstlane(found->n);
+        const int src = __ffsll((unsigned long long)__ballot(at >= 0)) - 1;
+        t.expert = readlane(at, src);
+        const int first = readlane(lo0, src), m = readlane(m0, src);
+        if (is_tail) {
+            t.rows = m % kFullRows;
+            t.row0 = first + m - t.rows;
+            t.n = item % n_tiles;
+        } else {
+            const int local = item - readlane(before, src) * n_tiles, group = local / (8 * n_tiles);
+            const int in = local % (8 * n_tiles), high = min(8, m / kFullRows - group * 8);
+            t.rows = kFullRows;
+            t.row0 = first + (group * 8 + in % high) * kFullRows;
+            t.n = in / high;
+        }
         return true;
     }
 };
@@ -442,83 +517,108 @@ __device__ __forceinline__ void check_rows(const int32_t* offsets, int E, int ro
     if (blockIdx.x == 0 && threadIdx.x == 0 && offsets[E] > rows) report(err, EP_DEVERR_CAPACITY);
 }
 
+// The products' loaders, turned to a tile one operand after the other.
 template <bool KN>
-struct MatmulLoaders;
-template <>
-struct MatmulLoaders<false> {
-    RowsLoader<kFullRows, false> a;
-    RowsLoader<kTileN, true> b;
-    __device__ __forceinline__ void init_b(const MatmulArgs& m, const uint16_t* w, int n0) {
-        const uint32_t ld = (uint32_t)m.k_dim * 2;
-        const int cols = min(m.n_dim - n0, kTileN);
-        b.init(w + (int64_t)n0 * m.k_dim, (uint32_t)cols * ld, [&](int r) { return r < cols ? r * ld : kBufOutside; });
+struct MatmulLoaders {
+    const MatmulArgs& m;
+    RowsLoader<false> a;
+    std::conditional_t<KN, ColsLoader, RowsLoader<true>> b;
+
+    __device__ __forceinline__ void init() {
+        a.init((uint32_t)m.k_dim * 2, [](int r) { return r; });
+        if constexpr (KN)
+            b.init(m.n_dim);
+        else
+            b.init((uint32_t)m.k_dim * 2, [](int r) { return r; });
+    }
+    __device__ __forceinline__ void start_a(const Tile& t) {
+        a.start(m.x + (int64_t)t.row0 * m.k_dim, (uint32_t)t.rows * m.k_dim * 2, m.k_dim);
+    }
+    __device__ __forceinline__ void start_b(const Tile& t) {
+        const uint16_t* w = m.w + (int64_t)t.expert * m.n_dim * m.k_dim;
+        const int n0 = t.n * kTileN;
+        if constexpr (KN)
+            b.start(w, m.k_dim, n0);
+        else
+            b.start(w + (int64_t)n0 * m.k_dim, (uint32_t)min(m.n_dim - n0, kTileN) * m.k_dim * 2, m.k_dim);
     }
 };
-template <>
-struct MatmulLoaders<true> {
-    RowsLoader<kFullRows, false> a;
-    ColsLoader b;
-    __device__ __forceinline__ void init_b(const MatmulArgs& m, const uint16_t* w, int n0) { b.init(w, m.n_dim, n0); }
-};
-
-// Waves: WM over rows, 8 / WM over columns; a wave's block is MS x NS sub-tiles
-// of 16 x 16. `after_product` runs between the product and its results.
-template <int WM, int MS, bool KN, class After>
-__device__ __forceinline__ void matmul_tile(const MatmulArgs& a, const Tile& t, MatmulLoaders<KN>& l, char* lds,
-                                            After after_product) {
-    constexpr int WN = 8 / WM, NS = 16 / WN;
-    const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
-    const int N = a.n_dim;
-    RowsReader ra;
-    ra.init(wm * MS * 16);
-    std::conditional_t<KN, ColsReader<NS, true>, RowsPairReader> rb;
-    rb.init(wn * NS * 16);
-    f32x4 acc[MS][NS] = {};
-    multiply<MS, NS>(l.a, l.b, ra, rb, a.k_dim, lds, acc);
-    after_product();
+// A wave's block of results, MS x NS sub-tiles at (row0, col0) of a row-major
+// matrix of `cols` columns, as bf16 or 32-bit: 8 consecutive columns a lane and
+// pair of sub-tiles. The addresses are a scalar base and one offset per lane.
+// rows_left, cols_left: of the matrix from (row0, col0) on.
+template <bool F32, int MS, int NS>
+__device__ __forceinline__ void store_block(void* out, int64_t row0, int col0, int cols, int rows_left, int cols_left,
+                                            const f32x4 (&acc)[MS][NS]) {
+    constexpr int kSize = F32 ? 4 : 2;
     const int i = lane_id() & 15, q = lane_id() >> 4;
-    const int n0 = t.n * kTileN + wn * NS * 16 + q * 8;
-    uint16_t* base = a.y + (int64_t)t.row0 * N;
+    char* base = static_cast<char*>(out) + (row0 * cols + col0) * kSize;
+    const uint32_t lane_off = (uint32_t)(i * cols + q * 8) * kSize;
+    const bool inside = rows_left >= MS * 16 && cols_left >= NS * 16;  // no edge in the block
 #pragma unroll
     for (int mi = 0; mi < MS; ++mi) {
-        const int m = (wm * MS + mi) * 16 + i;
-        if (m >= t.rows) continue;
+        char* row = base + (int64_t)mi * 16 * cols * kSize;
 #pragma unroll
         for (int p = 0; p < NS / 2; ++p) {
             const f32x4 v = acc[mi][2 * p], w = acc[mi][2 * p + 1];
-            const u32x4 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]),
-                             pack_bf16(w[2], w[3])};
-            if (n0 + p * 32 < N) st16(base + (int64_t)m * N + n0 + p * 32, o);
+            if (!inside && (mi * 16 + i >= rows_left || p * 32 + q * 8 >= cols_left)) continue;
+            char* o = row + p * 32 * kSize + lane_off;
+            if constexpr (F32) {
+                *reinterpret_cast<f32x4*>(o) = v;
+                *reinterpret_cast<f32x4*>(o + 16) = w;
+            } else {
+                const u32x4 b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]),
+                                 pack_bf16(w[2], w[3])};
+                st16(o, b);
+            }
         }
     }
 }
 
-// One workgroup per CU takes tiles until there are none. The first two steps
-// of the next tile are requested before the results of this one are stored, so
-// that a tile's start and end run beside each other.
+// Waves: WM over rows, 8 / WM over columns; a wave's block is MS x NS sub-tiles
+// of 16 x 16.
+template <int WM, int MS, bool KN, class Next>
+__device__ __forceinline__ void matmul_tile(const MatmulArgs& a, const Tile& t, MatmulLoaders<KN>& l, char* lds,
+                                            Next next) {
+    constexpr int WN = 8 / WM, NS = 16 / WN;
+    const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
+    RowsReader ra;
+    ra.init(wm * MS * 16);
+    std::conditional_t<KN, ColsReader<true>, RowsPairReader<4>> rb;
+    rb.init(wn * NS * 16);
+    f32x4 acc[MS][NS] = {};
+    multiply<MS, NS>(l.a, l.b, ra, rb, a.k_dim, lds, acc);
+    next();
+    const int m = wm * MS * 16, n = t.n * kTileN + wn * NS * 16;
+    store_block<false>(a.y, t.row0 + m, n, a.n_dim, t.rows - m, a.n_dim - n, acc);
+}
+
+// One workgroup per CU takes tiles until there are none. The first steps of the
+// next tile are requested before the results of this one are stored.
 template <bool KN>
 __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(MatmulArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
     check_rows(a.offsets, a.E, a.rows, a.err);
     Tiles tiles;
-    tiles.init(a.offsets, a.E, a.rows, (a.n_dim + kTileN - 1) / kTileN, lds);
-    MatmulLoaders<KN> l;
+    tiles.init(a.offsets, a.E, a.rows, (a.n_dim + kTileN - 1) / kTileN);
+    MatmulLoaders<KN> l = {a};
+    l.init();
     Tile t;
-    auto start = [&](int seq) {
+    int seq = blockIdx.x / 8;
+    auto start = [&] {
         if (!tiles.find(seq, t)) return false;
-        const uint32_t ld = (uint32_t)a.k_dim * 2;
-        const int rows = t.rows;
-        l.a.init(a.x + (int64_t)t.row0 * a.k_dim, (uint32_t)rows * ld,
-                 [&](int r) { return r < rows ? r * ld : kBufOutside; });
-        l.init_b(a, a.w + (int64_t)t.expert * a.n_dim * a.k_dim, t.n * kTileN);
-        first_steps(l.a, l.b, a.k_dim, lds);
+        l.start_a(t);
+        l.start_b(t);
+        first_steps(l.a, l.b, lds);
         return true;
     };
-    int seq = blockIdx.x / 8;
-    bool more = start(seq);
+    bool more = start();
     while (more) {
         const Tile now = t;
-        auto next = [&] { more = start(seq += gridDim.x / 8); };
+        auto next = [&] {
+            seq += gridDim.x / 8;
+            more = start();
+        };
         if (now.rows > 128)
             matmul_tile<2, 8, KN>(a, now, l, lds, next);
         else if (now.rows > 64)
@@ -551,35 +651,50 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 __device__ __forceinline__ float block_scale(float amax) { return amax < 1e-33f ? 1.0f : amax / 448.0f; }
 
 struct SwigluLoaders {
-    RowsLoader<kFullRows, false> a;
-    RowsLoader<kTileN, true> b;
+    const SwigluArgs& m;
+    RowsLoader<false> a;
+    RowsLoader<true> b;
+
+    __device__ __forceinline__ void init() {
+        const uint32_t ld = (uint32_t)m.H * 2;
+        const int F = m.F;
+        a.init(ld, [](int r) { return r; });
+        b.init(ld, [=](int r) { return r / 64 * 32 + r % 32 + (r % 64 < 32 ? 0 : F); });
+    }
+    __device__ __forceinline__ void start_a(const Tile& t) {
+        a.start(m.x + (int64_t)t.row0 * m.H, (uint32_t)t.rows * m.H * 2, m.H);
+    }
+    // Gate rows past F are read as up rows; their results are not stored.
+    __device__ __forceinline__ void start_b(const Tile& t) {
+        const int f0 = t.n * 128;
+        b.start(m.w13 + ((int64_t)t.expert * 2 * m.F + f0) * m.H, (uint32_t)(2 * m.F - f0) * m.H * 2, m.H);
+    }
 };
 
 // A column tile is 128 values of f: of each 64 LDS rows of the second operand
 // the first 32 are gate rows, the last 32 the up rows of the same f, so that
 // one lane holds both. V: consecutive values of f that a lane holds.
-template <int WM, int MS, bool SAVE, class After>
-__device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, SwigluLoaders& l, char* lds,
-                                            After after_product) {
+template <int WM, int MS, bool SAVE, class Next>
+__device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, SwigluLoaders& l, char* lds, Next next) {
     constexpr int WN = 8 / WM, NS = 16 / WN, HS = NS / 2, ROWS = WM * MS * 16, V = 4 * HS;
     const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
     const int i = lane_id() & 15, q = lane_id() >> 4;
     RowsReader ra;
-    RowsPairReader rb;
+    RowsPairReader<NS == 4 ? 4 : 32> rb;
     ra.init(wm * MS * 16);
     int f;
     if constexpr (NS == 4) {
         rb.init(wn * 64);
         f = t.n * 128 + wn * 32 + q * 8;
     } else {  // two waves share 64 LDS rows: u tells them apart, sub-tile 0 is gate, 1 up
-        rb.init((wn >> 1) * 64 + (wn & 1) * 4, 32);
+        rb.init((wn >> 1) * 64 + (wn & 1) * 4);
         f = t.n * 128 + (wn >> 1) * 32 + q * 8 + (wn & 1) * 4;
     }
     f32x4 acc[MS][NS] = {};
     multiply<MS, NS>(l.a, l.b, ra, rb, a.H, lds, acc);
-    after_product();
+    next();
 
-    float* amax = reinterpret_cast<float*>(lds + kRingB + 2 * kPart);  // [WN][ROWS][2], in the free slot
+    float* amax = reinterpret_cast<float*>(lds + first_ring().b_free);  // [WN][ROWS][2]
     if constexpr (SAVE) {
 #pragma unroll
         for (int mi = 0; mi < MS; ++mi) {
@@ -646,27 +761,25 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_kernel(SwigluArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
     check_rows(a.offsets, a.E, a.rows, a.err);
     Tiles tiles;
-    tiles.init(a.offsets, a.E, a.rows, (a.F + 127) / 128, lds);
-    SwigluLoaders l;
+    tiles.init(a.offsets, a.E, a.rows, (a.F + 127) / 128);
+    SwigluLoaders l = {a};
+    l.init();
     Tile t;
-    auto start = [&](int seq) {
+    int seq = blockIdx.x / 8;
+    auto start = [&] {
         if (!tiles.find(seq, t)) return false;
-        const uint32_t ld = (uint32_t)a.H * 2;
-        const int rows = t.rows, f0 = t.n * 128;
-        l.a.init(a.x + (int64_t)t.row0 * a.H, (uint32_t)rows * ld,
-                 [&](int r) { return r < rows ? r * ld : kBufOutside; });
-        l.b.init(a.w13 + (int64_t)t.expert * 2 * a.F * a.H, (uint32_t)(2 * a.F) * ld, [&](int r) {
-            const int f = f0 + r / 64 * 32 + r % 32;
-            return f < a.F ? (uint32_t)(f + (r % 64 < 32 ? 0 : a.F)) * ld : kBufOutside;
-        });
-        first_steps(l.a, l.b, a.H, lds);
+        l.start_a(t);
+        l.start_b(t);
+        first_steps(l.a, l.b, lds);
         return true;
     };
-    int seq = blockIdx.x / 8;
-    bool more = start(seq);
+    bool more = start();
     while (more) {
         const Tile now = t;
-        auto next = [&] { more = start(seq += gridDim.x / 8); };
+        auto next = [&] {
+            seq += gridDim.x / 8;
+            more = start();
+        };
         if (now.rows > 128)
             swiglu_tile<2, 8, SAVE>(a, now, l, lds, next);
         else if (now.rows > 64)
@@ -689,6 +802,53 @@ struct WgradArgs {
     uint32_t* err;
 };
 
+// Turns the loaders to the tile after (no more steps if there is none).
+template <class Loaders, class T>
+struct NextTile {
+    Loaders& l;
+    const T& t;
+    bool more;
+    __device__ __forceinline__ void a() {
+        if (more)
+            l.start_a(t);
+        else
+            l.a.k_dim = 0;
+    }
+    __device__ __forceinline__ void b() {
+        if (more)
+            l.start_b(t);
+        else
+            l.b.k_dim = 0;
+    }
+};
+
+struct Place {
+    int e, n0, k0, row0, rows;
+};
+template <bool FP8>
+struct WgradLoaders {
+    const WgradArgs& m;
+    ColsLoader a;
+    std::conditional_t<FP8, Fp8Loader, ColsLoader> b;
+
+    __device__ __forceinline__ void init() {
+        a.init(m.n_dim);
+        if constexpr (FP8)
+            b.init(m.x8, m.x_scales, m.k_dim);
+        else
+            b.init(m.k_dim);
+    }
+    __device__ __forceinline__ void start_a(const Place& t) {
+        a.start(m.dy + (int64_t)t.row0 * m.n_dim, t.rows, t.n0);
+    }
+    __device__ __forceinline__ void start_b(const Place& t) {
+        if constexpr (FP8)
+            b.start(t.row0, t.rows, t.k0);
+        else
+            b.start(m.x + (int64_t)t.row0 * m.k_dim, t.rows, t.k0);
+    }
+};
+
 // Tiles of 256 x 256 of each expert's matrix, all of an expert after the
 // other, contracted over the expert's rows; the workgroups of an XCD take a
 // contiguous run of them, in groups of up to 8 tiles along n.
@@ -701,17 +861,12 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     const int total = a.E * tiles_k * tiles_n, per = (total + 7) / 8;
     const int first = (blockIdx.x % 8) * per, mine = min(max(total - first, 0), per);
     const int wave = uniform_wave(), wm = wave / WN, wn = wave % WN;
-    const int i = lane_id() & 15, q = lane_id() >> 4;
-    ColsReader<MS, false> ra;
+    ColsReader<false> ra;
     ra.init(wm * MS * 16);
-    ColsReader<NS, true> rb;
+    ColsReader<true> rb;
     rb.init(wn * NS * 16);
-    ColsLoader la;
-    std::conditional_t<FP8, Fp8Loader, ColsLoader> lb;
-    struct Place {
-        int e, n0, k0, rows;
-    } t;
-    auto start = [&](int seq) {
+    WgradLoaders<FP8> l = {a};
+    auto place = [&](int seq, Place& t) {
         if (seq >= mine) return false;
         const int item = first + seq;
         t.e = item / (tiles_k * tiles_n);
@@ -720,46 +875,34 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
         t.n0 = (group * 8 + in % high) * kFullRows;
         t.k0 = in / high * kTileN;
         const int lo = min(max(a.offsets[t.e], 0), a.rows), hi = min(max(a.offsets[t.e + 1], lo), a.rows);
+        t.row0 = __builtin_amdgcn_readfirstlane(lo);
         t.rows = __builtin_amdgcn_readfirstlane(hi - lo);
-        const int64_t row0 = __builtin_amdgcn_readfirstlane(lo);
-        la.init(a.dy + row0 * a.n_dim, a.n_dim, t.n0);
-        if constexpr (FP8)
-            lb.init(a.x8 + row0 * a.k_dim, a.x_scales + row0 * (a.k_dim / 128), a.k_dim, t.k0);
-        else
-            lb.init(a.x + row0 * a.k_dim, a.k_dim, t.k0);
-        first_steps(la, lb, t.rows, lds);
         return true;
     };
     int seq = blockIdx.x / 8;
-    bool more = start(seq);
-    while (more) {
-        const Place now = t;
+    Place now, after;
+    if (!place(seq, now)) return;
+    l.init();
+    l.start_a(now);
+    l.start_b(now);
+    first_steps(l.a, l.b, lds);
+    wait_copies<0>();
+    barrier_only();
+    Ring ring = first_ring();
+    bool behind = false;
+    for (;;) {
+        const bool more = place(seq += gridDim.x / 8, after);
+        const NextTile<WgradLoaders<FP8>, Place> next = {l, after, more};
         f32x4 acc[MS][NS] = {};
-        multiply<MS, NS>(la, lb, ra, rb, now.rows, lds, acc);
-        more = start(seq += gridDim.x / 8);
-        const int k0 = now.k0 + wn * NS * 16 + q * 8;
-#pragma unroll
-        for (int mi = 0; mi < MS; ++mi) {
-            const int n = now.n0 + (wm * MS + mi) * 16 + i;
-            if (n >= a.n_dim) continue;
-            const int64_t row = ((int64_t)now.e * a.n_dim + n) * a.k_dim;
-#pragma unroll
-            for (int p = 0; p < NS / 2; ++p) {
-                const int k = k0 + p * 32;
-                if (k >= a.k_dim) continue;
-                const f32x4 v = acc[mi][2 * p], w = acc[mi][2 * p + 1];
-                if constexpr (F32) {
-                    float* o = static_cast<float*>(a.dw) + row + k;
-                    *reinterpret_cast<f32x4*>(o) = v;
-                    *reinterpret_cast<f32x4*>(o + 4) = w;
-                } else {
-                    const u32x4 o = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]),
-                                     pack_bf16(w[2], w[3])};
-                    st16(static_cast<uint16_t*>(a.dw) + row + k, o);
-                }
-            }
-        }
+        multiply_stream<MS, NS, F32 ? 32 : 16>(l.a, l.b, ra, rb, stream_steps<decltype(l.b)>(now.rows), lds, ring,
+                                               behind, acc, next);
+        const int n = now.n0 + wm * MS * 16, k = now.k0 + wn * NS * 16;
+        store_block<F32>(a.dw, (int64_t)now.e * a.n_dim + n, k, a.k_dim, a.n_dim - n, a.k_dim - k, acc);
+        if (!more) break;
+        behind = now.n0 + kFullRows <= a.n_dim && now.k0 + kTileN <= a.k_dim;
+        now = after;
     }
+    wait_copies<0>();
 }
 
 // One workgroup per CU at most (it takes all of the CU's LDS), in multiples of
@@ -810,7 +953,8 @@ hipError_t launch_expert_wgrad(const ep_shape& s, const ep_layout& L, const uint
     const WgradArgs a = {L.expert_offsets, dy, x, x8, x_scales, dw, s.E, (int)rows, n_dim, k_dim, err_words(ws)};
     void (*const kernels[2][2])(WgradArgs) = {{wgrad_kernel<false, false>, wgrad_kernel<false, true>},
                                               {wgrad_kernel<true, false>, wgrad_kernel<true, true>}};
-    return launch_tiles(kernels[x8 != nullptr][dtype == EP_GRAD_F32], expert_wgrad_tiles(s.E, n_dim, k_dim), a, st);
+    // Without rows the second operand may be NULL, which only the bf16 form never reads.
+    return launch_tiles(kernels[x8 && rows > 0][dtype == EP_GRAD_F32], expert_wgrad_tiles(s.E, n_dim, k_dim), a, st);
 }
 
 }  // namespace ep
