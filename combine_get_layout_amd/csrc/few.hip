@@ -16,14 +16,13 @@ namespace {
 
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / kWave;
-constexpr int kUpCols = 32;    // values of f per workgroup of the first launch
 constexpr int kDownCols = 16;  // values of h per workgroup of the second
 constexpr int kDownSpan = 256; // contracted values per unit of work of the second launch
 
-// One (used expert, token) pair: the token's first lane with that expert (-1:
-// none) and the sum of its lanes' weights.
+// One token of a used expert: token << 16 | row of its inner activations (token
+// * K + its first lane with that expert), and the sum of its lanes' weights.
 struct Route {
-    int lane;
+    int id;
     float w;
 };
 
@@ -38,8 +37,8 @@ struct FewArgs {
     const float* s2;
     uint16_t* out;
     uint32_t* err;
-    int* used;        // number of used experts, then their ids
-    Route* routes;    // [used][T]
+    int* used;        // number of used experts, then expert | tokens << 16 of each
+    Route* routes;    // [used][T], each expert's tokens in ascending order
     uint16_t* act;    // [T*K][F], row = first lane of (token, expert)
 };
 
@@ -92,29 +91,29 @@ __device__ __forceinline__ Found find_expert(const FewArgs& a, uint32_t* bits, s
     f.expert = src * 64 + __ffsll((unsigned long long)w) - 1;
 
     bool mine = false;
+    Route r = {-1, 0.f};
     if (wave < 2) {
-        Route r = {-1, 0.f};
         if (tid < a.T) {
             for (int k = 0; k < a.K; ++k) {
                 if (a.topk[tid * a.K + k] != f.expert) continue;
-                if (r.lane < 0) r.lane = k;
+                if (r.id < 0) r.id = tid << 16 | (tid * a.K + k);
                 r.w += a.topk_w[tid * a.K + k];
             }
-            if (blockIdx.x == 0) a.routes[(int64_t)want * a.T + tid] = r;
         }
-        mine = r.lane >= 0;
+        mine = r.id >= 0;
         const uint64_t m = __ballot(mine);
-        if (wave == 0 && lane == 0) scratch[0] = __popcll(m);
-        if (wave == 1 && lane == 0) scratch[1] = __popcll(m);
-        scratch[2 + tid] = mine ? r.lane : -1;
+        if (lane == 0) scratch[wave] = __popcll(m);
     }
     __syncthreads();
+    f.tokens = scratch[0] + scratch[1];
     if (wave < 2 && mine) {
         const uint64_t m = __ballot(true);
         const int at = (wave ? scratch[0] : 0) + __popcll(m & ((1ull << lane) - 1));
         token[at] = (short)tid;
+        scratch[2 + at] = r.id & 0xFFFF;
+        if (blockIdx.x == 0) a.routes[(int64_t)want * a.T + at] = r;
     }
-    f.tokens = scratch[0] + scratch[1];
+    if (blockIdx.x == 0 && tid == 0) a.used[1 + want] = f.expert | f.tokens << 16;
     __syncthreads();
     return f;
 }
@@ -132,56 +131,71 @@ struct UpShared {
 };
 
 // Tokens [t0, t0 + 16 * NT) of the expert's list, all NT tiles in use.
-template <bool FP8, int NT>
+template <bool FP8, int RT, int NT>
 __device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, UpShared& sh, int t0) {
     constexpr int kStep = FP8 ? 128 : 64, kX = FP8 ? 4 : 2, kBytes = FP8 ? 1 : 2;
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
     const int i = lane & 15, q = lane >> 4;
-    const int f0 = blockIdx.x * kUpCols, cols = min(kUpCols, a.F - f0);
+    constexpr int GT = RT / 2, kCols = GT * 16;
+    const int f0 = blockIdx.x * kCols, cols = min(kCols, a.F - f0);
     const uint32_t ld = (uint32_t)a.H * kBytes;
     const char* w = a.w13 + ((int64_t)found.expert * 2 * a.F + f0) * ld;
     // Gate rows, up rows and the tokens' rows; rows past F read as zeros.
     const auto d_gate = buf_resource(w, cols * ld), d_up = buf_resource(w + (int64_t)a.F * ld, cols * ld);
     const auto d_x = buf_resource(a.x, (uint32_t)a.T * a.H * 2);
-    const uint32_t row0 = i * ld + q * 16, row1 = row0 + 16 * ld;
+    const uint32_t row0 = i * ld + q * 16;
     const int blocks = a.H / 128;
-    const float* sc = FP8 ? a.s13 + ((int64_t)found.expert * 2 * a.F + min(f0 + i, a.F - 1)) * blocks : nullptr;
-    const int64_t sc1 = (int64_t)(min(f0 + 16 + i, a.F - 1) - min(f0 + i, a.F - 1)) * blocks;
-    const int64_t sc_up = (int64_t)a.F * blocks;
-    const int steps = (a.H + kStep - 1) / kStep;
-    uint32_t xr[NT];
+    uint32_t sc[RT];  // this lane's weight row's scales, from a.s13 + those of the expert
+    const float* scales = FP8 ? a.s13 + (int64_t)found.expert * 2 * a.F * blocks : nullptr;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-        xr[n] = (uint32_t)sh.token[min(t0 + n * 16 + i, found.tokens - 1)] * a.H * 2 + q * (FP8 ? 32 : 16);
-    f32x4 acc[4][NT] = {};
+    for (int r = 0; r < RT; ++r) sc[r] = (uint32_t)(r / GT * a.F + min(f0 + r % GT * 16 + i, a.F - 1)) * blocks;
+    const int steps = (a.H + kStep - 1) / kStep;
+    // The L1 takes a 16-byte load four lanes at a time, whatever these have in
+    // common, and that is what this kernel would run out of first: lanes
+    // without a token load nothing, and one load of a scale serves four steps.
+    uint32_t xr[NT];
+    bool has[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        has[n] = t0 + n * 16 + i < found.tokens;
+        xr[n] = has[n] ? (uint32_t)sh.token[t0 + n * 16 + i] * a.H * 2 + q * (FP8 ? 32 : 16) : 0u;
+    }
+    f32x4 acc[RT][NT] = {};
+    float four[RT] = {};
     // One step's loads at a time: the other waves' loads (three or more to a
     // SIMD) cover the wait.
-    for (int s = wave; s < steps; s += kFewWaves) {
-        u32x4 wv[4][2], xv[NT][kX];
-        float sv[4];
+    for (int s = wave, it = 0; s < steps; s += kFewWaves, ++it) {
+        u32x4 wv[RT][2], xv[NT][kX];
+        float sv[RT];
+        if (FP8 && it % 4 == 0) {
+            // Lane (i, q) takes the scale of the q-th of the next four steps.
+            const int mine = min(s + q * kFewWaves, steps - 1);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) four[r] = scales[sc[r] + mine];
+        }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const uint32_t at = s * 128 + p * 64;  // bytes of a weight row
             // Values past H (the last step of a bf16 row): past the end.
             const uint32_t far = !FP8 && s * kStep + (p * 4 + q) * 8 >= a.H ? kBufFar : 0u;
-            wv[0][p] = buf_load16(d_gate, row0 + far, at);
-            wv[1][p] = buf_load16(d_gate, row1 + far, at);
-            wv[2][p] = buf_load16(d_up, row0 + far, at);
-            wv[3][p] = buf_load16(d_up, row1 + far, at);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                wv[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, at);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int h = 0; h < kX / 2; ++h)
-                    xv[n][p * (kX / 2) + h] = buf_load16(d_x, xr[n] + far, at * (FP8 ? 2 : 1) + h * 16);
+                for (int h = 0; h < kX / 2; ++h) {
+                    u32x4 v = {0u, 0u, 0u, 0u};
+                    if (has[n]) v = buf_load16(d_x, xr[n] + far, at * (FP8 ? 2 : 1) + h * 16);
+                    xv[n][p * (kX / 2) + h] = v;
+                }
         }
         if constexpr (FP8) {
-            sv[0] = sc[s];
-            sv[1] = sc[sc1 + s];
-            sv[2] = sc[sc_up + s];
-            sv[3] = sc[sc_up + sc1 + s];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) sv[r] = __shfl(four[r], i + it % 4 * 16);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < RT; ++r) {
             bf16x8 wf[kX];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -210,70 +224,64 @@ __device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, 
         }
     }
     settle(acc);
-    // Sum the waves' parts: thread -> (token of 16, f of 32).
+    // Sum the waves' parts, 32 values of f at a time: thread -> (token of 16, f of 32).
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int g = 0; g < GT; g += 2) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sh.part[wave][r][q * 4 + j][i] = acc[r][n][j];
-        __syncthreads();
-        const int tk = tid >> 5, c = tid & 31;
-        const int at = t0 + n * 16 + tk, f = f0 + c;
-        if (at < found.tokens && f < a.F) {
-            float g = 0.f, u = 0.f;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int v = 0; v < kFewWaves; ++v) {
-                g += sh.part[v][c >> 4][tk][c & 15];
-                u += sh.part[v][2 + (c >> 4)][tk][c & 15];
+                for (int j = 0; j < 4; ++j)
+                    sh.part[wave][r][q * 4 + j][i] = acc[(r >> 1) * GT + g + (r & 1)][n][j];
+            __syncthreads();
+            const int tk = tid >> 5, c = tid & 31;
+            const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
+            if (at < found.tokens && f < a.F) {
+                float gate = 0.f, up = 0.f;
+#pragma unroll
+                for (int v = 0; v < kFewWaves; ++v) {
+                    gate += sh.part[v][c >> 4][tk][c & 15];
+                    up += sh.part[v][2 + (c >> 4)][tk][c & 15];
+                }
+                const float r = gate / (1.0f + __expf(-gate)) * up;
+                // Rounded to bf16 for the second product's matrix instruction.
+                a.act[(int64_t)sh.scratch[2 + at] * a.F + f] = (uint16_t)f32_to_bf16(r);
             }
-            const float r = g / (1.0f + __expf(-g)) * u;
-            const int t = sh.token[at];
-            // Rounded to bf16 for the second product's matrix instruction.
-            a.act[((int64_t)t * a.K + sh.scratch[2 + t]) * a.F + f] = (uint16_t)f32_to_bf16(r);
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
-template <bool FP8, int NT>
+template <bool FP8, int RT, int NT>
 __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_up_kernel(FewArgs a) {
     __shared__ UpShared sh;
     const int tid = threadIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.err[0] = 0u;
     const Found found = find_expert(a, sh.bits, sh.token, sh.scratch);
-    if (blockIdx.x == 0 && tid == 0) {
-        if (blockIdx.y == 0) a.used[0] = found.used;
-        if (found.expert >= 0) a.used[1 + blockIdx.y] = found.expert;
-    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
-    if constexpr (NT == 1) {
-        up_tokens<FP8, 1>(a, found, sh, 0);
-    } else {
-        for (int t0 = 0; t0 < found.tokens; t0 += 64) {
-            const int left = found.tokens - t0;
-            if (left > 48)
-                up_tokens<FP8, 4>(a, found, sh, t0);
-            else if (left > 32)
-                up_tokens<FP8, 3>(a, found, sh, t0);
-            else if (left > 16)
-                up_tokens<FP8, 2>(a, found, sh, t0);
-            else
-                up_tokens<FP8, 1>(a, found, sh, t0);
-        }
+    for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {
+        if (NT > 1 && found.tokens - t0 > 16)
+            up_tokens<FP8, RT, NT>(a, found, sh, t0);
+        else
+            up_tokens<FP8, RT, 1>(a, found, sh, t0);
     }
 }
 
 // Second launch: workgroup x computes 16 values of h for every token. Unit u =
 // (used expert, span of 256 values of f); the 8 waves take the units in turn. A
-// unit's product goes into a temporary and is then added, weighted, to the
-// tokens routed to its expert alone, so that an expert's infinities or NaN
-// stay with its own tokens.
-template <bool FP8, int NT>
-__global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_down_kernel(FewArgs a) {
+// unit's 16 weight rows and its expert's tokens' activations are loaded at once
+// (the routes, which say where the latter are, a unit ahead), multiplied into
+// temporaries and added, weighted, to the wave's sums of those tokens in LDS:
+// an expert's infinities or NaN stay with its own tokens, and the matrix
+// instruction's 16 columns are tokens of the expert, however many others there
+// are. The waves' sums are added at the end in a fixed order.
+template <bool FP8>
+__global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
     constexpr int kLoads = FP8 ? 4 : 8, kBytes = FP8 ? 1 : 2;
-    __shared__ float part[kFewWaves][NT][16][17];
-    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+    extern __shared__ float sums[];  // [kFewWaves][T][17]
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     if (blockIdx.x == 0) {
         bool bad = false;
         for (int n = tid; n < a.T * a.K; n += kFewThreads) bad |= expert_bad(a.topk[n], a.E);
@@ -284,86 +292,104 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_down_kernel(
     const int hr = min(h0 + i, a.H - 1);
     const int spans = (a.F + kDownSpan - 1) / kDownSpan;
     const int units = a.used[0] * spans;
-    const int nt = (a.T + 15) / 16;
-    f32x4 acc[NT] = {};
-    struct Buf {
-        u32x4 w[kLoads];
-        float s[2];
+    float* mine = sums + wave * a.T * 17;
+    for (int n = lane; n < a.T * 17; n += kWave) mine[n] = 0.f;
+
+    // As in the first launch, loads are spared: a tile's routes are read by one
+    // quarter of the wave (lane i < 16: token t0 + i of the expert) and handed
+    // on between lanes, and lanes without a token load no activations.
+    auto load_route = [&](int rank, int tokens, int t0) {
+        Route r = {0, 0.f};
+        if (q == 0 && t0 + i < tokens) r = a.routes[(int64_t)rank * a.T + t0 + i];
+        return r;
     };
-    auto load = [&](Buf& b, int u) {
-        const int rank = u / spans, span = u % spans;
-        const int64_t e = a.used[1 + rank];
-        const char* p = a.w2 + (e * a.H + hr) * a.F * kBytes;
-        const u32x4 zero = {0u, 0u, 0u, 0u};
+    const uint32_t ld = (uint32_t)a.F * kBytes;
+    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)min(kDownCols, a.H - h0) * ld;
+    auto load_act = [&](int id, bool has, int span, u32x4 (&v)[8]) {
+        const uint16_t* p = a.act + (int64_t)(id & 0xFFFF) * a.F + span * kDownSpan;
+        const bool full = (span + 1) * kDownSpan <= a.F;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) v[m] = u32x4{0u, 0u, 0u, 0u};
+        if (has && full) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) v[m] = ld16(p + (FP8 ? ((m >> 1) * 4 + q) * 16 + (m & 1) * 8 : (m * 4 + q) * 8));
+        } else if (has) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                const int k = FP8 ? ((m >> 1) * 4 + q) * 16 + (m & 1) * 8 : (m * 4 + q) * 8;
+                if (span * kDownSpan + k < a.F) v[m] = ld16(p + k);
+            }
+        }
+    };
+    int u = wave, entry = 0;
+    Route route = {0, 0.f};
+    if (u < units) {
+        entry = __builtin_amdgcn_readfirstlane(a.used[1 + u / spans]);
+        route = load_route(u / spans, entry >> 16, 0);
+    }
+    while (u < units) {
+        const int rank = u / spans, span = u % spans, tokens = entry >> 16;
+        const int64_t e = entry & 0xFFFF;
+        u32x4 w[kLoads], v[8];
+        float s0 = 0.f, s1 = 0.f;
+        const auto d = buf_resource(a.w2 + (e * a.H + h0) * ld, w_bytes);
+        const bool full = (span + 1) * kDownSpan <= a.F;
 #pragma unroll
         for (int n = 0; n < kLoads; ++n) {
-            const int k = span * kDownSpan + (n * 4 + q) * (16 / kBytes);
-            const bool in = k < a.F;
-            b.w[n] = ld16(p + (in ? k : 0) * kBytes);
-            if (!in) b.w[n] = zero;
+            const uint32_t far = !full && span * kDownSpan + (n * 4 + q) * (16 / kBytes) >= a.F ? kBufFar : 0u;
+            w[n] = buf_load16(d, w_off + far, span * kDownSpan * kBytes + n * 64);
         }
-        if constexpr (FP8) {
-            const float* s = a.s2 + (e * a.H + hr) * (a.F / 128) + span * 2;
-            b.s[0] = s[0];
-            b.s[1] = span * kDownSpan + 128 < a.F ? s[1] : 0.f;
+        if constexpr (FP8) {  // lanes q = 0, 1: the span's two blocks
+            float sv = 0.f;
+            if (q < 2 && span * 2 + q < a.F / 128) sv = a.s2[(e * a.H + hr) * (a.F / 128) + span * 2 + q];
+            s0 = __shfl(sv, i);
+            s1 = __shfl(sv, i + 16);
         }
-    };
-    auto compute = [&](const Buf& b, int u) {
-        const int rank = u / spans, span = u % spans;
-        const Route* routes = a.routes + (int64_t)rank * a.T;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && n >= nt) continue;
-            const int t = n * 16 + i;
-            const int k1 = t < a.T ? routes[t].lane : -1;
-            if (!__ballot(k1 >= 0)) continue;
-            const uint16_t* p = a.act + ((int64_t)min(t, a.T - 1) * a.K + max(k1, 0)) * a.F;
+        load_act(__shfl(route.id, i), i < tokens, span, v);
+        const int next = u + kFewWaves;
+        int next_entry = 0;
+        Route next_route = route;
+        if (next < units) {
+            next_entry = __builtin_amdgcn_readfirstlane(a.used[1 + next / spans]);
+            next_route = load_route(next / spans, next_entry >> 16, 0);
+        }
+        for (int t0 = 0; t0 < tokens; t0 += 16) {
+            if (t0) {  // more than 16 tokens: the weights stay, the tokens change
+                route = load_route(rank, tokens, t0);
+                load_act(__shfl(route.id, i), t0 + i < tokens, span, v);
+            }
             f32x4 c[1][2] = {};
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
-                int k;
-                if constexpr (FP8)
-                    k = span * kDownSpan + ((m >> 1) * 4 + q) * 16 + (m & 1) * 8;
-                else
-                    k = span * kDownSpan + (m * 4 + q) * 8;
-                u32x4 v = {0u, 0u, 0u, 0u};
-                if (k1 >= 0 && k < a.F) v = ld16(p + k);
                 bf16x8 wf;
                 if constexpr (FP8)
-                    wf = e4m3_to_bf16(b.w[m >> 1][(m & 1) * 2], b.w[m >> 1][(m & 1) * 2 + 1]);
+                    wf = e4m3_to_bf16(w[m >> 1][(m & 1) * 2], w[m >> 1][(m & 1) * 2 + 1]);
                 else
-                    wf = as_bf16(b.w[m]);
+                    wf = as_bf16(w[m]);
                 // FP8: the first four fragments are the span's first block of 128.
-                c[0][FP8 ? m >> 2 : 0] = mfma_bf16(as_bf16(v), wf, c[0][FP8 ? m >> 2 : 0]);
+                f32x4& d = c[0][FP8 ? m >> 2 : 0];
+                d = mfma_bf16(as_bf16(v[m]), wf, d);
             }
             settle(c);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int tj = n * 16 + q * 4 + j;
-                const Route r = tj < a.T ? routes[tj] : Route{-1, 0.f};
-                const float v = FP8 ? fmaf(b.s[1], c[0][1][j], b.s[0] * c[0][0][j]) : c[0][0][j];
-                if (r.lane >= 0) acc[n][j] = fmaf(r.w, v, acc[n][j]);
+                const int id = __shfl(route.id, q * 4 + j);
+                const float weight = __shfl(route.w, q * 4 + j);
+                if (t0 + q * 4 + j < tokens) {
+                    float* sum = mine + (id >> 16) * 17 + i;
+                    *sum = fmaf(weight, FP8 ? fmaf(s1, c[0][1][j], s0 * c[0][0][j]) : c[0][0][j], *sum);
+                }
             }
         }
-    };
-    for (int u = wave; u < units; u += kFewWaves) {
-        Buf b;
-        load(b, u);
-        compute(b, u);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (NT > 1 && n >= nt) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[wave][n][q * 4 + j][i] = acc[n][j];
+        u = next, entry = next_entry, route = next_route;
     }
     __syncthreads();
-    for (int n = tid; n < nt * 256; n += kFewThreads) {
+    for (int n = tid; n < a.T * 16; n += kFewThreads) {
         const int t = n >> 4, h = h0 + (n & 15);
-        if (t >= a.T || h >= a.H) continue;
+        if (h >= a.H) continue;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) v += part[w][t >> 4][t & 15][n & 15];
+        for (int w = 0; w < kFewWaves; ++w) v += sums[(w * a.T + t) * 17 + (n & 15)];
         a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
     }
 }
@@ -396,15 +422,16 @@ hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_exper
                        fp8 ? (const char*)x.w2_fp8 : (const char*)x.w2, x.w2_scales, out, err,
                        reinterpret_cast<int*>(ws + l.used), reinterpret_cast<Route*>(ws + l.routes),
                        reinterpret_cast<uint16_t*>(ws + l.act)};
-    const dim3 up((x.F + kUpCols - 1) / kUpCols, (unsigned)std::min<int64_t>(s.E, (int64_t)s.T * s.K));
+    // Up to 16 tokens: 4 row tiles and one token tile. More: 8 and 2, so that the
+    // tokens' rows, which then weigh, are read half as often.
+    const int many = s.T > 16, cols = many ? 64 : 32;
+    const dim3 up((x.F + cols - 1) / cols, (unsigned)std::min<int64_t>(s.E, (int64_t)s.T * s.K));
     const dim3 down((s.H + kDownCols - 1) / kDownCols);
-    void (*const ups[2][2])(FewArgs) = {{few_up_kernel<false, 1>, few_up_kernel<false, 4>},
-                                        {few_up_kernel<true, 1>, few_up_kernel<true, 4>}};
-    void (*const downs[2][2])(FewArgs) = {{few_down_kernel<false, 1>, few_down_kernel<false, 8>},
-                                          {few_down_kernel<true, 1>, few_down_kernel<true, 8>}};
-    const int many = s.T > 16;
+    void (*const ups[2][2])(FewArgs) = {{few_up_kernel<false, 4, 1>, few_up_kernel<false, 8, 2>},
+                                        {few_up_kernel<true, 4, 1>, few_up_kernel<true, 8, 2>}};
     hipLaunchKernelGGL(ups[fp8][many], up, dim3(kFewThreads), 0, st, a);
-    hipLaunchKernelGGL(downs[fp8][many], down, dim3(kFewThreads), 0, st, a);
+    const size_t lds = sizeof(float) * kFewWaves * 17 * s.T;  // 69,632 bytes at most
+    hipLaunchKernelGGL(fp8 ? few_down_kernel<true> : few_down_kernel<false>, down, dim3(kFewThreads), lds, st, a);
     return hipGetLastError();
 }
 
