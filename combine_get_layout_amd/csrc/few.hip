@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / kWave;
-constexpr int kDownCols = 16;  // values of h per workgroup of the second
+constexpr int kDownCols = 16;  // values of h per workgroup of the second launch
 constexpr int kDownSpan = 256; // contracted values per unit of work of the second launch
 
 // One token of a used expert: token << 16 | row of its inner activations (token
@@ -229,15 +229,16 @@ __device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, 
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int g = 0; g < GT; g += 2) {
+            constexpr int kSub = GT < 2 ? 1 : 2;  // sub-tiles of 16 values in this pass
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 2 * kSub; ++r)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    sh.part[wave][r][q * 4 + j][i] = acc[(r >> 1) * GT + g + (r & 1)][n][j];
+                    sh.part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][n][j];
             __syncthreads();
             const int tk = tid >> 5, c = tid & 31;
             const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
-            if (at < found.tokens && f < a.F) {
+            if (at < found.tokens && f < a.F && c < 16 * kSub) {
                 float gate = 0.f, up = 0.f;
 #pragma unroll
                 for (int v = 0; v < kFewWaves; ++v) {
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
         if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_EXPERT_ID);
     }
     const int i = lane & 15, q = lane >> 4;
-    const int h0 = blockIdx.x * kDownCols;
+    const int h0 = blockIdx.x * kDownCols, cols = min(kDownCols, a.H - h0);
     const int hr = min(h0 + i, a.H - 1);
     const int spans = (a.F + kDownSpan - 1) / kDownSpan;
     const int units = a.used[0] * spans;
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
         return r;
     };
     const uint32_t ld = (uint32_t)a.F * kBytes;
-    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)min(kDownCols, a.H - h0) * ld;
+    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld;
     auto load_act = [&](int id, bool has, int span, u32x4 (&v)[8]) {
         const uint16_t* p = a.act + (int64_t)(id & 0xFFFF) * a.F + span * kDownSpan;
         const bool full = (span + 1) * kDownSpan <= a.F;
@@ -386,7 +387,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
     __syncthreads();
     for (int n = tid; n < a.T * 16; n += kFewThreads) {
         const int t = n >> 4, h = h0 + (n & 15);
-        if (h >= a.H) continue;
+        if ((n & 15) >= cols) continue;
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kFewWaves; ++w) v += sums[(w * a.T + t) * 17 + (n & 15)];
@@ -422,14 +423,22 @@ hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_exper
                        fp8 ? (const char*)x.w2_fp8 : (const char*)x.w2, x.w2_scales, out, err,
                        reinterpret_cast<int*>(ws + l.used), reinterpret_cast<Route*>(ws + l.routes),
                        reinterpret_cast<uint16_t*>(ws + l.act)};
-    // Up to 16 tokens: 4 row tiles and one token tile. More: 8 and 2, so that the
-    // tokens' rows, which then weigh, are read half as often.
-    const int many = s.T > 16, cols = many ? 64 : 32;
-    const dim3 up((x.F + cols - 1) / cols, (unsigned)std::min<int64_t>(s.E, (int64_t)s.T * s.K));
+    const int many = s.T > 16;
+    const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K);
+    // Values of f per workgroup of the first launch (x 2 = weight rows). Above 16
+    // tokens 64, and two token tiles at a time: the tokens' rows, which then
+    // weigh, are read half as often (64 tokens, 64 experts of 4096 x 1536: 548 us,
+    // with 32: 576; one token tile and 32: 571, but at 128 tokens 702 against 607).
+    // Up to 16 tokens 32, or 16 where that gives fewer than 1,024 workgroups, which
+    // leave the memory idle (one token, top-8 of 4096 x 1536: 66 us with 16, 75
+    // with 32; 13 tokens, 33 experts of 2056 x 712: 63.5 and 70).
+    const bool narrow = (int64_t)((x.F + 31) / 32) * experts < 1024;
+    const int cols = many ? 64 : narrow ? 16 : 32;
+    const dim3 up((x.F + cols - 1) / cols, (unsigned)experts);
     const dim3 down((s.H + kDownCols - 1) / kDownCols);
-    void (*const ups[2][2])(FewArgs) = {{few_up_kernel<false, 4, 1>, few_up_kernel<false, 8, 2>},
-                                        {few_up_kernel<true, 4, 1>, few_up_kernel<true, 8, 2>}};
-    hipLaunchKernelGGL(ups[fp8][many], up, dim3(kFewThreads), 0, st, a);
+    void (*const ups[2][3])(FewArgs) = {{few_up_kernel<false, 4, 1>, few_up_kernel<false, 8, 2>, few_up_kernel<false, 2, 1>},
+                                        {few_up_kernel<true, 4, 1>, few_up_kernel<true, 8, 2>, few_up_kernel<true, 2, 1>}};
+    hipLaunchKernelGGL(ups[fp8][many ? 1 : narrow ? 2 : 0], up, dim3(kFewThreads), 0, st, a);
     const size_t lds = sizeof(float) * kFewWaves * 17 * s.T;  // 69,632 bytes at most
     hipLaunchKernelGGL(fp8 ? few_down_kernel<true> : few_down_kernel<false>, down, dim3(kFewThreads), lds, st, a);
     return hipGetLastError();
