@@ -327,6 +327,7 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB&
                                          f32x4 (&acc)[MS][NS]) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
     const int steps = (k_dim + kStep - 1) / kStep;
+    constexpr int kCopiesA = (MS * NS * 8 + 63) / 64;  // of the tile's MS x 16 x NS / 2 rows, 64 each
     wait_copies<0>();
     barrier_only();
     Fragments<MS, NS> f[2];
@@ -347,7 +348,8 @@ __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB&
             barrier_only();
             la.begin((s + slot + 2) * kStep);
             half_step<MS, NS>(ra, rb, lds + (slot ^ 1) * kPart, lds + r.b_next, 0, f[1], f[0], acc, [&](int g) {
-                if (g < LA::kLoads) la.copy(g, at + slot * kPart);
+                // Copies of rows that the tile's shape does not have are left out.
+                if (g < kCopiesA) la.copy(g, at + slot * kPart);
             });
             r = {r.a_next, r.a_now, r.b_next, r.b_free, r.b_now};
         }
@@ -420,81 +422,77 @@ struct Tile {
     int expert;
     int row0;  // first row of the tile
     int rows;  // rows of the tile that exist
+    int height;  // rows that the tile's shape holds, at most 256
     int n;     // column tile
 };
 
-// The tiles of a launch. Every expert has floor(m / 256) full tiles and one
-// tail of m % 256 rows, each times `n_tiles`; full tiles come first (tails fill
-// the gaps at the end). Workgroups go to the 8 XCDs in turn, so each XCD takes
-// a contiguous run of tiles, and its workgroups take them in turn: within an
-// expert groups of up to 8 row tiles, the column tiles of a group one after the
-// other, so that the 32 tiles that an XCD works on at a time are about 8 x 4 (4
-// x 8 at 1,024 rows) and share their operands through its L2.
+// The tiles of a launch: every expert's m rows are cut evenly into ceil(m / 256)
+// row tiles (in multiples of 32 rows), times `n_tiles`. Workgroups go to the 8
+// XCDs in turn; each XCD takes a contiguous run of the tiles, and its workgroups
+// take them in turn: within an expert groups of up to 8 row tiles, the column
+// tiles of a group one after the other, so that the 32 tiles that an XCD works
+// on at a time are about 8 x 4 (4 x 8 at 1,024 rows) and, being of one height
+// and so in step, share their operands through its L2. Full tiles and a short
+// last one lose that: 32 experts of 1,040 rows (gate/up product, 7168 x 2048)
+// took 1,846 us with the short tiles beside the full ones, 1,716 with them at
+// the end, where they read all the weights again.
 struct Tiles {
     const int32_t* offsets;
     int rows, n_tiles;
-    int per;     // experts of a lane (each wave covers all and searches for itself)
+    int per;  // experts of a lane (each wave covers all and searches for itself)
     int E;
-    int pf, pt;  // full and tail row tiles of the experts before this lane's
-    int total_f, total_t;
+    int before;  // row tiles of the experts before this lane's
+    int total;
 
-    __device__ __forceinline__ void bounds(int e, int& lo, int& hi) const {
+    // Rows [lo, lo + m) of expert e.
+    __device__ __forceinline__ void bounds(int e, int& lo, int& m) const {
         lo = min(max(offsets[e], 0), rows);
-        hi = min(max(offsets[e + 1], lo), rows);
+        m = min(max(offsets[e + 1], lo), rows) - lo;
     }
+    __device__ __forceinline__ static int row_tiles(int m) { return (m + kFullRows - 1) / kFullRows; }
+
     __device__ __forceinline__ void init(const int32_t* offs, int experts, int n_rows, int n) {
         offsets = offs, rows = n_rows, n_tiles = n, E = experts;
         per = (E + kWave - 1) / kWave;
         const int lane = lane_id(), e0 = min(E, lane * per), e1 = min(E, e0 + per);
-        int full = 0, tail = 0;
+        int count = 0;
         for (int e = e0; e < e1; ++e) {
-            int lo, hi;
-            bounds(e, lo, hi);
-            full += (hi - lo) / kFullRows;
-            tail += (hi - lo) % kFullRows != 0;
+            int lo, m;
+            bounds(e, lo, m);
+            count += row_tiles(m);
         }
-        int sf = full, st = tail;
+        int sum = count;
         for (int d = 1; d < kWave; d <<= 1) {
-            const int a = __shfl_up(sf, d), b = __shfl_up(st, d);
-            if (lane >= d) sf += a, st += b;
+            const int v = __shfl_up(sum, d);
+            if (lane >= d) sum += v;
         }
-        pf = sf - full, pt = st - tail;
-        total_f = readlane(sf, kWave - 1);
-        total_t = readlane(st, kWave - 1);
+        before = sum - count;
+        total = readlane(sum, kWave - 1) * n_tiles;
     }
     // The seq-th tile of this workgroup's XCD; false if there is none.
     __device__ __forceinline__ bool find(int seq, Tile& t) const {
-        const int xcd = blockIdx.x % 8;
-        const int all_f = total_f * n_tiles, all_t = total_t * n_tiles;
-        const int per_f = (all_f + 7) / 8, per_t = (all_t + 7) / 8;
-        const int mine_f = min(max(all_f - xcd * per_f, 0), per_f), mine_t = min(max(all_t - xcd * per_t, 0), per_t);
-        const bool is_tail = seq >= mine_f;
-        if (is_tail && seq - mine_f >= mine_t) return false;
-        const int item = is_tail ? xcd * per_t + seq - mine_f : xcd * per_f + seq;
+        const int share = (total + 7) / 8, item = (int)(blockIdx.x % 8) * share + seq;
+        if (seq >= share || item >= total) return false;
         const int target = item / n_tiles;  // lies in its expert's range of row tiles
         const int e0 = min(E, lane_id() * per), e1 = min(E, e0 + per);
-        int f = pf, l = pt, at = -1, lo0 = 0, m0 = 0, before = 0;
+        int f = before, at = -1, lo0 = 0, m0 = 0, f0 = 0;
         for (int e = e0; e < e1; ++e) {
-            int lo, hi;
-            bounds(e, lo, hi);
-            const int m = hi - lo, nf = m / kFullRows, nt = m % kFullRows != 0;
-            if (is_tail ? nt && target == l : target >= f && target < f + nf) at = e, lo0 = lo, m0 = m, before = f;
-            f += nf, l += nt;
+            int lo, m;
+            bounds(e, lo, m);
+            const int n = row_tiles(m);
+            if (target >= f && target < f + n) at = e, lo0 = lo, m0 = m, f0 = f;
+            f += n;
         }
         const int src = __ffsll((unsigned long long)__ballot(at >= 0)) - 1;
+        const int m = readlane(m0, src);
+        const int local = item - readlane(f0, src) * n_tiles, group = local / (8 * n_tiles);
+        const int in = local % (8 * n_tiles), high = min(8, row_tiles(m) - group * 8);
+        t.height = ((m + row_tiles(m) - 1) / row_tiles(m) + 31) / 32 * 32;
+        const int row = (group * 8 + in % high) * t.height;
         t.expert = readlane(at, src);
-        const int first = readlane(lo0, src), m = readlane(m0, src);
-        if (is_tail) {
-            t.rows = m % kFullRows;
-            t.row0 = first + m - t.rows;
-            t.n = item % n_tiles;
-        } else {
-            const int local = item - readlane(before, src) * n_tiles, group = local / (8 * n_tiles);
-            const int in = local % (8 * n_tiles), high = min(8, m / kFullRows - group * 8);
-            t.rows = kFullRows;
-            t.row0 = first + (group * 8 + in % high) * kFullRows;
-            t.n = in / high;
-        }
+        t.row0 = readlane(lo0, src) + row;
+        t.rows = min(t.height, m - row);  // at least 1: all tiles but the last hold at most (tiles - 1) * 256 < m
+        t.n = in / high;
         return true;
     }
 };
@@ -543,6 +541,25 @@ struct MatmulLoaders {
             b.start(w + (int64_t)n0 * m.k_dim, (uint32_t)min(m.n_dim - n0, kTileN) * m.k_dim * 2, m.k_dim);
     }
 };
+// Calls f(waves over rows, sub-tiles of a wave along rows) for a tile height.
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <class F>
+__device__ __forceinline__ void by_height(int height, F f) {
+    if (height > 224)
+        f(Int<2>(), Int<8>());
+    else if (height > 192)
+        f(Int<2>(), Int<7>());
+    else if (height > 160)
+        f(Int<2>(), Int<6>());
+    else if (height > 128)
+        f(Int<2>(), Int<5>());
+    else if (height > 64)
+        f(Int<2>(), Int<4>());
+    else
+        f(Int<1>(), Int<4>());
+}
+
 // A wave's block of results, MS x NS sub-tiles at (row0, col0) of a row-major
 // matrix of `cols` columns, as bf16 or 32-bit: 8 consecutive columns a lane and
 // pair of sub-tiles. The addresses are a scalar base and one offset per lane.
@@ -619,12 +636,10 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(MatmulArgs a) {
             seq += gridDim.x / 8;
             more = start();
         };
-        if (now.rows > 128)
-            matmul_tile<2, 8, KN>(a, now, l, lds, next);
-        else if (now.rows > 64)
-            matmul_tile<2, 4, KN>(a, now, l, lds, next);
-        else
-            matmul_tile<1, 4, KN>(a, now, l, lds, next);
+        const auto run = [&](auto wm, auto ms) {
+            matmul_tile<wm.value, ms.value, KN>(a, now, l, lds, next);
+        };
+        by_height(now.height, run);
     }
 }
 
@@ -780,12 +795,10 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_kernel(SwigluArgs a) {
             seq += gridDim.x / 8;
             more = start();
         };
-        if (now.rows > 128)
-            swiglu_tile<2, 8, SAVE>(a, now, l, lds, next);
-        else if (now.rows > 64)
-            swiglu_tile<2, 4, SAVE>(a, now, l, lds, next);
-        else
-            swiglu_tile<1, 4, SAVE>(a, now, l, lds, next);
+        const auto run = [&](auto wm, auto ms) {
+            swiglu_tile<wm.value, ms.value, SAVE>(a, now, l, lds, next);
+        };
+        by_height(now.height, run);
     }
 }
 
