@@ -443,6 +443,8 @@ int ep_source_dispatch_fused(const ep_shape* shape, const ep_sources* sources, c
                                           static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
 
+constexpr int64_t kMaxExpertRows = INT32_MAX - 65536;  // also the most tiles of a call
+
 // Checks shared by the expert products over expand-mode rows.
 static int check_expert_rows(const ep_shape* shape, const ep_layout* layout, int64_t rows, int64_t a, int64_t b,
                              void* ws, size_t ws_bytes) {
@@ -450,7 +452,8 @@ static int check_expert_rows(const ep_shape* shape, const ep_layout* layout, int
     if (rc != EP_OK) return rc;
     if ((rc = check_ws(shape, ws, ws_bytes)) != EP_OK) return rc;
     if (!layout || rows < 0 || a < 8 || b < 8 || a % 8 != 0 || b % 8 != 0) return EP_ERR_ARG;
-    if (rows > INT32_MAX || a > EP_MAX_DIM || b > EP_MAX_DIM) return EP_ERR_UNSUPPORTED;
+    // Row and tile numbers, and a little past them, are 32-bit on the device.
+    if (rows > kMaxExpertRows || a > EP_MAX_DIM || b > EP_MAX_DIM) return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }
 
@@ -463,7 +466,7 @@ int ep_expert_matmul(const ep_shape* shape, const ep_layout* layout, const uint1
     if (!layout->expert_offsets || !w || (rows > 0 && (!x || !y))) return EP_ERR_ARG;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(layout->expert_offsets, 4))
         return EP_ERR_ARG;
-    if (expert_matmul_tiles(rows, shape->E, n_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (expert_matmul_tiles(rows, shape->E, n_dim) > kMaxExpertRows) return EP_ERR_UNSUPPORTED;
     return hip_status(launch_expert_matmul(*shape, *layout, x, rows, k_dim, w, n_dim, w_order, y,
                                            static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
@@ -481,7 +484,7 @@ int ep_expert_swiglu(const ep_shape* shape, const ep_layout* layout, const uint1
         return EP_ERR_ARG;
     // 32-bit offsets inside one expert's matrix.
     if (4 * (int64_t)F * shape->H >= INT32_MAX - 15) return EP_ERR_UNSUPPORTED;
-    if (expert_swiglu_tiles(rows, shape->E, F) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (expert_swiglu_tiles(rows, shape->E, F) > kMaxExpertRows) return EP_ERR_UNSUPPORTED;
     return hip_status(launch_expert_swiglu(*shape, *layout, x, rows, w13, F, act, gu_fp8, gu_scales,
                                            static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }
@@ -516,7 +519,7 @@ int ep_expert_wgrad(const ep_shape* shape, const ep_layout* layout, const uint16
     if (!aligned(dy, 16) || !aligned(x->x, 16) || !aligned(x->x_fp8, 16) || !aligned(x->x_scales, 16) ||
         !aligned(dw, 16) || !aligned(layout->expert_offsets, 4))
         return EP_ERR_ARG;
-    if (expert_wgrad_tiles(shape->E, n_dim, k_dim) > INT32_MAX) return EP_ERR_UNSUPPORTED;
+    if (expert_wgrad_tiles(shape->E, n_dim, k_dim) > kMaxExpertRows) return EP_ERR_UNSUPPORTED;
     return hip_status(launch_expert_wgrad(*shape, *layout, dy, rows, n_dim, x->x, x->x_fp8, x->x_scales, k_dim, dw,
                                           dtype, static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }

@@ -56,9 +56,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_resource(const void* p, ui
 // register in between. Written out because the compiler's own form waits for
 // all such copies before any LDS read; the kernels wait once per tile with
 // wait_copies. No output register, so nothing is overwritten while the copy is
-// in flight.
+// in flight. The five wait states before the load are what a descriptor written
+// by a vector instruction (a lane read) needs, and more than m0 does.
 __device__ __forceinline__ void copy16_to_lds(u32x4 r, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "s"(lds)
                  : "memory");
 }
 template <int N>
