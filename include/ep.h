@@ -479,8 +479,7 @@ int ep_expert_matmul(const ep_shape *shape, const ep_layout *layout, const uint1
  * and, when gu_fp8 is non-NULL, for every block of 128 values of [g, u]:
  *   gu_scales = m / 448, m the block's largest magnitude (1 if m < 1e-33)
  *   gu_fp8 = e4m3_rne(v * (1 / gu_scales)).
- * A block that holds an infinity or NaN keeps no finite meaning: its infinite
- * values (with an infinity, all its values) read back as NaN.
+ * A NaN reads back as NaN; all values of a block with an infinity do.
  * x: [rows][H], w13: [E][2F][H] (gate rows, then up rows), act: [rows][F] bf16;
  * gu_fp8: [rows][2F], gu_scales: [rows][2F/128], both or neither (F % 128 ==
  * 0 with them). 4 * F * H must stay below 2^31 - 16 (EP_ERR_UNSUPPORTED). */

@@ -140,6 +140,72 @@ def act_bound(gate, up, s, act, dg, du):
     return 1.1 * dg * (up.abs() + du) + (gate * s).abs() * du + (gate.abs() + 20) * U23 * act.abs()
 
 
+# Rows of an expert on both sides of every tile height (64, 128, 160, 192, 224,
+# 256 rows), of two and three tiles, and none.
+HEIGHTS = [0, 1, 33, 64, 65, 128, 0, 129, 160, 161, 192, 193, 224, 225, 256, 257, 300, 515, 0]
+
+
+def by_counts(counts, H=128):
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    N, E = int(off[-1]), len(counts)
+    shape = ep.make_shape(max(N, 1), H, 1, E, 1)
+    return off, N, shape, ep.alloc_workspace(shape)
+
+
+@pytest.mark.parametrize("k", [8, 96, 136, 200])  # one to four steps of the contracted axis, odd and even
+@pytest.mark.parametrize("back", [False, True], ids=["nk", "kn"])
+def test_matmul_tile_heights(back, k):
+    off, N, shape, ws = by_counts(HEIGHTS)
+    E, n = len(HEIGHTS), 264
+    g = torch.Generator().manual_seed(k)
+    x, wt = randn(g, N, k), randn(g, *((E, k, n) if back else (E, n, k)), scale=k ** -0.5)
+    y = torch.full((N, n), 7.0, dtype=BF16, device="cuda")
+    xd, wd, od = gpu(x, wt, off)
+    ep.ep_expert_matmul(shape, dict(expert_offsets=od), xd, N, k, wd, n,
+                        ep.EP_WEIGHT_KN if back else ep.EP_WEIGHT_NK, y, ws)
+    m = wt.double() if back else wt.double().transpose(1, 2)
+    ref = per_expert(off, lambda e, s: x[s].double() @ m[e], None)
+    acc = k * U23 * per_expert(off, lambda e, s: x[s].double().abs() @ m[e].abs(), None)
+    check(y, ref, acc + HALF_BF16 * (ref.abs() + acc), "y")
+
+
+def test_swiglu_tile_heights():
+    H, F = 72, 384
+    off, N, shape, ws = by_counts(HEIGHTS, H)
+    g = torch.Generator().manual_seed(3)
+    x, w13 = randn(g, N, H), randn(g, len(HEIGHTS), 2 * F, H, scale=H ** -0.5)
+    act = torch.empty((N, F), dtype=BF16, device="cuda")
+    q, sc = torch.empty((N, 2 * F), dtype=U8, device="cuda"), torch.empty((N, 2 * F // 128), device="cuda")
+    xd, wd, od = gpu(x, w13, off)
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=od), xd, N, wd, F, act, q, sc, ws)
+    gu = per_expert(off, lambda e, s: x[s].double() @ w13[e].double().T, None)
+    acc = H * U23 * per_expert(off, lambda e, s: x[s].double().abs() @ w13[e].double().abs().T, None)
+    gate, up, s, ref = silu_parts(gu, F)
+    b = act_bound(gate, up, s, ref, acc[:, :F], acc[:, F:])
+    check(act, ref, b + HALF_BF16 * (ref.abs() + b), "act")
+    rep = sc.double().cpu().repeat_interleave(128, 1)
+    off_by = acc + 4 * U23 * gu.abs()
+    check(q.cpu().view(F8).double() * rep, gu, off_by + HALF_E4M3 * (gu.abs() + off_by) + 2.0 ** -10 * rep, "checkpoint")
+
+
+@pytest.mark.parametrize("back", [False, True], ids=["nk", "kn"])
+def test_matmul_more_tiles_than_workgroups(back):
+    """Several tiles to a workgroup, of different heights one after the other."""
+    counts = [(37 * e) % 290 for e in range(40)]
+    off, N, shape, ws = by_counts(counts)
+    E, k, n = len(counts), 200, 2056
+    g = torch.Generator().manual_seed(5)
+    x, wt = randn(g, N, k), randn(g, *((E, k, n) if back else (E, n, k)), scale=k ** -0.5)
+    y = torch.full((N, n), 7.0, dtype=BF16, device="cuda")
+    xd, wd, od = gpu(x, wt, off)
+    ep.ep_expert_matmul(shape, dict(expert_offsets=od), xd, N, k, wd, n,
+                        ep.EP_WEIGHT_KN if back else ep.EP_WEIGHT_NK, y, ws)
+    m = wt.double() if back else wt.double().transpose(1, 2)
+    ref = per_expert(off, lambda e, s: x[s].double() @ m[e], None)
+    acc = k * U23 * per_expert(off, lambda e, s: x[s].double().abs() @ m[e].abs(), None)
+    check(y, ref, acc + HALF_BF16 * (ref.abs() + acc), "y")
+
+
 SWIGLU = [
     (1, 1, 1, 8, 128, {}),
     (3, 2, 5, 72, 128, {}),
@@ -360,6 +426,110 @@ def test_wgrad(case, fp8, wide):
         outer = dy[N].double().unsqueeze(1) * x[N].unsqueeze(0)
         both = mag[0] + outer.abs()
         check((more.double() - dw.double())[0], outer, 2 * (N + 1) * U23 * both, "difference by one row")
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["rows", "fp8rows"])
+def test_wgrad_many_tiles_of_all_lengths(fp8, wide):
+    """Several tiles to a workgroup: experts without rows, of one row, of 1, 2, 3
+    and more steps of 64 rows, one after the other in one stream."""
+    counts = [0, 1, 0, 63, 64, 65, 128, 0, 0, 129, 192, 200, 5, 300, 0, 1, 256, 70, 10, 0]
+    off, N, shape, ws = by_counts(counts)
+    E, n, k = len(counts), 1032, 768
+    g = torch.Generator().manual_seed(7)
+    dy = randn(g, N, n)
+    if fp8:
+        q, sc = checkpoint(g, N, k // 2)
+        x, rows = q.double() * sc.double().repeat_interleave(128, 1), dict(x_fp8=q.cuda(), x_scales=sc.cuda())
+    else:
+        xb = randn(g, N, k)
+        x, rows = xb.double(), dict(x=xb.cuda())
+    dw = torch.full((E, n, k), 7.0, dtype=F32 if wide else BF16, device="cuda")
+    dyd, od = gpu(dy, off)
+    ep.ep_expert_wgrad(shape, dict(expert_offsets=od), dyd, N, n, rows, k, dw,
+                       ep.EP_GRAD_F32 if wide else ep.EP_GRAD_BF16, ws)
+    parts = [slice(int(off[e]), int(off[e + 1])) for e in range(E)]
+    for e, p in enumerate(parts):
+        ref = dy[p].double().T @ x[p]
+        mag = dy[p].double().abs().T @ x[p].abs()
+        acc = counts[e] * U23 * mag + (HALF_BF16 * mag * (1 + counts[e] * U23) + U23 * mag if fp8 else 0)
+        check(dw[e], ref, acc if wide else acc + HALF_BF16 * (ref.abs() + acc), f"dw of expert {e}")
+
+
+def test_wgrad_of_one_expert_repeats_bit_for_bit():
+    """No order of summation depends on timing."""
+    off, N, shape, ws = by_counts([400, 0, 333])
+    g = torch.Generator().manual_seed(8)
+    dy, x = randn(g, N, 520).cuda(), randn(g, N, 264).cuda()
+    od = off.cuda()
+    outs = []
+    for _ in range(3):
+        dw = torch.empty((3, 520, 264), device="cuda")
+        ep.ep_expert_wgrad(shape, dict(expert_offsets=od), dy, N, 520, dict(x=x), 264, dw, ep.EP_GRAD_F32, ws)
+        outs.append(dw)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def near(got, ref, mag, n, what):
+    """One rounding to bf16 and n products summed in 32 bits."""
+    check(got, ref.cpu(), (n * U23 * mag + HALF_BF16 * (ref.abs() + n * U23 * mag)).cpu(), what)
+
+
+def test_offsets_past_32_bits():
+    """Rows, weights and results behind the first 4 GiB of their arrays."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, n = 8192, 64
+    counts = [290_000, 40]
+    off = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    N = sum(counts)
+    x = torch.randn((N, k), generator=g, device="cuda", dtype=BF16)  # 4.75 GB
+    w = torch.randn((2, n, k), generator=g, device="cuda", dtype=BF16)
+    shape = ep.make_shape(8, k, 1, 2, 1)
+    ws = ep.alloc_workspace(shape)
+    y = torch.empty((N, n), dtype=BF16, device="cuda")
+    L = dict(expert_offsets=off)
+    ep.ep_expert_matmul(shape, L, x, N, k, w, n, ep.EP_WEIGHT_NK, y, ws)
+    for e, rows in ((0, slice(289_900, 290_000)), (1, slice(290_000, N))):
+        a, b = x[rows].double(), w[e].double()
+        near(y[rows], a @ b.T, a.abs() @ b.abs().T, k, "rows")
+    # Results past 4 GiB: the other way round.
+    back = torch.empty((N, k), dtype=BF16, device="cuda")
+    ep.ep_expert_matmul(shape, L, y, N, n, w, k, ep.EP_WEIGHT_KN, back, ws)
+    a, b = y[290_000:].double(), w[1].double()
+    near(back[290_000:], a @ b, a.abs() @ b.abs(), n, "results")
+    # The gradient of the last expert reads only its rows.
+    dw = torch.empty((2, n, k), device="cuda")
+    ep.ep_expert_wgrad(shape, L, y, N, n, dict(x=x), k, dw, ep.EP_GRAD_F32, ws)
+    a, b = y[290_000:].double(), x[290_000:].double()
+    check(dw[1], (a.T @ b).cpu(), (40 * U23 * (a.abs().T @ b.abs())).cpu(), "dw")
+    del x, y, back, dw
+    # Weights past 4 GiB, of the products and of the few-token layer.
+    E, H, F = 90, 4096, 4096
+    w13 = torch.randn((E, 2 * F, H), generator=g, device="cuda", dtype=BF16).mul_(H ** -0.5)  # 6 GB
+    w2 = torch.randn((E, H, F), generator=g, device="cuda", dtype=BF16).mul_(F ** -0.5)
+    T = 3
+    xt = torch.randn((T, H), generator=g, device="cuda", dtype=BF16)
+    idx = torch.tensor([[E - 1], [E - 2], [0]], device="cuda")
+    wt = torch.ones((T, 1), device="cuda")
+    s2 = ep.make_shape(T, H, 1, E, 1)
+    out = torch.empty((T, H), dtype=BF16, device="cuda")
+    ep.ep_moe_few(s2, dict(x=xt, topk_idx=idx, topk_weights=wt), dict(F=F, w13=w13, w2=w2), out,
+                  ep.alloc_few_workspace(s2, F))
+    act = torch.empty((1, F), dtype=BF16, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = 1
+    ep.ep_expert_swiglu(s2, dict(expert_offsets=off), xt[:1].contiguous(), 1, w13, F, act, None, None,
+                        ep.alloc_workspace(s2))
+    for t in range(T):
+        e = int(idx[t, 0])
+        ref, bound = few_reference(xt[t:t + 1].cpu(), w13[e:e + 1].cpu(), w2[e:e + 1].cpu(),
+                                   torch.zeros((1, 1), dtype=torch.int64), wt[:1].cpu(), F)
+        check(out[t:t + 1], ref, bound, f"token {t}")
+    gu = xt[:1].double() @ w13[E - 1].double().T
+    acc = H * U23 * (xt[:1].double().abs() @ w13[E - 1].double().abs().T)
+    gate, up, sg, ref = silu_parts(gu, F)
+    b = act_bound(gate, up, sg, ref, acc[:, :F], acc[:, F:])
+    check(act, ref.cpu(), (b + HALF_BF16 * (ref.abs() + b)).cpu(), "act")
 
 
 FEW = [
@@ -674,3 +844,45 @@ def test_calls_run_on_the_given_stream():
     st.synchronize()
     for n in ("out", "dx", "dw13", "dw2", "d_w"):
         assert torch.equal(b[n], ref[n]), n
+
+
+def test_calls_at_once():
+    """Two streams at once: the few-token layer on a workspace each, the
+    products on one workspace between them (they use its error words alone)."""
+    T, H, F, E, K = 32, 512, 384, 12, 4
+    idx, w, x, dout, w13, w2 = gpu(*layer_case(T, H, F, E, K))
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_workspace(shape)
+    counts = [50, 0, 300, 7, 90, 1, 256, 33, 64, 12, 100, 5]
+    off, N, _, _ = by_counts(counts)
+    off = off.cuda()
+    rows = randn(torch.Generator().manual_seed(3), N, H).cuda()
+    d = randn(torch.Generator().manual_seed(4), N, F).cuda()
+    L = dict(expert_offsets=off)
+
+    def work(few_ws):
+        out = torch.empty((T, H), dtype=BF16, device="cuda")
+        ep.ep_moe_few(shape, dict(x=x, topk_idx=idx, topk_weights=w), dict(F=F, w13=w13, w2=w2), out, few_ws)
+        act = torch.empty((N, F), dtype=BF16, device="cuda")
+        q, sc = torch.empty((N, 2 * F), dtype=U8, device="cuda"), torch.empty((N, 2 * F // 128), device="cuda")
+        ep.ep_expert_swiglu(shape, L, rows, N, w13, F, act, q, sc, ws)
+        y = torch.empty((N, H), dtype=BF16, device="cuda")
+        ep.ep_expert_matmul(shape, L, act, N, F, w2, H, ep.EP_WEIGHT_NK, y, ws)
+        dw = torch.empty((E, F, H), device="cuda")
+        ep.ep_expert_wgrad(shape, L, d, N, F, dict(x=rows), H, dw, ep.EP_GRAD_F32, ws)
+        return out, act, q, sc, y, dw
+
+    ref = work(ep.alloc_few_workspace(shape, F))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [ep.alloc_few_workspace(shape, F) for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for st, few_ws in zip(streams, spaces):
+            with torch.cuda.stream(st):
+                got.append(work(few_ws))
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, ref):
+            assert torch.equal(a.view(U8), b.view(U8))
