@@ -126,7 +126,7 @@ hipError_t launch_expert_wgrad(const ep_shape& s, const ep_layout& L, const uint
                                int dtype, char* ws, hipStream_t st);
 
 // Workspace of the few-token layer: error words, the number of used experts
-// and their ids, (expert, token) routes, the inner activations [T*K][F] bf16.
+// and their ids, (expert, token) routes, the inner activations [T*K][2][F] bf16.
 struct WsFew {
     size_t used, routes, act, total;
 };

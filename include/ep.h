@@ -539,8 +539,10 @@ size_t ep_few_workspace_bytes(const ep_shape *shape, int32_t F);
 /* The whole expert layer for at most EP_FEW_MAX_TOKENS tokens (decoding),
  * without layout, dispatch and combine:
  *   out[t] = bf16_rne(sum over the distinct experts e of t's lanes of
- *            w * W2[e] bf16_rne(silu(g) * u)),  w = the sum of the weights of
- *            t's lanes with expert e, [g; u] = W13[e] x[t]
+ *            w * W2[e] (silu(g) * u)),  w = the sum of the weights of t's
+ *            lanes with expert e, [g; u] = W13[e] x[t]
+ * silu(g) * u enters the second product as two bf16 values, itself rounded and
+ * what that leaves (off by 2^-16 of it at most, where |silu(g) * u| > 1e-33).
  * tokens: x, topk_idx and topk_weights required. A token without a valid lane
  * gets zeros. An expert's non-finite results reach only its own tokens. Starts
  * a pass: clears error word 0, then sets EP_DEVERR_EXPERT_ID for ids < -1 or

@@ -566,7 +566,7 @@ def few_reference(x, w13, w2, idx, w, F):
         acc = H * U23 * (xd[ts].abs() @ a.abs().T)
         gate, up, s, act = silu_parts(gu, F)
         da = act_bound(gate, up, s, act, acc[:, :F], acc[:, F:])
-        da = da + HALF_BF16 * (act.abs() + da)
+        da = da + 2.0 ** -16 * (act.abs() + da)  # two bf16 values: the rest is rounded, 2^-8 of 2^-8
         we = (w.double() * hit).sum(1)[ts].unsqueeze(1)
         wabs = (w.double().abs() * hit).sum(1)[ts].unsqueeze(1)
         out[ts] += we * (act @ b2.T)
