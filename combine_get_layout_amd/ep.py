@@ -196,13 +196,22 @@ def _ws(ws):
     return _ptr(ws, "workspace"), ws.numel() * ws.element_size()
 
 
+_LAYOUT_BYTES = dict(
+    tokens_per_expert=lambda s: 4 * s.E, tokens_per_rank=lambda s: 4 * s.R,
+    tokens_per_group=lambda s: 4 * s.G, expert_offsets=lambda s: 4 * (s.E + 1),
+    rank_offsets=lambda s: 4 * (s.R + 1), group_offsets=lambda s: 4 * (s.G + 1),
+    is_token_in_rank=lambda s: s.T * s.R, is_token_in_group=lambda s: s.T * s.G,
+    slot=lambda s: 4 * s.T * s.K, group_slot=lambda s: 4 * s.T * s.K,
+    expert_slot=lambda s: 4 * s.T * s.K)
+
+
 def _layout_struct(shape: ep_shape, layout: dict) -> ep_layout:
-    T, K, E, R, G = shape.T, shape.K, shape.E, shape.R, shape.G
-    need = dict(tokens_per_expert=4 * E, tokens_per_rank=4 * R, tokens_per_group=4 * G,
-                expert_offsets=4 * (E + 1), rank_offsets=4 * (R + 1), group_offsets=4 * (G + 1),
-                is_token_in_rank=T * R, is_token_in_group=T * G, slot=4 * T * K,
-                group_slot=4 * T * K, expert_slot=4 * T * K)
-    return ep_layout(*[_ptr(layout.get(n), n, need[n]) for n in LAYOUT_FIELDS])
+    L = ep_layout()
+    for n in LAYOUT_FIELDS:
+        t = layout.get(n)
+        if t is not None:
+            setattr(L, n, _ptr(t, n, _LAYOUT_BYTES[n](shape)))
+    return L
 
 
 def _seg_of(tokens: dict) -> int:
