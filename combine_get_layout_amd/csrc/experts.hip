@@ -40,8 +40,8 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // rows that a wave's transposing read touches then cover the banks evenly.
 //
 // Steps of 64 rather than 32 indices, so that every copy takes whole 128-byte
-// lines: with 64-byte pieces the copies filled the L2's requests (1,060
-// against 1,120 TFLOP/s at 32 experts of 1,024 x 7168 x 4096, else alike).
+// lines: with 64-byte pieces the copies filled the L2's requests (6% less at 32
+// experts of 1,024 x 7168 x 4096, else alike).
 __device__ __forceinline__ int pairs_swizzle(int r) { return ((r >> 1) & 1) | ((r >> 3) & 3) << 1; }
 __device__ __forceinline__ int cols_swizzle(int k) { return (k & 3) | ((k >> 3) & 3) << 2; }
 
@@ -314,14 +314,24 @@ __device__ __forceinline__ void first_steps(LA& la, LB& lb, char* lds) {
 // slot of step s - 1), in the second half those of the first operand's (into
 // the slot of step s, whose last fragments have then been read): one for each
 // four matrix instructions from the half's start, so that they have nearly one
-// and nearly one and a half step's time (a step is 1.1 us) to arrive.
+// and nearly one and a half step's time to arrive.
 //
-// Two forms, by what measured better. `multiply`, a tile of its own: from
-// first_steps, which the caller issues beside the results of the tile before,
-// two steps to a turn of the loop, so that the slots are constants.
-// `multiply_stream`: steps past the tile's last are the next tile's first, to which
-// `next` turns the loaders, so that the copies have no gap between short
-// tiles; the slots go round in registers.
+// Bound: a step of a full tile is 1.08 us of matrix instructions at the 1.9 GHz
+// that the card holds under them, and takes 1.5: 1,390 TFLOP/s at 32 experts of
+// 1,024 x 7168 x 4096, beside 1,580 of a large library product. What is missing
+// are copies that arrive late (all of them from cache: 1,540; neither copies
+// nor LDS reads: 1,665). One workgroup per CU: a second would halve the tiles,
+// and with them the use that is made of what is read.
+//
+// Two forms, by what measured better (TFLOP/s at that size, each on the same
+// card). `multiply`, a tile of its own: from first_steps, which the caller
+// issues beside the results of the tile before, two steps to a turn of the
+// loop, so that the slots are constants: products 1,385 (1,349 streamed), with
+// KN weights 1,408 (1,363). `multiply_stream`: steps past the tile's last are
+// the next tile's first, to which `next` turns the loaders, so that the copies
+// have no gap between short tiles; the slots go round in registers: weight
+// gradients (16 steps a tile) 1,135 (1,098 by tiles of their own), from FP8
+// rows 984 (936).
 template <int MS, int NS, class LA, class LB, class RA, class RB>
 __device__ __forceinline__ void multiply(LA& la, LB& lb, const RA& ra, const RB& rb, int k_dim, char* lds,
                                          f32x4 (&acc)[MS][NS]) {
@@ -451,23 +461,28 @@ struct Tiles {
     }
     __device__ __forceinline__ static int row_tiles(int m) { return (m + kFullRows - 1) / kFullRows; }
 
-    __device__ __forceinline__ void init(const int32_t* offs, int experts, int n_rows, int n) {
+    // Offsets that decrease give no tiles (their number might pass 32 bits).
+    __device__ __forceinline__ void init(const int32_t* offs, int experts, int n_rows, int n, uint32_t* err) {
         offsets = offs, rows = n_rows, n_tiles = n, E = experts;
         per = (E + kWave - 1) / kWave;
         const int lane = lane_id(), e0 = min(E, lane * per), e1 = min(E, e0 + per);
         int count = 0;
+        bool bad = false;
         for (int e = e0; e < e1; ++e) {
             int lo, m;
             bounds(e, lo, m);
             count += row_tiles(m);
+            bad |= offsets[e + 1] < offsets[e];
         }
+        bad = __ballot(bad);
         int sum = count;
         for (int d = 1; d < kWave; d <<= 1) {
             const int v = __shfl_up(sum, d);
             if (lane >= d) sum += v;
         }
         before = sum - count;
-        total = readlane(sum, kWave - 1) * n_tiles;
+        total = bad ? 0 : readlane(sum, kWave - 1) * n_tiles;
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (bad || offsets[E] > rows)) report(err, EP_DEVERR_CAPACITY);
     }
     // The seq-th tile of this workgroup's XCD; false if there is none.
     __device__ __forceinline__ bool find(int seq, Tile& t) const {
@@ -511,10 +526,6 @@ struct MatmulArgs {
     uint32_t* err;
 };
 
-__device__ __forceinline__ void check_rows(const int32_t* offsets, int E, int rows, uint32_t* err) {
-    if (blockIdx.x == 0 && threadIdx.x == 0 && offsets[E] > rows) report(err, EP_DEVERR_CAPACITY);
-}
-
 // The products' loaders, turned to a tile one operand after the other.
 template <bool KN>
 struct MatmulLoaders {
@@ -542,6 +553,10 @@ struct MatmulLoaders {
     }
 };
 // Calls f(waves over rows, sub-tiles of a wave along rows) for a tile height.
+// The matrix instructions of rows that a tile does not have are spared: 32
+// experts of 7168 x 4096 took 312, 335, 355, 374, 401, 860 and 1,582 us with 40,
+// 100, 150, 184, 216, 520 and 1,040 rows, and 336, 369, 391, 401, 415, 986 and
+// 1,668 us with 256-row tiles alone.
 template <int V>
 using Int = std::integral_constant<int, V>;
 template <class F>
@@ -650,9 +665,8 @@ __device__ __forceinline__ void matmul_tile(const MatmulArgs& a, const Tile& t, 
 template <bool KN>
 __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(MatmulArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
-    check_rows(a.offsets, a.E, a.rows, a.err);
     Tiles tiles;
-    tiles.init(a.offsets, a.E, a.rows, (a.n_dim + kTileN - 1) / kTileN);
+    tiles.init(a.offsets, a.E, a.rows, (a.n_dim + kTileN - 1) / kTileN, a.err);
     MatmulLoaders<KN> l = {a};
     l.init();
     Tile t;
@@ -809,9 +823,8 @@ __device__ __forceinline__ void swiglu_tile(const SwigluArgs& a, const Tile& t, 
 template <bool SAVE>
 __global__ __launch_bounds__(kThreads, 2) void swiglu_kernel(SwigluArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
-    check_rows(a.offsets, a.E, a.rows, a.err);
     Tiles tiles;
-    tiles.init(a.offsets, a.E, a.rows, (a.F + 127) / 128);
+    tiles.init(a.offsets, a.E, a.rows, (a.F + 127) / 128, a.err);
     SwigluLoaders l = {a};
     l.init();
     Tile t;
@@ -904,7 +917,7 @@ template <bool FP8, bool F32>
 __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
     constexpr int WN = 4, MS = 8, NS = 4;
-    check_rows(a.offsets, a.E, a.rows, a.err);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.offsets[a.E] > a.rows) report(a.err, EP_DEVERR_CAPACITY);
     const int tiles_k = (a.k_dim + kTileN - 1) / kTileN, tiles_n = (a.n_dim + kFullRows - 1) / kFullRows;
     const int total = a.E * tiles_k * tiles_n, per = (total + 7) / 8;
     const int first = (blockIdx.x % 8) * per, mine = min(max(total - first, 0), per);

@@ -4,6 +4,9 @@
 // With s = 1 / (1 + exp(-g)), d the gradient of the expert's output taken back
 // through W2 (before the routing weight w) and a = g s u:
 //   d_g = w d u s (1 + g (1 - s)),  d_u = w d g s,  act_w = w a,  d_w = <d, a>.
+//
+// Bound: one pass over the row, 10 F bytes and its scales. 32,768 rows of F = 2048
+// (676 MB): 129 us, 5.2 TB/s, beside 4.9 of a large copy.
 #include "ep_internal.h"
 #include "ep_mfma.h"
 
@@ -24,7 +27,8 @@ struct SwigluGradArgs {
     uint32_t* err;
 };
 
-// One wave per (token, lane): its row in passes of 512 values, 8 per thread.
+// One wave per (token, lane): its row in passes of 512 values, 8 per thread, so
+// that the row's sum <d, a> needs no atomics and no second launch.
 __global__ __launch_bounds__(kBlockThreads) void swiglu_grad_kernel(SwigluGradArgs a) {
     const int lane = lane_id();
     const int64_t n = (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();

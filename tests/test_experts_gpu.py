@@ -886,3 +886,28 @@ def test_calls_at_once():
     for g in got:
         for a, b in zip(g, ref):
             assert torch.equal(a.view(U8), b.view(U8))
+
+
+def test_offsets_that_decrease():
+    """The products compute nothing and say so; weight gradients stay inside the arrays."""
+    N, k, n, F = 48, 64, 72, 128
+    shape = ep.make_shape(N, k, 1, 3, 1)
+    g = torch.Generator().manual_seed(4)
+    x, w, w13 = gpu(randn(g, N, k), randn(g, 3, n, k), randn(g, 3, 2 * F, k))
+    off = torch.tensor([0, 40, 16, 48], dtype=torch.int32, device="cuda")
+    ws = ep.alloc_workspace(shape)
+    y = torch.full((N, n), 7.0, dtype=BF16, device="cuda")
+    act = torch.full((N, F), 7.0, dtype=BF16, device="cuda")
+    for call in (lambda: ep.ep_expert_matmul(shape, dict(expert_offsets=off), x, N, k, w, n, ep.EP_WEIGHT_NK, y, ws),
+                 lambda: ep.ep_expert_swiglu(shape, dict(expert_offsets=off), x, N, w13, F, act, None, None, ws)):
+        ep.ep_clear_errors(ws)
+        call()
+        assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY
+    assert (y == 7.0).all() and (act == 7.0).all()
+    dy = randn(g, N, n)
+    dw = torch.empty((3, n, k), dtype=F32, device="cuda")
+    ep.ep_expert_wgrad(shape, dict(expert_offsets=off), dy.cuda(), N, n, dict(x=x), k, dw, ep.EP_GRAD_F32, ws)
+    assert (dw[1] == 0).all()
+    for e, s in ((0, slice(0, 40)), (2, slice(16, 48))):
+        a, b = dy[s].double(), x[s].cpu().double()
+        check(dw[e], a.T @ b, 48 * U23 * (a.abs().T @ b.abs()), "dw")
