@@ -282,11 +282,13 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_up_kernel(Fe
 }
 
 // Second launch: workgroup x computes 16 values of h for every token. Unit u =
-// (used expert, span of 256 values of f); the 8 waves take the units in turn. A
-// unit's 16 weight rows and its expert's tokens' activations are loaded at once
-// (the routes, which say where the latter are, a unit ahead), multiplied into
-// temporaries and added, weighted, to the wave's sums of those tokens in LDS:
-// an expert's infinities or NaN stay with its own tokens, and the matrix
+// (used expert, span of 256 values of f); each of the 8 waves takes a run of
+// them. A unit's 16 weight rows and its expert's tokens' activations are loaded at once
+// (the routes, which say where the latter are, a unit ahead) and multiplied. The
+// spans of an expert add up in registers while it has one tile of tokens, and
+// are then added, weighted, to the wave's sums of those tokens in LDS (a run of
+// units rather than every 8th, each added there at once, took 2 to 6% off both
+// launches together): an expert's infinities or NaN stay with its own tokens, and the matrix
 // instruction's 16 rows are 8 tokens of the expert, however many others there
 // are, as rounded values (rows 0 to 7) and as what those leave (rows 8 to 15).
 // Rounded values alone, 16 tokens at a time, were 1 to 2% faster up to 64 tokens
@@ -337,13 +339,15 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
             }
         }
     };
-    int u = wave, entry = 0;
+    int u = (int)((int64_t)units * wave / kFewWaves), entry = 0;
+    const int end = (int)((int64_t)units * (wave + 1) / kFewWaves);
     Route route = {0, 0.f};
-    if (u < units) {
+    float acc[4] = {};
+    if (u < end) {
         entry = __builtin_amdgcn_readfirstlane(a.used[1 + u / spans]);
         route = load_route(u / spans, entry >> 16, 0);
     }
-    while (u < units) {
+    while (u < end) {
         const int rank = u / spans, span = u % spans, tokens = entry >> 16;
         const int64_t e = entry & 0xFFFF;
         u32x4 w[kLoads], v[8];
@@ -362,10 +366,11 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
             s1 = __shfl(sv, i + 16);
         }
         load_act(__shfl(route.id, i & 7), (i & 7) < tokens, span, v);
-        const int next = u + kFewWaves;
-        int next_entry = 0;
+        const int next = u + 1;
+        int next_entry = entry;
         Route next_route = route;
-        if (next < units) {
+        const bool last = next == end || span + 1 == spans;  // of the expert's spans here
+        if (last && next < end) {
             next_entry = __builtin_amdgcn_readfirstlane(a.used[1 + next / spans]);
             next_route = load_route(next / spans, next_entry >> 16, 0);
         }
@@ -390,12 +395,15 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
                 load_act(__shfl(route.id, n), t0 + 8 + (i & 7) < tokens, span, v);
             }
 #pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += FP8 ? fmaf(s1, c[0][1][j], s0 * c[0][0][j]) : c[0][0][j];
+            if (tokens <= 8 && !last) break;
+#pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = (t0 & 8) + (q & 1) * 4 + j;
                 const int id = __shfl(now.id, n);
                 const float weight = __shfl(now.w, n);
-                float dot = FP8 ? fmaf(s1, c[0][1][j], s0 * c[0][0][j]) : c[0][0][j];
-                dot += __shfl_xor(dot, 32);  // rows 8 to 15: the rests' products
+                const float dot = acc[j] + __shfl_xor(acc[j], 32);  // rows 8 to 15: the rests' products
+                acc[j] = 0.f;
                 if (q < 2 && t0 + q * 4 + j < tokens) {
                     float* sum = mine + (id >> 16) * 17 + i;
                     *sum = fmaf(weight, dot, *sum);
