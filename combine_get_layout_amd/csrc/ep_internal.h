@@ -126,9 +126,10 @@ hipError_t launch_expert_wgrad(const ep_shape& s, const ep_layout& L, const uint
                                int dtype, char* ws, hipStream_t st);
 
 // Workspace of the few-token layer: error words, the number of used experts
-// and their ids, (expert, token) routes, the inner activations [T*K][2][F] bf16.
+// and their ids, (expert, token) routes, the inner activations [T*K][2][F] bf16,
+// counts and parts of the output of workgroups that share some of it.
 struct WsFew {
-    size_t used, routes, act, total;
+    size_t used, routes, act, joined, part, total;
 };
 WsFew ws_few(const ep_shape& s, int F);
 hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_experts& x, uint16_t* out, char* ws,

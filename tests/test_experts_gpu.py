@@ -546,6 +546,7 @@ FEW = [
     (128, 128, 128, 4096, 4, {}),        # the largest number of experts
     (100, 64, 48, 3, 64, dict(repeat=True)),
     (5, 1032, 712, 6, 6, {}),
+    (103, 512, 1024, 10, 8, {}),         # workgroups that share outputs, many tokens to each expert
 ]
 
 
@@ -911,3 +912,31 @@ def test_offsets_that_decrease():
     for e, s in ((0, slice(0, 40)), (2, slice(16, 48))):
         a, b = dy[s].double(), x[s].cpu().double()
         check(dw[e], a.T @ b, 48 * U23 * (a.abs().T @ b.abs()), "dw")
+
+
+def test_few_repeats_bit_for_bit():
+    """Workgroups that share outputs finish in any order; eager calls and replays agree."""
+    T, H, F, E, K = 40, 264, 1032, 12, 4
+    g = torch.Generator().manual_seed(8)
+    idx, w = routing(T, K, E, 3)
+    x, w13, w2 = gpu(randn(g, T, H), randn(g, E, 2 * F, H, scale=H ** -0.5), randn(g, E, H, F, scale=F ** -0.5))
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_few_workspace(shape, F).fill_(0xAB)
+    ep.ep_clear_errors(ws)
+    tokens = dict(x=x, topk_idx=idx.cuda(), topk_weights=w.cuda())
+    out = torch.empty((T, H), dtype=BF16, device="cuda")
+    ep.ep_moe_few(shape, tokens, dict(F=F, w13=w13, w2=w2), out, ws)
+    first = out.clone()
+    ref, bound = few_reference(x.cpu(), w13.cpu(), w2.cpu(), idx, w, F)
+    check(first, ref, bound, "out")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ep.ep_moe_few(shape, tokens, dict(F=F, w13=w13, w2=w2), out, ws)
+    for n in range(20):
+        out.fill_(7.0)
+        if n % 2:
+            graph.replay()
+        else:
+            ep.ep_moe_few(shape, tokens, dict(F=F, w13=w13, w2=w2), out, ws)
+        assert torch.equal(out, first), n
+    assert ep.ep_check_errors(ws) == 0
