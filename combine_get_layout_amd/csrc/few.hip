@@ -502,16 +502,19 @@ hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_exper
                        reinterpret_cast<int*>(ws + l.used), reinterpret_cast<Route*>(ws + l.routes),
                        reinterpret_cast<uint16_t*>(ws + l.act), reinterpret_cast<int*>(ws + l.joined),
                        reinterpret_cast<float*>(ws + l.part), down_splits(s, x.F)};
-    const int many = s.T > 16;
     const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K);
-    // Values of f per workgroup of the first launch (x 2 = weight rows). Above 16
-    // tokens 64, and two token tiles at a time: the tokens' rows, which then
-    // weigh, are read half as often (64 tokens, 64 experts of 4096 x 1536: 548 us,
-    // with 32: 576; one token tile and 32: 571, but at 128 tokens 702 against 607;
-    // all before the second launch took its values in two parts).
-    // Up to 16 tokens 32, or 16 where that gives fewer than 1,024 workgroups, which
-    // leave the memory idle (one token, top-8 of 4096 x 1536: 66 us with 16, 75
-    // with 32; 13 tokens, 33 experts of 2056 x 712: 63.5 and 70).
+    // Values of f per workgroup of the first launch (x 2 = weight rows), by the
+    // tokens that an expert has on the average. 64, and two token tiles at a time,
+    // where these are more than 16, or more than 4 and there are 1,024 workgroups:
+    // the tokens' rows, which then weigh, are read half as often (64 tokens, top-8
+    // of 64 experts of 4096 x 1536: 558 us, with 32 and one tile 581; 128 tokens: 669
+    // and 766; but 32 tokens, FP8 weights of 7168 x 2048: 710 and 696; 106 tokens,
+    // top-3 of 63 experts of 1536 x 896: 96 and 87; 33 tokens, top-4 of 39 experts of
+    // 664 x 504: 31.5 and 26.5). Else 32, or 16 where that gives fewer than 1,024
+    // workgroups, which leave the memory idle (one token, top-8 of 4096 x 1536: 66
+    // us with 16, 75 with 32; 13 tokens, 33 experts of 2056 x 712: 63.5 and 70).
+    const int64_t lanes = (int64_t)s.T * s.K, wide = (x.F + 63) / 64 * experts;
+    const bool many = s.T > 16 && (lanes > 16 * experts || (wide >= 1024 && lanes > 4 * experts));
     const bool narrow = (int64_t)((x.F + 31) / 32) * experts < 1024;
     const int cols = many ? 64 : narrow ? 16 : 32;
     const dim3 up((x.F + cols - 1) / cols, (unsigned)experts);
