@@ -6,11 +6,12 @@
 //
 // Bound: the used experts' weights are read once from HBM; every other array
 // is small and stays in L2. One token, top-8 of 64 experts of 7168 x 2048: 89 +
-// 52 us for 470 + 235 MB (5.3 and 4.5 TB/s, beside 4.9 of a large copy). 32
-// tokens of the same with FP8 weights: 428 + 293 us for 1.91 + 0.96 GB (4.5 and
-// 3.3 TB/s): the second launch has one unit's loads at a time in flight per
-// wave, and with registers for two (a third of the waves less) it was slower.
-// The smallest calls are bound by the launches: 4.4 + 4.1 us on the GPU for one
+// 50 us for 470 + 235 MB (5.3 and 4.7 TB/s, beside 4.9 of a large copy). 32
+// tokens of the same with FP8 weights: 412 + 277 us for 1.94 + 0.97 GB (4.7 and
+// 3.5 TB/s): the second launch has one unit's loads at a time in flight per
+// wave, and with registers for more (a third of the waves less) it was slower;
+// loads past the caches cost 18%, as a line is read in two halves.
+// The smallest calls are bound by the launches: 4.4 + 4.3 us on the GPU for one
 // token through 2 experts of 256 x 512.
 #include <algorithm>
 
