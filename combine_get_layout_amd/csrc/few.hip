@@ -25,7 +25,10 @@ constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / kWave;
 constexpr int kDownCols = 16;  // values of h per workgroup of the second launch
 constexpr int kDownSpan = 256; // contracted values per unit of work of the second launch
-constexpr int kDownGroups = 512;  // workgroups that fill the chip, two per CU
+// Workgroups of the second launch where they share outputs, two per CU: 106 tokens,
+// top-3 of 63 experts of 1536 x 896 take 87 us both launches together (256: 95);
+// 46 tokens, top-6 of 62 experts of 896 x 640 49 (1024: 56).
+constexpr int kDownGroups = 512;
 
 // One token of a used expert: token << 16 | row of its inner activations (token
 // * K + its first lane with that expert), and the sum of its lanes' weights.
