@@ -917,7 +917,6 @@ template <bool FP8, bool F32>
 __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes];
     constexpr int WN = 4, MS = 8, NS = 4;
-    if (blockIdx.x == 0 && threadIdx.x == 0 && a.offsets[a.E] > a.rows) report(a.err, EP_DEVERR_CAPACITY);
     const int tiles_k = (a.k_dim + kTileN - 1) / kTileN, tiles_n = (a.n_dim + kFullRows - 1) / kFullRows;
     const int total = a.E * tiles_k * tiles_n, per = (total + 7) / 8;
     const int first = (blockIdx.x % 8) * per, mine = min(max(total - first, 0), per);
@@ -947,6 +946,11 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     l.start_a(now);
     l.start_b(now);
     first_steps(l.a, l.b, lds);
+    if (blockIdx.x == 0) {  // has a tile always; looks the offsets over while its first copies arrive
+        bool bad = a.offsets[a.E] > a.rows;
+        for (int e = threadIdx.x; e < a.E; e += kThreads) bad |= a.offsets[e + 1] < a.offsets[e];
+        if (__ballot(bad) && lane_id() == 0) report(a.err, EP_DEVERR_CAPACITY);
+    }
     wait_copies<0>();
     barrier_only();
     Ring ring = first_ring();

@@ -940,3 +940,66 @@ def test_few_repeats_bit_for_bit():
             ep.ep_moe_few(shape, tokens, dict(F=F, w13=w13, w2=w2), out, ws)
         assert torch.equal(out, first), n
     assert ep.ep_check_errors(ws) == 0
+
+
+def cleared(shape):
+    ws = ep.alloc_workspace(shape)
+    ep.ep_clear_errors(ws)
+    return ws
+
+
+# Offsets that no layout gives, over 48 rows: a decrease, one behind which the last is
+# in range, a last one past the rows (alone, and with an inner one).
+BAD_OFFSETS = [(0, 40, 16, 48), (0, 60, 50, 48), (0, 60, 40, 40), (0, 20, 40, 49), (0, 48, 52, 60)]
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["rows", "fp8rows"])
+@pytest.mark.parametrize("offs", BAD_OFFSETS, ids=str)
+def test_wgrad_reports_bad_offsets(offs, fp8, wide):
+    """The error is set; each expert's gradient is that of its range, cut to the arrays."""
+    N, n, k = 48, 72, 128
+    shape = ep.make_shape(N, 128, 1, 3, 1)
+    g = torch.Generator().manual_seed(4)
+    dy = randn(g, N, n)
+    if fp8:
+        q, sc = checkpoint(g, N, k // 2)
+        x, rows = q.double() * sc.double().repeat_interleave(128, 1), dict(x_fp8=q.cuda(), x_scales=sc.cuda())
+    else:
+        xb = randn(g, N, k)
+        x, rows = xb.double(), dict(x=xb.cuda())
+    dyd = dy.cuda()
+    ws = cleared(shape)
+    dw = torch.full((3, n, k), 7.0, dtype=F32 if wide else BF16, device="cuda")
+    call = lambda o: ep.ep_expert_wgrad(shape, dict(expert_offsets=torch.tensor(o, dtype=torch.int32, device="cuda")),
+                                        dyd, N, n, rows, k, dw, ep.EP_GRAD_F32 if wide else ep.EP_GRAD_BF16, ws)
+    call(offs)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY
+    for e in range(3):
+        lo = min(offs[e], N)
+        s = slice(lo, min(max(offs[e + 1], lo), N))
+        a, b = dy[s].double(), x[s]
+        mag = a.abs().T @ b.abs()
+        acc = 48 * U23 * mag + (HALF_BF16 * mag * (1 + 48 * U23) + U23 * mag if fp8 else 0)
+        check(dw[e], a.T @ b, acc if wide else acc + HALF_BF16 * ((a.T @ b).abs() + acc), f"dw of expert {e}")
+    ep.ep_clear_errors(ws)
+    call((0, 20, 20, 48))
+    assert ep.ep_check_errors(ws) == 0
+
+
+def test_wgrad_reports_bad_offsets_of_many_experts():
+    """A decrease anywhere among more experts than a workgroup has threads."""
+    E, N, n, k = 1500, 64, 8, 8
+    shape = ep.make_shape(N, 128, 1, E, 1)
+    g = torch.Generator().manual_seed(4)
+    dy, x = gpu(randn(g, N, n), randn(g, N, k))
+    dw = torch.empty((E, n, k), dtype=BF16, device="cuda")
+    ws = cleared(shape)
+    for at in (None, 1, 511, 512, 513, 1024, E - 1):
+        off = torch.full((E + 1,), 32, dtype=torch.int32)
+        off[0] = 0
+        if at is not None:
+            off[at] = 33
+        ep.ep_clear_errors(ws)
+        ep.ep_expert_wgrad(shape, dict(expert_offsets=off.cuda()), dy, N, n, dict(x=x), k, dw, ep.EP_GRAD_BF16, ws)
+        assert ep.ep_check_errors(ws) == (0 if at is None else ep.EP_DEVERR_CAPACITY), at
