@@ -974,12 +974,12 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
 // the 8 XCDs.
 template <class Args>
 hipError_t launch_tiles(void (*kernel)(Args), int64_t tiles, const Args& a, hipStream_t st) {
-    if (tiles <= 0) return hipSuccess;
     LaunchInfo info;
     hipError_t e = launch_info(st, reinterpret_cast<const void*>(kernel), kThreads, &info);
     if (e != hipSuccess) return e;
     const int64_t most = std::max(info.cus / 8 * 8, 8);
-    const unsigned grid = (unsigned)std::min(most, (tiles + 7) / 8 * 8);
+    // A call without rows has no tiles and only looks its offsets over.
+    const unsigned grid = (unsigned)std::min(most, std::max<int64_t>(tiles + 7, 8) / 8 * 8);
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }

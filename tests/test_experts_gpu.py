@@ -1003,3 +1003,20 @@ def test_wgrad_reports_bad_offsets_of_many_experts():
         ep.ep_clear_errors(ws)
         ep.ep_expert_wgrad(shape, dict(expert_offsets=off.cuda()), dy, N, n, dict(x=x), k, dw, ep.EP_GRAD_BF16, ws)
         assert ep.ep_check_errors(ws) == (0 if at is None else ep.EP_DEVERR_CAPACITY), at
+
+
+def test_products_without_rows_report_offsets_past_them():
+    E, k, n, F = 3, 64, 72, 128
+    shape = ep.make_shape(8, k, 1, E, 1)
+    g = torch.Generator().manual_seed(4)
+    w, w13 = gpu(randn(g, E, n, k), randn(g, E, 2 * F, k))
+    ws = cleared(shape)
+    calls = [lambda L: ep.ep_expert_matmul(shape, L, None, 0, k, w, n, ep.EP_WEIGHT_NK, None, ws),
+             lambda L: ep.ep_expert_matmul(shape, L, None, 0, n, w, k, ep.EP_WEIGHT_KN, None, ws),
+             lambda L: ep.ep_expert_swiglu(shape, L, None, 0, w13, F, None, None, None, ws)]
+    for offs, want in (((0, 0, 0, 0), 0), ((0, 0, 3, 3), ep.EP_DEVERR_CAPACITY), ((0, 1, 0, 0), ep.EP_DEVERR_CAPACITY)):
+        L = dict(expert_offsets=torch.tensor(offs, dtype=torch.int32, device="cuda"))
+        for i, call in enumerate(calls):
+            ep.ep_clear_errors(ws)
+            call(L)
+            assert ep.ep_check_errors(ws) == want, (offs, i)
