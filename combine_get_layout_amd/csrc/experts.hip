@@ -461,7 +461,8 @@ struct Tiles {
     }
     __device__ __forceinline__ static int row_tiles(int m) { return (m + kFullRows - 1) / kFullRows; }
 
-    // Offsets that decrease give no tiles (their number might pass 32 bits).
+    // Offsets that are negative or decrease give no tiles (of the latter their number
+    // might pass 32 bits).
     __device__ __forceinline__ void init(const int32_t* offs, int experts, int n_rows, int n, uint32_t* err) {
         offsets = offs, rows = n_rows, n_tiles = n, E = experts;
         per = (E + kWave - 1) / kWave;
@@ -472,7 +473,7 @@ struct Tiles {
             int lo, m;
             bounds(e, lo, m);
             count += row_tiles(m);
-            bad |= offsets[e + 1] < offsets[e];
+            bad |= offsets[e] < 0 || offsets[e + 1] < offsets[e];
         }
         bad = __ballot(bad);
         int sum = count;
@@ -948,7 +949,8 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs a) {
     first_steps(l.a, l.b, lds);
     if (blockIdx.x == 0) {  // has a tile always; looks the offsets over while its first copies arrive
         bool bad = a.offsets[a.E] > a.rows;
-        for (int e = threadIdx.x; e < a.E; e += kThreads) bad |= a.offsets[e + 1] < a.offsets[e];
+        for (int e = threadIdx.x; e < a.E; e += kThreads)
+            bad |= a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e];
         if (__ballot(bad) && lane_id() == 0) report(a.err, EP_DEVERR_CAPACITY);
     }
     wait_copies<0>();

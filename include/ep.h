@@ -447,14 +447,15 @@ int ep_source_dispatch_fused(const ep_shape *shape, const ep_sources *sources, c
  * Rows of expert e are [expert_offsets[e], expert_offsets[e+1]) of the given
  * arrays, which hold `rows` rows; rows at and past expert_offsets[E] are
  * neither read nor written, rows >= `rows` are left out and set
- * EP_DEVERR_CAPACITY, and so do offsets that decrease (ep_expert_matmul and
- * ep_expert_swiglu then compute nothing, ep_expert_wgrad sums each expert's
- * own range). An expert may have no rows. Sums are held in 32 bits and rounded
- * once to the output's type (round to nearest even). Matrix dimensions are
- * multiples of 8 up to EP_MAX_DIM; all arrays here need 16 B aligned base
- * pointers, except topk_weights and its gradient (4 B). Outputs must not
- * overlap inputs. Calls that only use the workspace for its error words (all
- * but ep_moe_few) may overlap on one workspace.
+ * EP_DEVERR_CAPACITY, and so do offsets that decrease or are negative
+ * (ep_expert_matmul and ep_expert_swiglu then compute nothing, ep_expert_wgrad
+ * sums the rows that exist of each expert's own range). An expert may have no
+ * rows. Sums are held in 32 bits and rounded once to the output's type (round
+ * to nearest even). Matrix dimensions are multiples of 8 up to EP_MAX_DIM; all
+ * arrays here need 16 B aligned base pointers, except topk_weights and its
+ * gradient (4 B). Outputs must not overlap inputs. Calls that only use the
+ * workspace for its error words (all but ep_moe_few) may overlap on one
+ * workspace.
  *
  * A whole training step of a layer, from these calls:
  *   forward   ep_get_layout, ep_dispatch_expand, ep_expert_swiglu (act and the

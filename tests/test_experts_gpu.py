@@ -1020,3 +1020,24 @@ def test_products_without_rows_report_offsets_past_them():
             ep.ep_clear_errors(ws)
             call(L)
             assert ep.ep_check_errors(ws) == want, (offs, i)
+
+
+def test_negative_offsets_are_bad_ones():
+    """An expert cannot begin before the first row: products compute nothing, all report."""
+    N, k, n, F, E = 48, 64, 72, 128, 3
+    shape = ep.make_shape(N, k, 1, E, 1)
+    g = torch.Generator().manual_seed(4)
+    x, w, w13, dy = gpu(randn(g, N, k), randn(g, E, n, k), randn(g, E, 2 * F, k), randn(g, N, n))
+    ws = cleared(shape)
+    y = torch.full((N, n), 7.0, dtype=BF16, device="cuda")
+    act = torch.full((N, F), 7.0, dtype=BF16, device="cuda")
+    dw = torch.empty((E, n, k), device="cuda")
+    for offs in ((-5, 10, 20, 48), (-3, -2, -1, 48), (-4, -3, -2, -1)):
+        L = dict(expert_offsets=torch.tensor(offs, dtype=torch.int32, device="cuda"))
+        for call in (lambda: ep.ep_expert_matmul(shape, L, x, N, k, w, n, ep.EP_WEIGHT_NK, y, ws),
+                     lambda: ep.ep_expert_swiglu(shape, L, x, N, w13, F, act, None, None, ws),
+                     lambda: ep.ep_expert_wgrad(shape, L, dy, N, n, dict(x=x), k, dw, ep.EP_GRAD_F32, ws)):
+            ep.ep_clear_errors(ws)
+            call()
+            assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY, offs
+    assert (y == 7.0).all() and (act == 7.0).all()
