@@ -261,12 +261,14 @@ __device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, 
                 }
                 const float r = gate / (1.0f + __expf(-gate)) * up;
                 // Two bf16 values for the second product's matrix instruction, the
-                // rounded one and what it leaves (0 where that is no number).
-                const uint32_t hi = f32_to_bf16(r);
-                const float rest = r - __uint_as_float(hi << 16);
+                // rounded one (of a finite value bf16's largest at most) and what it
+                // leaves (nothing of an infinity or NaN).
+                uint32_t hi = f32_to_bf16(r);
+                if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
+                const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
                 uint16_t* act = a.act + (int64_t)sh.scratch[2 + at] * 2 * a.F + f;
                 act[0] = (uint16_t)hi;
-                act[a.F] = (uint16_t)f32_to_bf16(rest == rest ? rest : 0.f);
+                act[a.F] = (uint16_t)f32_to_bf16(rest);
             }
             __syncthreads();
         }

@@ -1041,3 +1041,35 @@ def test_negative_offsets_are_bad_ones():
             call()
             assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY, offs
     assert (y == 7.0).all() and (act == 7.0).all()
+
+
+def few_by_hand(x, w13, w2, F, T, weight=1.0):
+    """ep_moe_few of one expert with the given (mostly zero) matrices."""
+    H = x.shape[1]
+    shape = ep.make_shape(T, H, 1, 1, 1)
+    ws = ep.alloc_few_workspace(shape, F)
+    out = torch.empty((T, H), dtype=BF16, device="cuda")
+    tokens = dict(x=x.cuda(), topk_idx=torch.zeros((T, 1), dtype=torch.int64, device="cuda"),
+                  topk_weights=torch.full((T, 1), weight, device="cuda"))
+    ep.ep_moe_few(shape, tokens, dict(F=F, w13=w13.cuda(), w2=w2.cuda()), out, ws)
+    assert ep.ep_check_errors(ws) == 0
+    return out.double().cpu()
+
+
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_few_inner_values_past_the_largest_bf16(sign, T):
+    """gate = 2^64, up = +-(2^64 - 2^54): silu(gate) * up = +-2^128 (1 - 2^-10) is finite in
+    32 bits and rounds to infinity in bf16; times 2^-100 it is 2^28 (1 - 2^-10), all powers
+    and sums exact but the last rounding."""
+    H, F = 16, 8
+    x = torch.zeros((T, H), dtype=BF16)
+    x[:, 0] = x[:, 1] = 2.0 ** 32
+    w13, w2 = torch.zeros((1, 2 * F, H), dtype=BF16), torch.zeros((1, H, F), dtype=BF16)
+    w13[0, 0, 0] = 2.0 ** 32
+    w13[0, F, 0], w13[0, F, 1] = sign * 2.0 ** 32, -sign * 2.0 ** 22
+    w2[0, :, 0] = 2.0 ** -100
+    ref = torch.full((T, H), sign * 2.0 ** 28 * (1 - 2.0 ** -10), dtype=F64)
+    # exp(-2^64) is 0: silu(gate) is exact; what the two bf16 values leave is 2^-16 of it.
+    b = 2.0 ** -16 * ref.abs()
+    check(few_by_hand(x, w13, w2, F, T), ref, b + HALF_BF16 * (ref.abs() + b), "out")
