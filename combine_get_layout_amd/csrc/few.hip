@@ -425,7 +425,11 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(FewArgs a) {
                 const int n = (t0 & 8) + (q & 1) * 4 + j;
                 const int id = __shfl(now.id, n);
                 const float weight = __shfl(now.w, n);
-                const float dot = acc[j] + __shfl_xor(acc[j], 32);  // rows 8 to 15: the rests' products
+                // Rows 8 to 15: the rests' products. Where the value's is not finite (an
+                // infinite weight) the rest's, of either sign or 0 * infinity, is no part
+                // of the sum.
+                const float rest = __shfl_xor(acc[j], 32);
+                const float dot = __builtin_isfinite(acc[j]) ? acc[j] + rest : acc[j];
                 acc[j] = 0.f;
                 if (q < 2 && t0 + q * 4 + j < tokens) {
                     float* sum = mine + (id >> 16) * 17 + i;

@@ -1073,3 +1073,27 @@ def test_few_inner_values_past_the_largest_bf16(sign, T):
     # exp(-2^64) is 0: silu(gate) is exact; what the two bf16 values leave is 2^-16 of it.
     b = 2.0 ** -16 * ref.abs()
     check(few_by_hand(x, w13, w2, F, T), ref, b + HALF_BF16 * (ref.abs() + b), "out")
+
+
+@pytest.mark.parametrize("F", [8, 264, 512])
+def test_few_keeps_the_sign_of_infinite_second_weights(F):
+    """One infinite W2 entry meets inner values that bf16 holds exactly (their rest is 0),
+    and ones that it rounds up and down (their rest has either sign): the output is the
+    infinity of the value's sign, as the sum's definition says; other outputs stay."""
+    T, H = 11, 16
+    g = torch.Generator().manual_seed(12)
+    x = randn(g, T, H)
+    x[:, 0] = 1.0
+    w13, w2 = randn(g, 1, 2 * F, H, scale=H ** -0.5), randn(g, 1, H, F, scale=F ** -0.5)
+    w13[0, 0], w13[0, F] = 0, 0
+    w13[0, 0, 0], w13[0, F, 0] = 96.0, 0.5  # silu(96) * 0.5 = 48: no rest
+    clean, bound = few_reference(x, w13, w2, torch.zeros((T, 1), dtype=torch.int64), torch.full((T, 1), 0.5), F)
+    w2[0, 3, 0], w2[0, 4, F - 1], w2[0, 5, 2] = float("inf"), float("-inf"), float("inf")
+    out = few_by_hand(x, w13, w2, F, T, weight=0.5)
+    gu = x.double() @ w13[0].double().T
+    act = silu_parts(gu, F)[3]
+    assert (act[:, [0, 2, F - 1]].abs() > 1e-6).all()  # far from zero against the 32-bit sums' error
+    for h, f, v in ((3, 0, 1.0), (4, F - 1, -1.0), (5, 2, 1.0)):
+        assert torch.equal(out[:, h], v * torch.sign(act[:, f]) * float("inf")), h
+    rest = [h for h in range(H) if h not in (3, 4, 5)]
+    check(out[:, rest], clean[:, rest], bound[:, rest], "other outputs")
