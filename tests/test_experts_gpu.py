@@ -1097,3 +1097,94 @@ def test_few_keeps_the_sign_of_infinite_second_weights(F):
         assert torch.equal(out[:, h], v * torch.sign(act[:, f]) * float("inf")), h
     rest = [h for h in range(H) if h not in (3, 4, 5)]
     check(out[:, rest], clean[:, rest], bound[:, rest], "other outputs")
+
+
+def test_swiglu_leaves_out_rows_past_the_capacity():
+    E, H, F, N, have = 3, 64, 128, 50, 33
+    g = torch.Generator().manual_seed(4)
+    x, w13 = randn(g, have, H), randn(g, E, 2 * F, H, scale=H ** -0.5)
+    off = torch.tensor([0, 20, 40, N], dtype=torch.int32)
+    shape = ep.make_shape(N, H, 1, E, 1)
+    ws = cleared(shape)
+    act = torch.empty((have, F), dtype=BF16, device="cuda")
+    xd, wd, od = gpu(x, w13, off)
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=od), xd, have, wd, F, act, None, None, ws)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_CAPACITY
+    cut = off.clamp(max=have)
+    gu = per_expert(cut, lambda e, s: x[s].double() @ w13[e].double().T, None)
+    acc = H * U23 * per_expert(cut, lambda e, s: x[s].double().abs() @ w13[e].double().abs().T, None)
+    gate, up, s, ref = silu_parts(gu, F)
+    b = act_bound(gate, up, s, ref, acc[:, :F], acc[:, F:])
+    check(act, ref, b + HALF_BF16 * (ref.abs() + b), "act")
+
+
+def check_there(got, ref, bound, what):
+    """check, on the device that holds the values (large results)."""
+    over = (got.double() - ref).abs() - bound
+    assert not torch.isnan(over).any(), f"{what}: NaN"
+    assert (over <= 0).all(), f"{what}: {over.max().item():.3g} over its bound"
+
+
+@pytest.mark.parametrize("save", [False, True], ids=["act", "checkpoint"])
+def test_swiglu_more_tiles_than_workgroups(save):
+    """Three tiles to a workgroup, of different heights and experts one after the other:
+    the next tile's first steps arrive while block maxima and results are written."""
+    counts = [(37 * e) % 290 for e in range(40)]
+    H, F = 200, 2176 if save else 2184
+    off, N, shape, ws = by_counts(counts, H)
+    assert sum(-(-c // 256) for c in counts) * -(-F // 128) > 2 * 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((N, H), generator=g, device="cuda").to(BF16)
+    w13 = (torch.randn((len(counts), 2 * F, H), generator=g, device="cuda") * H ** -0.5).to(BF16)
+    act = torch.full((N, F), 7.0, dtype=BF16, device="cuda")
+    q = torch.full((N, 2 * F), 0x55, dtype=U8, device="cuda") if save else None
+    sc = torch.full((N, 2 * F // 128), 7.0, device="cuda") if save else None
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=off.cuda()), x, N, w13, F, act, q, sc, ws)
+    assert ep.ep_check_errors(ws) == 0
+    for e in range(len(counts)):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if r.stop == r.start:
+            continue
+        a, b = x[r].double(), w13[e].double()
+        gu, acc = a @ b.T, H * U23 * (a.abs() @ b.abs().T)
+        gate, up, s, ref = silu_parts(gu, F)
+        d = act_bound(gate, up, s, ref, acc[:, :F], acc[:, F:])
+        check_there(act[r], ref, d + HALF_BF16 * (ref.abs() + d), f"act of expert {e}")
+        if save:
+            m = gu.reshape(len(gu), -1, 128).abs().amax(2)
+            check_there(sc[r], m / 448, acc.reshape(len(gu), -1, 128).amax(2) / 448 + 4 * U23 * m / 448, f"scales {e}")
+            rep = sc[r].double().repeat_interleave(128, 1)
+            by = acc + 4 * U23 * gu.abs()
+            check_there(q[r].view(F8).double() * rep, gu, by + HALF_E4M3 * (gu.abs() + by) + 2.0 ** -10 * rep,
+                        f"checkpoint of expert {e}")
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["rows", "fp8rows"])
+def test_wgrad_streams_over_many_tiles(fp8, wide):
+    """Four tiles and more to a workgroup, each of another expert than the last: tiles of
+    no rows, of one, two, three and more steps between two others, with and without edges."""
+    counts = [0, 1, 0, 63, 64, 65, 128, 0, 0, 129, 192, 200, 5, 300, 0, 1, 256, 70, 10, 0] * 2
+    off, N, shape, ws = by_counts(counts)
+    E, n, k = len(counts), 1032, 1408
+    assert E * -(-n // 256) * -(-k // 256) >= 4 * 256
+    g = torch.Generator(device="cuda").manual_seed(7)
+    dy = torch.randn((N, n), generator=g, device="cuda").to(BF16)
+    if fp8:
+        v = torch.randn((N, k), generator=g, device="cuda")
+        sc = v.reshape(N, -1, 128).abs().amax(2) / 448
+        q = (v / sc.repeat_interleave(128, 1)).to(F8)
+        x, rows = q.double() * sc.double().repeat_interleave(128, 1), dict(x_fp8=q, x_scales=sc)
+    else:
+        xb = torch.randn((N, k), generator=g, device="cuda").to(BF16)
+        x, rows = xb.double(), dict(x=xb)
+    dw = torch.full((E, n, k), 7.0, dtype=F32 if wide else BF16, device="cuda")
+    ep.ep_expert_wgrad(shape, dict(expert_offsets=off.cuda()), dy, N, n, rows, k, dw,
+                       ep.EP_GRAD_F32 if wide else ep.EP_GRAD_BF16, ws)
+    assert ep.ep_check_errors(ws) == 0
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        a, b = dy[r].double(), x[r]
+        ref, mag = a.T @ b, a.abs().T @ b.abs()
+        acc = counts[e] * U23 * mag + (HALF_BF16 * mag * (1 + counts[e] * U23) + U23 * mag if fp8 else 0)
+        check_there(dw[e], ref, acc if wide else acc + HALF_BF16 * (ref.abs() + acc), f"dw of expert {e}")
