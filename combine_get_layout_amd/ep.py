@@ -176,7 +176,9 @@ def _ptr(t, name="tensor", nbytes=0):
 
 
 def _stream(stream):
-    if stream is None:  # the handle of torch.cuda.current_stream(), without making its object
+    if stream is None:
+        # The handle of torch.cuda.current_stream(), without making its object (2.4 us of the
+        # 16 of a small call); _cuda_getDevice runs torch's own initialisation and its checks.
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream

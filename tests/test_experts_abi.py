@@ -131,3 +131,20 @@ def test_binding_refuses_host_and_short_tensors(lib, shape):
         ep.ep_expert_matmul(shape, L, t, 1, 8, P, 8, 0, P, t)
     with pytest.raises(ValueError, match="GPU tensor"):
         ep.ep_moe_few(shape, dict(x=t, topk_idx=P, topk_weights=P), dict(F=128, w13=P, w2=P), P, t)
+
+
+def test_stream_lookup_keeps_torchs_checks(monkeypatch):
+    """A call without a stream goes through torch's own initialisation, which refuses a process
+    forked from one that holds the GPU; a given stream is taken as it is."""
+    import torch
+
+    class Stream:
+        cuda_stream = 0x51
+
+    def refuse():
+        raise RuntimeError("Cannot re-initialize CUDA in forked subprocess")
+
+    assert ep._stream(7) == 7 and ep._stream(Stream) == 0x51
+    monkeypatch.setattr(torch.cuda, "_lazy_init", refuse)
+    with pytest.raises(RuntimeError, match="forked subprocess"):
+        ep._stream(None)
