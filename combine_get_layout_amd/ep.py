@@ -154,19 +154,26 @@ def lib() -> ctypes.CDLL:
     return L
 
 
-def _ptr(t, name="tensor", nbytes=0):
+def _ptr(t, name="tensor", nbytes=0, device=None):
     """Device address of a tensor argument (None passes through as NULL).
 
-    A tensor must live on the GPU, be contiguous and hold at least `nbytes`
-    bytes (the size the C ABI reads or writes for the given shape); anything
-    else raises before a kernel can touch memory it does not own. A plain int
-    is taken as a device address the caller vouches for."""
+    A tensor must live on the GPU (on `device` where one is given), be contiguous
+    and hold at least `nbytes` bytes (the size the C ABI reads or writes for the
+    given shape); anything else raises before a kernel can touch memory it does
+    not own. A plain int is taken as a device address the caller vouches for."""
     if t is None:
         return None
     if isinstance(t, int):
         return t
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a GPU tensor")
+    if device is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a GPU tensor")
+    else:
+        on = t.get_device()
+        if on < 0:
+            raise ValueError(f"{name}: must be a GPU tensor")
+        if on != device:
+            raise ValueError(f"{name}: on device {on}, the workspace on device {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     have = t.numel() * t.element_size()
@@ -183,6 +190,20 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _stream_on(stream, device):
+    """The handle of a stream that runs on `device`, where the call's tensors are: a
+    kernel would fault on another device's memory. No stream or the NULL stream
+    run on the current device; a stream given as a bare handle is the caller's to
+    match."""
+    handle = _stream(stream)
+    if handle and isinstance(stream, int):
+        return handle
+    runs = torch._C._cuda_getDevice() if stream is None or not handle else stream.device_index
+    if runs != device:
+        raise ValueError(f"workspace: on device {device}, the call's stream on device {runs}")
+    return handle
 
 
 def _check(rc: int, what: str):
@@ -207,12 +228,12 @@ _LAYOUT_BYTES = dict(
     expert_slot=lambda s: 4 * s.T * s.K)
 
 
-def _layout_struct(shape: ep_shape, layout: dict) -> ep_layout:
+def _layout_struct(shape: ep_shape, layout: dict, device=None) -> ep_layout:
     L = ep_layout()
     for n in LAYOUT_FIELDS:
         t = layout.get(n)
         if t is not None:
-            setattr(L, n, _ptr(t, n, _LAYOUT_BYTES[n](shape)))
+            setattr(L, n, _ptr(t, n, _LAYOUT_BYTES[n](shape), device))
     return L
 
 
@@ -222,12 +243,12 @@ def _seg_of(tokens: dict) -> int:
             (EP_SEG_SCALES if tokens.get("x_scales") is not None else 0))
 
 
-def _tokens_struct(shape: ep_shape, tokens: dict) -> ep_tokens:
+def _tokens_struct(shape: ep_shape, tokens: dict, device=None) -> ep_tokens:
     T, H, K = shape.T, shape.H, shape.K
     need = dict(x=2 * T * H, x_fp8=T * H, x_scales=4 * T * (H // 128), topk_idx=8 * T * K,
                 topk_weights=4 * T * K)
-    return ep_tokens(*[_ptr(tokens.get(n), n, need[n]) for n in ("x", "x_fp8", "x_scales",
-                                                                  "topk_idx", "topk_weights")])
+    return ep_tokens(*[_ptr(tokens.get(n), n, need[n], device) for n in ("x", "x_fp8", "x_scales",
+                                                                          "topk_idx", "topk_weights")])
 
 
 def _recv_struct(shape: ep_shape, recv: dict, capacity: int) -> ep_recv:
@@ -412,51 +433,55 @@ def ep_source_dispatch_fused(shape, sources: dict, tokens: dict, epoch: int, sta
 
 def ep_expert_matmul(shape, layout: dict, x, rows: int, k_dim: int, w, n_dim: int, w_order: int, y, ws,
                      stream=None):
-    L = _layout_struct(shape, layout)
+    dev = ws.get_device()
+    L = _layout_struct(shape, layout, dev)
     n = max(int(rows), 0)
-    _check(lib().ep_expert_matmul(ctypes.byref(shape), ctypes.byref(L), _ptr(x, "x", 2 * n * k_dim),
-                                  int(rows), int(k_dim), _ptr(w, "w", 2 * shape.E * n_dim * k_dim),
-                                  int(n_dim), int(w_order), _ptr(y, "y", 2 * n * n_dim), *_ws(ws),
-                                  _stream(stream)), "ep_expert_matmul")
+    _check(lib().ep_expert_matmul(ctypes.byref(shape), ctypes.byref(L), _ptr(x, "x", 2 * n * k_dim, dev),
+                                  int(rows), int(k_dim), _ptr(w, "w", 2 * shape.E * n_dim * k_dim, dev),
+                                  int(n_dim), int(w_order), _ptr(y, "y", 2 * n * n_dim, dev), *_ws(ws),
+                                  _stream_on(stream, dev)), "ep_expert_matmul")
 
 
 def ep_expert_swiglu(shape, layout: dict, x, rows: int, w13, F: int, act, gu_fp8, gu_scales, ws,
                      stream=None):
-    L = _layout_struct(shape, layout)
+    dev = ws.get_device()
+    L = _layout_struct(shape, layout, dev)
     n = max(int(rows), 0)
-    _check(lib().ep_expert_swiglu(ctypes.byref(shape), ctypes.byref(L), _ptr(x, "x", 2 * n * shape.H),
-                                  int(rows), _ptr(w13, "w13", 4 * shape.E * F * shape.H), int(F),
-                                  _ptr(act, "act", 2 * n * F), _ptr(gu_fp8, "gu_fp8", 2 * n * F),
-                                  _ptr(gu_scales, "gu_scales", 8 * n * (F // 128)), *_ws(ws),
-                                  _stream(stream)), "ep_expert_swiglu")
+    _check(lib().ep_expert_swiglu(ctypes.byref(shape), ctypes.byref(L), _ptr(x, "x", 2 * n * shape.H, dev),
+                                  int(rows), _ptr(w13, "w13", 4 * shape.E * F * shape.H, dev), int(F),
+                                  _ptr(act, "act", 2 * n * F, dev), _ptr(gu_fp8, "gu_fp8", 2 * n * F, dev),
+                                  _ptr(gu_scales, "gu_scales", 8 * n * (F // 128), dev), *_ws(ws),
+                                  _stream_on(stream, dev)), "ep_expert_swiglu")
 
 
 def ep_swiglu_grad(shape, layout: dict, F: int, gu_fp8, gu_scales, d_act, rows: int, topk_weights, d_gu,
                    act_w, d_topk_weights, ws, stream=None):
-    L = _layout_struct(shape, layout)
+    dev = ws.get_device()
+    L = _layout_struct(shape, layout, dev)
     n, lanes = max(int(rows), 0), shape.T * shape.K
     _check(lib().ep_swiglu_grad(ctypes.byref(shape), ctypes.byref(L), int(F),
-                                _ptr(gu_fp8, "gu_fp8", 2 * n * F),
-                                _ptr(gu_scales, "gu_scales", 8 * n * (F // 128)),
-                                _ptr(d_act, "d_act", 2 * n * F), int(rows),
-                                _ptr(topk_weights, "topk_weights", 4 * lanes),
-                                _ptr(d_gu, "d_gu", 4 * n * F), _ptr(act_w, "act_w", 2 * n * F),
-                                _ptr(d_topk_weights, "d_topk_weights", 4 * lanes), *_ws(ws),
-                                _stream(stream)), "ep_swiglu_grad")
+                                _ptr(gu_fp8, "gu_fp8", 2 * n * F, dev),
+                                _ptr(gu_scales, "gu_scales", 8 * n * (F // 128), dev),
+                                _ptr(d_act, "d_act", 2 * n * F, dev), int(rows),
+                                _ptr(topk_weights, "topk_weights", 4 * lanes, dev),
+                                _ptr(d_gu, "d_gu", 4 * n * F, dev), _ptr(act_w, "act_w", 2 * n * F, dev),
+                                _ptr(d_topk_weights, "d_topk_weights", 4 * lanes, dev), *_ws(ws),
+                                _stream_on(stream, dev)), "ep_swiglu_grad")
 
 
 def ep_expert_wgrad(shape, layout: dict, dy, rows: int, n_dim: int, x: dict, k_dim: int, dw, dtype: int,
                     ws, stream=None):
     """x: {"x": bf16 rows} or {"x_fp8": e4m3 rows, "x_scales": scales}."""
-    L = _layout_struct(shape, layout)
+    dev = ws.get_device()
+    L = _layout_struct(shape, layout, dev)
     n = max(int(rows), 0)
-    X = ep_rows(_ptr(x.get("x"), "x", 2 * n * k_dim), _ptr(x.get("x_fp8"), "x_fp8", n * k_dim),
-                _ptr(x.get("x_scales"), "x_scales", 4 * n * (k_dim // 128)))
+    X = ep_rows(_ptr(x.get("x"), "x", 2 * n * k_dim, dev), _ptr(x.get("x_fp8"), "x_fp8", n * k_dim, dev),
+                _ptr(x.get("x_scales"), "x_scales", 4 * n * (k_dim // 128), dev))
     size = 4 if int(dtype) == EP_GRAD_F32 else 2
-    _check(lib().ep_expert_wgrad(ctypes.byref(shape), ctypes.byref(L), _ptr(dy, "dy", 2 * n * n_dim),
+    _check(lib().ep_expert_wgrad(ctypes.byref(shape), ctypes.byref(L), _ptr(dy, "dy", 2 * n * n_dim, dev),
                                  int(rows), int(n_dim), ctypes.byref(X), int(k_dim),
-                                 _ptr(dw, "dw", size * shape.E * n_dim * k_dim), int(dtype), *_ws(ws),
-                                 _stream(stream)), "ep_expert_wgrad")
+                                 _ptr(dw, "dw", size * shape.E * n_dim * k_dim, dev), int(dtype), *_ws(ws),
+                                 _stream_on(stream, dev)), "ep_expert_wgrad")
 
 
 def ep_few_workspace_bytes(shape: ep_shape, F: int) -> int:
@@ -466,13 +491,14 @@ def ep_few_workspace_bytes(shape: ep_shape, F: int) -> int:
 def ep_moe_few(shape, tokens: dict, experts: dict, out, ws, stream=None):
     """experts: {"F", "w13", "w2"} (bf16) or {"F", "w13_fp8", "w13_scales",
     "w2_fp8", "w2_scales"}."""
-    tk = _tokens_struct(shape, tokens)
+    dev = ws.get_device()
+    tk = _tokens_struct(shape, tokens, dev)
     E, H, F = shape.E, shape.H, int(experts["F"])
     need = dict(w13=4 * E * F * H, w2=2 * E * H * F, w13_fp8=2 * E * F * H,
                 w13_scales=8 * E * F * (H // 128), w2_fp8=E * H * F, w2_scales=4 * E * H * (F // 128))
-    X = ep_experts(F, *[_ptr(experts.get(n), n, need[n]) for n in need])
+    X = ep_experts(F, *[_ptr(experts.get(n), n, need[n], dev) for n in need])
     _check(lib().ep_moe_few(ctypes.byref(shape), ctypes.byref(tk), ctypes.byref(X),
-                            _ptr(out, "out", 2 * shape.T * H), *_ws(ws), _stream(stream)), "ep_moe_few")
+                            _ptr(out, "out", 2 * shape.T * H, dev), *_ws(ws), _stream_on(stream, dev)), "ep_moe_few")
 
 
 def ep_clear_errors(ws, stream=None):

@@ -145,6 +145,75 @@ def test_stream_lookup_keeps_torchs_checks(monkeypatch):
         raise RuntimeError("Cannot re-initialize CUDA in forked subprocess")
 
     assert ep._stream(7) == 7 and ep._stream(Stream) == 0x51
+    if torch.cuda.is_initialized():
+        pytest.skip("torch has made these checks in this process already")
     monkeypatch.setattr(torch.cuda, "_lazy_init", refuse)
     with pytest.raises(RuntimeError, match="forked subprocess"):
         ep._stream(None)
+
+
+class OnDevice:
+    """What the binding asks of a tensor, on a given device."""
+    is_cuda = True
+
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 40
+
+    def element_size(self):
+        return 1
+
+    def data_ptr(self):
+        return P + 4  # the library refuses it: no launch
+
+
+class StreamOf:
+    cuda_stream = 0x51
+
+    def __init__(self, device):
+        self.device_index = device
+
+
+# Each entry point with one tensor (and its workspace) on given devices.
+CALLS = dict(
+    matmul=lambda s, L, t, ws, st: ep.ep_expert_matmul(s, L, t, 1, 64, P, 128, 0, P, ws, stream=st),
+    matmul_y=lambda s, L, t, ws, st: ep.ep_expert_matmul(s, L, P, 1, 64, P, 128, 0, t, ws, stream=st),
+    matmul_offsets=lambda s, L, t, ws, st: ep.ep_expert_matmul(s, dict(expert_offsets=t), P, 1, 64, P, 128, 0, P, ws,
+                                                               stream=st),
+    swiglu=lambda s, L, t, ws, st: ep.ep_expert_swiglu(s, L, P, 1, t, 128, P, P, P, ws, stream=st),
+    swiglu_scales=lambda s, L, t, ws, st: ep.ep_expert_swiglu(s, L, P, 1, P, 128, P, P, t, ws, stream=st),
+    grad=lambda s, L, t, ws, st: ep.ep_swiglu_grad(s, dict(expert_slot=P), 128, P, P, P, 1, t, P, P, P, ws, stream=st),
+    grad_d_w=lambda s, L, t, ws, st: ep.ep_swiglu_grad(s, dict(expert_slot=P), 128, P, P, P, 1, P, P, P, t, ws, stream=st),
+    wgrad=lambda s, L, t, ws, st: ep.ep_expert_wgrad(s, L, P, 1, 64, dict(x=t), 128, P, 0, ws, stream=st),
+    wgrad_dw=lambda s, L, t, ws, st: ep.ep_expert_wgrad(s, L, P, 1, 64, dict(x=P), 128, t, 0, ws, stream=st),
+    few=lambda s, L, t, ws, st: ep.ep_moe_few(s, dict(x=P, topk_idx=t, topk_weights=P), dict(F=128, w13=P, w2=P), P, ws,
+                                              stream=st),
+    few_w2=lambda s, L, t, ws, st: ep.ep_moe_few(s, dict(x=P, topk_idx=P, topk_weights=P), dict(F=128, w13=P, w2=t), P,
+                                                 ws, stream=st),
+)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_binding_refuses_tensors_of_another_device(lib, shape, monkeypatch, name):
+    """The kernel runs on its stream's device (the current one without a stream), where
+    another device's memory would fault. A tensor of the right device reaches the library, which
+    refuses the address."""
+    import torch
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x30 + device)
+    call, L = CALLS[name], dict(expert_offsets=P)
+    for stream, own, other in ((None, 0, 1), (StreamOf(1), 1, 0), (0, 0, 1)):
+        for devices in ((other, own), (own, other), (other, other)):
+            with pytest.raises(ValueError, match="device"):
+                call(shape, L, OnDevice(devices[0]), OnDevice(devices[1]), stream)
+        with pytest.raises(RuntimeError, match="invalid|argument"):
+            call(shape, L, OnDevice(own), OnDevice(own), stream)

@@ -1188,3 +1188,21 @@ def test_wgrad_streams_over_many_tiles(fp8, wide):
         ref, mag = a.T @ b, a.abs().T @ b.abs()
         acc = counts[e] * U23 * mag + (HALF_BF16 * mag * (1 + counts[e] * U23) + U23 * mag if fp8 else 0)
         check_there(dw[e], ref, acc if wide else acc + HALF_BF16 * (ref.abs() + acc), f"dw of expert {e}")
+
+
+@pytest.mark.parametrize("how", ["none", "default", "null", "object", "handle"])
+def test_calls_take_a_stream(how):
+    """No stream, the default one, and another as torch's object or its handle."""
+    T, H, F, E, K = 16, 128, 128, 4, 2
+    idx, w, x, _, w13, w2 = gpu(*layer_case(T, H, F, E, K))
+    shape = ep.make_shape(T, H, K, E, 1)
+    tokens, experts = dict(x=x, topk_idx=idx, topk_weights=w), dict(F=F, w13=w13, w2=w2)
+    ref = torch.empty((T, H), dtype=BF16, device="cuda")
+    ep.ep_moe_few(shape, tokens, experts, ref, ep.alloc_few_workspace(shape, F))
+    out, ws = torch.zeros_like(ref), ep.alloc_few_workspace(shape, F)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    stream = dict(none=None, default=torch.cuda.default_stream(), null=0, object=st, handle=st.cuda_stream)[how]
+    ep.ep_moe_few(shape, tokens, experts, out, ws, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
