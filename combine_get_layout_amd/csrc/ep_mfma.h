@@ -1,6 +1,6 @@
-// ep_mfma.h -- tiles of the expert products on CDNA4's matrix cores: buffer
-// descriptors, direct global-to-LDS loads, the swizzled LDS layouts and the
-// matrix instruction with its operand layout.
+// ep_mfma.h -- what the expert operators share of CDNA4's matrix cores: buffer
+// descriptors, direct global-to-LDS loads, the matrix instruction with its
+// operand layout, and the packing of results.
 //
 // One v_mfma_f32_16x16x32_bf16 multiplies a 16 x 32 by a 32 x 16 block.
 // Lane l holds, of each operand, row (of the second: column) l % 16 and the 8
@@ -54,8 +54,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_resource(const void* p, ui
 // Copy 16 bytes per lane from descriptor r at byte offset `off` (per lane)
 // into LDS at byte address lds + 16 * lane (lds wave-uniform), without a
 // register in between. Written out because the compiler's own form waits for
-// all such copies before any LDS read; the kernels wait once per tile with
-// wait_copies. No output register, so nothing is overwritten while the copy is
+// all such copies before any LDS read; the kernels wait once per step with
+// wait_copies, for the copies that the step needs. No output register, so nothing is overwritten while the copy is
 // in flight. The five wait states before the load are what a descriptor written
 // by a vector instruction (a lane read) needs, and more than m0 does.
 __device__ __forceinline__ void copy16_to_lds(u32x4 r, uint32_t off, uint32_t lds) {

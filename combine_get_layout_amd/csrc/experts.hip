@@ -706,13 +706,18 @@ struct SwigluArgs {
     uint32_t* err;
 };
 
+// The reciprocal is the instruction's own, within one unit in the last place of
+// 32 bits; the product is rounded to bf16 next.
 __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // Scale of a block of 128 values with the largest magnitude amax: amax / 448,
 // so that the largest value is e4m3's largest; 1 where amax / 448 would be
-// too small to invert (all values then round to 0).
+// too small to invert (all values then round to 0). The codes are of v * (1 /
+// scale), one 32-bit rounding more than v / scale, which moves about 2 of 10^7
+// more values over a boundary of e4m3's rounding; divisions took 1% of the
+// kernel's time.
 __device__ __forceinline__ float block_scale(float amax) { return amax < 1e-33f ? 1.0f : amax / 448.0f; }
 
 struct SwigluLoaders {

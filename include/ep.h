@@ -517,7 +517,8 @@ typedef struct ep_rows {
  *   dw[e][n][k] = sum over rows i of e of dy[i][n] * x[i][k]
  * dy: [rows][n_dim] bf16; x: bf16 rows, or the FP8 rows with their scales
  * that dispatch delivers (k_dim % 128 == 0; each value q * scale is rounded
- * to bf16 for the matrix instruction). dw: [E][n_dim][k_dim], bf16 or fp32
+ * to bf16 for the matrix instruction, by 2^-8 of it at most, for results of
+ * either type). dw: [E][n_dim][k_dim], bf16 or fp32
  * (dtype EP_GRAD_*), overwritten. */
 int ep_expert_wgrad(const ep_shape *shape, const ep_layout *layout, const uint16_t *dy, int64_t rows,
                     int32_t n_dim, const ep_rows *x, int32_t k_dim, void *dw, int dtype, void *ws,
