@@ -68,3 +68,14 @@ def test_committed_summaries_are_well_formed():
         for name, k in rec["kernels"].items():
             assert k["source_sha"] is None or len(k["source_sha"]) == 16, (f, name)
             assert k["hbm_bytes_per_launch"] >= 0
+
+
+@pytest.mark.parametrize("label,opts", bench.TARGET_CONFIGS, ids=[label for label, _ in bench.TARGET_CONFIGS])
+def test_committed_counters_were_taken_from_the_present_sources(label, opts):
+    """A change to the kernels' sources or to what all kernels share takes the counters of
+    every configuration again: without them bench.py reports no traffic."""
+    d = json.load(open(os.path.join(ROOT, "profiles", f"traffic_{label}.json")))
+    counted = [k for k in d["kernels"] if k in bench.KERNEL_FILES]
+    assert "combine_kernel" in counted and len(counted) >= 2
+    for kernel in counted:
+        assert bench.committed_traffic(label, kernel) == d["kernels"][kernel]["hbm_bytes_per_launch"], kernel
