@@ -6,7 +6,7 @@
 //
 // Bound: the used experts' weights are read once from HBM; every other array
 // is small and stays in L2. One token, top-8 of 64 experts of 7168 x 2048: 89 +
-// 50 us for 470 + 235 MB (5.3 and 4.7 TB/s, beside 4.9 of a large copy). 32
+// 50 us for 470 + 235 MB (5.3 and 4.7 TB/s, beside 5.0 of a large copy). 32
 // tokens of the same with FP8 weights: 412 + 277 us for 1.94 + 0.97 GB (4.7 and
 // 3.5 TB/s): the second launch has one unit's loads at a time in flight per
 // wave, and with registers for more (a third of the waves less) it was slower;

@@ -9,7 +9,7 @@
 // instruction's own, within one unit in the last place.
 //
 // Bound: one pass over the row, 10 F bytes and its scales. 32,768 rows of F = 2048
-// (676 MB): 129 us, 5.2 TB/s, beside 4.9 of a large copy.
+// (676 MB): 129 us, 5.2 TB/s, beside 5.0 of a large copy.
 #include "ep_internal.h"
 #include "ep_mfma.h"
 
