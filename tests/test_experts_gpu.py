@@ -1206,3 +1206,144 @@ def test_calls_take_a_stream(how):
     ep.ep_moe_few(shape, tokens, experts, out, ws, stream=stream)
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+MOST = 1 << 20  # EP_MAX_DIM
+
+
+def device_randn(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").mul_(scale).to(BF16)
+
+
+@pytest.mark.parametrize("k,n", [(MOST, 8), (8, MOST), (MOST - 8, 264), (264, MOST - 8)])
+def test_products_at_the_largest_dimensions(k, n):
+    """Both weight orders and the weight gradient; rows of two experts around an empty one."""
+    off = torch.tensor([0, 3, 3, 5], dtype=torch.int32, device="cuda")
+    N, E = 5, 3
+    shape = ep.make_shape(N, 128, 1, E, 1)
+    ws = cleared(shape)
+    L = dict(expert_offsets=off)
+    x, w = device_randn(1, N, k), device_randn(2, E, n, k, scale=k ** -0.5)
+    y = torch.full((N, n), 7.0, dtype=BF16, device="cuda")
+    for order in (ep.EP_WEIGHT_NK, ep.EP_WEIGHT_KN):
+        wt = w if order == ep.EP_WEIGHT_NK else w.transpose(1, 2).contiguous()
+        ep.ep_expert_matmul(shape, L, x, N, k, wt, n, order, y, ws)
+        for e, r in ((0, slice(0, 3)), (2, slice(3, 5))):
+            a, b = x[r].double(), w[e].double()
+            ref, acc = a @ b.T, k * U23 * (a.abs() @ b.abs().T)
+            check_there(y[r], ref, acc + HALF_BF16 * (ref.abs() + acc), f"y of expert {e}, order {order}")
+    dw = torch.full((E, n, k), 7.0, device="cuda")
+    ep.ep_expert_wgrad(shape, L, y, N, n, dict(x=x), k, dw, ep.EP_GRAD_F32, ws)
+    for e, r in ((0, slice(0, 3)), (1, slice(0, 0)), (2, slice(3, 5))):
+        a, b = y[r].double(), x[r].double()
+        check_there(dw[e], a.T @ b, 3 * U23 * (a.abs().T @ b.abs()), f"dw of expert {e}")
+    assert ep.ep_check_errors(ws) == 0
+
+
+@pytest.mark.parametrize("H,F", [(MOST, 8), (8, MOST), (8192, 65528)])
+def test_swiglu_at_the_largest_dimensions(H, F):
+    """The last is the largest matrix of one expert: 4 F H just below 2^31 - 16."""
+    N, E = 3, 1
+    shape = ep.make_shape(N, H, 1, E, 1)
+    ws = cleared(shape)
+    x, w13 = device_randn(1, N, H), device_randn(2, E, 2 * F, H, scale=H ** -0.5)
+    act = torch.full((N, F), 7.0, dtype=BF16, device="cuda")
+    off = torch.tensor([0, N], dtype=torch.int32, device="cuda")
+    ep.ep_expert_swiglu(shape, dict(expert_offsets=off), x, N, w13, F, act, None, None, ws)
+    assert ep.ep_check_errors(ws) == 0
+    xd = x.double()
+    for lo in range(0, F, 1 << 14):
+        hi = min(F, lo + (1 << 14))
+        w = torch.cat([w13[0, lo:hi], w13[0, F + lo:F + hi]]).double()
+        gu, acc = xd @ w.T, H * U23 * (xd.abs() @ w.abs().T)
+        m = hi - lo
+        gate, up, s, ref = silu_parts(gu, m)
+        b = act_bound(gate, up, s, ref, acc[:, :m], acc[:, m:])
+        check_there(act[:, lo:hi], ref, b + HALF_BF16 * (ref.abs() + b), f"act from {lo}")
+
+
+def test_swiglu_grad_at_the_largest_dimension():
+    F, T = MOST, 2
+    shape = ep.make_shape(T, 128, 1, 1, 1)
+    ws = cleared(shape)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn((T, 2 * F), generator=g, device="cuda").to(F8)
+    sc = torch.rand((T, 2 * F // 128), generator=g, device="cuda") + 0.5
+    d, w = device_randn(4, T, F), torch.tensor([[0.5], [-0.25]], device="cuda")
+    slot = torch.tensor([[1], [0]], dtype=torch.int32, device="cuda")
+    d_gu, act_w = torch.empty((T, 2 * F), dtype=BF16, device="cuda"), torch.empty((T, F), dtype=BF16, device="cuda")
+    d_w = torch.empty((T, 1), device="cuda")
+    ep.ep_swiglu_grad(shape, dict(expert_slot=slot), F, q, sc, d, T, w, d_gu, act_w, d_w, ws)
+    assert ep.ep_check_errors(ws) == 0
+    gate, up, s, act = silu_parts(q.double() * sc.double().repeat_interleave(128, 1), F)
+    row_w, dd, rel = w.flip(0).double(), d.double(), (gate.abs() + 24) * U23
+    ref = torch.cat([row_w * dd * up * s * (1 + gate * (1 - s)), row_w * dd * gate * s], 1)
+    b = torch.cat([(row_w * dd * up * s).abs() * (1 + gate.abs()) * rel, ref[:, F:].abs() * rel], 1)
+    check_there(d_gu, ref, b + HALF_BF16 * (ref.abs() + b), "d_gu")
+    ref = row_w * act
+    check_there(act_w, ref, ref.abs() * rel + HALF_BF16 * ref.abs() * (1 + rel), "act_w")
+    # A lane's partial sums hold F / 64 terms each, six more join them.
+    each = (dd * act).abs()
+    check_there(d_w.flip(0)[:, 0], (dd * act).sum(1), (each * (rel + (F // 64 + 8) * U23)).sum(1), "d_topk_weights")
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("H,F", [(MOST, 8), (8, MOST)])
+def test_few_at_the_largest_dimensions(H, F, fp8):
+    T, K, E = 3, 2, 2
+    if fp8:
+        H, F = max(H, 128), max(F, 128)
+    x = device_randn(1, T, H)
+    w13, w2 = device_randn(2, E, 2 * F, H, scale=H ** -0.5), device_randn(3, E, H, F, scale=F ** -0.5)
+    idx = torch.tensor([[0, 1], [1, -1], [0, 0]])
+    w = torch.tensor([[0.5, -0.5], [1.0, 3.0], [0.25, 0.5]])
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_few_workspace(shape, F).fill_(0xAB)
+    ep.ep_clear_errors(ws)
+    if fp8:
+        (q13, s13, w13), (q2, s2, w2) = eight(w13), eight(w2)
+        experts = dict(F=F, w13_fp8=q13, w13_scales=s13, w2_fp8=q2, w2_scales=s2)
+    else:
+        experts = dict(F=F, w13=w13, w2=w2)
+    out = torch.full((T, H), 7.0, dtype=BF16, device="cuda")
+    ep.ep_moe_few(shape, dict(x=x, topk_idx=idx.cuda(), topk_weights=w.cuda()), experts, out, ws)
+    assert ep.ep_check_errors(ws) == 0
+    ref, bound = few_reference(x.cpu(), w13.cpu(), w2.cpu(), idx, w, F)
+    check(out, ref, bound, "out")
+
+
+def test_few_with_most_lanes_and_experts():
+    """128 tokens of 64 lanes over 4,096 experts: 8,192 lanes, most experts used."""
+    T, K, E, H, F = 128, 64, 4096, 24, 16
+    g = torch.Generator().manual_seed(9)
+    idx, w = routing(T, K, E, 17)
+    x, w13, w2 = randn(g, T, H), randn(g, E, 2 * F, H, scale=H ** -0.5), randn(g, E, H, F, scale=F ** -0.5)
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_few_workspace(shape, F).fill_(0xAB)
+    ep.ep_clear_errors(ws)
+    out = torch.full((T, H), 7.0, dtype=BF16, device="cuda")
+    ep.ep_moe_few(shape, dict(x=x.cuda(), topk_idx=idx.cuda(), topk_weights=w.cuda()),
+                  dict(F=F, w13=w13.cuda(), w2=w2.cuda()), out, ws)
+    assert ep.ep_check_errors(ws) == 0
+    ref, bound = few_reference(x, w13, w2, idx, w, F)
+    # few_reference allows 80 sums of experts' parts; these tokens have 64 each: enough.
+    check(out, ref, bound, "out")
+
+
+@pytest.mark.parametrize("F", [128, 2056])
+def test_few_without_any_lane(F):
+    """All lanes skipped, or of ids that 32 bits would take for valid ones: zeros, and for the
+    latter the error (F: with and without shared outputs)."""
+    T, H, E, K = 9, 264, 4, 3
+    x, w13, w2 = device_randn(1, T, H), device_randn(2, E, 2 * F, H), device_randn(3, E, H, F)
+    w = torch.full((T, K), float("nan"), device="cuda")
+    shape = ep.make_shape(T, H, K, E, 1)
+    ws = ep.alloc_few_workspace(shape, F).fill_(0xAB)
+    for ident, want in ((-1, 0), ((1 << 32) + 1, ep.EP_DEVERR_EXPERT_ID), (-(1 << 32), ep.EP_DEVERR_EXPERT_ID)):
+        ep.ep_clear_errors(ws)
+        out = torch.full((T, H), 7.0, dtype=BF16, device="cuda")
+        ep.ep_moe_few(shape, dict(x=x, topk_idx=torch.full((T, K), ident, device="cuda"), topk_weights=w),
+                      dict(F=F, w13=w13, w2=w2), out, ws)
+        assert ep.ep_check_errors(ws) == want
+        assert (out == 0).all()
