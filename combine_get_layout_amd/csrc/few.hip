@@ -515,16 +515,22 @@ hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_exper
     const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K);
     // Values of f per workgroup of the first launch (x 2 = weight rows), by the
     // tokens that an expert has on the average. 64, and two token tiles at a time,
-    // where these are more than 16, or more than 4 and there are 1,024 workgroups:
-    // the tokens' rows, which then weigh, are read half as often (64 tokens, top-8
-    // of 64 experts of 4096 x 1536: 558 us, with 32 and one tile 581; 128 tokens: 669
-    // and 766; but 32 tokens, FP8 weights of 7168 x 2048: 710 and 696; 106 tokens,
-    // top-3 of 63 experts of 1536 x 896: 96 and 87; 33 tokens, top-4 of 39 experts of
-    // 664 x 504: 31.5 and 26.5). Else 32, or 16 where that gives fewer than 1,024
+    // where these are more than 16, or where there are 1,024 workgroups and they
+    // are more than 4, with FP8 weights (half the bytes beside the same tokens'
+    // rows and twice the arithmetic) more than 8: the tokens' rows, which then
+    // weigh, are read half as often. Top-8 of 64 experts, 64 against 32 values and
+    // one tile, both launches, at 3, 4, 4.5, 6, 8, 12 and 16 tokens an expert:
+    //   4096 x 1536        470 483 498 515 541 596 652, 442 486 531 540 574 648 779
+    //   7168 x 2048        1041 1080 1101 1152 1228 1351 1490,
+    //                      1049 1094 1119 1175 1254 1492 1824
+    //   FP8, 7168 x 2048   672 697 716 769 832 965 1101, 650 678 701 763 847 1004 1252
+    //   FP8, 2048 x 1024   114 121 123 132 143 166 179, 106 113 115 125 137 168 196
+    // With fewer workgroups (top-3 of 63 experts of 1536 x 896) at 1.7, 4.6 and 6.1
+    // tokens 96 140 144, 90 126 129. Else 32, or 16 where that gives fewer than 1,024
     // workgroups, which leave the memory idle (one token, top-8 of 4096 x 1536: 66
     // us with 16, 75 with 32; 13 tokens, 33 experts of 2056 x 712: 63.5 and 70).
     const int64_t lanes = (int64_t)s.T * s.K, wide = (x.F + 63) / 64 * experts;
-    const bool many = s.T > 16 && (lanes > 16 * experts || (wide >= 1024 && lanes > 4 * experts));
+    const bool many = s.T > 16 && (lanes > 16 * experts || (wide >= 1024 && lanes > (fp8 ? 8 : 4) * experts));
     const bool narrow = (int64_t)((x.F + 31) / 32) * experts < 1024;
     const int cols = many ? 64 : narrow ? 16 : 32;
     const dim3 up((x.F + cols - 1) / cols, (unsigned)experts);
