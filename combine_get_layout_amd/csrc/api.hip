@@ -2,6 +2,7 @@
 // and record sizing, and the kernel launches (declared in include/ep.h).
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <mutex>
 
 #include "ep.h"
@@ -548,6 +549,105 @@ int ep_moe_few(const ep_shape* shape, const ep_tokens* tokens, const ep_experts*
         return EP_ERR_ARG;
     return hip_status(launch_moe_few(*shape, *tokens, x, out, static_cast<char*>(ws),
                                      static_cast<hipStream_t>(stream)));
+}
+
+static int check_norm(const ep_shape* shape, int stream_type) {
+    int rc = check_shape(shape);
+    if (rc != EP_OK) return rc;
+    if (stream_type != EP_STREAM_BF16 && stream_type != EP_STREAM_F32) return EP_ERR_ARG;
+    return shape->H > EP_MAX_DIM ? EP_ERR_UNSUPPORTED : EP_OK;
+}
+
+int ep_rms_norm(const ep_shape* shape, const uint16_t* x, const void* residual, int stream_type,
+                const uint16_t* gain, float eps, const ep_norm_out* out, void* stream) {
+    int rc = check_norm(shape, stream_type);
+    if (rc != EP_OK) return rc;
+    if (!out || !(eps > 0.0f) || !(eps <= FLT_MAX)) return EP_ERR_ARG;
+    const ep_norm_out& o = *out;
+    if (!o.y_fp8 != !o.y_scales || (o.y_fp8 && shape->H % 128 != 0)) return EP_ERR_ARG;
+    if (shape->T > 0 && (!x || !gain || (!o.h && !o.y && !o.y_fp8 && !o.rstd))) return EP_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gain, 16) || !aligned(o.h, 16) || !aligned(o.y, 16) ||
+        !aligned(o.y_fp8, 16) || !aligned(o.y_scales, 4) || !aligned(o.rstd, 4))
+        return EP_ERR_ARG;
+    return hip_status(launch_rms_norm(*shape, x, residual, stream_type, gain, eps, o, static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_norm_workspace_bytes(const ep_shape* shape) {
+    if (check_norm(shape, EP_STREAM_BF16) != EP_OK) return 0;
+    return ws_norm(*shape);
+}
+
+int ep_rms_norm_grad(const ep_shape* shape, const void* h, int stream_type, const uint16_t* gain,
+                     const float* rstd, const uint16_t* dy, const void* d_stream, void* d_h,
+                     uint16_t* d_x, float* d_gain, void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_norm(shape, stream_type);
+    if (rc != EP_OK) return rc;
+    if (!ws || !aligned(ws, 256) || ws_bytes < ws_norm(*shape)) return EP_ERR_ARG;
+    if (!d_gain && shape->T > 0 && !d_h && !d_x) return EP_ERR_ARG;
+    if (shape->T > 0 && (!h || !gain || !rstd || !dy)) return EP_ERR_ARG;
+    if (!aligned(h, 16) || !aligned(gain, 16) || !aligned(rstd, 4) || !aligned(dy, 16) || !aligned(d_stream, 16) ||
+        !aligned(d_h, 16) || !aligned(d_x, 16) || !aligned(d_gain, 16))
+        return EP_ERR_ARG;
+    return hip_status(launch_rms_norm_grad(*shape, h, stream_type, gain, rstd, dy, d_stream, d_h, d_x, d_gain,
+                                           static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+static int check_route(const ep_shape* shape, const float* logits, const ep_router* r, void* ws, size_t ws_bytes) {
+    int rc = check_shape(shape);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_ws(shape, ws, ws_bytes)) != EP_OK) return rc;
+    if (!r || (r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID)) return EP_ERR_ARG;
+    if (r->top_groups < 1 || r->top_groups > shape->G || r->group_top < 1 || r->group_top > 2) return EP_ERR_ARG;
+    if ((r->normalize & ~1) || !(r->scale >= -FLT_MAX && r->scale <= FLT_MAX)) return EP_ERR_ARG;
+    if ((shape->T > 0 && !logits) || !aligned(logits, 4) || !aligned(r->bias, 4)) return EP_ERR_ARG;
+    if (r->top_groups < shape->G && shape->G > 64) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+int ep_route(const ep_shape* shape, const float* logits, const ep_router* router, int64_t* topk_idx,
+             float* topk_weights, void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_route(shape, logits, router, ws, ws_bytes);
+    if (rc != EP_OK) return rc;
+    if ((shape->T > 0 && !topk_idx) || !aligned(topk_idx, 8) || !aligned(topk_weights, 4)) return EP_ERR_ARG;
+    return hip_status(launch_route(*shape, logits, *router, topk_idx, topk_weights, static_cast<char*>(ws),
+                                   static_cast<hipStream_t>(stream)));
+}
+
+int ep_route_grad(const ep_shape* shape, const float* logits, const ep_router* router,
+                  const int64_t* topk_idx, const float* d_topk_weights, void* d_logits, int dtype,
+                  void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_route(shape, logits, router, ws, ws_bytes);
+    if (rc != EP_OK) return rc;
+    if (dtype != EP_GRAD_BF16 && dtype != EP_GRAD_F32) return EP_ERR_ARG;
+    if (shape->T > 0 && (!topk_idx || !d_topk_weights || !d_logits)) return EP_ERR_ARG;
+    if (!aligned(topk_idx, 8) || !aligned(d_topk_weights, 4) || !aligned(d_logits, 16)) return EP_ERR_ARG;
+    return hip_status(launch_route_grad(*shape, logits, *router, topk_idx, d_topk_weights, d_logits, dtype,
+                                        static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_few_w4_workspace_bytes(const ep_shape* shape, int32_t F) {
+    if (ep_few_workspace_bytes(shape, F) == 0) return 0;
+    return ws_few_w4(*shape, F).total;
+}
+
+int ep_moe_few_w4(const ep_shape* shape, const ep_tokens* tokens, const ep_experts_w4* experts,
+                  uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+    int rc = check_shape(shape);
+    if (rc != EP_OK) return rc;
+    if (!tokens || !experts || (experts->form != EP_W4_INT && experts->form != EP_W4_E2M1)) return EP_ERR_ARG;
+    const ep_experts_w4& x = *experts;
+    const int step = x.form == EP_W4_INT ? 128 : 32;  // columns that share a scale
+    if (x.F < step || x.F % step != 0 || shape->H % step != 0) return EP_ERR_ARG;
+    if (shape->T > EP_FEW_MAX_TOKENS || x.F > EP_MAX_DIM || shape->H > EP_MAX_DIM) return EP_ERR_UNSUPPORTED;
+    if (!ws || !aligned(ws, 256) || ws_bytes < ws_few_w4(*shape, x.F).total) return EP_ERR_ARG;
+    if (!x.w13 || !x.w13_scales || !x.w2 || !x.w2_scales) return EP_ERR_ARG;
+    if (shape->T > 0 && (!tokens->x || !tokens->topk_idx || !tokens->topk_weights || !out)) return EP_ERR_ARG;
+    if (!aligned(tokens->x, 16) || !aligned(tokens->topk_idx, 8) || !aligned(tokens->topk_weights, 4) ||
+        !aligned(out, 16) || !aligned(x.w13, 16) || !aligned(x.w13_scales, 16) || !aligned(x.w2, 16) ||
+        !aligned(x.w2_scales, 16))
+        return EP_ERR_ARG;
+    return hip_status(launch_moe_few_w4(*shape, *tokens, x, out, static_cast<char*>(ws),
+                                        static_cast<hipStream_t>(stream)));
 }
 
 int ep_clear_errors(void* ws, void* stream) {

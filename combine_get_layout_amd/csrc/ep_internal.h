@@ -134,6 +134,22 @@ struct WsFew {
 WsFew ws_few(const ep_shape& s, int F);
 hipError_t launch_moe_few(const ep_shape& s, const ep_tokens& tk, const ep_experts& x, uint16_t* out, char* ws,
                           hipStream_t st);
+WsFew ws_few_w4(const ep_shape& s, int F);
+hipError_t launch_moe_few_w4(const ep_shape& s, const ep_tokens& tk, const ep_experts_w4& x, uint16_t* out, char* ws,
+                             hipStream_t st);
+
+// Norm and router. ws_norm: bytes of the gradient's workspace (256, then the
+// parts of d_gain).
+size_t ws_norm(const ep_shape& s);
+hipError_t launch_rms_norm(const ep_shape& s, const uint16_t* x, const void* res, int stream_type,
+                           const uint16_t* gain, float eps, const ep_norm_out& o, hipStream_t st);
+hipError_t launch_rms_norm_grad(const ep_shape& s, const void* h, int stream_type, const uint16_t* gain,
+                                const float* rstd, const uint16_t* dy, const void* d_stream, void* d_h, uint16_t* d_x,
+                                float* d_gain, char* ws, hipStream_t st);
+hipError_t launch_route(const ep_shape& s, const float* logits, const ep_router& r, int64_t* topk, float* w, char* ws,
+                        hipStream_t st);
+hipError_t launch_route_grad(const ep_shape& s, const float* logits, const ep_router& r, const int64_t* topk,
+                             const float* d_w, void* d_logits, int dtype, char* ws, hipStream_t st);
 constexpr uint32_t kSourceFusedTimeoutUs = 100000;  // longest wait for one batch flag of that launch
 
 }  // namespace ep

@@ -17,25 +17,17 @@
 
 #include "ep_internal.h"
 #include "ep_mfma.h"
+#include "few_route.h"
 
 namespace ep {
 namespace {
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWaves = kFewThreads / kWave;
 constexpr int kDownCols = 16;  // values of h per workgroup of the second launch
 constexpr int kDownSpan = 256; // contracted values per unit of work of the second launch
 // Workgroups of the second launch where they share outputs, two per CU: 106 tokens,
 // top-3 of 63 experts of 1536 x 896 take 87 us both launches together (256: 95);
 // 46 tokens, top-6 of 62 experts of 896 x 640 49 (1024: 56).
 constexpr int kDownGroups = 512;
-
-// One token of a used expert: token << 16 | row of its inner activations (token
-// * K + its first lane with that expert), and the sum of its lanes' weights.
-struct Route {
-    int id;
-    float w;
-};
 
 struct FewArgs {
     int T, H, K, E, F;
@@ -68,68 +60,6 @@ __device__ __forceinline__ bf16x8 e4m3_to_bf16(uint32_t lo, uint32_t hi) {
     r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1];
     r[4] = c[0], r[5] = c[1], r[6] = d[0], r[7] = d[1];
     return r;
-}
-
-// The blockIdx.y-th used expert in ascending order (-1 if there are fewer)
-// and its tokens in ascending order. Each workgroup finds them for itself:
-// the ids are a few KB in L2.
-struct Found {
-    int expert, used, tokens;
-};
-__device__ __forceinline__ Found find_expert(const FewArgs& a, uint32_t* bits, short* token, int* scratch) {
-    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
-    if (tid < EP_MAX_EXPERTS / 32) bits[tid] = 0u;
-    __syncthreads();
-    for (int i = tid; i < a.T * a.K; i += kFewThreads) {
-        const int64_t e = a.topk[i];
-        if (expert_ok(e, a.E)) atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    const uint64_t word = (uint64_t)bits[2 * lane] | (uint64_t)bits[2 * lane + 1] << 32;
-    const int n = __popcll(word);
-    int sum = n;
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int v = __shfl_up(sum, d);
-        if (lane >= d) sum += v;
-    }
-    Found f;
-    f.used = readlane(sum, kWave - 1);
-    f.expert = -1;
-    f.tokens = 0;
-    const int want = blockIdx.y;
-    const uint64_t in = __ballot(want >= sum - n && want < sum);
-    if (!in) return f;
-    const int src = __ffsll((unsigned long long)in) - 1;
-    uint64_t w = (uint64_t)(uint32_t)readlane((int)word, src) | (uint64_t)(uint32_t)readlane((int)(word >> 32), src) << 32;
-    for (int skip = want - readlane(sum - n, src); skip > 0; --skip) w &= w - 1;
-    f.expert = src * 64 + __ffsll((unsigned long long)w) - 1;
-
-    bool mine = false;
-    Route r = {-1, 0.f};
-    if (wave < 2) {
-        if (tid < a.T) {
-            for (int k = 0; k < a.K; ++k) {
-                if (a.topk[tid * a.K + k] != f.expert) continue;
-                if (r.id < 0) r.id = tid << 16 | (tid * a.K + k);
-                r.w += a.topk_w[tid * a.K + k];
-            }
-        }
-        mine = r.id >= 0;
-        const uint64_t m = __ballot(mine);
-        if (lane == 0) scratch[wave] = __popcll(m);
-    }
-    __syncthreads();
-    f.tokens = scratch[0] + scratch[1];
-    if (wave < 2 && mine) {
-        const uint64_t m = __ballot(true);
-        const int at = (wave ? scratch[0] : 0) + __popcll(m & ((1ull << lane) - 1));
-        token[at] = (short)tid;
-        scratch[2 + at] = r.id & 0xFFFF;
-        if (blockIdx.x == 0) a.routes[(int64_t)want * a.T + at] = r;
-    }
-    if (blockIdx.x == 0 && tid == 0) a.used[1 + want] = f.expert | f.tokens << 16;
-    __syncthreads();
-    return f;
 }
 
 // First launch: workgroup (x, y) computes 32 values of f for the tokens of the

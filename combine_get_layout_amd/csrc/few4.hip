@@ -1,0 +1,448 @@
+// few4.hip -- ep_moe_few_w4 on gfx950: the expert layer for a few tokens with
+// 4-bit weights, in the two launches of ep_moe_few.
+#include <algorithm>
+
+#include "ep_internal.h"
+#include "ep_mfma.h"
+#include "few_route.h"
+
+namespace ep {
+namespace {
+
+constexpr int kSpan = 256;  // contracted values per step (first launch) and per unit of work (second)
+constexpr int kDownGroups = 512;  // workgroups of the second launch where they share outputs, two per CU
+
+struct Few4Args {
+    int T, H, K, E, F;
+    const uint16_t* x;
+    const int64_t* topk;
+    const float* topk_w;
+    const uint8_t* w13;
+    const char* s13;
+    const uint8_t* w2;
+    const char* s2;
+    uint16_t* out;
+    uint32_t* err;
+    int* used;        // number of used experts, then expert | tokens << 16 of each
+    Route* routes;    // [used][T], each expert's tokens in ascending order
+    uint16_t* act;    // [T*K][2][F], row = first lane of (token, expert): values, rests
+    int* joined;      // [H/16, rounded up]: workgroups of the second launch that have stored their part
+    float* part;      // [splits][T][H]
+    int splits;       // workgroups of the second launch that share values of h
+};
+
+__device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// Eight codes (a byte holds two, the first in its low half) to bf16, exactly.
+// EP_W4_E2M1: the instruction's own conversion, times a power of two.
+// EP_W4_INT: code c as the e4m3 byte c, which stands for c * 2^-9 (codes below 8
+// as e4m3's denormals, the others as its first binade), times 2^9; the 8 that
+// codes stand above their values is taken off the products (`minus_eight`).
+template <int FORM>
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, float scale) {
+    bf16x2 a, b, c, d;
+    if constexpr (FORM == EP_W4_E2M1) {
+        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+    } else {
+        const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+        const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+    }
+    bf16x8 r;
+    r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1];
+    r[4] = c[0], r[5] = c[1], r[6] = d[0], r[7] = d[1];
+    return r;
+}
+
+// Scale of a row's columns from 128 * p + 32 * q on (p counts the row's blocks
+// of 128): blocks of 128 share a bf16, blocks of 32 have a byte.
+template <int FORM>
+__device__ __forceinline__ float load_scale(const char* scales, int64_t row, int cols, int p, int q) {
+    if constexpr (FORM == EP_W4_INT) {
+        if (p * 128 >= cols) return 0.f;
+        return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(scales)[row * (cols / 128) + p] << 16);
+    } else {
+        const int block = p * 4 + q;
+        if (block * 32 >= cols) return 1.0f;
+        return __uint_as_float((uint32_t) reinterpret_cast<const uint8_t*>(scales)[row * (cols / 32) + block] << 23);
+    }
+}
+
+// First launch: workgroup (x, y) computes RT / 2 * 16 values of f for the tokens
+// of the y-th used expert.
+struct Up4Shared {
+    uint32_t bits[EP_MAX_EXPERTS / 32];
+    short token[128];
+    int scratch[2 + 128];
+    float part[kFewWaves][4][16][17];
+};
+
+// Tokens [t0, t0 + 16 * NT) of the expert's list.
+template <int FORM, int RT, int NT>
+__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, int t0) {
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+    const int i = lane & 15, q = lane >> 4;
+    constexpr int GT = RT / 2, kCols = GT * 16;
+    const int f0 = blockIdx.x * kCols, cols = min(kCols, a.F - f0);
+    const uint32_t ld = (uint32_t)a.H / 2;
+    const uint8_t* w = a.w13 + ((int64_t)found.expert * 2 * a.F + f0) * ld;
+    // Gate rows, up rows and the tokens' rows; rows past F read as zeros.
+    const auto d_gate = buf_resource(w, cols * ld), d_up = buf_resource(w + (int64_t)a.F * ld, cols * ld);
+    const auto d_x = buf_resource(a.x, (uint32_t)a.T * a.H * 2);
+    const uint32_t row0 = i * ld + q * 16;
+    int64_t srow[RT];  // this lane's weight rows' scales
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        srow[r] = (int64_t)found.expert * 2 * a.F + r / GT * a.F + min(f0 + r % GT * 16 + i, a.F - 1);
+    const int steps = (a.H + kSpan - 1) / kSpan;
+    uint32_t xr[NT];
+    bool has[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        has[n] = t0 + n * 16 + i < found.tokens;
+        xr[n] = has[n] ? (uint32_t)sh.token[t0 + n * 16 + i] * a.H * 2 + q * 64 : 0u;
+    }
+    bf16x8 minus_eight;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
+    f32x4 acc[RT][NT] = {};
+    for (int s = wave; s < steps; s += kFewWaves) {
+        u32x4 wv[RT][2], xv[NT][8];
+        float sv[RT][2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            // Columns past H: past the end, zeros.
+            const uint32_t far = s * kSpan + p * 128 + q * 32 >= a.H ? kBufFar : 0u;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                wv[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, s * 128 + p * 64);
+                sv[r][p] = load_scale<FORM>(a.s13, srow[r], a.H, s * 2 + p, q);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    u32x4 v = {0u, 0u, 0u, 0u};
+                    if (has[n]) v = buf_load16(d_x, xr[n] + far, s * 512 + p * 256 + m * 16);
+                    xv[n][p * 4 + m] = v;
+                }
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            f32x4 base[NT] = {};
+            if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) base[n] = mfma_bf16(as_bf16(xv[n][p * 4 + m]), minus_eight, base[n]);
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                bf16x8 wf[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(wv[r][p][m], sv[r][p]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 c = FORM == EP_W4_INT ? base[n] : acc[r][n];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) c = mfma_bf16(as_bf16(xv[n][p * 4 + m]), wf[m], c);
+                    if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(sv[r][p], c[j], acc[r][n][j]);
+                    } else {
+                        acc[r][n] = c;
+                    }
+                }
+            }
+        }
+    }
+    settle(acc);
+    // Sum the waves' parts, 32 values of f at a time: thread -> (token of 16, f of 32).
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int g = 0; g < GT; g += 2) {
+            constexpr int kSub = GT < 2 ? 1 : 2;  // sub-tiles of 16 values in this pass
+#pragma unroll
+            for (int r = 0; r < 2 * kSub; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sh.part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][n][j];
+            __syncthreads();
+            const int tk = tid >> 5, c = tid & 31;
+            const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
+            if (at < found.tokens && f < a.F && c < 16 * kSub) {
+                float gate = 0.f, up = 0.f;
+#pragma unroll
+                for (int v = 0; v < kFewWaves; ++v) {
+                    gate += sh.part[v][c >> 4][tk][c & 15];
+                    up += sh.part[v][2 + (c >> 4)][tk][c & 15];
+                }
+                const float r = gate / (1.0f + __expf(-gate)) * up;
+                // Two bf16 values for the second product's matrix instruction, the
+                // rounded one (of a finite value bf16's largest at most) and what it
+                // leaves (nothing of an infinity or NaN).
+                uint32_t hi = f32_to_bf16(r);
+                if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
+                const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
+                uint16_t* act = a.act + (int64_t)sh.scratch[2 + at] * 2 * a.F + f;
+                act[0] = (uint16_t)hi;
+                act[a.F] = (uint16_t)f32_to_bf16(rest);
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <int FORM, int RT, int NT>
+__global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few4_up_kernel(Few4Args a) {
+    __shared__ Up4Shared sh;
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        if (tid == 0) a.err[0] = 0u;
+        if (a.splits > 1)
+            for (int n = tid; n * 16 < a.H; n += kFewThreads) a.joined[n] = 0;
+    }
+    const Found found = find_expert(a, sh.bits, sh.token, sh.scratch);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
+    if (found.expert < 0) return;
+    for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {
+        if (NT > 1 && found.tokens - t0 > 16)
+            up4_tokens<FORM, RT, NT>(a, found, sh, t0);
+        else
+            up4_tokens<FORM, RT, 1>(a, found, sh, t0);
+    }
+}
+
+// Second launch: workgroup x computes RT * 16 values of h for every token, or,
+// where `splits` workgroups (grid y) share them, its part. Unit u = (used expert,
+// span of 256 values of f); each wave takes a run of units. The matrix
+// instruction's 16 rows are 8 tokens of the expert, as rounded values (rows 0 to
+// 7) and as what those leave (rows 8 to 15). Sums per token lie in LDS, one set a
+// wave, and are added at the end in a fixed order.
+template <int FORM, int RT>
+__global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
+    constexpr int kCols = RT * 16, kLd = kCols + 1;
+    extern __shared__ float sums[];  // [kFewWaves][T][kLd]
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        bool bad = false;
+        for (int n = tid; n < a.T * a.K; n += kFewThreads) bad |= expert_bad(a.topk[n], a.E);
+        if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_EXPERT_ID);
+    }
+    const int i = lane & 15, q = lane >> 4;
+    const int h0 = blockIdx.x * kCols, cols = min(kCols, a.H - h0);
+    const int spans = (a.F + kSpan - 1) / kSpan;
+    const int units = a.used[0] * spans;
+    float* mine = sums + wave * a.T * kLd;
+    for (int n = lane; n < a.T * kLd; n += kWave) mine[n] = 0.f;
+    bf16x8 minus_eight;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
+
+    auto load_route = [&](int rank, int tokens, int t0) {
+        Route r = {0, 0.f};
+        if (q == 0 && t0 + i < tokens) r = a.routes[(int64_t)rank * a.T + t0 + i];
+        return r;
+    };
+    const uint32_t ld = (uint32_t)a.F / 2;
+    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld;
+    auto load_act = [&](int id, bool has, int span, u32x4 (&v)[8]) {
+        const uint16_t* p = a.act + ((int64_t)(id & 0xFFFF) * 2 + (i >> 3)) * a.F + span * kSpan;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            const int k = (m >> 2) * 128 + q * 32 + (m & 3) * 8;
+            v[m] = u32x4{0u, 0u, 0u, 0u};
+            if (has && span * kSpan + k < a.F) v[m] = ld16(p + k);
+        }
+    };
+    const int run = blockIdx.y * kFewWaves + wave, runs = a.splits * kFewWaves;
+    int u = (int)((int64_t)units * run / runs), entry = 0;
+    const int end = (int)((int64_t)units * (run + 1) / runs);
+    Route route = {0, 0.f};
+    float acc[RT][4] = {};
+    if (u < end) {
+        entry = __builtin_amdgcn_readfirstlane(a.used[1 + u / spans]);
+        route = load_route(u / spans, entry >> 16, 0);
+    }
+    while (u < end) {
+        const int rank = u / spans, span = u % spans, tokens = entry >> 16;
+        const int64_t e = entry & 0xFFFF;
+        u32x4 w[RT][2], v[8];
+        float sv[RT][2];
+        const auto d = buf_resource(a.w2 + (e * a.H + h0) * ld, w_bytes);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t far = span * kSpan + p * 128 + q * 32 >= a.F ? kBufFar : 0u;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                w[r][p] = buf_load16(d, w_off + r * 16 * ld + far, span * 128 + p * 64);
+                sv[r][p] = load_scale<FORM>(a.s2, e * a.H + min(h0 + r * 16 + i, a.H - 1), a.F, span * 2 + p, q);
+            }
+        }
+        load_act(__shfl(route.id, i & 7), (i & 7) < tokens, span, v);
+        const int next = u + 1;
+        int next_entry = entry;
+        Route next_route = route;
+        const bool last = next == end || span + 1 == spans;  // of the expert's spans here
+        if (last && next < end) {
+            next_entry = __builtin_amdgcn_readfirstlane(a.used[1 + next / spans]);
+            next_route = load_route(next / spans, next_entry >> 16, 0);
+        }
+        for (int t0 = 0; t0 < tokens; t0 += 8) {
+            f32x4 c[RT][2] = {};
+            if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(as_bf16(v[p * 4 + m]), minus_eight, c[0][p]);
+#pragma unroll
+                    for (int r = 1; r < RT; ++r) c[r][p] = c[0][p];
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        c[r][p] = mfma_bf16(as_bf16(v[p * 4 + m]), codes_to_bf16<FORM>(w[r][p][m], sv[r][p]), c[r][p]);
+            settle(c);
+            const Route now = route;
+            if (t0 + 8 < tokens) {  // more than 8 tokens: the weights stay, the tokens change
+                if (t0 & 8) route = load_route(rank, tokens, t0 + 8);
+                const int n = (~t0 & 8) + (i & 7);
+                load_act(__shfl(route.id, n), t0 + 8 + (i & 7) < tokens, span, v);
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[r][j] += FORM == EP_W4_INT ? fmaf(sv[r][1], c[r][1][j], sv[r][0] * c[r][0][j]) : c[r][0][j] + c[r][1][j];
+            if (tokens <= 8 && !last) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = (t0 & 8) + (q & 1) * 4 + j;
+                const int id = __shfl(now.id, n);
+                const float weight = __shfl(now.w, n);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    // Rows 8 to 15: the rests' products. Where the value's is not finite the
+                    // rest's is no part of the sum.
+                    const float rest = __shfl_xor(acc[r][j], 32);
+                    const float dot = __builtin_isfinite(acc[r][j]) ? acc[r][j] + rest : acc[r][j];
+                    acc[r][j] = 0.f;
+                    if (q < 2 && t0 + q * 4 + j < tokens) {
+                        float* sum = mine + (id >> 16) * kLd + r * 16 + i;
+                        *sum = fmaf(weight, dot, *sum);
+                    }
+                }
+            }
+        }
+        u = next, entry = next_entry, route = next_route;
+    }
+    __syncthreads();
+    for (int n = tid; n < a.T * kCols; n += kFewThreads) {
+        const int t = n / kCols, h = h0 + n % kCols;
+        if (n % kCols >= cols) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) v += sums[(w * a.T + t) * kLd + n % kCols];
+        if (a.splits == 1)
+            a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
+        else
+            __hip_atomic_store(a.part + ((int64_t)blockIdx.y * a.T + t) * a.H + h, v, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (a.splits == 1) return;
+    __shared__ int before;
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are acknowledged
+    __syncthreads();
+    if (tid == 0)
+        before = __hip_atomic_fetch_add(a.joined + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before != a.splits - 1) return;
+    for (int n = tid; n < a.T * kCols; n += kFewThreads) {
+        const int t = n / kCols, h = h0 + n % kCols;
+        if (n % kCols >= cols) continue;
+        float v = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < a.splits; ++p)
+            v += __hip_atomic_load(a.part + ((int64_t)p * a.T + t) * a.H + h, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
+    }
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// 16-value tiles of h per workgroup of the second launch.
+int down_tiles(const ep_shape& s) { return s.T <= 32 ? 2 : 1; }
+
+// Workgroups of the second launch for the same values of h: as many as fill the
+// chip, with a unit for every wave.
+int down_splits(const ep_shape& s, int F) {
+    const int64_t units = std::min<int64_t>(s.E, (int64_t)s.T * s.K) * ((F + kSpan - 1) / kSpan);
+    const int64_t cols = (s.H + 16 * down_tiles(s) - 1) / (16 * down_tiles(s));
+    return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), units / kFewWaves));
+}
+
+template <int FORM>
+void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
+    const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K), lanes = (int64_t)s.T * s.K;
+    const int64_t wide = (a.F + 63) / 64 * experts;
+    const bool many = s.T > 16 && (lanes > 16 * experts || (wide >= 1024 && lanes > 4 * experts));
+    const bool narrow = (int64_t)((a.F + 31) / 32) * experts < 1024;
+    const int cols = many ? 64 : narrow ? 16 : 32;
+    const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
+    hipLaunchKernelGGL((many ? few4_up_kernel<FORM, 8, 2> : narrow ? few4_up_kernel<FORM, 2, 1> : few4_up_kernel<FORM, 4, 1>),
+                       up, dim3(kFewThreads), 0, st, a);
+    const int tiles = down_tiles(s);
+    const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
+    const size_t lds = sizeof(float) * kFewWaves * (16 * tiles + 1) * s.T;  // 69,632 bytes at most
+    hipLaunchKernelGGL((tiles == 2 ? few4_down_kernel<FORM, 2> : few4_down_kernel<FORM, 1>), down, dim3(kFewThreads), lds,
+                       st, a);
+}
+
+}  // namespace
+
+WsFew ws_few_w4(const ep_shape& s, int F) {
+    WsFew w;
+    const size_t lanes = (size_t)s.T * s.K, used = std::min<size_t>(s.E, lanes);
+    w.used = 256;
+    w.routes = w.used + align256(4 * (1 + used));
+    w.act = w.routes + align256(sizeof(Route) * used * s.T);
+    w.joined = w.act + align256(4 * lanes * F);
+    w.part = w.joined + align256(4 * (((size_t)s.H + 15) / 16));
+    const size_t splits = down_splits(s, F);
+    w.total = w.part + (splits > 1 ? align256(4 * splits * s.T * s.H) : 0);
+    return w;
+}
+
+hipError_t launch_moe_few_w4(const ep_shape& s, const ep_tokens& tk, const ep_experts_w4& x, uint16_t* out, char* ws,
+                             hipStream_t st) {
+    uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+    if (s.T == 0) {
+        hipError_t e = launch_zero_words(err, 1, st);
+        return e != hipSuccess ? e : hipGetLastError();
+    }
+    const WsFew l = ws_few_w4(s, x.F);
+    const Few4Args a = {s.T, s.H, s.K, s.E, x.F, tk.x, tk.topk_idx, tk.topk_weights, x.w13,
+                        static_cast<const char*>(x.w13_scales), x.w2, static_cast<const char*>(x.w2_scales), out, err,
+                        reinterpret_cast<int*>(ws + l.used), reinterpret_cast<Route*>(ws + l.routes),
+                        reinterpret_cast<uint16_t*>(ws + l.act), reinterpret_cast<int*>(ws + l.joined),
+                        reinterpret_cast<float*>(ws + l.part), down_splits(s, x.F)};
+    if (x.form == EP_W4_INT)
+        launch<EP_W4_INT>(a, s, st);
+    else
+        launch<EP_W4_E2M1>(a, s, st);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -1,0 +1,450 @@
+// norm.hip -- ep_rms_norm and ep_rms_norm_grad on gfx950.
+#include <algorithm>
+
+#include "ep_internal.h"
+#include "ep_mfma.h"
+#include "ep_wave.h"
+
+namespace ep {
+namespace {
+
+struct NormArgs {
+    int T, H;
+    float eps;
+    const uint16_t* x;
+    const char* res;
+    const uint16_t* gain;
+    char* h;
+    uint16_t* y;
+    uint8_t* q;
+    float* scales;
+    float* rstd;
+};
+
+// Eight values of a bf16 or fp32 array.
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(v[j]), f[2 * j + 1] = bf16_hi(v[j]);
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+    return v;
+}
+template <bool WIDE>
+struct Eight {  // as loaded
+    u32x4 v[WIDE ? 2 : 1];
+};
+template <bool WIDE>
+__device__ __forceinline__ Eight<WIDE> load8(const void* base, int64_t at) {
+    Eight<WIDE> r;
+    if constexpr (WIDE) {
+        r.v[0] = ld16(static_cast<const float*>(base) + at);
+        r.v[1] = ld16(static_cast<const float*>(base) + at + 4);
+    } else {
+        r.v[0] = ld16(static_cast<const uint16_t*>(base) + at);
+    }
+    return r;
+}
+template <bool WIDE>
+__device__ __forceinline__ void floats8(const Eight<WIDE>& r, float (&f)[8]) {
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r.v[j >> 2][j & 3]);
+    } else {
+        unpack8(r.v[0], f);
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store8(void* base, int64_t at, const float (&f)[8]) {
+    if constexpr (WIDE) {
+        u32x4 a, b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = __float_as_uint(f[j]), b[j] = __float_as_uint(f[4 + j]);
+        st16(static_cast<float*>(base) + at, a);
+        st16(static_cast<float*>(base) + at + 4, b);
+    } else {
+        st16(static_cast<uint16_t*>(base) + at, pack8(f));
+    }
+}
+
+// Sum over the LANES consecutive threads that share a row, in each of them.
+template <int LANES>
+__device__ __forceinline__ float share_sum(float v, float* scratch) {
+    static_assert(LANES % kWave == 0, "whole waves");
+    v = wave_sum(v);
+    if constexpr (LANES == kWave) return v;
+    constexpr int kWaves = LANES / kWave;
+    const int wave = wave_in_block();
+    if (lane_id() == 0) scratch[wave] = v;
+    __syncthreads();
+    const float* s = scratch + wave / kWaves * kWaves;
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += s[w];
+    return v;
+}
+
+// One vector of eight: the normed values to the outputs.
+__device__ __forceinline__ void put_normed(const NormArgs& a, int64_t t, int c, const float (&v)[8]) {
+    if (a.y) st16(a.y + t * a.H + c, pack8(v));
+    if (a.q) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+        m = row_max(m);  // 16 lanes hold 128 channels
+        const float s = m < 1e-33f ? 1.0f : m * (1.0f / 448.0f);
+        const float inv = __builtin_amdgcn_rcpf(s);
+        u32x2 q;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            q[j] = pack_e4m3(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv, v[4 * j + 3] * inv);
+        *reinterpret_cast<u32x2*>(a.q + t * a.H + c) = q;
+        if (c % 128 == 0) a.scales[t * (a.H / 128) + c / 128] = s;
+    }
+}
+
+// LANES threads to a row, NV vectors of eight values to a thread (0: as many as
+// it takes, in two passes over the row).
+template <int LANES, int NV, bool WIDE>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(NormArgs a) {
+    constexpr int kThreads = LANES < 256 ? 256 : LANES;
+    __shared__ float scratch[kThreads / kWave];
+    const int tid = threadIdx.x % LANES;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    if (LANES <= kWave && row >= a.T) return;  // a workgroup with barriers has one row, which exists
+    const int64_t base = row * a.H;
+    // h of vector c: from memory, stored where it is asked for.
+    auto add = [&](int c, const Eight<false>& xv, const Eight<WIDE>& rv, float(&h)[8]) {
+        floats8<false>(xv, h);
+        if (a.res) {
+            float r[8];
+            floats8<WIDE>(rv, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] += r[j];
+            if constexpr (!WIDE) unpack8(pack8(h), h);
+        }
+        if (a.h) store8<WIDE>(a.h, base + c, h);
+    };
+    if constexpr (NV > 0) {
+        float h[NV][8];
+        Eight<false> xv[NV];
+        Eight<WIDE> rv[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = (n * LANES + tid) * 8;
+            if (c < a.H) {
+                xv[n] = load8<false>(a.x, base + c);
+                if (a.res) rv[n] = load8<WIDE>(a.res, base + c);
+            }
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = (n * LANES + tid) * 8;
+            if (c < a.H) {
+                add(c, xv[n], rv[n], h[n]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(h[n][j], h[n][j], sum);
+            }
+        }
+        sum = share_sum<LANES>(sum, scratch);
+        const float r = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+        if (a.rstd && tid == 0) a.rstd[row] = r;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = (n * LANES + tid) * 8;
+            if (c < a.H) {
+                float g[8];
+                unpack8(ld16(a.gain + c), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] *= h[n][j] * r;
+                put_normed(a, row, c, g);
+            }
+        }
+    } else {
+        float sum = 0.f;
+        for (int c = tid * 8; c < a.H; c += LANES * 8) {
+            float h[8];
+            Eight<WIDE> rv;
+            if (a.res) rv = load8<WIDE>(a.res, base + c);
+            add(c, load8<false>(a.x, base + c), rv, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(h[j], h[j], sum);
+        }
+        sum = share_sum<LANES>(sum, scratch);
+        const float r = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+        if (a.rstd && tid == 0) a.rstd[row] = r;
+        for (int c = tid * 8; c < a.H; c += LANES * 8) {
+            float h[8], g[8];
+            if (a.h) {  // as this thread stored it (residual may be gone)
+                floats8<WIDE>(load8<WIDE>(a.h, base + c), h);
+            } else {
+                Eight<WIDE> rv;
+                if (a.res) rv = load8<WIDE>(a.res, base + c);
+                add(c, load8<false>(a.x, base + c), rv, h);
+            }
+            unpack8(ld16(a.gain + c), g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] *= h[j] * r;
+            put_normed(a, row, c, g);
+        }
+    }
+}
+
+struct NormGradArgs {
+    int T, H;
+    const char* h;
+    const uint16_t* gain;
+    const float* rstd;
+    const uint16_t* dy;
+    const char* ds;
+    char* dh;
+    uint16_t* dx;
+    float* part;  // [workgroups][H]: each workgroup's rows' part of d_gain, or null
+};
+
+constexpr int kGradThreads = 512;
+
+// A workgroup takes every gridDim.x-th group of kGradThreads / LANES rows and
+// keeps its part of d_gain in registers.
+template <int LANES, int NV, bool WIDE>
+__global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads) void norm_grad_kernel(NormGradArgs a) {
+    constexpr int kThreads = kGradThreads < LANES ? LANES : kGradThreads, kRows = kThreads / LANES;
+    __shared__ float scratch[2][kThreads / kWave];
+    __shared__ float sums[kRows > 1 ? kThreads * 8 : 1];
+    const int tid = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const float inv_h = 1.0f / (float)a.H;
+    float dg[NV][8] = {};
+    const int groups = (a.T + kRows - 1) / kRows;
+    for (int64_t n0 = blockIdx.x, turn = 0; n0 < groups; n0 += gridDim.x, turn ^= 1) {
+        const int64_t row = n0 * kRows + sub, base = row * a.H;
+        const bool in = row < a.T;
+        Eight<false> dyv[NV];
+        Eight<WIDE> hv[NV], sv[NV];
+        const float r = in ? a.rstd[row] : 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = (n * LANES + tid) * 8;
+            if (in && c < a.H) {
+                dyv[n] = load8<false>(a.dy, base + c);
+                hv[n] = load8<WIDE>(a.h, base + c);
+                if (a.ds) sv[n] = load8<WIDE>(a.ds, base + c);
+            }
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = (n * LANES + tid) * 8;
+            if (in && c < a.H) {
+                float dy[8], h[8], g[8];
+                floats8<false>(dyv[n], dy);
+                floats8<WIDE>(hv[n], h);
+                unpack8(ld16(a.gain + c), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    dot = fmaf(dy[j] * g[j], h[j], dot);
+                    dg[n][j] = fmaf(dy[j], h[j] * r, dg[n][j]);
+                }
+            }
+        }
+        // The other half of scratch next time: a wave may still read this one.
+        dot = share_sum<LANES>(dot, scratch[turn]);
+        const float k = r * r * (dot * inv_h);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = (n * LANES + tid) * 8;
+            if (in && c < a.H && (a.dh || a.dx)) {
+                float dy[8], h[8], g[8], s[8] = {};
+                floats8<false>(dyv[n], dy);
+                floats8<WIDE>(hv[n], h);
+                if (a.ds) floats8<WIDE>(sv[n], s);
+                unpack8(ld16(a.gain + c), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = fmaf(r, fmaf(-k, h[j], dy[j] * g[j]), s[j]);
+                if (a.dh) store8<WIDE>(a.dh, base + c, s);
+                if (a.dx) st16(a.dx + base + c, pack8(s));
+            }
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * a.H;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c = (n * LANES + tid) * 8;
+        if constexpr (kRows > 1) {  // the workgroup's rows together, in order
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sums[j * kThreads + threadIdx.x] = dg[n][j];
+            __syncthreads();
+            if (sub == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int s = 1; s < kRows; ++s) dg[n][j] += sums[j * kThreads + s * LANES + tid];
+            }
+        }
+        if (sub == 0 && c < a.H) store8<true>(part, c, dg[n]);
+    }
+}
+
+// Rows too long for registers: one row to a workgroup at a time, in two passes,
+// without d_gain.
+template <bool WIDE>
+__global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
+    __shared__ float scratch[16];
+    const int64_t row = blockIdx.x, base = row * a.H;
+    const float r = a.rstd[row];
+    float dot = 0.f;
+    for (int c = threadIdx.x * 8; c < a.H; c += 8192) {
+        float dy[8], h[8], g[8];
+        floats8<false>(load8<false>(a.dy, base + c), dy);
+        floats8<WIDE>(load8<WIDE>(a.h, base + c), h);
+        unpack8(ld16(a.gain + c), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot = fmaf(dy[j] * g[j], h[j], dot);
+    }
+    dot = share_sum<1024>(dot, scratch);
+    const float k = r * r * (dot / (float)a.H);
+    for (int c = threadIdx.x * 8; c < a.H; c += 8192) {
+        float dy[8], h[8], g[8], s[8] = {};
+        floats8<false>(load8<false>(a.dy, base + c), dy);
+        floats8<WIDE>(load8<WIDE>(a.h, base + c), h);
+        unpack8(ld16(a.gain + c), g);
+        if (a.ds) floats8<WIDE>(load8<WIDE>(a.ds, base + c), s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = fmaf(r, fmaf(-k, h[j], dy[j] * g[j]), s[j]);
+        if (a.dh) store8<WIDE>(a.dh, base + c, s);
+        if (a.dx) st16(a.dx + base + c, pack8(s));
+    }
+}
+
+// Their d_gain: a thread takes eight columns and every gridDim.y-th row.
+template <bool WIDE>
+__global__ __launch_bounds__(256) void norm_gain_long_kernel(NormGradArgs a) {
+    const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c >= a.H) return;
+    float dg[8] = {};
+    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
+        float dy[8], h[8];
+        const float r = a.rstd[t];
+        floats8<false>(load8<false>(a.dy, t * a.H + c), dy);
+        floats8<WIDE>(load8<WIDE>(a.h, t * a.H + c), h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[j] = fmaf(dy[j], h[j] * r, dg[j]);
+    }
+    store8<true>(a.part + (int64_t)blockIdx.y * a.H, c, dg);
+}
+
+// d_gain from the parts: 64 columns to a workgroup, 16 threads of four columns
+// by 16 runs of parts.
+__global__ __launch_bounds__(256) void norm_gain_kernel(const float* part, int parts, int H, float* d_gain) {
+    __shared__ float4 sums[16][16];
+    const int col = threadIdx.x & 15, run = threadIdx.x >> 4, c = blockIdx.x * 64 + col * 4;
+    float4 s = {0.f, 0.f, 0.f, 0.f};
+    if (c < H) {
+        const int end = (run + 1) * parts / 16;
+#pragma unroll 4
+        for (int p = run * parts / 16; p < end; ++p) {
+            const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * H + c);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+    }
+    sums[run][col] = s;
+    __syncthreads();
+    if (run == 0 && c < H) {
+#pragma unroll
+        for (int n = 1; n < 16; ++n) {
+            const float4 v = sums[n][col];
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        *reinterpret_cast<float4*>(d_gain + c) = s;
+    }
+}
+
+constexpr int kGradGroups = 512;  // workgroups of norm_grad_kernel at most
+constexpr int kLongH = 32768;     // longest row held in registers
+
+int grad_parts(int T, int H) {
+    if (H > kLongH) return std::min(T, 64);
+    const int lanes = H <= 2048 ? 64 : H <= 8192 ? 256 : 1024, rows = std::max(1, kGradThreads / lanes);
+    return std::min((T + rows - 1) / rows, kGradGroups);
+}
+
+template <bool WIDE>
+void launch_norm(const NormArgs& a, hipStream_t st) {
+    const int vecs = (a.H + 7) / 8;
+    auto go = [&](auto kernel, int lanes) {
+        const int threads = std::max(lanes, 256), rows = threads / lanes;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(threads), 0, st, a);
+    };
+    if (vecs <= 64) return go(norm_kernel<64, 1, WIDE>, 64);
+    if (vecs <= 128) return go(norm_kernel<64, 2, WIDE>, 64);
+    if (vecs <= 256) return go(norm_kernel<64, 4, WIDE>, 64);
+    if (vecs <= 512) return go(norm_kernel<256, 2, WIDE>, 256);
+    if (vecs <= 1024) return go(norm_kernel<256, 4, WIDE>, 256);
+    if (vecs <= 2048) return go(norm_kernel<1024, 2, WIDE>, 1024);
+    if (vecs <= 4096) return go(norm_kernel<1024, 4, WIDE>, 1024);
+    go(norm_kernel<1024, 0, WIDE>, 1024);
+}
+
+template <bool WIDE>
+void launch_norm_grad(const NormGradArgs& a, int parts, hipStream_t st) {
+    const int vecs = (a.H + 7) / 8;
+    if (a.H > kLongH) {
+        if (a.dh || a.dx) hipLaunchKernelGGL(norm_grad_long_kernel<WIDE>, dim3((unsigned)a.T), dim3(1024), 0, st, a);
+        if (a.part)
+            hipLaunchKernelGGL(norm_gain_long_kernel<WIDE>, dim3((unsigned)((vecs + 255) / 256), (unsigned)parts),
+                               dim3(256), 0, st, a);
+        return;
+    }
+    auto go = [&](auto kernel, int lanes) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(std::max(lanes, kGradThreads)), 0, st, a);
+    };
+    if (vecs <= 64) return go(norm_grad_kernel<64, 1, WIDE>, 64);
+    if (vecs <= 128) return go(norm_grad_kernel<64, 2, WIDE>, 64);
+    if (vecs <= 256) return go(norm_grad_kernel<64, 4, WIDE>, 64);
+    if (vecs <= 512) return go(norm_grad_kernel<256, 2, WIDE>, 256);
+    if (vecs <= 1024) return go(norm_grad_kernel<256, 4, WIDE>, 256);
+    if (vecs <= 2048) return go(norm_grad_kernel<1024, 2, WIDE>, 1024);
+    go(norm_grad_kernel<1024, 4, WIDE>, 1024);
+}
+
+}  // namespace
+
+size_t ws_norm(const ep_shape& s) {
+    return 256 + (sizeof(float) * (size_t)grad_parts(s.T, s.H) * s.H + 255) / 256 * 256;
+}
+
+hipError_t launch_rms_norm(const ep_shape& s, const uint16_t* x, const void* res, int stream_type,
+                           const uint16_t* gain, float eps, const ep_norm_out& o, hipStream_t st) {
+    if (s.T == 0) return hipSuccess;
+    const NormArgs a = {s.T, s.H, eps, x, static_cast<const char*>(res), gain, static_cast<char*>(o.h), o.y, o.y_fp8,
+                        o.y_scales, o.rstd};
+    if (stream_type == EP_STREAM_F32)
+        launch_norm<true>(a, st);
+    else
+        launch_norm<false>(a, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_grad(const ep_shape& s, const void* h, int stream_type, const uint16_t* gain,
+                                const float* rstd, const uint16_t* dy, const void* d_stream, void* d_h, uint16_t* d_x,
+                                float* d_gain, char* ws, hipStream_t st) {
+    const int parts = grad_parts(s.T, s.H);
+    float* part = reinterpret_cast<float*>(ws + 256);
+    const NormGradArgs a = {s.T, s.H, static_cast<const char*>(h), gain, rstd, dy, static_cast<const char*>(d_stream),
+                            static_cast<char*>(d_h), d_x, d_gain ? part : nullptr};
+    if (s.T > 0) {
+        if (stream_type == EP_STREAM_F32)
+            launch_norm_grad<true>(a, parts, st);
+        else
+            launch_norm_grad<false>(a, parts, st);
+    }
+    if (d_gain)
+        hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((s.H + 63) / 64)), dim3(256), 0, st, part, parts, s.H, d_gain);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_PKG, "libep.so")
 EP_OK, EP_ERR_ARG, EP_ERR_UNSUPPORTED, EP_ERR_HIP, EP_ERR_DEVICE, EP_ERR_SCRATCH = 0, -1, -2, -3, -4, -5
 EP_LAYOUT_SCRATCH_BYTES = 4 << 20
 EP_DEVERR_EXPERT_ID, EP_DEVERR_CAPACITY, EP_DEVERR_FLAG, EP_DEVERR_TIMEOUT = 1, 2, 4, 8
+EP_DEVERR_LOGIT = 16
 EP_FUSED_WITHHOLD = 1
 EP_SEG_BF16, EP_SEG_FP8, EP_SEG_SCALES = 1, 2, 4
 EP_FMT_PLAIN, EP_FMT_CHUNKED = 0, 1
@@ -28,6 +29,9 @@ EP_HIER_SCALEOUT, EP_HIER_FORWARD = 1, 2
 EP_WEIGHT_NK, EP_WEIGHT_KN = 0, 1
 EP_GRAD_BF16, EP_GRAD_F32 = 0, 1
 EP_FEW_MAX_TOKENS = 128
+EP_STREAM_BF16, EP_STREAM_F32 = 0, 1
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_W4_INT, EP_W4_E2M1 = 0, 1
 
 _P = ctypes.c_void_p
 
@@ -74,6 +78,20 @@ class ep_experts(ctypes.Structure):
                                                             "w2_fp8", "w2_scales")]
 
 
+class ep_norm_out(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("h", "y", "y_fp8", "y_scales", "rstd")]
+
+
+class ep_router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "top_groups", "group_top", "normalize")] + \
+               [("scale", ctypes.c_float), ("bias", _P)]
+
+
+class ep_experts_w4(ctypes.Structure):
+    _fields_ = [("F", ctypes.c_int32), ("form", ctypes.c_int32)] + \
+               [(n, _P) for n in ("w13", "w13_scales", "w2", "w2_scales")]
+
+
 EXPORTS = ("ep_workspace_bytes", "ep_record_bytes", "ep_chunked_record_bytes", "ep_get_layout",
            "ep_get_layout_noalloc",
            "ep_dispatch", "ep_dispatch_expand", "ep_hierarchical_dispatch",
@@ -82,6 +100,8 @@ EXPORTS = ("ep_workspace_bytes", "ep_record_bytes", "ep_chunked_record_bytes", "
            "ep_source_workspace_bytes", "ep_source_layout", "ep_source_dispatch",
            "ep_copy_epilogue", "ep_source_dispatch_fused", "ep_expert_matmul", "ep_expert_swiglu",
            "ep_swiglu_grad", "ep_expert_wgrad", "ep_few_workspace_bytes", "ep_moe_few",
+           "ep_rms_norm", "ep_norm_workspace_bytes", "ep_rms_norm_grad", "ep_route", "ep_route_grad",
+           "ep_few_w4_workspace_bytes", "ep_moe_few_w4",
            "ep_clear_errors", "ep_check_errors", "ep_check_sticky_errors",
            "ep_status_string")
 
@@ -136,6 +156,16 @@ def lib() -> ctypes.CDLL:
     L.ep_few_workspace_bytes.argtypes = [sp, i32]
     L.ep_few_workspace_bytes.restype = sz
     L.ep_moe_few.argtypes = [sp, ctypes.POINTER(ep_tokens), ctypes.POINTER(ep_experts), _P, _P, sz, _P]
+    f32, rp = ctypes.c_float, ctypes.POINTER(ep_router)
+    L.ep_rms_norm.argtypes = [sp, _P, _P, ci, _P, f32, ctypes.POINTER(ep_norm_out), _P]
+    L.ep_norm_workspace_bytes.argtypes = [sp]
+    L.ep_norm_workspace_bytes.restype = sz
+    L.ep_rms_norm_grad.argtypes = [sp, _P, ci, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
+    L.ep_route.argtypes = [sp, _P, rp, _P, _P, _P, sz, _P]
+    L.ep_route_grad.argtypes = [sp, _P, rp, _P, _P, _P, ci, _P, sz, _P]
+    L.ep_few_w4_workspace_bytes.argtypes = [sp, i32]
+    L.ep_few_w4_workspace_bytes.restype = sz
+    L.ep_moe_few_w4.argtypes = [sp, ctypes.POINTER(ep_tokens), ctypes.POINTER(ep_experts_w4), _P, _P, sz, _P]
     L.ep_clear_errors.argtypes = [_P, _P]
     L.ep_check_errors.argtypes = [_P, _P, ctypes.POINTER(u32)]
     L.ep_check_sticky_errors.argtypes = [_P, _P, ctypes.POINTER(u32)]
@@ -146,7 +176,8 @@ def lib() -> ctypes.CDLL:
               "ep_combine", "ep_combine_expand", "ep_combine_two_level", "ep_source_layout",
               "ep_source_dispatch", "ep_copy_epilogue", "ep_source_dispatch_fused",
               "ep_expert_matmul", "ep_expert_swiglu", "ep_swiglu_grad", "ep_expert_wgrad",
-              "ep_moe_few", "ep_clear_errors",
+              "ep_moe_few", "ep_rms_norm", "ep_rms_norm_grad", "ep_route", "ep_route_grad",
+              "ep_moe_few_w4", "ep_clear_errors",
               "ep_check_errors",
               "ep_check_sticky_errors"):
         getattr(L, f).restype = ctypes.c_int
@@ -501,6 +532,86 @@ def ep_moe_few(shape, tokens: dict, experts: dict, out, ws, stream=None):
                             _ptr(out, "out", 2 * shape.T * H, dev), *_ws(ws), _stream_on(stream, dev)), "ep_moe_few")
 
 
+def ep_rms_norm(shape, x, residual, stream_type: int, gain, eps: float, out: dict, stream=None):
+    """out: any of "h", "y", "y_fp8" with "y_scales", "rstd" (h may be residual)."""
+    T, H = shape.T, shape.H
+    # No workspace: the call runs where x is.
+    dev = x.get_device() if isinstance(x, torch.Tensor) else None
+    if dev is not None and dev < 0:
+        raise ValueError("x: must be a GPU tensor")
+    wide = 4 if int(stream_type) == EP_STREAM_F32 else 2
+    need = dict(h=wide * T * H, y=2 * T * H, y_fp8=T * H, y_scales=4 * T * (H // 128), rstd=4 * T)
+    O = ep_norm_out(*[_ptr(out.get(n), n, need[n], dev) for n in need])
+    _check(lib().ep_rms_norm(ctypes.byref(shape), _ptr(x, "x", 2 * T * H, dev),
+                             _ptr(residual, "residual", wide * T * H, dev), int(stream_type),
+                             _ptr(gain, "gain", 2 * H, dev), float(eps), ctypes.byref(O),
+                             _stream(stream) if dev is None else _stream_on(stream, dev)), "ep_rms_norm")
+
+
+def ep_norm_workspace_bytes(shape: ep_shape) -> int:
+    return int(lib().ep_norm_workspace_bytes(ctypes.byref(shape)))
+
+
+def ep_rms_norm_grad(shape, h, stream_type: int, gain, rstd, dy, d_stream, d_h, d_x, d_gain, ws, stream=None):
+    dev = ws.get_device()
+    T, H = shape.T, shape.H
+    n = (4 if int(stream_type) == EP_STREAM_F32 else 2) * T * H
+    _check(lib().ep_rms_norm_grad(ctypes.byref(shape), _ptr(h, "h", n, dev), int(stream_type),
+                                  _ptr(gain, "gain", 2 * H, dev), _ptr(rstd, "rstd", 4 * T, dev),
+                                  _ptr(dy, "dy", 2 * T * H, dev), _ptr(d_stream, "d_stream", n, dev),
+                                  _ptr(d_h, "d_h", n, dev), _ptr(d_x, "d_x", 2 * T * H, dev),
+                                  _ptr(d_gain, "d_gain", 4 * H, dev), *_ws(ws), _stream_on(stream, dev)),
+           "ep_rms_norm_grad")
+
+
+def _router_struct(shape: ep_shape, router: dict, device) -> ep_router:
+    return ep_router(int(router["score"]), int(router.get("top_groups", shape.G)), int(router.get("group_top", 1)),
+                     int(router.get("normalize", 1)), float(router.get("scale", 1.0)),
+                     _ptr(router.get("bias"), "bias", 4 * shape.E, device))
+
+
+def ep_route(shape, logits, router: dict, topk_idx, topk_weights, ws, stream=None):
+    """router: {"score"} and, where they differ from the defaults, "top_groups" (all), "group_top" (1),
+    "normalize" (True), "scale" (1.0), "bias" (None)."""
+    dev = ws.get_device()
+    R = _router_struct(shape, router, dev)
+    T, K = shape.T, shape.K
+    _check(lib().ep_route(ctypes.byref(shape), _ptr(logits, "logits", 4 * T * shape.E, dev), ctypes.byref(R),
+                          _ptr(topk_idx, "topk_idx", 8 * T * K, dev),
+                          _ptr(topk_weights, "topk_weights", 4 * T * K, dev), *_ws(ws), _stream_on(stream, dev)),
+           "ep_route")
+
+
+def ep_route_grad(shape, logits, router: dict, topk_idx, d_topk_weights, d_logits, dtype: int, ws, stream=None):
+    """router: as for ep_route."""
+    dev = ws.get_device()
+    R = _router_struct(shape, router, dev)
+    T, E, K = shape.T, shape.E, shape.K
+    size = 4 if int(dtype) == EP_GRAD_F32 else 2
+    _check(lib().ep_route_grad(ctypes.byref(shape), _ptr(logits, "logits", 4 * T * E, dev), ctypes.byref(R),
+                               _ptr(topk_idx, "topk_idx", 8 * T * K, dev),
+                               _ptr(d_topk_weights, "d_topk_weights", 4 * T * K, dev),
+                               _ptr(d_logits, "d_logits", size * T * E, dev), int(dtype), *_ws(ws),
+                               _stream_on(stream, dev)), "ep_route_grad")
+
+
+def ep_few_w4_workspace_bytes(shape: ep_shape, F: int) -> int:
+    return int(lib().ep_few_w4_workspace_bytes(ctypes.byref(shape), int(F)))
+
+
+def ep_moe_few_w4(shape, tokens: dict, experts: dict, out, ws, stream=None):
+    """experts: {"F", "form" (EP_W4_*), "w13", "w13_scales", "w2", "w2_scales"}."""
+    dev = ws.get_device()
+    tk = _tokens_struct(shape, tokens, dev)
+    E, H, F, form = shape.E, shape.H, int(experts["F"]), int(experts["form"])
+    per = 2 / 128 if form == EP_W4_INT else 1 / 32  # bytes of scales a column
+    need = dict(w13=E * F * H, w13_scales=int(2 * E * F * H * per), w2=E * H * F // 2, w2_scales=int(E * H * F * per))
+    X = ep_experts_w4(F, form, *[_ptr(experts.get(n), n, need[n], dev) for n in need])
+    _check(lib().ep_moe_few_w4(ctypes.byref(shape), ctypes.byref(tk), ctypes.byref(X),
+                               _ptr(out, "out", 2 * shape.T * H, dev), *_ws(ws), _stream_on(stream, dev)),
+           "ep_moe_few_w4")
+
+
 def ep_clear_errors(ws, stream=None):
     _check(lib().ep_clear_errors(_ptr(ws, "workspace"), _stream(stream)), "ep_clear_errors")
 
@@ -553,6 +664,22 @@ def alloc_few_workspace(shape: ep_shape, F: int, device="cuda") -> torch.Tensor:
     n = ep_few_workspace_bytes(shape, F)
     if n == 0:
         raise RuntimeError("ep_few_workspace_bytes: unsupported shape or inner size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_norm_workspace(shape: ep_shape, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of ep_rms_norm_grad."""
+    n = ep_norm_workspace_bytes(shape)
+    if n == 0:
+        raise RuntimeError("ep_norm_workspace_bytes: unsupported shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_few_w4_workspace(shape: ep_shape, F: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of ep_moe_few_w4."""
+    n = ep_few_w4_workspace_bytes(shape, F)
+    if n == 0:
+        raise RuntimeError("ep_few_w4_workspace_bytes: unsupported shape or inner size")
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 

@@ -62,6 +62,7 @@ extern "C" {
 #define EP_DEVERR_CAPACITY 2u   /* a row index >= the given buffer capacity (not written / not read) */
 #define EP_DEVERR_FLAG 4u       /* a 512 B chunk flag != epoch (row dropped / skipped) */
 #define EP_DEVERR_TIMEOUT 8u    /* a bounded wait for a batch flag gave up (batch not forwarded) */
+#define EP_DEVERR_LOGIT 16u     /* a router logit or bias is NaN (taken as -infinity) */
 
 /* Payload pieces present in a token record (ep_record_bytes). */
 #define EP_SEG_BF16 1
@@ -84,6 +85,19 @@ extern "C" {
 /* Element type of a weight gradient (ep_expert_wgrad). */
 #define EP_GRAD_BF16 0
 #define EP_GRAD_F32 1
+
+/* Element type of the residual stream (ep_rms_norm, ep_rms_norm_grad). */
+#define EP_STREAM_BF16 0
+#define EP_STREAM_F32 1
+
+/* Scores that a router makes of its logits (ep_route). */
+#define EP_SCORE_SOFTMAX 0 /* exp(l[e]) / sum over all experts e' of exp(l[e']) */
+#define EP_SCORE_SIGMOID 1 /* 1 / (1 + exp(-l[e])) */
+
+/* Forms of 4-bit weights (ep_moe_few_w4). */
+#define EP_W4_INT 0  /* code - 8, times a bf16 scale for each row and 128 columns */
+#define EP_W4_E2M1 1 /* e2m1 (sign, 2 bits of exponent, 1 of fraction), times 2^(s - 127) for each
+                        row and 32 columns, s one byte (255: NaN) */
 
 /* Supported limits (EP_ERR_UNSUPPORTED beyond them). */
 #define EP_FEW_MAX_TOKENS 128 /* tokens of ep_moe_few */
@@ -555,6 +569,132 @@ size_t ep_few_workspace_bytes(const ep_shape *shape, int32_t F);
  * workspace must not overlap. */
 int ep_moe_few(const ep_shape *shape, const ep_tokens *tokens, const ep_experts *experts,
                uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Before the dispatch: norm and router ----------------------------------
+ * What makes the rows and the routing that ep_dispatch, ep_dispatch_expand and
+ * ep_moe_few take, and takes the gradients that the backward pass hands back.
+ * One layer, in calls (l = the router's product y W^T in 32 bits, a plain
+ * matrix product that the caller makes):
+ *   forward   ep_rms_norm (y bf16 and / or y_fp8 with y_scales, the stream h,
+ *             rstd), l, ep_route, ep_get_layout, ..., ep_combine_expand -> x of
+ *             the next ep_rms_norm (which adds it to the stream)
+ *   backward  ..., ep_swiglu_grad (d_topk_weights) -> ep_route_grad (d_logits;
+ *             ep_expert_matmul and ep_expert_wgrad with one expert take them
+ *             on in bf16, E % 8 == 0), d_y = the rows' and the router's part ->
+ *             ep_rms_norm_grad -> the stream's gradient and the gain's
+ * No call writes a row past shape->T. Sums are held in 32 bits. */
+
+/* Outputs of ep_rms_norm; NULL ones are left out. */
+typedef struct ep_norm_out {
+    void *h;          /* [T*H] the stream with x added, in the stream's type; may be `residual` itself */
+    uint16_t *y;      /* [T*H] bf16 */
+    uint8_t *y_fp8;   /* [T*H] e4m3, with y_scales (H % 128 == 0) */
+    float *y_scales;  /* [T*H/128] */
+    float *rstd;      /* [T] for ep_rms_norm_grad */
+} ep_norm_out;
+
+/* Root-mean-square norm of a residual stream: for each token t < T
+ *   h[t] = x[t] + residual[t], rounded to the stream's type (x[t] alone
+ *          where residual is NULL),
+ *   rstd[t] = 1 / sqrt(mean over H of h[t]^2 + eps),
+ *   v = h[t] * rstd[t] * gain,
+ *   y[t] = bf16_rne(v), and for every 128 channels, m their largest |v|,
+ *   y_scales = m / 448 (1 if m < 1e-33), y_fp8 = e4m3_rne(v * (1 / y_scales)).
+ * x: [T*H] bf16, residual: [T*H] of stream_type (EP_STREAM_*) or NULL, gain:
+ * [H] bf16, eps > 0 and finite, H <= EP_MAX_DIM. The norm is that of h as
+ * stored, so its gradient needs h alone. A row whose mean square passes 32
+ * bits has rstd 0. x, residual, gain, h, y and y_fp8 need 16 B aligned base
+ * pointers. out->h may be residual (same address); apart from that outputs
+ * must not overlap inputs or each other. At least one output. */
+int ep_rms_norm(const ep_shape *shape, const uint16_t *x, const void *residual, int stream_type,
+                const uint16_t *gain, float eps, const ep_norm_out *out, void *stream);
+
+/* Bytes of workspace of ep_rms_norm_grad (>= 256). Host only; 0 on bad args. */
+size_t ep_norm_workspace_bytes(const ep_shape *shape);
+
+/* Gradient of ep_rms_norm: with a = dy[t] * gain, r = rstd[t],
+ *   d = d_stream[t] + r * (a - h[t] * r^2 * mean over H of a * h[t])
+ *   d_h[t] = d in the stream's type (the gradient of residual, and of x),
+ *   d_x[t] = bf16_rne(d) (for x where the stream has 32 bits),
+ *   d_gain = sum over t of dy[t] * h[t] * r.
+ * h: [T*H] of stream_type as ep_rms_norm stored it (x itself for a bf16 stream
+ * without residual); dy: [T*H] bf16; d_stream: [T*H] of stream_type, the
+ * gradient that h has from the layers after, or NULL; d_h: like d_stream, may
+ * be it (same address); d_x: [T*H] bf16; d_gain: [H] fp32, overwritten (0 with
+ * T = 0). d_h, d_x and d_gain may be NULL, not all of them. The sum over t is
+ * made in a fixed order: calls repeat bit for bit. 16 B aligned base pointers;
+ * rstd 4 B. ws: ep_norm_workspace_bytes, 256 B aligned, needs no
+ * initialisation; calls on one workspace must not overlap. */
+int ep_rms_norm_grad(const ep_shape *shape, const void *h, int stream_type, const uint16_t *gain,
+                     const float *rstd, const uint16_t *dy, const void *d_stream, void *d_h,
+                     uint16_t *d_x, float *d_gain, void *ws, size_t ws_bytes, void *stream);
+
+/* How a router chooses and weighs. */
+typedef struct ep_router {
+    int32_t score;      /* EP_SCORE_* */
+    int32_t top_groups; /* groups of shape->G that a token's experts may lie in, 1..G (G: any);
+                           less than G: G <= 64 (EP_ERR_UNSUPPORTED) */
+    int32_t group_top;  /* a group ranks by the sum of its 1 or 2 largest keys */
+    int32_t normalize;  /* 1: weights of a token add up to `scale`; 0: they are scores times scale */
+    float scale;        /* finite */
+    const float *bias;  /* [E] added to the scores for the choice alone, or NULL */
+} ep_router;
+
+/* Router: K experts of each token and their weights from its logits.
+ *   s[e] = the score (EP_SCORE_*) of l = logits[t*E + e]
+ *   key[e] = s[e] + bias[e], in 64 bits; where bias is NULL and the groups do
+ *            not rank by sums of two, the logit itself (which orders alike)
+ *   groups (top_groups < G; group g holds experts [g*E/G, (g+1)*E/G), as in
+ *            the layout): the top_groups groups with the largest sums of
+ *            their group_top largest keys
+ *   topk_idx[t*K + k] = the expert with the k-th largest key of those groups
+ *   topk_weights[t*K + k] = scale * s / (sum of the K chosen s + 1e-20)  (normalize)
+ *                           scale * s                                    (otherwise)
+ * Equal keys go to the lower id. A masked expert, whose logit or key is
+ * -infinity, is never chosen and counts for nothing in a group's sum; lanes
+ * left without an expert get -1 and weight 0, as do all of a token without
+ * unmasked experts. Experts with a logit of +infinity share a softmax evenly.
+ * NaN logits and biases are taken as -infinity and set EP_DEVERR_LOGIT.
+ * logits: [T*E] fp32, topk_idx: [T*K], topk_weights: [T*K] fp32 (may be NULL).
+ * ws: ep_workspace_bytes(shape), for its error words; the call clears none
+ * (ep_get_layout clears word 0, word 1 keeps the report). */
+int ep_route(const ep_shape *shape, const float *logits, const ep_router *router, int64_t *topk_idx,
+             float *topk_weights, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of ep_route's weights for the logits, the choice held fixed (bias,
+ * groups and keys have none): with g[k] = scale * d_topk_weights[t*K + k],
+ * S = sum of the chosen s + 1e-20,
+ *   d_s[k] = (g[k] - sum_j g[j] s[j] / S) / S  (normalize),  g[k]  (otherwise)
+ *   d_logits[t*E + e] = s[e] * (d_s[e] - sum_k d_s[k] s[k])  (softmax)
+ *                       s[e] * (1 - s[e]) * d_s[e]           (sigmoid)
+ * d_s[e] summed over the lanes that hold e, 0 for the others. Lanes with -1
+ * have no part; ids < -1 or >= E neither, and set EP_DEVERR_EXPERT_ID. Masked
+ * experts get 0. d_logits: [T*E], bf16 or fp32 (dtype EP_GRAD_*), 16 B
+ * aligned. ws as in ep_route. */
+int ep_route_grad(const ep_shape *shape, const float *logits, const ep_router *router,
+                  const int64_t *topk_idx, const float *d_topk_weights, void *d_logits, int dtype,
+                  void *ws, size_t ws_bytes, void *stream);
+
+/* Weights of the experts in 4 bits: of a row's columns c the code of an even
+ * one lies in the low half of byte c / 2, of an odd one in the high half. */
+typedef struct ep_experts_w4 {
+    int32_t F;               /* inner size; EP_W4_INT: F and H % 128 == 0, EP_W4_E2M1: % 32 */
+    int32_t form;            /* EP_W4_* */
+    const uint8_t *w13;      /* [E][2F][H/2]: gate rows, then up rows */
+    const void *w13_scales;  /* [E][2F][H/128] bf16 or [E][2F][H/32] bytes */
+    const uint8_t *w2;       /* [E][H][F/2] */
+    const void *w2_scales;   /* [E][H][F/128] bf16 or [E][H][F/32] bytes */
+} ep_experts_w4;
+
+/* Bytes of workspace of ep_moe_few_w4, as ep_few_workspace_bytes. */
+size_t ep_few_w4_workspace_bytes(const ep_shape *shape, int32_t F);
+
+/* ep_moe_few with 4-bit weights: the same result for the values that codes and
+ * scales stand for (these are exact in the products, sums are held in 32
+ * bits), the same tokens, errors, workspace rules and limits. Longer batches
+ * go in parts of EP_FEW_MAX_TOKENS. Base pointers 16 B aligned. */
+int ep_moe_few_w4(const ep_shape *shape, const ep_tokens *tokens, const ep_experts_w4 *experts,
+                  uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
 /* Clear both workspace error words (a stream-ordered kernel, no memset
  * node). */

@@ -1,0 +1,482 @@
+"""The few-token layer with 4-bit weights (ep_moe_few_w4) against plain 64-bit
+arithmetic on the values that codes and scales stand for, and the layers that
+the norm, the router and the expert operators make together.
+
+Tolerances as in test_experts_gpu.py: a sum of n products in 32 bits is off by
+at most n * 2^-23 of the sum of their magnitudes. EP_W4_INT sums x * code and
+takes 8 * x off, so the magnitudes there are x * (code + 8) * scale.
+"""
+import pytest
+import torch
+
+from combine_get_layout_amd import ep
+from test_experts_gpu import (BF16, F32, F64, HALF_BF16, HALF_E4M3, U8, U23, act_bound, check, cleared, gpu, randn, routing,
+                              silu_parts)
+
+pytestmark = pytest.mark.gpu
+
+INT, E2M1 = 0, 1
+TABLE = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=F64)
+FORMS = pytest.mark.parametrize("form", [INT, E2M1], ids=["int", "e2m1"])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ep.lib()
+
+
+def values(code, scales, form):
+    """The values, and the magnitudes that enter the sums, of [..., n, k / 2] packed codes."""
+    c = torch.stack([code & 15, code >> 4], -1).flatten(-2).long()
+    if form == INT:
+        s = scales.double().repeat_interleave(128, -1)
+        return (c - 8).double() * s, (c + 8).double() * s.abs()
+    v = TABLE.to(c.device)[c] * torch.pow(2.0, scales.double() - 127).repeat_interleave(32, -1)
+    return v, v.abs()
+
+
+def four(g, E, n, k, form, spread=3):
+    """Random codes and scales of matrices that keep a vector's size."""
+    code = torch.randint(0, 256, (E, n, k // 2), generator=g).to(U8)
+    if form == INT:
+        s = (torch.rand((E, n, k // 128), generator=g) + 0.5) * (k ** -0.5 / 4.6)
+        s *= torch.where(torch.rand(s.shape, generator=g) < 0.3, -1.0, 1.0)
+        return code, s.to(BF16)
+    mid = 127 - round(torch.tensor(k ** 0.5 * 3).log2().item())
+    return code, torch.randint(mid - spread, mid + spread, (E, n, k // 32), generator=g).to(U8)
+
+
+def few_reference(x, w13, w2, idx, w, F, form):
+    """out and its bound in 64 bits; w13, w2: (codes, scales)."""
+    T, H = x.shape
+    out, bound = torch.zeros((T, H), dtype=F64), torch.zeros((T, H), dtype=F64)
+    xd = x.double()
+    for e in range(len(w13[0])):
+        hit = (idx == e)
+        ts = hit.any(1).nonzero()[:, 0]
+        if not len(ts):
+            continue
+        (a, am), (b2, bm) = values(w13[0][e], w13[1][e], form), values(w2[0][e], w2[1][e], form)
+        gu = xd[ts] @ a.T
+        acc = H * U23 * (xd[ts].abs() @ am.T)
+        gate, up, s, act = silu_parts(gu, F)
+        da = act_bound(gate, up, s, act, acc[:, :F], acc[:, F:])
+        da = da + 2.0 ** -16 * (act.abs() + da)  # two bf16 values: the rest is rounded, 2^-8 of 2^-8
+        we = (w.double() * hit).sum(1)[ts].unsqueeze(1)
+        wabs = (w.double().abs() * hit).sum(1)[ts].unsqueeze(1)
+        out[ts] += we * (act @ b2.T)
+        mag = (act.abs() + da) @ bm.T
+        bound[ts] += wabs * (da @ b2.abs().T + F * U23 * mag) + 80 * U23 * wabs * mag
+    bound = bound + 8 * U23 * out.abs()
+    return out, bound + HALF_BF16 * (out.abs() + bound)
+
+
+def experts(w13, w2, F, form):
+    return dict(F=F, form=form, w13=w13[0].cuda(), w13_scales=w13[1].cuda(), w2=w2[0].cuda(), w2_scales=w2[1].cuda())
+
+
+def few_call(x, idx, w, X, E, ws=None, out=None):
+    T, H = x.shape
+    shape = ep.make_shape(T, H, idx.shape[1], E, 1)
+    if ws is None:
+        ws = ep.alloc_few_w4_workspace(shape, X["F"]).fill_(0xAB)
+        ep.ep_clear_errors(ws)
+    if out is None:
+        out = torch.full((T, H), 7.0, dtype=BF16, device="cuda")
+    ep.ep_moe_few_w4(shape, dict(x=x.cuda(), topk_idx=idx.cuda(), topk_weights=w.cuda()), X, out, ws)
+    return out, ws
+
+
+FEW = [
+    # (T, H, F, E, K, options): sizes in steps of 32 (of 128 for integers)
+    (1, 256, 512, 16, 2, {}),
+    (1, 32, 32, 1, 1, {}),
+    (2, 96, 64, 3, 2, {}),
+    (13, 288, 160, 40, 3, dict(skip=0.2)),
+    (16, 640, 384, 8, 8, {}),
+    (17, 128, 256, 5, 4, dict(repeat=True)),
+    (33, 224, 288, 4, 2, {}),
+    (128, 160, 96, 2, 1, {}),            # 64 tokens and more to one expert
+    (36, 128, 128, 1, 1, {}),            # three token tiles of one expert
+    (128, 128, 128, 1024, 4, {}),        # many experts
+    (100, 64, 96, 3, 64, dict(repeat=True)),
+    (5, 1056, 736, 6, 6, {}),
+    (103, 512, 1024, 10, 8, {}),         # workgroups that share outputs, many tokens to each expert
+    (32, 1024, 512, 12, 5, {}),
+    (9, 2080, 544, 7, 2, {}),
+    (65, 1312, 672, 30, 6, dict(skip=0.1)),
+]
+
+
+def few_case(case, form):
+    T, H, F, E, K, opt = case
+    if form == INT:
+        H, F = -(-H // 128) * 128, -(-F // 128) * 128
+    g = torch.Generator().manual_seed(9)
+    idx, w = routing(T, K, E, 17, **opt)
+    return H, F, randn(g, T, H), idx, w, four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+
+
+@FORMS
+@pytest.mark.parametrize("case", FEW, ids=str)
+def test_few_w4(case, form):
+    H, F, x, idx, w, w13, w2 = few_case(case, form)
+    X = experts(w13, w2, F, form)
+    out, ws = few_call(x, idx, w, X, case[3])
+    assert ep.ep_check_errors(ws) == 0
+    ref, bound = few_reference(x, w13, w2, idx, w, F, form)
+    check(out, ref, bound, "out")
+    again, _ = few_call(x, idx, w, X, case[3], ws=ws)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+
+
+@FORMS
+def test_few_w4_every_code(form):
+    """Identity inputs read each weight back: every code at every place of a row, exactly."""
+    H, F = 256, 128
+    T = 64
+    code13 = torch.zeros((1, 2 * F, H // 2), dtype=U8)
+    r, c = torch.arange(2 * F).unsqueeze(1), torch.arange(H)
+    full = (r + c + c // 16).remainder(16).to(U8)
+    code13[0] = full[:, 0::2] | full[:, 1::2] << 4
+    s13 = torch.ones((1, 2 * F, H // 128)).to(BF16) if form == INT else torch.full((1, 2 * F, H // 32), 127).to(U8)
+    v13 = values(code13, s13, form)[0][0]
+    # Gate rows of +8 and more saturate; compare the first product through up rows only: gate = 64.
+    code13[0, :F] = 0x88 if form == INT else 0
+    code2 = torch.zeros((1, H, F // 2), dtype=U8)
+    one = 9 if form == INT else 2  # the code of 1
+    eight = torch.full((F // 2,), 0x88 if form == INT else 0, dtype=torch.long)
+    for h in range(F):
+        row = eight.clone()
+        row[h // 2] = (row[h // 2] & (0xF0 if h % 2 == 0 else 0x0F)) | one << (4 * (h % 2))
+        code2[0, h] = row.to(U8)
+    code2[0, F:] = 0x88 if form == INT else 0
+    s2 = torch.ones((1, H, F // 128)).to(BF16) if form == INT else torch.full((1, H, F // 32), 127).to(U8)
+    # The last column carries the gate: x = e_t + 64 e_last, gate rows have 1 there; t < 255.
+    code13[0, :F, -1] = (code13[0, :F, -1] & 0x0F) | one << 4
+    v13 = values(code13, s13, form)[0][0]
+    for t0 in range(0, H - 1, T):
+        n = min(T, H - 1 - t0)
+        x = torch.zeros((n, H))
+        x[torch.arange(n), t0 + torch.arange(n)] = 1.0
+        x[:, -1] = 64.0
+        x = x.to(BF16)
+        out, ws = few_call(x, torch.zeros((n, 1), dtype=torch.int64), torch.ones((n, 1)),
+                           experts((code13, s13), (code2, s2), F, form), 1)
+        gu = x.double() @ v13.T
+        assert (gu[:, :F] == 64).all()  # silu(64) = 64 in 32 bits
+        ref = 64 * gu[:, F:]            # exact in 32 bits; one rounding to bf16
+        check(out[:, :F], ref, HALF_BF16 * ref.abs() + 4 * U23 * ref.abs(), "weights read back")
+        assert (out[:, F:] == 0).all()
+
+
+def test_few_w4_scales_of_all_sizes():
+    """Powers of two from 2^-127 to 2^60 and NaN (255), in the second matrix, one row each."""
+    T, H, F = 3, 256, 32
+    g = torch.Generator().manual_seed(3)
+    x, w13 = randn(g, T, H), four(g, 1, 2 * F, H, E2M1)
+    code2 = torch.randint(0, 256, (1, H, F // 2), generator=g).to(U8)
+    s2 = torch.arange(H).clamp(max=187).to(U8).reshape(1, H, 1).clone()
+    s2[0, 200] = 255
+    idx, w = torch.zeros((T, 1), dtype=torch.int64), torch.ones((T, 1))
+    out, _ = few_call(x, idx, w, experts(w13, (code2, s2), F, E2M1), 1)
+    assert torch.isnan(out[:, 200]).all()
+    keep = [h for h in range(H) if h != 200]
+    ref, bound = few_reference(x, w13, (code2, torch.where(s2 == 255, 127, s2.long()).to(U8)), idx, w, F, E2M1)
+    # Below 2^-126 products and sums lose bits: a step of 2^-149 each.
+    check(out[:, keep].double(), ref[:, keep], bound[:, keep] + F * 2.0 ** -133 * 64, "out")
+
+
+@FORMS
+def test_few_w4_keeps_nonfinite_values_with_their_tokens(form):
+    """A NaN scale of one expert, NaN and infinite inputs reach only their own tokens; bad ids are
+    reported and skipped; a token without a lane gets zeros."""
+    T, H, F, E, K = 6, 128, 256, 4, 2
+    g = torch.Generator().manual_seed(2)
+    x, w13, w2 = randn(g, T, H), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    idx = torch.tensor([[0, 1], [1, 2], [-1, -1], [3, 0], [0, 99], [-7, 1]])
+    w = torch.full((T, K), 0.5)
+    clean = torch.where((idx < 0) | (idx >= E), -1, idx)
+    ref, bound = few_reference(x, w13, w2, clean, w, F, form)
+    bad13, bad2, badx = (w13[0], w13[1].clone()), (w2[0], w2[1].clone()), x.clone()
+    bad13[1][2, 3, 0] = float("nan") if form == INT else 255  # expert 2: token 1 only
+    bad2[1][3] = float("nan") if form == INT else 255         # expert 3: token 3 only
+    badx[4] = float("nan")                                    # token 4 only
+    out, ws = few_call(badx, idx, w, experts(bad13, bad2, F, form), E)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_EXPERT_ID
+    for t in (0, 2, 5):
+        check(out[t], ref[t], bound[t], f"token {t}")
+    assert (out[2] == 0).all()
+    assert torch.isnan(out[3]).all() and torch.isnan(out[4]).all() and torch.isnan(out[1]).all()
+
+
+@FORMS
+@pytest.mark.parametrize("F", [128, 2048])
+def test_few_w4_without_any_lane(form, F):
+    """All lanes skipped, or of ids that 32 bits would take for valid ones: zeros, and for the latter
+    the error (F: with and without shared outputs)."""
+    T, H, E, K = 9, 256, 4, 3
+    g = torch.Generator().manual_seed(1)
+    X = experts(four(g, E, 2 * F, H, form), four(g, E, H, F, form), F, form)
+    w = torch.full((T, K), float("nan"))
+    for ident, want in ((-1, 0), ((1 << 32) + 1, ep.EP_DEVERR_EXPERT_ID), (-(1 << 32), ep.EP_DEVERR_EXPERT_ID)):
+        out, ws = few_call(randn(g, T, H), torch.full((T, K), ident), w, X, E)
+        assert ep.ep_check_errors(ws) == want
+        assert (out == 0).all()
+
+
+@FORMS
+def test_few_w4_with_most_lanes_and_experts(form):
+    """128 tokens of 64 lanes over 4,096 experts: 8,192 lanes, most experts used."""
+    T, K, E = 128, 64, 4096
+    H, F = (128, 128) if form == INT else (32, 64)
+    g = torch.Generator().manual_seed(9)
+    idx, w = routing(T, K, E, 17)
+    x, w13, w2 = randn(g, T, H), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    out, ws = few_call(x, idx, w, experts(w13, w2, F, form), E)
+    assert ep.ep_check_errors(ws) == 0
+    ref, bound = few_reference(x, w13, w2, idx, w, F, form)
+    check(out, ref, bound, "out")
+
+
+@FORMS
+@pytest.mark.parametrize("wide", ["H", "F"])
+def test_few_w4_at_the_largest_dimensions(form, wide):
+    small = 128 if form == INT else 32
+    H, F = (1 << 20, small) if wide == "H" else (small, 1 << 20)
+    T, K, E = 3, 2, 2
+    g = torch.Generator().manual_seed(5)
+    idx = torch.tensor([[0, 1], [1, -1], [0, 0]])
+    w = torch.tensor([[0.5, -0.5], [1.0, 3.0], [0.25, 0.5]])
+    x, w13, w2 = randn(g, T, H), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    out, ws = few_call(x, idx, w, experts(w13, w2, F, form), E)
+    assert ep.ep_check_errors(ws) == 0
+    ref, bound = few_reference(x, w13, w2, idx, w, F, form)
+    check(out, ref, bound, "out")
+
+
+@FORMS
+def test_few_w4_in_graphs_and_on_two_streams(form):
+    """Two captured calls on a workspace each, replayed in turn with new inputs beside eager calls;
+    then two streams at once. Every result equals the first eager one, bit for bit."""
+    T, H, F, E, K = 40, 256, 1024, 12, 4
+    g = torch.Generator().manual_seed(8)
+    X = experts(four(g, E, 2 * F, H, form), four(g, E, H, F, form), F, form)
+    inputs = [gpu(randn(g, T, H), *routing(T, K, E, s, skip=0.1)) for s in (1, 2)]
+    ref = [few_call(*i, X, E)[0].clone() for i in inputs]
+    static = [[t.clone() for t in i] for i in inputs]
+    spaces = [few_call(*i, X, E)[1] for i in inputs]
+    outs = [torch.empty_like(r) for r in ref]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in inputs]
+    for n, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            few_call(*static[n], X, E, ws=spaces[n], out=outs[n])
+    for turn in range(6):
+        for n in (0, 1):
+            for s, t in zip(static[n], inputs[(n + turn) % 2]):
+                s.copy_(t)
+            graphs[n].replay()
+        few_call(*inputs[0], X, E)
+        torch.cuda.synchronize()
+        for n in (0, 1):
+            assert torch.equal(outs[n], ref[(n + turn) % 2]), (turn, n)
+        torch.randn(1000, device="cuda").sum().item()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(6):
+        for n in (0, 1):
+            with torch.cuda.stream(streams[n]):
+                got.append((n, few_call(*inputs[n], X, E, ws=spaces[n])[0]))
+    torch.cuda.synchronize()
+    for n, out in got:
+        assert torch.equal(out, ref[n])
+
+
+# --------------------------------------------------------------------------
+# Together: norm, router, experts
+# --------------------------------------------------------------------------
+
+def rel(a, r):
+    return ((a.double().cpu() - r).norm() / r.norm()).item()
+
+
+@FORMS
+@pytest.mark.parametrize("T", [1, 24])
+def test_decoding_layers(T, form):
+    """Three layers of a decoding step, the stream updated in place: norm, router product, router, expert
+    layer. Each against 64 bits on its own inputs, and the ids those of the definition.
+
+    y is rounded once (2^-8), the layer's output once; a layer's output is off by the former in 2-norm
+    times what the experts do to a relative change of their input: silu(g) u is at most quadratic, so 2 *
+    2^-8 and 2^-8 of its own rounding bound the norm."""
+    H, F, E, K, G = 256, 384, 16, 4, 4
+    g = torch.Generator().manual_seed(12)
+    stream = torch.randn((T, H), generator=g).to(BF16).cuda()
+    x = randn(g, T, H).cuda()
+    shape = ep.make_shape(T, H, K, E, G, G)
+    ws, few_ws = cleared(shape), ep.alloc_few_w4_workspace(shape, F)
+    ep.ep_clear_errors(few_ws)
+    for layer in range(3):
+        gain = (1 + 0.2 * torch.randn(H, generator=g)).to(BF16).cuda()
+        wr = torch.randn((E, H), generator=g).cuda() * H ** -0.5
+        bias = 0.05 * torch.randn(E, generator=g).cuda()
+        w13, w2 = four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+        before = stream.double() + x.double()
+        y = torch.empty((T, H), dtype=BF16, device="cuda")
+        ep.ep_rms_norm(shape, x, stream, ep.EP_STREAM_BF16, gain, 1e-6, dict(h=stream, y=y))
+        logits = y.float() @ wr.T
+        router = dict(score=ep.EP_SCORE_SIGMOID, top_groups=2, group_top=2, scale=2.5, bias=bias)
+        idx, w = torch.empty((T, K), dtype=torch.int64, device="cuda"), torch.empty((T, K), device="cuda")
+        ep.ep_route(shape, logits, router, idx, w, ws)
+        x = torch.empty((T, H), dtype=BF16, device="cuda")
+        ep.ep_moe_few_w4(shape, dict(x=y, topk_idx=idx, topk_weights=w), experts(w13, w2, F, form), x, few_ws)
+        assert ep.ep_check_sticky_errors(ws) == 0 and ep.ep_check_sticky_errors(few_ws) == 0
+
+        assert rel(stream, before.cpu()) <= HALF_BF16
+        h = stream.double()
+        y64 = h / torch.sqrt(h.pow(2).mean(1, keepdim=True) + 1e-6) * gain.double()
+        s = torch.sigmoid(logits.double())
+        key = s + bias.double()
+        best = key.view(T, G, E // G).topk(2, dim=2).values.sum(2).topk(2, dim=1).indices
+        allowed = torch.zeros((T, G), dtype=torch.bool, device="cuda").scatter_(1, best, True)
+        key = torch.where(allowed.repeat_interleave(E // G, 1), key, -1e9)
+        assert torch.equal(key.topk(K, dim=1).indices, idx)
+        lane = s.gather(1, idx)
+        ref, _ = few_reference(y64.cpu(), w13, w2, idx.cpu(), (2.5 * lane / lane.sum(1, keepdim=True)).cpu(), F, form)
+        assert rel(x, ref) <= 3 * HALF_BF16, layer
+
+
+def training_step(shape, F, router, args, b):
+    """Norm, router, dispatch of bf16 and 8-bit rows, experts, combine, and all of it backward."""
+    x, res, gain, wr, w13, w2, dout, d_h_later = args
+    T, H, K, E = shape.T, shape.H, shape.K, shape.E
+    N = T * K
+
+    def buf(name, *size, dtype=BF16):
+        if name not in b:
+            b[name] = torch.zeros(size, dtype=dtype, device="cuda")
+        return b[name]
+
+    if "L" not in b:
+        b["L"], b["ws"] = ep.alloc_layout(shape, expand=True), ep.alloc_workspace(shape)
+        ep.ep_clear_errors(b["ws"])
+        b["nws"] = ep.alloc_norm_workspace(shape)
+        b["recv"] = ep.alloc_recv(shape, N, fp8=True, scales=True)
+        b["d_recv"] = ep.alloc_recv(shape, N, meta=False)
+        b["ones"] = torch.ones((T, K), device="cuda")
+        b["one_expert"] = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    L, ws = b["L"], b["ws"]
+    h, y, rstd = buf("h", T, H, dtype=F32), buf("y", T, H), buf("rstd", T, dtype=F32)
+    y8, ys = buf("y8", T, H, dtype=U8), buf("ys", T, H // 128, dtype=F32)
+    ep.ep_rms_norm(shape, x, res, ep.EP_STREAM_F32, gain, 1e-6, dict(h=h, y=y, y_fp8=y8, y_scales=ys, rstd=rstd))
+    logits = buf("logits", T, E, dtype=F32)
+    torch.matmul(y.float(), wr.float().T, out=logits)
+    idx, w = buf("idx", T, K, dtype=torch.int64), buf("w", T, K, dtype=F32)
+    ep.ep_route(shape, logits, router, idx, w, ws)
+    ep.ep_get_layout(shape, idx, L, ws)
+    ep.ep_dispatch_expand(shape, L, dict(x=y, x_fp8=y8, x_scales=ys, topk_idx=idx, topk_weights=w), b["recv"], N, ws)
+    act, q, sc = buf("act", N, F), buf("q", N, 2 * F, dtype=U8), buf("sc", N, 2 * F // 128, dtype=F32)
+    ep.ep_expert_swiglu(shape, L, b["recv"]["x"], N, w13, F, act, q, sc, ws)
+    ye, out = buf("ye", N, H), buf("out", T, H)
+    ep.ep_expert_matmul(shape, L, act, N, F, w2, H, ep.EP_WEIGHT_NK, ye, ws)
+    ep.ep_combine_expand(shape, L, ye, N, 2 * H, ep.EP_FMT_PLAIN, 0, w, out, ws)
+
+    ep.ep_dispatch_expand(shape, L, dict(x=dout, topk_idx=idx), b["d_recv"], N, ws)
+    dye = b["d_recv"]["x"]
+    d_act, d_gu, act_w = buf("d_act", N, F), buf("d_gu", N, 2 * F), buf("act_w", N, F)
+    d_w, d_logits = buf("d_w", T, K, dtype=F32), buf("d_logits", T, E)
+    ep.ep_expert_matmul(shape, L, dye, N, H, w2, F, ep.EP_WEIGHT_KN, d_act, ws)
+    ep.ep_swiglu_grad(shape, L, F, q, sc, d_act, N, w, d_gu, act_w, d_w, ws)
+    dw2, dw13 = buf("dw2", E, H, F, dtype=F32), buf("dw13", E, 2 * F, H, dtype=F32)
+    ep.ep_expert_wgrad(shape, L, dye, N, H, dict(x=act_w), F, dw2, ep.EP_GRAD_F32, ws)
+    rows8 = dict(x_fp8=b["recv"]["x_fp8"], x_scales=b["recv"]["x_scales"])
+    ep.ep_expert_wgrad(shape, L, d_gu, N, 2 * F, rows8, H, dw13, ep.EP_GRAD_F32, ws)
+    dxr, dy = buf("dxr", N, H), buf("dy", T, H)
+    ep.ep_expert_matmul(shape, L, d_gu, N, 2 * F, w13, H, ep.EP_WEIGHT_KN, dxr, ws)
+    ep.ep_combine_expand(shape, L, dxr, N, 2 * H, ep.EP_FMT_PLAIN, 0, b["ones"], dy, ws)
+    ep.ep_route_grad(shape, logits, router, idx, d_w, d_logits, ep.EP_GRAD_BF16, ws)
+    dense, L1 = ep.make_shape(T, H, 1, 1, 1), dict(expert_offsets=b["one_expert"])
+    dwr, dyr = buf("dwr", 1, E, H, dtype=F32), buf("dyr", T, H)
+    ep.ep_expert_wgrad(dense, L1, d_logits, T, E, dict(x=y), H, dwr, ep.EP_GRAD_F32, ws)
+    ep.ep_expert_matmul(dense, L1, d_logits, T, E, wr, H, ep.EP_WEIGHT_KN, dyr, ws)
+    dy.add_(dyr)
+    d_h, d_x, d_gain = buf("d_h", T, H, dtype=F32), buf("d_x", T, H), buf("d_gain", H, dtype=F32)
+    ep.ep_rms_norm_grad(shape, h, ep.EP_STREAM_F32, gain, rstd, dy, d_h_later, d_h, d_x, d_gain, b["nws"])
+    return b
+
+
+def training_case(T, H, F, E, seed=6):
+    g = torch.Generator().manual_seed(seed)
+    return [randn(g, T, H), torch.randn((T, H), generator=g), (1 + 0.2 * torch.randn(H, generator=g)).to(BF16),
+            randn(g, E, H, scale=H ** -0.5), randn(g, E, 2 * F, H, scale=H ** -0.5), randn(g, E, H, F, scale=F ** -0.5),
+            randn(g, T, H), torch.randn((T, H), generator=g)]
+
+
+@pytest.mark.parametrize("score", [ep.EP_SCORE_SOFTMAX, ep.EP_SCORE_SIGMOID], ids=["softmax", "sigmoid"])
+def test_training_layer_forward_and_backward(score):
+    """A layer's training step from the stream on, against automatic differentiation in 64 bits with the
+    same choice of experts.
+
+    The output passes four roundings to bf16 (y twice as strong, silu(g) u being at most quadratic; act,
+    ye, out): 5 * 2^-8. The backward uses g and u from 8 bits and the rows from 8 bits (2^-4 at most each,
+    which enters through products of two: 2 * 2^-4) beside bf16 roundings on the way, at most eight."""
+    T, H, F, E, K = 150, 256, 256, 8, 3
+    args = training_case(T, H, F, E)
+    shape = ep.make_shape(T, H, K, E, 1)
+    router = dict(score=score, normalize=True, scale=1.5)
+    b = training_step(shape, F, router, gpu(*args), {})
+    assert ep.ep_check_sticky_errors(b["ws"]) == 0
+    x, res, gain, wr, w13, w2 = (t.double().requires_grad_() for t in args[:6])
+    h = x + res
+    y = h / torch.sqrt(h.pow(2).mean(1, keepdim=True) + 1e-6) * gain
+    logits = y @ wr.T
+    s = torch.softmax(logits, 1) if score == ep.EP_SCORE_SOFTMAX else torch.sigmoid(logits)
+    idx = b["idx"].cpu()
+    w = s.gather(1, idx)
+    w = 1.5 * w / w.sum(1, keepdim=True)
+    out = torch.zeros((T, H), dtype=F64)
+    for e in range(E):
+        t, k = (idx == e).nonzero(as_tuple=True)
+        gu = y[t] @ w13[e].T
+        a = gu[:, :F] * torch.sigmoid(gu[:, :F]) * gu[:, F:]
+        out = out.index_add(0, t, w[t, k].unsqueeze(1) * (a @ w2[e].T))
+    ((out * args[6].double()).sum() + (h * args[7].double()).sum()).backward()
+    assert rel(b["out"], out.detach()) <= 5 * HALF_BF16
+    grads = dict(d_h=res.grad, d_x=x.grad, d_gain=gain.grad, dw13=w13.grad, dw2=w2.grad)
+    for name, ref in grads.items():
+        assert rel(b[name], ref) <= 2 * HALF_E4M3 + 8 * HALF_BF16, name
+    assert rel(b["dwr"][0], wr.grad) <= 2 * HALF_E4M3 + 8 * HALF_BF16
+
+
+def test_training_layer_in_a_graph():
+    """Captured while the buffers of an eager step live, replayed with new inputs and eager work between;
+    every replay equals the eager result bit for bit."""
+    T, H, F, E, K = 100, 128, 128, 8, 2  # the router's products take E in multiples of 8
+    shape = ep.make_shape(T, H, K, E, 1)
+    router = dict(score=ep.EP_SCORE_SOFTMAX, normalize=False)
+    inputs = [gpu(*training_case(T, H, F, E, seed)) for seed in (1, 2, 3)]
+    names = ("h", "out", "idx", "d_h", "d_x", "d_gain", "dw13", "dw2", "dwr", "d_logits")
+    eager = []
+    for args in inputs:
+        b = training_step(shape, F, router, args, {})
+        torch.cuda.synchronize()
+        eager.append({n: b[n].clone() for n in names})
+    static, b = [t.clone() for t in inputs[0]], {}
+    training_step(shape, F, router, static, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        training_step(shape, F, router, static, b)
+    for i in (0, 1, 2, 1, 0):
+        for s, t in zip(static, inputs[i]):
+            s.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(b[n].view(U8), eager[i][n].view(U8)), (i, n)
+        torch.randn(1000, device="cuda").sum().item()
+        training_step(shape, F, router, inputs[i], {})
