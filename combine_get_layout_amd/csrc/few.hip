@@ -22,6 +22,8 @@
 namespace ep {
 namespace {
 
+constexpr int kFewThreads = 512;
+constexpr int kFewWaves = kFewThreads / kWave;
 constexpr int kDownCols = 16;  // values of h per workgroup of the second launch
 constexpr int kDownSpan = 256; // contracted values per unit of work of the second launch
 // Workgroups of the second launch where they share outputs, two per CU: 106 tokens,
@@ -214,7 +216,7 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_up_kernel(Fe
         if (a.splits > 1)
             for (int n = tid; n * kDownCols < a.H; n += kFewThreads) a.joined[n] = 0;
     }
-    const Found found = find_expert(a, sh.bits, sh.token, sh.scratch);
+    const Found found = find_expert<kFewThreads>(a, sh.bits, sh.token, sh.scratch);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
     for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {

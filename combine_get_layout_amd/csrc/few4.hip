@@ -9,8 +9,14 @@
 namespace ep {
 namespace {
 
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
 constexpr int kSpan = 256;  // contracted values per step (first launch) and per unit of work (second)
 constexpr int kDownGroups = 512;  // workgroups of the second launch where they share outputs, two per CU
+
+// The offset of a lane that loads nothing: past the end of x and, with kBufFar
+// added, still past it.
+constexpr uint32_t kBufNone = 0x40000000u;
 
 struct Few4Args {
     int T, H, K, E, F;
@@ -60,19 +66,28 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, float scale) {
     return r;
 }
 
-// Scale of a row's columns from 128 * p + 32 * q on (p counts the row's blocks
-// of 128): blocks of 128 share a bf16, blocks of 32 have a byte.
+// Scales: of a row's blocks of 128 columns a bf16 each, or a byte for 32 of them.
+// Loaded as they lie (past the descriptor's end: 0, beside codes of 0), made a
+// float where they are used, so that no load is waited for before the others
+// have been sent off.
 template <int FORM>
-__device__ __forceinline__ float load_scale(const char* scales, int64_t row, int cols, int p, int q) {
-    if constexpr (FORM == EP_W4_INT) {
-        if (p * 128 >= cols) return 0.f;
-        return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(scales)[row * (cols / 128) + p] << 16);
-    } else {
-        const int block = p * 4 + q;
-        if (block * 32 >= cols) return 1.0f;
-        return __uint_as_float((uint32_t) reinterpret_cast<const uint8_t*>(scales)[row * (cols / 32) + block] << 23);
+struct ScaleRow {
+    static constexpr int kShare = FORM == EP_W4_INT ? 128 : 32, kBytes = FORM == EP_W4_INT ? 2 : 1;
+    static __device__ __forceinline__ uint32_t bytes(int cols) { return (uint32_t)(cols / kShare) * kBytes; }
+    // Of a row's columns from 128 * p + 32 * q on, past the scalar offset's.
+    static __device__ __forceinline__ uint32_t offset(int p, int q) {
+        return FORM == EP_W4_INT ? p * 2u : p * 4u + q;
     }
-}
+    static __device__ __forceinline__ uint32_t load(__amdgpu_buffer_rsrc_t d, uint32_t off, uint32_t scalar_off) {
+        if constexpr (FORM == EP_W4_INT)
+            return __builtin_amdgcn_raw_buffer_load_b16(d, (int)off, (int)scalar_off, 0);
+        else
+            return __builtin_amdgcn_raw_buffer_load_b8(d, (int)off, (int)scalar_off, 0);
+    }
+    static __device__ __forceinline__ float value(uint32_t v) {
+        return __uint_as_float(v << (FORM == EP_W4_INT ? 16 : 23));
+    }
+};
 
 // First launch: workgroup (x, y) computes RT / 2 * 16 values of f for the tokens
 // of the y-th used expert.
@@ -80,13 +95,22 @@ struct Up4Shared {
     uint32_t bits[EP_MAX_EXPERTS / 32];
     short token[128];
     int scratch[2 + 128];
-    float part[kFewWaves][4][16][17];
+    float part[kWaves][4][16][17];
+};
+
+// What a wave loads for one step.
+template <int RT, int NT>
+struct UpStage {
+    u32x4 w[RT][2];
+    uint32_t scale[RT][2];
+    u32x4 x[NT][8];
 };
 
 // Tokens [t0, t0 + 16 * NT) of the expert's list.
 template <int FORM, int RT, int NT>
 __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, int t0) {
-    const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
+    using Scale = ScaleRow<FORM>;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     const int i = lane & 15, q = lane >> 4;
     constexpr int GT = RT / 2, kCols = GT * 16;
     const int f0 = blockIdx.x * kCols, cols = min(kCols, a.F - f0);
@@ -96,43 +120,39 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
     const auto d_gate = buf_resource(w, cols * ld), d_up = buf_resource(w + (int64_t)a.F * ld, cols * ld);
     const auto d_x = buf_resource(a.x, (uint32_t)a.T * a.H * 2);
     const uint32_t row0 = i * ld + q * 16;
-    int64_t srow[RT];  // this lane's weight rows' scales
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        srow[r] = (int64_t)found.expert * 2 * a.F + r / GT * a.F + min(f0 + r % GT * 16 + i, a.F - 1);
+    const uint32_t lds = Scale::bytes(a.H);
+    const char* sc = a.s13 + ((int64_t)found.expert * 2 * a.F + f0) * lds;
+    const auto s_gate = buf_resource(sc, cols * lds), s_up = buf_resource(sc + (int64_t)a.F * lds, cols * lds);
     const int steps = (a.H + kSpan - 1) / kSpan;
     uint32_t xr[NT];
     bool has[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         has[n] = t0 + n * 16 + i < found.tokens;
-        xr[n] = has[n] ? (uint32_t)sh.token[t0 + n * 16 + i] * a.H * 2 + q * 64 : 0u;
+        xr[n] = has[n] ? (uint32_t)sh.token[t0 + n * 16 + i] * a.H * 2 + q * 64 : kBufNone;
     }
     bf16x8 minus_eight;
 #pragma unroll
     for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
     f32x4 acc[RT][NT] = {};
-    for (int s = wave; s < steps; s += kFewWaves) {
-        u32x4 wv[RT][2], xv[NT][8];
-        float sv[RT][2];
+    auto load = [&](int s, UpStage<RT, NT>& g) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             // Columns past H: past the end, zeros.
             const uint32_t far = s * kSpan + p * 128 + q * 32 >= a.H ? kBufFar : 0u;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                wv[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, s * 128 + p * 64);
-                sv[r][p] = load_scale<FORM>(a.s13, srow[r], a.H, s * 2 + p, q);
+                g.w[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, s * 128 + p * 64);
+                g.scale[r][p] = Scale::load(r < GT ? s_gate : s_up, (i + r % GT * 16) * lds + Scale::offset(p, q) + far,
+                                            s * (256 / Scale::kShare * Scale::kBytes));
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    u32x4 v = {0u, 0u, 0u, 0u};
-                    if (has[n]) v = buf_load16(d_x, xr[n] + far, s * 512 + p * 256 + m * 16);
-                    xv[n][p * 4 + m] = v;
-                }
+                for (int m = 0; m < 4; ++m) g.x[n][p * 4 + m] = buf_load16(d_x, xr[n] + far, s * 512 + p * 256 + m * 16);
         }
+    };
+    auto multiply = [&](const UpStage<RT, NT>& g) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             f32x4 base[NT] = {};
@@ -140,30 +160,46 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) base[n] = mfma_bf16(as_bf16(xv[n][p * 4 + m]), minus_eight, base[n]);
+                    for (int m = 0; m < 4; ++m) base[n] = mfma_bf16(as_bf16(g.x[n][p * 4 + m]), minus_eight, base[n]);
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
+                const float scale = Scale::value(g.scale[r][p]);
                 bf16x8 wf[4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(wv[r][p][m], sv[r][p]);
+                for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(g.w[r][p][m], scale);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     f32x4 c = FORM == EP_W4_INT ? base[n] : acc[r][n];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) c = mfma_bf16(as_bf16(xv[n][p * 4 + m]), wf[m], c);
+                    for (int m = 0; m < 4; ++m) c = mfma_bf16(as_bf16(g.x[n][p * 4 + m]), wf[m], c);
                     if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(sv[r][p], c[j], acc[r][n][j]);
+                        for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(scale, c[j], acc[r][n][j]);
                     } else {
                         acc[r][n] = c;
                     }
                 }
             }
         }
+    };
+    // The next step's loads are in flight while this one is multiplied; those past
+    // the last step find nothing (a branch around them would make the compiler
+    // wait for everything).
+    UpStage<RT, NT> g0, g1;
+    load(wave, g0);
+    for (int s = wave; s < steps; s += 2 * kWaves) {
+        load(s + kWaves, g1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(g0);
+        __builtin_amdgcn_sched_barrier(0);
+        load(s + 2 * kWaves, g0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(g1);
+        __builtin_amdgcn_sched_barrier(0);
     }
     settle(acc);
-    // Sum the waves' parts, 32 values of f at a time: thread -> (token of 16, f of 32).
+    // Sum the waves' parts, 32 values of f at a time.
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -175,12 +211,14 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                 for (int j = 0; j < 4; ++j)
                     sh.part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][n][j];
             __syncthreads();
-            const int tk = tid >> 5, c = tid & 31;
-            const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
-            if (at < found.tokens && f < a.F && c < 16 * kSub) {
+#pragma unroll
+            for (int c0 = 0; c0 < 16 * 32; c0 += kThreads) {
+                const int tk = (c0 + tid) >> 5, c = tid & 31;
+                const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
+                if (at >= found.tokens || f >= a.F || c >= 16 * kSub) continue;
                 float gate = 0.f, up = 0.f;
 #pragma unroll
-                for (int v = 0; v < kFewWaves; ++v) {
+                for (int v = 0; v < kWaves; ++v) {
                     gate += sh.part[v][c >> 4][tk][c & 15];
                     up += sh.part[v][2 + (c >> 4)][tk][c & 15];
                 }
@@ -201,15 +239,15 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 }
 
 template <int FORM, int RT, int NT>
-__global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few4_up_kernel(Few4Args a) {
+__global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     __shared__ Up4Shared sh;
     const int tid = threadIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) a.err[0] = 0u;
         if (a.splits > 1)
-            for (int n = tid; n * 16 < a.H; n += kFewThreads) a.joined[n] = 0;
+            for (int n = tid; n * 16 < a.H; n += kThreads) a.joined[n] = 0;
     }
-    const Found found = find_expert(a, sh.bits, sh.token, sh.scratch);
+    const Found found = find_expert<kThreads>(a, sh.bits, sh.token, sh.scratch);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
     for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {
@@ -220,6 +258,13 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few4_up_kernel(F
     }
 }
 
+// What a wave loads for one unit, besides the tokens' activations.
+template <int RT>
+struct DownStage {
+    u32x4 w[RT][2];
+    uint32_t scale[RT][2];
+};
+
 // Second launch: workgroup x computes RT * 16 values of h for every token, or,
 // where `splits` workgroups (grid y) share them, its part. Unit u = (used expert,
 // span of 256 values of f); each wave takes a run of units. The matrix
@@ -227,13 +272,14 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few4_up_kernel(F
 // 7) and as what those leave (rows 8 to 15). Sums per token lie in LDS, one set a
 // wave, and are added at the end in a fixed order.
 template <int FORM, int RT>
-__global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
+__global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
+    using Scale = ScaleRow<FORM>;
     constexpr int kCols = RT * 16, kLd = kCols + 1;
-    extern __shared__ float sums[];  // [kFewWaves][T][kLd]
+    extern __shared__ float sums[];  // [kWaves][T][kLd]
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         bool bad = false;
-        for (int n = tid; n < a.T * a.K; n += kFewThreads) bad |= expert_bad(a.topk[n], a.E);
+        for (int n = tid; n < a.T * a.K; n += kThreads) bad |= expert_bad(a.topk[n], a.E);
         if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_EXPERT_ID);
     }
     const int i = lane & 15, q = lane >> 4;
@@ -246,56 +292,54 @@ __global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
 
+    const uint32_t ld = (uint32_t)a.F / 2;
+    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld, lds = Scale::bytes(a.F);
+    auto load_entry = [&](int rank) { return __builtin_amdgcn_readfirstlane(a.used[1 + rank]); };
     auto load_route = [&](int rank, int tokens, int t0) {
         Route r = {0, 0.f};
         if (q == 0 && t0 + i < tokens) r = a.routes[(int64_t)rank * a.T + t0 + i];
         return r;
     };
-    const uint32_t ld = (uint32_t)a.F / 2;
-    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld;
+    const auto d_act = buf_resource(a.act, (uint32_t)(a.T * a.K) * 4 * a.F);
     auto load_act = [&](int id, bool has, int span, u32x4 (&v)[8]) {
-        const uint16_t* p = a.act + ((int64_t)(id & 0xFFFF) * 2 + (i >> 3)) * a.F + span * kSpan;
+        const uint32_t off = has ? (uint32_t)((id & 0xFFFF) * 2 + (i >> 3)) * a.F * 2 + q * 64 : kBufFar;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            const int k = (m >> 2) * 128 + q * 32 + (m & 3) * 8;
-            v[m] = u32x4{0u, 0u, 0u, 0u};
-            if (has && span * kSpan + k < a.F) v[m] = ld16(p + k);
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t far = span * kSpan + p * 128 + q * 32 >= a.F ? kBufFar : off;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) v[p * 4 + m] = buf_load16(d_act, far, span * 512 + p * 256 + m * 16);
         }
     };
-    const int run = blockIdx.y * kFewWaves + wave, runs = a.splits * kFewWaves;
-    int u = (int)((int64_t)units * run / runs), entry = 0;
-    const int end = (int)((int64_t)units * (run + 1) / runs);
-    Route route = {0, 0.f};
-    float acc[RT][4] = {};
-    if (u < end) {
-        entry = __builtin_amdgcn_readfirstlane(a.used[1 + u / spans]);
-        route = load_route(u / spans, entry >> 16, 0);
-    }
-    while (u < end) {
-        const int rank = u / spans, span = u % spans, tokens = entry >> 16;
-        const int64_t e = entry & 0xFFFF;
-        u32x4 w[RT][2], v[8];
-        float sv[RT][2];
+    auto load_weights = [&](int64_t e, int span, DownStage<RT>& g) {
         const auto d = buf_resource(a.w2 + (e * a.H + h0) * ld, w_bytes);
+        const auto ds = buf_resource(a.s2 + (e * a.H + h0) * lds, cols * lds);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const uint32_t far = span * kSpan + p * 128 + q * 32 >= a.F ? kBufFar : 0u;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                w[r][p] = buf_load16(d, w_off + r * 16 * ld + far, span * 128 + p * 64);
-                sv[r][p] = load_scale<FORM>(a.s2, e * a.H + min(h0 + r * 16 + i, a.H - 1), a.F, span * 2 + p, q);
+                g.w[r][p] = buf_load16(d, w_off + r * 16 * ld + far, span * 128 + p * 64);
+                g.scale[r][p] = Scale::load(ds, (i + r * 16) * lds + Scale::offset(p, q) + far,
+                                            span * (256 / Scale::kShare * Scale::kBytes));
             }
         }
-        load_act(__shfl(route.id, i & 7), (i & 7) < tokens, span, v);
-        const int next = u + 1;
-        int next_entry = entry;
-        Route next_route = route;
-        const bool last = next == end || span + 1 == spans;  // of the expert's spans here
-        if (last && next < end) {
-            next_entry = __builtin_amdgcn_readfirstlane(a.used[1 + next / spans]);
-            next_route = load_route(next / spans, next_entry >> 16, 0);
-        }
+    };
+    const int run = blockIdx.y * kWaves + wave, runs = a.splits * kWaves;
+    int u = (int)((int64_t)units * run / runs);
+    const int end = (int)((int64_t)units * (run + 1) / runs);
+    float acc[RT][4] = {};
+    int rank = u / spans, span = u % spans, entry = 0;
+    Route route = {0, 0.f};
+
+    // One unit whose weights and first activations are there.
+    auto unit = [&](DownStage<RT>& g, u32x4 (&v)[8], bool last) {
+        const int tokens = entry >> 16;
         for (int t0 = 0; t0 < tokens; t0 += 8) {
+            // The conversion stays in the loop: its results take four times the registers.
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) asm volatile("" : "+v"(g.w[r][p]));
             f32x4 c[RT][2] = {};
             if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
@@ -312,7 +356,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-                        c[r][p] = mfma_bf16(as_bf16(v[p * 4 + m]), codes_to_bf16<FORM>(w[r][p][m], sv[r][p]), c[r][p]);
+                        c[r][p] = mfma_bf16(as_bf16(v[p * 4 + m]),
+                                            codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(g.scale[r][p])), c[r][p]);
             settle(c);
             const Route now = route;
             if (t0 + 8 < tokens) {  // more than 8 tokens: the weights stay, the tokens change
@@ -324,7 +369,9 @@ __global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc[r][j] += FORM == EP_W4_INT ? fmaf(sv[r][1], c[r][1][j], sv[r][0] * c[r][0][j]) : c[r][0][j] + c[r][1][j];
+                    acc[r][j] += FORM == EP_W4_INT ? fmaf(Scale::value(g.scale[r][1]), c[r][1][j],
+                                                          Scale::value(g.scale[r][0]) * c[r][0][j])
+                                                   : c[r][0][j] + c[r][1][j];
             if (tokens <= 8 && !last) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -345,15 +392,45 @@ __global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
                 }
             }
         }
-        u = next, entry = next_entry, route = next_route;
+    };
+    DownStage<RT> g0, g1;
+    u32x4 v0[8], v1[8];
+    Route route0 = {0, 0.f};  // the expert's first 16 tokens
+    if (u < end) {
+        entry = load_entry(rank);
+        load_weights(entry & 0xFFFF, span, g0);
+        route = route0 = load_route(rank, entry >> 16, 0);
+        load_act(__shfl(route.id, i & 7), (i & 7) < entry >> 16, span, v0);
+    }
+    // Two units a turn; the next unit's loads are in flight while this one is multiplied.
+    auto turn = [&](DownStage<RT>& g, u32x4 (&v)[8], DownStage<RT>& gn, u32x4 (&vn)[8]) {
+        const bool more = u + 1 < end, same = span + 1 < spans;
+        // Behind the last unit: a span past the row's end, which finds nothing.
+        const int next_rank = same || !more ? rank : rank + 1, next_span = !more ? spans : same ? span + 1 : 0;
+        int next_entry = entry;
+        Route next_route = route0;
+        if (next_rank != rank) {
+            next_entry = load_entry(next_rank);
+            next_route = load_route(next_rank, next_entry >> 16, 0);
+        }
+        load_weights(next_entry & 0xFFFF, next_span, gn);
+        load_act(__shfl(next_route.id, i & 7), (i & 7) < next_entry >> 16, next_span, vn);
+        __builtin_amdgcn_sched_barrier(0);
+        unit(g, v, !more || !same);
+        __builtin_amdgcn_sched_barrier(0);
+        ++u, rank = next_rank, span = next_span, entry = next_entry, route = route0 = next_route;
+    };
+    while (u < end) {
+        turn(g0, v0, g1, v1);
+        if (u < end) turn(g1, v1, g0, v0);
     }
     __syncthreads();
-    for (int n = tid; n < a.T * kCols; n += kFewThreads) {
+    for (int n = tid; n < a.T * kCols; n += kThreads) {
         const int t = n / kCols, h = h0 + n % kCols;
         if (n % kCols >= cols) continue;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) v += sums[(w * a.T + t) * kLd + n % kCols];
+        for (int w = 0; w < kWaves; ++w) v += sums[(w * a.T + t) * kLd + n % kCols];
         if (a.splits == 1)
             a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
         else
@@ -368,7 +445,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
         before = __hip_atomic_fetch_add(a.joined + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (before != a.splits - 1) return;
-    for (int n = tid; n < a.T * kCols; n += kFewThreads) {
+    for (int n = tid; n < a.T * kCols; n += kThreads) {
         const int t = n / kCols, h = h0 + n % kCols;
         if (n % kCols >= cols) continue;
         float v = 0.f;
@@ -382,31 +459,30 @@ __global__ __launch_bounds__(kFewThreads, 4) void few4_down_kernel(Few4Args a) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// 16-value tiles of h per workgroup of the second launch.
-int down_tiles(const ep_shape& s) { return s.T <= 32 ? 2 : 1; }
+// 16-value tiles of h per workgroup of the second launch, as LDS holds their sums.
+int down_tiles(const ep_shape& s) { return s.T <= 64 ? 4 : 2; }
 
 // Workgroups of the second launch for the same values of h: as many as fill the
 // chip, with a unit for every wave.
 int down_splits(const ep_shape& s, int F) {
     const int64_t units = std::min<int64_t>(s.E, (int64_t)s.T * s.K) * ((F + kSpan - 1) / kSpan);
     const int64_t cols = (s.H + 16 * down_tiles(s) - 1) / (16 * down_tiles(s));
-    return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), units / kFewWaves));
+    return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), units / kWaves));
 }
 
 template <int FORM>
 void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K), lanes = (int64_t)s.T * s.K;
-    const int64_t wide = (a.F + 63) / 64 * experts;
-    const bool many = s.T > 16 && (lanes > 16 * experts || (wide >= 1024 && lanes > 4 * experts));
-    const bool narrow = (int64_t)((a.F + 31) / 32) * experts < 1024;
-    const int cols = many ? 64 : narrow ? 16 : 32;
+    const bool many = s.T > 16 && lanes > 16 * experts;
+    const bool narrow = (int64_t)((a.F + 31) / 32) * experts < 512;
+    const int cols = !many && narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
-    hipLaunchKernelGGL((many ? few4_up_kernel<FORM, 8, 2> : narrow ? few4_up_kernel<FORM, 2, 1> : few4_up_kernel<FORM, 4, 1>),
-                       up, dim3(kFewThreads), 0, st, a);
+    hipLaunchKernelGGL((many ? few4_up_kernel<FORM, 4, 2> : narrow ? few4_up_kernel<FORM, 2, 1> : few4_up_kernel<FORM, 4, 1>),
+                       up, dim3(kThreads), 0, st, a);
     const int tiles = down_tiles(s);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
-    const size_t lds = sizeof(float) * kFewWaves * (16 * tiles + 1) * s.T;  // 69,632 bytes at most
-    hipLaunchKernelGGL((tiles == 2 ? few4_down_kernel<FORM, 2> : few4_down_kernel<FORM, 1>), down, dim3(kFewThreads), lds,
+    const size_t lds = sizeof(float) * kWaves * (16 * tiles + 1) * s.T;  // 67,584 bytes at most
+    hipLaunchKernelGGL((tiles == 4 ? few4_down_kernel<FORM, 4> : few4_down_kernel<FORM, 2>), down, dim3(kThreads), lds,
                        st, a);
 }
 

@@ -7,9 +7,6 @@
 namespace ep {
 namespace {
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWaves = kFewThreads / kWave;
-
 // One token of a used expert: token << 16 | row of its inner activations (token
 // * K + its first lane with that expert), and the sum of its lanes' weights.
 struct Route {
@@ -23,12 +20,12 @@ struct Route {
 struct Found {
     int expert, used, tokens;
 };
-template <class Args>
+template <int THREADS, class Args>
 __device__ __forceinline__ Found find_expert(const Args& a, uint32_t* bits, short* token, int* scratch) {
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
     if (tid < EP_MAX_EXPERTS / 32) bits[tid] = 0u;
     __syncthreads();
-    for (int i = tid; i < a.T * a.K; i += kFewThreads) {
+    for (int i = tid; i < a.T * a.K; i += THREADS) {
         const int64_t e = a.topk[i];
         if (expert_ok(e, a.E)) atomicOr(&bits[e >> 5], 1u << (e & 31));
     }
