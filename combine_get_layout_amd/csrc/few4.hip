@@ -73,7 +73,8 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, float scale) {
 template <int FORM>
 struct ScaleRow {
     static constexpr int kShare = FORM == EP_W4_INT ? 128 : 32, kBytes = FORM == EP_W4_INT ? 2 : 1;
-    static __device__ __forceinline__ uint32_t bytes(int cols) { return (uint32_t)(cols / kShare) * kBytes; }
+    static constexpr int kStep = kSpan / kShare * kBytes;  // bytes of a row's scales for one step
+    static __host__ __device__ __forceinline__ uint32_t bytes(int cols) { return (uint32_t)(cols / kShare) * kBytes; }
     // Of a row's columns from 128 * p + 32 * q on, past the scalar offset's.
     static __device__ __forceinline__ uint32_t offset(int p, int q) {
         return FORM == EP_W4_INT ? p * 2u : p * 4u + q;
@@ -83,6 +84,10 @@ struct ScaleRow {
             return __builtin_amdgcn_raw_buffer_load_b16(d, (int)off, (int)scalar_off, 0);
         else
             return __builtin_amdgcn_raw_buffer_load_b8(d, (int)off, (int)scalar_off, 0);
+    }
+    static __device__ __forceinline__ uint32_t from_lds(const uint8_t* p) {
+        if constexpr (FORM == EP_W4_INT) return *reinterpret_cast<const uint16_t*>(p);
+        return *p;
     }
     static __device__ __forceinline__ float value(uint32_t v) {
         return __uint_as_float(v << (FORM == EP_W4_INT ? 16 : 23));
@@ -98,17 +103,21 @@ struct Up4Shared {
     float part[kWaves][4][16][17];
 };
 
-// What a wave loads for one step.
-template <int RT, int NT>
+// What a wave loads for one step; the scales unless they lie in LDS.
+template <int RT, int NT, bool LDS>
 struct UpStage {
     u32x4 w[RT][2];
-    uint32_t scale[RT][2];
+    uint32_t scale[LDS ? 1 : RT][2];
     u32x4 x[NT][8];
 };
 
+// Bytes of a row's scales at most for them to lie in LDS.
+constexpr int kLdsScales = 512;
+
 // Tokens [t0, t0 + 16 * NT) of the expert's list.
-template <int FORM, int RT, int NT>
-__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, int t0) {
+template <int FORM, int RT, int NT, bool LDS>
+__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, const uint8_t* scales,
+                                           int t0) {
     using Scale = ScaleRow<FORM>;
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     const int i = lane & 15, q = lane >> 4;
@@ -135,7 +144,7 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 #pragma unroll
     for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
     f32x4 acc[RT][NT] = {};
-    auto load = [&](int s, UpStage<RT, NT>& g) {
+    auto load = [&](int s, UpStage<RT, NT, LDS>& g) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             // Columns past H: past the end, zeros.
@@ -143,8 +152,9 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 g.w[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, s * 128 + p * 64);
-                g.scale[r][p] = Scale::load(r < GT ? s_gate : s_up, (i + r % GT * 16) * lds + Scale::offset(p, q) + far,
-                                            s * (256 / Scale::kShare * Scale::kBytes));
+                if constexpr (!LDS)
+                    g.scale[r][p] = Scale::load(r < GT ? s_gate : s_up, (i + r % GT * 16) * lds + Scale::offset(p, q) + far,
+                                                s * Scale::kStep);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -152,9 +162,11 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                 for (int m = 0; m < 4; ++m) g.x[n][p * 4 + m] = buf_load16(d_x, xr[n] + far, s * 512 + p * 256 + m * 16);
         }
     };
-    auto multiply = [&](const UpStage<RT, NT>& g) {
+    auto multiply = [&](const UpStage<RT, NT, LDS>& g, int s) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
+            // Past the row's scales: those of the row's start, beside codes of 0.
+            const uint32_t at = s * kSpan + p * 128 + q * 32 >= a.H ? 0u : s * Scale::kStep + Scale::offset(p, q);
             f32x4 base[NT] = {};
             if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
@@ -164,7 +176,12 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const float scale = Scale::value(g.scale[r][p]);
+                uint32_t bits;
+                if constexpr (LDS)
+                    bits = Scale::from_lds(scales + (r * 16 + i) * lds + at);
+                else
+                    bits = g.scale[r][p];
+                const float scale = Scale::value(bits);
                 bf16x8 wf[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(g.w[r][p][m], scale);
@@ -186,16 +203,16 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
     // The next step's loads are in flight while this one is multiplied; those past
     // the last step find nothing (a branch around them would make the compiler
     // wait for everything).
-    UpStage<RT, NT> g0, g1;
+    UpStage<RT, NT, LDS> g0, g1;
     load(wave, g0);
     for (int s = wave; s < steps; s += 2 * kWaves) {
         load(s + kWaves, g1);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(g0);
+        multiply(g0, s);
         __builtin_amdgcn_sched_barrier(0);
         load(s + 2 * kWaves, g0);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(g1);
+        multiply(g1, s + kWaves);
         __builtin_amdgcn_sched_barrier(0);
     }
     settle(acc);
@@ -238,9 +255,11 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
     }
 }
 
-template <int FORM, int RT, int NT>
+template <int FORM, int RT, int NT, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     __shared__ Up4Shared sh;
+    extern __shared__ u32x4 lds_vectors[];
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);  // [gate rows, up rows][bytes of a row's scales]
     const int tid = threadIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) a.err[0] = 0u;
@@ -250,11 +269,24 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     const Found found = find_expert<kThreads>(a, sh.bits, sh.token, sh.scratch);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
+    if constexpr (LDS) {
+        // 16 rows' scales lie one after the other, in whole vectors. From memory each
+        // step would take a line of 128 bytes for the 4 or 8 that it needs of a row.
+        constexpr int kRows = RT * 8;  // gate rows, and as many up rows
+        const uint32_t lds = ScaleRow<FORM>::bytes(a.H);
+        const int f0 = blockIdx.x * kRows, n = min(kRows, a.F - f0) * lds / 16;
+        const char* from = a.s13 + ((int64_t)found.expert * 2 * a.F + f0) * lds;
+        for (int v = tid; v < n; v += kThreads) {
+            st16(scales + v * 16, ld16(from + v * 16));
+            st16(scales + kRows * lds + v * 16, ld16(from + (int64_t)a.F * lds + v * 16));
+        }
+        __syncthreads();
+    }
     for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {
         if (NT > 1 && found.tokens - t0 > 16)
-            up4_tokens<FORM, RT, NT>(a, found, sh, t0);
+            up4_tokens<FORM, RT, NT, LDS>(a, found, sh, scales, t0);
         else
-            up4_tokens<FORM, RT, 1>(a, found, sh, t0);
+            up4_tokens<FORM, RT, 1, LDS>(a, found, sh, scales, t0);
     }
 }
 
@@ -320,7 +352,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
             for (int r = 0; r < RT; ++r) {
                 g.w[r][p] = buf_load16(d, w_off + r * 16 * ld + far, span * 128 + p * 64);
                 g.scale[r][p] = Scale::load(ds, (i + r * 16) * lds + Scale::offset(p, q) + far,
-                                            span * (256 / Scale::kShare * Scale::kBytes));
+                                            span * Scale::kStep);
             }
         }
     };
@@ -473,12 +505,17 @@ int down_splits(const ep_shape& s, int F) {
 template <int FORM>
 void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K), lanes = (int64_t)s.T * s.K;
-    const bool many = s.T > 16 && lanes > 16 * experts;
-    const bool narrow = (int64_t)((a.F + 31) / 32) * experts < 512;
+    const uint32_t row = ScaleRow<FORM>::bytes(a.H);
+    const bool lds_scales = row <= kLdsScales;
+    const bool many = lds_scales && s.T > 16 && lanes > 16 * experts;
+    const bool narrow = !lds_scales || (int64_t)((a.F + 31) / 32) * experts < 512;
     const int cols = !many && narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
-    hipLaunchKernelGGL((many ? few4_up_kernel<FORM, 4, 2> : narrow ? few4_up_kernel<FORM, 2, 1> : few4_up_kernel<FORM, 4, 1>),
-                       up, dim3(kThreads), 0, st, a);
+    void (*const kernel)(Few4Args) = !lds_scales ? few4_up_kernel<FORM, 2, 1, false>
+                                     : many      ? few4_up_kernel<FORM, 4, 2, true>
+                                     : narrow    ? few4_up_kernel<FORM, 2, 1, true>
+                                                 : few4_up_kernel<FORM, 4, 1, true>;
+    hipLaunchKernelGGL(kernel, up, dim3(kThreads), lds_scales ? 2 * cols * row : 0, st, a);
     const int tiles = down_tiles(s);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
     const size_t lds = sizeof(float) * kWaves * (16 * tiles + 1) * s.T;  // 67,584 bytes at most
