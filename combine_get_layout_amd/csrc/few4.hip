@@ -290,12 +290,17 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     }
 }
 
-// What a wave loads for one unit, besides the tokens' activations.
-template <int RT>
+// What a wave loads for one unit; the scales as its own run of an expert's, where
+// they lie in LDS.
+template <int RT, bool LDS>
 struct DownStage {
     u32x4 w[RT][2];
-    uint32_t scale[RT][2];
+    uint32_t scale[LDS ? 1 : RT][2];
+    u32x4 act[8];
 };
+
+// Bytes of a row's scales at most for a wave to hold those of its rows in LDS.
+constexpr int kLdsScales2 = 64;
 
 // Second launch: workgroup x computes RT * 16 values of h for every token, or,
 // where `splits` workgroups (grid y) share them, its part. Unit u = (used expert,
@@ -303,11 +308,15 @@ struct DownStage {
 // instruction's 16 rows are 8 tokens of the expert, as rounded values (rows 0 to
 // 7) and as what those leave (rows 8 to 15). Sums per token lie in LDS, one set a
 // wave, and are added at the end in a fixed order.
-template <int FORM, int RT>
+template <int FORM, int RT, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     using Scale = ScaleRow<FORM>;
     constexpr int kCols = RT * 16, kLd = kCols + 1;
-    extern __shared__ float sums[];  // [kWaves][T][kLd]
+    extern __shared__ u32x4 lds_vectors[];
+    // [kWaves][rows][bytes of a row's scales] and [kWaves][T][kLd]
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors) + (LDS ? uniform_wave() * kCols * Scale::bytes(a.F) : 0u);
+    float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds_vectors) +
+                                                 (LDS ? kWaves * kCols * Scale::bytes(a.F) : 0u));
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         bool bad = false;
@@ -316,8 +325,8 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     }
     const int i = lane & 15, q = lane >> 4;
     const int h0 = blockIdx.x * kCols, cols = min(kCols, a.H - h0);
-    const int spans = (a.F + kSpan - 1) / kSpan;
-    const int units = a.used[0] * spans;
+    const int spans = (a.F + kSpan - 1) / kSpan, used = a.used[0];
+    const int units = used * spans;
     float* mine = sums + wave * a.T * kLd;
     for (int n = lane; n < a.T * kLd; n += kWave) mine[n] = 0.f;
     bf16x8 minus_eight;
@@ -326,7 +335,23 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 
     const uint32_t ld = (uint32_t)a.F / 2;
     const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld, lds = Scale::bytes(a.F);
-    auto load_entry = [&](int rank) { return __builtin_amdgcn_readfirstlane(a.used[1 + rank]); };
+    const int run = blockIdx.y * kWaves + wave, runs = a.splits * kWaves;
+    int u = (int)((int64_t)units * run / runs);
+    const int end = (int)((int64_t)units * (run + 1) / runs);
+    int rank = u / spans, span = u % spans;
+
+    // 64 experts' entries at a time (one past the last is asked for, and none behind it).
+    int entries = 0, entries_from = -64;
+    auto entry_of = [&](int r) {
+        if (r >= entries_from + 64) {
+            entries_from = r;
+            entries = a.used[1 + min(r + lane, used - 1)];
+        }
+        return readlane(entries, r - entries_from);
+    };
+    // As loads are what a wave runs out of, a tile's routes are read by one quarter of
+    // it (lane i < 16: token t0 + i of the expert) and handed on between lanes, and
+    // lanes without a token load no activations.
     auto load_route = [&](int rank, int tokens, int t0) {
         Route r = {0, 0.f};
         if (q == 0 && t0 + i < tokens) r = a.routes[(int64_t)rank * a.T + t0 + i];
@@ -342,7 +367,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
             for (int m = 0; m < 4; ++m) v[p * 4 + m] = buf_load16(d_act, far, span * 512 + p * 256 + m * 16);
         }
     };
-    auto load_weights = [&](int64_t e, int span, DownStage<RT>& g) {
+    auto load_weights = [&](int64_t e, int span, DownStage<RT, LDS>& g) {
         const auto d = buf_resource(a.w2 + (e * a.H + h0) * ld, w_bytes);
         const auto ds = buf_resource(a.s2 + (e * a.H + h0) * lds, cols * lds);
 #pragma unroll
@@ -351,21 +376,34 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 g.w[r][p] = buf_load16(d, w_off + r * 16 * ld + far, span * 128 + p * 64);
-                g.scale[r][p] = Scale::load(ds, (i + r * 16) * lds + Scale::offset(p, q) + far,
-                                            span * Scale::kStep);
+                if constexpr (!LDS)
+                    g.scale[r][p] = Scale::load(ds, (i + r * 16) * lds + Scale::offset(p, q) + far, span * Scale::kStep);
             }
         }
     };
-    const int run = blockIdx.y * kWaves + wave, runs = a.splits * kWaves;
-    int u = (int)((int64_t)units * run / runs);
-    const int end = (int)((int64_t)units * (run + 1) / runs);
-    float acc[RT][4] = {};
-    int rank = u / spans, span = u % spans, entry = 0;
-    Route route = {0, 0.f};
+    // An expert's scales of these rows lie one after the other, in whole vectors.
+    u32x4 block[RT];
+    auto load_scales = [&](int64_t e, uint32_t far) {
+        const auto ds = buf_resource(a.s2 + (e * a.H + h0) * lds, cols * lds);
+#pragma unroll
+        for (int v = 0; v < RT; ++v) block[v] = buf_load16(ds, lane * 16 + far, v * 1024);
+    };
+    auto keep_scales = [&] {
+#pragma unroll
+        for (int v = 0; v < RT; ++v)
+            if ((v * 64 + lane) * 16 < (int)(kCols * lds)) st16(scales + (v * 64 + lane) * 16, block[v]);
+    };
 
-    // One unit whose weights and first activations are there.
-    auto unit = [&](DownStage<RT>& g, u32x4 (&v)[8], bool last) {
-        const int tokens = entry >> 16;
+    float acc[RT][4] = {};
+    // One unit, whose loads are there.
+    auto unit = [&](DownStage<RT, LDS>& g, int tokens, Route route, bool last) {
+        uint32_t bits[RT][2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t at = span * kSpan + p * 128 + q * 32 >= a.F ? 0u : span * Scale::kStep + Scale::offset(p, q);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) bits[r][p] = LDS ? Scale::from_lds(scales + (r * 16 + i) * lds + at) : g.scale[LDS ? 0 : r][p];
+        }
         for (int t0 = 0; t0 < tokens; t0 += 8) {
             // The conversion stays in the loop: its results take four times the registers.
 #pragma unroll
@@ -377,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(as_bf16(v[p * 4 + m]), minus_eight, c[0][p]);
+                    for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(as_bf16(g.act[p * 4 + m]), minus_eight, c[0][p]);
 #pragma unroll
                     for (int r = 1; r < RT; ++r) c[r][p] = c[0][p];
                 }
@@ -388,21 +426,21 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-                        c[r][p] = mfma_bf16(as_bf16(v[p * 4 + m]),
-                                            codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(g.scale[r][p])), c[r][p]);
+                        c[r][p] = mfma_bf16(as_bf16(g.act[p * 4 + m]),
+                                            codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(bits[r][p])), c[r][p]);
             settle(c);
             const Route now = route;
             if (t0 + 8 < tokens) {  // more than 8 tokens: the weights stay, the tokens change
                 if (t0 & 8) route = load_route(rank, tokens, t0 + 8);
                 const int n = (~t0 & 8) + (i & 7);
-                load_act(__shfl(route.id, n), t0 + 8 + (i & 7) < tokens, span, v);
+                load_act(__shfl(route.id, n), t0 + 8 + (i & 7) < tokens, span, g.act);
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc[r][j] += FORM == EP_W4_INT ? fmaf(Scale::value(g.scale[r][1]), c[r][1][j],
-                                                          Scale::value(g.scale[r][0]) * c[r][0][j])
+                    acc[r][j] += FORM == EP_W4_INT ? fmaf(Scale::value(bits[r][1]), c[r][1][j],
+                                                          Scale::value(bits[r][0]) * c[r][0][j])
                                                    : c[r][0][j] + c[r][1][j];
             if (tokens <= 8 && !last) break;
 #pragma unroll
@@ -425,36 +463,46 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
             }
         }
     };
-    DownStage<RT> g0, g1;
-    u32x4 v0[8], v1[8];
-    Route route0 = {0, 0.f};  // the expert's first 16 tokens
+    DownStage<RT, LDS> g0, g1;
+    int entry = 0;
+    Route route = {0, 0.f}, ahead = {0, 0.f};  // the first 16 tokens of this expert and of the next
     if (u < end) {
-        entry = load_entry(rank);
+        entry = entry_of(rank);
+        route = load_route(rank, entry >> 16, 0);
+        const int after = min(rank + 1, used - 1);
+        ahead = load_route(after, entry_of(after) >> 16, 0);
         load_weights(entry & 0xFFFF, span, g0);
-        route = route0 = load_route(rank, entry >> 16, 0);
-        load_act(__shfl(route.id, i & 7), (i & 7) < entry >> 16, span, v0);
-    }
-    // Two units a turn; the next unit's loads are in flight while this one is multiplied.
-    auto turn = [&](DownStage<RT>& g, u32x4 (&v)[8], DownStage<RT>& gn, u32x4 (&vn)[8]) {
-        const bool more = u + 1 < end, same = span + 1 < spans;
-        // Behind the last unit: a span past the row's end, which finds nothing.
-        const int next_rank = same || !more ? rank : rank + 1, next_span = !more ? spans : same ? span + 1 : 0;
-        int next_entry = entry;
-        Route next_route = route0;
-        if (next_rank != rank) {
-            next_entry = load_entry(next_rank);
-            next_route = load_route(next_rank, next_entry >> 16, 0);
+        if constexpr (LDS) {
+            load_scales(entry & 0xFFFF, 0u);
+            keep_scales();
         }
+        load_act(__shfl(route.id, i & 7), (i & 7) < entry >> 16, span, g0.act);
+    }
+    // The next unit's loads, and the routes of the expert behind its own, are in flight
+    // while this one is multiplied. All of them are made on every turn, behind the last
+    // unit past the row's end: a branch around them would make the compiler wait for
+    // everything.
+    auto turn = [&](DownStage<RT, LDS>& g, DownStage<RT, LDS>& gn) {
+        const bool more = u + 1 < end, same = !more || span + 1 < spans;
+        const int next_rank = same ? rank : rank + 1, next_span = !more ? spans : same ? span + 1 : 0;
+        const int next_entry = entry_of(next_rank), after = min(next_rank + 1, used - 1);
+        const int after_tokens = entry_of(after) >> 16;
+        Route next = route;
+        if (!same) next = ahead;
         load_weights(next_entry & 0xFFFF, next_span, gn);
-        load_act(__shfl(next_route.id, i & 7), (i & 7) < next_entry >> 16, next_span, vn);
+        if constexpr (LDS) load_scales(next_entry & 0xFFFF, same ? kBufFar : 0u);
+        load_act(__shfl(next.id, i & 7), (i & 7) < next_entry >> 16, next_span, gn.act);
+        ahead = load_route(after, after_tokens, 0);
         __builtin_amdgcn_sched_barrier(0);
-        unit(g, v, !more || !same);
+        unit(g, entry >> 16, route, !more || !same);
         __builtin_amdgcn_sched_barrier(0);
-        ++u, rank = next_rank, span = next_span, entry = next_entry, route = route0 = next_route;
+        if constexpr (LDS)
+            if (!same) keep_scales();
+        ++u, rank = next_rank, span = next_span, entry = next_entry, route = next;
     };
     while (u < end) {
-        turn(g0, v0, g1, v1);
-        if (u < end) turn(g1, v1, g0, v0);
+        turn(g0, g1);
+        if (u < end) turn(g1, g0);
     }
     __syncthreads();
     for (int n = tid; n < a.T * kCols; n += kThreads) {
@@ -518,9 +566,13 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     hipLaunchKernelGGL(kernel, up, dim3(kThreads), lds_scales ? 2 * cols * row : 0, st, a);
     const int tiles = down_tiles(s);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
-    const size_t lds = sizeof(float) * kWaves * (16 * tiles + 1) * s.T;  // 67,584 bytes at most
-    hipLaunchKernelGGL((tiles == 4 ? few4_down_kernel<FORM, 4> : few4_down_kernel<FORM, 2>), down, dim3(kThreads), lds,
-                       st, a);
+    const uint32_t row2 = ScaleRow<FORM>::bytes(a.F);
+    const bool lds2 = row2 <= kLdsScales2;
+    // 66,560 + 16,384 bytes at most
+    const size_t lds = sizeof(float) * kWaves * (16 * tiles + 1) * s.T + (lds2 ? kWaves * 16 * tiles * row2 : 0);
+    void (*const second)(Few4Args) = tiles == 4 ? (lds2 ? few4_down_kernel<FORM, 4, true> : few4_down_kernel<FORM, 4, false>)
+                                                : (lds2 ? few4_down_kernel<FORM, 2, true> : few4_down_kernel<FORM, 2, false>);
+    hipLaunchKernelGGL(second, down, dim3(kThreads), lds, st, a);
 }
 
 }  // namespace
