@@ -78,7 +78,7 @@ __device__ __forceinline__ float share_sum(float v, float* scratch) {
     constexpr int kWaves = LANES / kWave;
     const int wave = wave_in_block();
     if (lane_id() == 0) scratch[wave] = v;
-    __syncthreads();
+    barrier_only();  // loads for later stay in flight
     const float* s = scratch + wave / kWaves * kWaves;
     v = 0.f;
 #pragma unroll
@@ -202,71 +202,130 @@ struct NormGradArgs {
     const char* ds;
     char* dh;
     uint16_t* dx;
-    float* part;  // [workgroups][H]: each workgroup's rows' part of d_gain, or null
+    float* part;    // [groups][H]: each workgroup's rows' part of d_gain, or null
+    float* d_gain;  // for gain_columns
+    int groups;     // workgroups that take rows
 };
 
 constexpr int kGradThreads = 512;
 
-// A workgroup takes every gridDim.x-th group of kGradThreads / LANES rows and
-// keeps its part of d_gain in registers.
+// d_gain of 64 columns in one workgroup: a thread takes eight of them and every
+// 64th row.
+template <bool WIDE>
+__device__ __forceinline__ void gain_columns(const NormGradArgs& a, int c0, float* sums) {
+    const int c = c0 + (threadIdx.x & 7) * 8, slice = threadIdx.x >> 3;
+    float dg[8] = {};
+    if (c < a.H) {
+#pragma unroll 4
+        for (int64_t t = slice; t < a.T; t += kGradThreads / 8) {
+            float dy[8], h[8];
+            const float r = a.rstd[t];
+            floats8<false>(load8<false>(a.dy, t * a.H + c), dy);
+            floats8<WIDE>(load8<WIDE>(a.h, t * a.H + c), h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dg[j] = fmaf(dy[j], h[j] * r, dg[j]);
+        }
+    }
+    // Slices lie next to each other in a wave's rows of 16 lanes: two to a row, then
+    // the rows, then the waves.
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        for (int d = 8; d < kWave; d <<= 1) dg[j] += __shfl_xor(dg[j], d);
+        if (lane_id() < 8) sums[wave_in_block() * 64 + lane_id() * 8 + j] = dg[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < 64 && c0 + (int)threadIdx.x < a.H) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGradThreads / kWave; ++w) s += sums[w * 64 + threadIdx.x];
+        a.d_gain[c0 + threadIdx.x] = s;
+    }
+}
+
+// LANES threads to a row, NV vectors of eight values to a thread. A workgroup takes
+// every a.groups-th run of rows and keeps its part of d_gain in registers. The next
+// rows' loads are in flight while these are summed and stored. Workgroups behind
+// those of the rows, where there are any, make d_gain itself.
 template <int LANES, int NV, bool WIDE>
-__global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads) void norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads, 4) void norm_grad_kernel(NormGradArgs a) {
     constexpr int kThreads = kGradThreads < LANES ? LANES : kGradThreads, kRows = kThreads / LANES;
     __shared__ float scratch[2][kThreads / kWave];
-    __shared__ float sums[kRows > 1 ? kThreads * 8 : 1];
+    __shared__ float sums[kRows > 1 ? kThreads * 8 : 512];
+    if ((int)blockIdx.x >= a.groups) {
+        if constexpr (kThreads == kGradThreads) gain_columns<WIDE>(a, ((int)blockIdx.x - a.groups) * 64, sums);
+        return;
+    }
     const int tid = threadIdx.x % LANES, sub = threadIdx.x / LANES;
     const float inv_h = 1.0f / (float)a.H;
     float dg[NV][8] = {};
-    const int groups = (a.T + kRows - 1) / kRows;
-    for (int64_t n0 = blockIdx.x, turn = 0; n0 < groups; n0 += gridDim.x, turn ^= 1) {
-        const int64_t row = n0 * kRows + sub, base = row * a.H;
-        const bool in = row < a.T;
-        Eight<false> dyv[NV];
-        Eight<WIDE> hv[NV], sv[NV];
-        const float r = in ? a.rstd[row] : 0.f;
+    struct Row {
+        Eight<false> dy[NV];
+        Eight<WIDE> h[NV], s[NV];
+        float r;
+    };
+    const int runs = (a.T + kRows - 1) / kRows;
+    // Rows past the last: the last again, and nothing is made of them.
+    auto load = [&](int run, Row& g) {
+        const int64_t row = min((int64_t)run * kRows + sub, (int64_t)a.T - 1), base = row * a.H;
+        g.r = a.rstd[row];
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int c = (n * LANES + tid) * 8;
-            if (in && c < a.H) {
-                dyv[n] = load8<false>(a.dy, base + c);
-                hv[n] = load8<WIDE>(a.h, base + c);
-                if (a.ds) sv[n] = load8<WIDE>(a.ds, base + c);
-            }
+            const int c = min((n * LANES + tid) * 8, a.H - 8);
+            g.dy[n] = load8<false>(a.dy, base + c);
+            g.h[n] = load8<WIDE>(a.h, base + c);
+            if (a.ds) g.s[n] = load8<WIDE>(a.ds, base + c);
         }
+    };
+    auto row = [&](int run, int turn, const Row& g) {
+        const int64_t row = (int64_t)run * kRows + sub, base = row * a.H;
+        const bool in = row < a.T;
         float dot = 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c = (n * LANES + tid) * 8;
             if (in && c < a.H) {
-                float dy[8], h[8], g[8];
-                floats8<false>(dyv[n], dy);
-                floats8<WIDE>(hv[n], h);
-                unpack8(ld16(a.gain + c), g);
+                float dy[8], h[8], w[8];
+                floats8<false>(g.dy[n], dy);
+                floats8<WIDE>(g.h[n], h);
+                unpack8(ld16(a.gain + c), w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    dot = fmaf(dy[j] * g[j], h[j], dot);
-                    dg[n][j] = fmaf(dy[j], h[j] * r, dg[n][j]);
+                    dot = fmaf(dy[j] * w[j], h[j], dot);
+                    dg[n][j] = fmaf(dy[j], h[j] * g.r, dg[n][j]);
                 }
             }
         }
+        if (!a.dh && !a.dx) return;
         // The other half of scratch next time: a wave may still read this one.
         dot = share_sum<LANES>(dot, scratch[turn]);
-        const float k = r * r * (dot * inv_h);
+        const float k = g.r * g.r * (dot * inv_h);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c = (n * LANES + tid) * 8;
-            if (in && c < a.H && (a.dh || a.dx)) {
-                float dy[8], h[8], g[8], s[8] = {};
-                floats8<false>(dyv[n], dy);
-                floats8<WIDE>(hv[n], h);
-                if (a.ds) floats8<WIDE>(sv[n], s);
-                unpack8(ld16(a.gain + c), g);
+            if (in && c < a.H) {
+                float dy[8], h[8], w[8], s[8] = {};
+                floats8<false>(g.dy[n], dy);
+                floats8<WIDE>(g.h[n], h);
+                if (a.ds) floats8<WIDE>(g.s[n], s);
+                unpack8(ld16(a.gain + c), w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = fmaf(r, fmaf(-k, h[j], dy[j] * g[j]), s[j]);
+                for (int j = 0; j < 8; ++j) s[j] = fmaf(g.r, fmaf(-k, h[j], dy[j] * w[j]), s[j]);
                 if (a.dh) store8<WIDE>(a.dh, base + c, s);
                 if (a.dx) st16(a.dx + base + c, pack8(s));
             }
         }
+    };
+    Row g0, g1;
+    load(blockIdx.x, g0);
+    for (int run = blockIdx.x; run < runs; run += 2 * a.groups) {
+        load(run + a.groups, g1);
+        __builtin_amdgcn_sched_barrier(0);
+        row(run, 0, g0);
+        __builtin_amdgcn_sched_barrier(0);
+        load(run + 2 * a.groups, g0);
+        __builtin_amdgcn_sched_barrier(0);
+        row(run + a.groups, 1, g1);
+        __builtin_amdgcn_sched_barrier(0);
     }
     if (!a.part) return;
     float* part = a.part + (int64_t)blockIdx.x * a.H;
@@ -363,14 +422,18 @@ __global__ __launch_bounds__(256) void norm_gain_kernel(const float* part, int p
     }
 }
 
-constexpr int kGradGroups = 512;  // workgroups of norm_grad_kernel at most
+constexpr int kGradGroups = 512;  // workgroups of norm_grad_kernel that take rows, two per CU
 constexpr int kLongH = 32768;     // longest row held in registers
+constexpr int64_t kBesideValues = 1 << 21;
 
+int grad_lanes(int H) { return H <= 1024 ? 64 : H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
 int grad_parts(int T, int H) {
     if (H > kLongH) return std::min(T, 64);
-    const int lanes = H <= 2048 ? 64 : H <= 8192 ? 256 : 1024, rows = std::max(1, kGradThreads / lanes);
+    const int rows = std::max(1, kGradThreads / grad_lanes(H));
     return std::min((T + rows - 1) / rows, kGradGroups);
 }
+// d_gain beside the rows in one launch: see launch_rms_norm_grad.
+bool gain_beside(int T, int H) { return H <= 8192 && (int64_t)T * H <= kBesideValues; }
 
 template <bool WIDE>
 void launch_norm(const NormArgs& a, hipStream_t st) {
@@ -399,14 +462,15 @@ void launch_norm_grad(const NormGradArgs& a, int parts, hipStream_t st) {
                                dim3(256), 0, st, a);
         return;
     }
+    const int columns = a.d_gain ? (a.H + 63) / 64 : 0;
     auto go = [&](auto kernel, int lanes) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(std::max(lanes, kGradThreads)), 0, st, a);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.groups + columns)), dim3(std::max(lanes, kGradThreads)), 0, st, a);
     };
     if (vecs <= 64) return go(norm_grad_kernel<64, 1, WIDE>, 64);
     if (vecs <= 128) return go(norm_grad_kernel<64, 2, WIDE>, 64);
-    if (vecs <= 256) return go(norm_grad_kernel<64, 4, WIDE>, 64);
+    if (vecs <= 256) return go(norm_grad_kernel<128, 2, WIDE>, 128);
     if (vecs <= 512) return go(norm_grad_kernel<256, 2, WIDE>, 256);
-    if (vecs <= 1024) return go(norm_grad_kernel<256, 4, WIDE>, 256);
+    if (vecs <= 1024) return go(norm_grad_kernel<512, 2, WIDE>, 512);
     if (vecs <= 2048) return go(norm_grad_kernel<1024, 2, WIDE>, 1024);
     go(norm_grad_kernel<1024, 4, WIDE>, 1024);
 }
@@ -434,15 +498,17 @@ hipError_t launch_rms_norm_grad(const ep_shape& s, const void* h, int stream_typ
                                 float* d_gain, char* ws, hipStream_t st) {
     const int parts = grad_parts(s.T, s.H);
     float* part = reinterpret_cast<float*>(ws + 256);
+    const bool rows = s.T > 0 && (d_h || d_x), beside = d_gain && s.T > 0 && gain_beside(s.T, s.H);
     const NormGradArgs a = {s.T, s.H, static_cast<const char*>(h), gain, rstd, dy, static_cast<const char*>(d_stream),
-                            static_cast<char*>(d_h), d_x, d_gain ? part : nullptr};
+                            static_cast<char*>(d_h), d_x, d_gain && !beside ? part : nullptr, beside ? d_gain : nullptr,
+                            beside && !rows ? 0 : parts};
     if (s.T > 0) {
         if (stream_type == EP_STREAM_F32)
             launch_norm_grad<true>(a, parts, st);
         else
             launch_norm_grad<false>(a, parts, st);
     }
-    if (d_gain)
+    if (d_gain && !beside)
         hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((s.H + 63) / 64)), dim3(256), 0, st, part, parts, s.H, d_gain);
     return hipGetLastError();
 }
