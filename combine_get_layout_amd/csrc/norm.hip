@@ -211,13 +211,13 @@ constexpr int kGradThreads = 512;
 
 // d_gain of 64 columns in one workgroup: a thread takes eight of them and every
 // 64th row.
-template <bool WIDE>
+template <int THREADS, bool WIDE>
 __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int c0, float* sums) {
     const int c = c0 + (threadIdx.x & 7) * 8, slice = threadIdx.x >> 3;
     float dg[8] = {};
     if (c < a.H) {
 #pragma unroll 4
-        for (int64_t t = slice; t < a.T; t += kGradThreads / 8) {
+        for (int64_t t = slice; t < a.T; t += THREADS / 8) {
             float dy[8], h[8];
             const float r = a.rstd[t];
             floats8<false>(load8<false>(a.dy, t * a.H + c), dy);
@@ -237,7 +237,7 @@ __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int c0, floa
     if (threadIdx.x < 64 && c0 + (int)threadIdx.x < a.H) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kGradThreads / kWave; ++w) s += sums[w * 64 + threadIdx.x];
+        for (int w = 0; w < THREADS / kWave; ++w) s += sums[w * 64 + threadIdx.x];
         a.d_gain[c0 + threadIdx.x] = s;
     }
 }
@@ -250,9 +250,9 @@ template <int LANES, int NV, bool WIDE>
 __global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads, 4) void norm_grad_kernel(NormGradArgs a) {
     constexpr int kThreads = kGradThreads < LANES ? LANES : kGradThreads, kRows = kThreads / LANES;
     __shared__ float scratch[2][kThreads / kWave];
-    __shared__ float sums[kRows > 1 ? kThreads * 8 : 512];
+    __shared__ float sums[kRows > 1 ? kThreads * 8 : kThreads];
     if ((int)blockIdx.x >= a.groups) {
-        if constexpr (kThreads == kGradThreads) gain_columns<WIDE>(a, ((int)blockIdx.x - a.groups) * 64, sums);
+        gain_columns<kThreads, WIDE>(a, ((int)blockIdx.x - a.groups) * 64, sums);
         return;
     }
     const int tid = threadIdx.x % LANES, sub = threadIdx.x / LANES;
@@ -316,8 +316,15 @@ __global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads, 4) voi
         }
     };
     Row g0, g1;
-    load(blockIdx.x, g0);
-    for (int run = blockIdx.x; run < runs; run += 2 * a.groups) {
+    if constexpr (NV > 2) {  // the rows of two turns would not fit the registers
+        for (int run = blockIdx.x, turn = 0; run < runs; run += a.groups, turn ^= 1) {
+            load(run, g0);
+            row(run, turn, g0);
+        }
+    } else {
+        load(blockIdx.x, g0);
+    }
+    for (int run = blockIdx.x; NV <= 2 && run < runs; run += 2 * a.groups) {
         load(run + a.groups, g1);
         __builtin_amdgcn_sched_barrier(0);
         row(run, 0, g0);
@@ -397,28 +404,27 @@ __global__ __launch_bounds__(256) void norm_gain_long_kernel(NormGradArgs a) {
 }
 
 // d_gain from the parts: 64 columns to a workgroup, 16 threads of four columns
-// by 16 runs of parts.
-__global__ __launch_bounds__(256) void norm_gain_kernel(const float* part, int parts, int H, float* d_gain) {
-    __shared__ float4 sums[16][16];
+// by 64 runs of parts.
+__global__ __launch_bounds__(1024) void norm_gain_kernel(const float* part, int parts, int H, float* d_gain) {
+    __shared__ float4 sums[64][16];
     const int col = threadIdx.x & 15, run = threadIdx.x >> 4, c = blockIdx.x * 64 + col * 4;
     float4 s = {0.f, 0.f, 0.f, 0.f};
     if (c < H) {
-        const int end = (run + 1) * parts / 16;
-#pragma unroll 4
-        for (int p = run * parts / 16; p < end; ++p) {
+        const int end = (run + 1) * parts / 64;
+#pragma unroll 8
+        for (int p = run * parts / 64; p < end; ++p) {
             const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * H + c);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
     }
     sums[run][col] = s;
     __syncthreads();
-    if (run == 0 && c < H) {
+    if (threadIdx.x < 64 && blockIdx.x * 64 + (int)threadIdx.x < H) {
+        const float* f = reinterpret_cast<const float*>(sums) + threadIdx.x;
+        float v = 0.f;
 #pragma unroll
-        for (int n = 1; n < 16; ++n) {
-            const float4 v = sums[n][col];
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        *reinterpret_cast<float4*>(d_gain + c) = s;
+        for (int n = 0; n < 64; ++n) v += f[n * 64];
+        d_gain[blockIdx.x * 64 + threadIdx.x] = v;
     }
 }
 
@@ -426,10 +432,16 @@ constexpr int kGradGroups = 512;  // workgroups of norm_grad_kernel that take ro
 constexpr int kLongH = 32768;     // longest row held in registers
 constexpr int64_t kBesideValues = 1 << 21;
 
-int grad_lanes(int H) { return H <= 1024 ? 64 : H <= 2048 ? 128 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
-int grad_parts(int T, int H) {
+// Threads to a row: with one vector of eight to a thread (a stream in 32 bits, whose
+// rows take more registers) or two.
+int grad_lanes(int H, bool wide) {
+    int lanes = 64;
+    while (lanes < 1024 && lanes * 8 * (wide ? 1 : 2) < H) lanes *= 2;
+    return lanes;
+}
+int grad_groups(int T, int H, bool wide) {
     if (H > kLongH) return std::min(T, 64);
-    const int rows = std::max(1, kGradThreads / grad_lanes(H));
+    const int rows = std::max(1, kGradThreads / grad_lanes(H, wide));
     return std::min((T + rows - 1) / rows, kGradGroups);
 }
 // d_gain beside the rows in one launch: see launch_rms_norm_grad.
@@ -466,19 +478,28 @@ void launch_norm_grad(const NormGradArgs& a, int parts, hipStream_t st) {
     auto go = [&](auto kernel, int lanes) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)(a.groups + columns)), dim3(std::max(lanes, kGradThreads)), 0, st, a);
     };
-    if (vecs <= 64) return go(norm_grad_kernel<64, 1, WIDE>, 64);
-    if (vecs <= 128) return go(norm_grad_kernel<64, 2, WIDE>, 64);
-    if (vecs <= 256) return go(norm_grad_kernel<128, 2, WIDE>, 128);
-    if (vecs <= 512) return go(norm_grad_kernel<256, 2, WIDE>, 256);
-    if (vecs <= 1024) return go(norm_grad_kernel<512, 2, WIDE>, 512);
-    if (vecs <= 2048) return go(norm_grad_kernel<1024, 2, WIDE>, 1024);
-    go(norm_grad_kernel<1024, 4, WIDE>, 1024);
+    const int lanes = grad_lanes(a.H, WIDE);
+    if (vecs <= 64) return go(norm_grad_kernel<64, 1, WIDE>, lanes);
+    if constexpr (WIDE) {
+        if (lanes == 128) return go(norm_grad_kernel<128, 1, WIDE>, lanes);
+        if (lanes == 256) return go(norm_grad_kernel<256, 1, WIDE>, lanes);
+        if (lanes == 512) return go(norm_grad_kernel<512, 1, WIDE>, lanes);
+        if (vecs <= 1024) return go(norm_grad_kernel<1024, 1, WIDE>, lanes);
+    } else {
+        if (lanes == 64) return go(norm_grad_kernel<64, 2, WIDE>, lanes);
+        if (lanes == 128) return go(norm_grad_kernel<128, 2, WIDE>, lanes);
+        if (lanes == 256) return go(norm_grad_kernel<256, 2, WIDE>, lanes);
+        if (lanes == 512) return go(norm_grad_kernel<512, 2, WIDE>, lanes);
+    }
+    if (vecs <= 2048) return go(norm_grad_kernel<1024, 2, WIDE>, lanes);
+    go(norm_grad_kernel<1024, 4, WIDE>, lanes);
 }
 
 }  // namespace
 
 size_t ws_norm(const ep_shape& s) {
-    return 256 + (sizeof(float) * (size_t)grad_parts(s.T, s.H) * s.H + 255) / 256 * 256;
+    const int groups = std::max(grad_groups(s.T, s.H, false), grad_groups(s.T, s.H, true));
+    return 256 + (sizeof(float) * (size_t)groups * s.H + 255) / 256 * 256;
 }
 
 hipError_t launch_rms_norm(const ep_shape& s, const uint16_t* x, const void* res, int stream_type,
@@ -496,7 +517,7 @@ hipError_t launch_rms_norm(const ep_shape& s, const uint16_t* x, const void* res
 hipError_t launch_rms_norm_grad(const ep_shape& s, const void* h, int stream_type, const uint16_t* gain,
                                 const float* rstd, const uint16_t* dy, const void* d_stream, void* d_h, uint16_t* d_x,
                                 float* d_gain, char* ws, hipStream_t st) {
-    const int parts = grad_parts(s.T, s.H);
+    const int parts = grad_groups(s.T, s.H, stream_type == EP_STREAM_F32);
     float* part = reinterpret_cast<float*>(ws + 256);
     const bool rows = s.T > 0 && (d_h || d_x), beside = d_gain && s.T > 0 && gain_beside(s.T, s.H);
     const NormGradArgs a = {s.T, s.H, static_cast<const char*>(h), gain, rstd, dy, static_cast<const char*>(d_stream),
@@ -509,7 +530,7 @@ hipError_t launch_rms_norm_grad(const ep_shape& s, const void* h, int stream_typ
             launch_norm_grad<false>(a, parts, st);
     }
     if (d_gain && !beside)
-        hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((s.H + 63) / 64)), dim3(256), 0, st, part, parts, s.H, d_gain);
+        hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((s.H + 63) / 64)), dim3(1024), 0, st, part, parts, s.H, d_gain);
     return hipGetLastError();
 }
 
