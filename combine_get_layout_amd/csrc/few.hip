@@ -70,9 +70,7 @@ __device__ __forceinline__ bf16x8 e4m3_to_bf16(uint32_t lo, uint32_t hi) {
 // straight from memory into the registers of the matrix instruction (each is
 // used once, so LDS would only add a trip); the tokens' values come from L2.
 struct UpShared {
-    uint32_t bits[EP_MAX_EXPERTS / 32];
-    short token[128];
-    int scratch[2 + 128];
+    FindShared find;
     float part[kFewWaves][4][16][17];
 };
 
@@ -104,7 +102,7 @@ __device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         has[n] = t0 + n * 16 + i < found.tokens;
-        xr[n] = has[n] ? (uint32_t)sh.token[t0 + n * 16 + i] * a.H * 2 + q * (FP8 ? 32 : 16) : 0u;
+        xr[n] = has[n] ? (uint32_t)sh.find.token[t0 + n * 16 + i] * a.H * 2 + q * (FP8 ? 32 : 16) : 0u;
     }
     f32x4 acc[RT][NT] = {};
     float four[RT] = {};
@@ -198,7 +196,7 @@ __device__ __forceinline__ void up_tokens(const FewArgs& a, const Found& found, 
                 uint32_t hi = f32_to_bf16(r);
                 if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
                 const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
-                uint16_t* act = a.act + (int64_t)sh.scratch[2 + at] * 2 * a.F + f;
+                uint16_t* act = a.act + (int64_t)sh.find.row[at] * 2 * a.F + f;
                 act[0] = (uint16_t)hi;
                 act[a.F] = (uint16_t)f32_to_bf16(rest);
             }
@@ -216,7 +214,7 @@ __global__ __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) void few_up_kernel(Fe
         if (a.splits > 1)
             for (int n = tid; n * kDownCols < a.H; n += kFewThreads) a.joined[n] = 0;
     }
-    const Found found = find_expert<kFewThreads>(a, sh.bits, sh.token, sh.scratch);
+    const Found found = find_expert<kFewThreads>(a, sh.find);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
     for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {

@@ -97,9 +97,7 @@ struct ScaleRow {
 // First launch: workgroup (x, y) computes RT / 2 * 16 values of f for the tokens
 // of the y-th used expert.
 struct Up4Shared {
-    uint32_t bits[EP_MAX_EXPERTS / 32];
-    short token[128];
-    int scratch[2 + 128];
+    FindShared find;
     float part[kWaves][4][16][17];
 };
 
@@ -138,7 +136,7 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         has[n] = t0 + n * 16 + i < found.tokens;
-        xr[n] = has[n] ? (uint32_t)sh.token[t0 + n * 16 + i] * a.H * 2 + q * 64 : kBufNone;
+        xr[n] = has[n] ? (uint32_t)sh.find.token[t0 + n * 16 + i] * a.H * 2 + q * 64 : kBufNone;
     }
     bf16x8 minus_eight;
 #pragma unroll
@@ -246,7 +244,7 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                 uint32_t hi = f32_to_bf16(r);
                 if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
                 const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
-                uint16_t* act = a.act + (int64_t)sh.scratch[2 + at] * 2 * a.F + f;
+                uint16_t* act = a.act + (int64_t)sh.find.row[at] * 2 * a.F + f;
                 act[0] = (uint16_t)hi;
                 act[a.F] = (uint16_t)f32_to_bf16(rest);
             }
@@ -266,7 +264,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
         if (a.splits > 1)
             for (int n = tid; n * 16 < a.H; n += kThreads) a.joined[n] = 0;
     }
-    const Found found = find_expert<kThreads>(a, sh.bits, sh.token, sh.scratch);
+    const Found found = find_expert<kThreads>(a, sh.find);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
     if constexpr (LDS) {

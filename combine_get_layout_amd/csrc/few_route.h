@@ -15,22 +15,33 @@ struct Route {
 };
 
 // The blockIdx.y-th used expert in ascending order (-1 if there are fewer)
-// and its tokens in ascending order. Each workgroup finds them for itself:
-// the ids are a few KB in L2.
+// and its tokens in ascending order. Each workgroup finds them for itself: it reads
+// the ids once and keeps them in LDS; the routes, which take the weights too, are
+// made by the workgroups with blockIdx.x = 0.
 struct Found {
     int expert, used, tokens;
 };
+constexpr int kNoExpert = 0xFFFF;
+struct FindShared {
+    uint32_t bits[EP_MAX_EXPERTS / 32];
+    short token[EP_FEW_MAX_TOKENS];         // the expert's tokens
+    short row[EP_FEW_MAX_TOKENS];           // and the rows of their inner activations
+    int scratch[2];
+    uint16_t ids[EP_FEW_MAX_TOKENS * EP_MAX_TOPK];
+};
 template <int THREADS, class Args>
-__device__ __forceinline__ Found find_expert(const Args& a, uint32_t* bits, short* token, int* scratch) {
+__device__ __forceinline__ Found find_expert(const Args& a, FindShared& sh) {
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_in_block();
-    if (tid < EP_MAX_EXPERTS / 32) bits[tid] = 0u;
+    if (tid < EP_MAX_EXPERTS / 32) sh.bits[tid] = 0u;
     __syncthreads();
     for (int i = tid; i < a.T * a.K; i += THREADS) {
         const int64_t e = a.topk[i];
-        if (expert_ok(e, a.E)) atomicOr(&bits[e >> 5], 1u << (e & 31));
+        const bool ok = expert_ok(e, a.E);
+        sh.ids[i] = (uint16_t)(ok ? (int)e : kNoExpert);
+        if (ok) atomicOr(&sh.bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    const uint64_t word = (uint64_t)bits[2 * lane] | (uint64_t)bits[2 * lane + 1] << 32;
+    const uint64_t word = (uint64_t)sh.bits[2 * lane] | (uint64_t)sh.bits[2 * lane + 1] << 32;
     const int n = __popcll(word);
     int sum = n;
     for (int d = 1; d < kWave; d <<= 1) {
@@ -54,22 +65,22 @@ __device__ __forceinline__ Found find_expert(const Args& a, uint32_t* bits, shor
     if (wave < 2) {
         if (tid < a.T) {
             for (int k = 0; k < a.K; ++k) {
-                if (a.topk[tid * a.K + k] != f.expert) continue;
+                if (sh.ids[tid * a.K + k] != f.expert) continue;
                 if (r.id < 0) r.id = tid << 16 | (tid * a.K + k);
-                r.w += a.topk_w[tid * a.K + k];
+                if (blockIdx.x == 0) r.w += a.topk_w[tid * a.K + k];
             }
         }
         mine = r.id >= 0;
         const uint64_t m = __ballot(mine);
-        if (lane == 0) scratch[wave] = __popcll(m);
+        if (lane == 0) sh.scratch[wave] = __popcll(m);
     }
     __syncthreads();
-    f.tokens = scratch[0] + scratch[1];
+    f.tokens = sh.scratch[0] + sh.scratch[1];
     if (wave < 2 && mine) {
         const uint64_t m = __ballot(true);
-        const int at = (wave ? scratch[0] : 0) + __popcll(m & ((1ull << lane) - 1));
-        token[at] = (short)tid;
-        scratch[2 + at] = r.id & 0xFFFF;
+        const int at = (wave ? sh.scratch[0] : 0) + __popcll(m & ((1ull << lane) - 1));
+        sh.token[at] = (short)tid;
+        sh.row[at] = (short)(r.id & 0xFFFF);
         if (blockIdx.x == 0) a.routes[(int64_t)want * a.T + at] = r;
     }
     if (blockIdx.x == 0 && tid == 0) a.used[1 + want] = f.expert | f.tokens << 16;

@@ -430,7 +430,6 @@ __global__ __launch_bounds__(1024) void norm_gain_kernel(const float* part, int 
 
 constexpr int kGradGroups = 512;  // workgroups of norm_grad_kernel that take rows, two per CU
 constexpr int kLongH = 32768;     // longest row held in registers
-constexpr int64_t kBesideValues = 1 << 21;
 
 // Threads to a row: with one vector of eight to a thread (a stream in 32 bits, whose
 // rows take more registers) or two.
@@ -444,8 +443,16 @@ int grad_groups(int T, int H, bool wide) {
     const int rows = std::max(1, kGradThreads / grad_lanes(H, wide));
     return std::min((T + rows - 1) / rows, kGradGroups);
 }
-// d_gain beside the rows in one launch: see launch_rms_norm_grad.
-bool gain_beside(int T, int H) { return H <= 8192 && (int64_t)T * H <= kBesideValues; }
+// Whether d_gain is made beside the rows in the same launch, by workgroups that
+// read dy and h once more, column by column, or from the rows' workgroups' parts in a
+// second one. us a call, in one launch and in two, bf16 stream:
+//   T x H   128 x 512   1024 x 512   4096 x 512   512 x 2056   1024 x 2056   2048 x 2056
+//   one     11.1        11.3         20.7         11.4         12.0          19.4
+//   two     13.9        13.9         14.0         14.0         14.1          15.3
+//   T x H   128 x 7168  512 x 7168   1024 x 7168  2048 x 7168
+//   one     11.1        11.6         20.0         33.2
+//   two     13.9        17.0         22.2         31.2
+bool gain_beside(int T, int H) { return T <= 1024 && (int64_t)T * H <= 1 << 23; }
 
 template <bool WIDE>
 void launch_norm(const NormArgs& a, hipStream_t st) {
