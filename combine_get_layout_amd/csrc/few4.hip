@@ -114,7 +114,7 @@ constexpr int kLdsScales = 512;
 
 // Tokens [t0, t0 + 16 * NT) of the expert's list.
 template <int FORM, int RT, int NT, bool LDS>
-__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, const uint8_t* scales,
+__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, uint8_t* scales,
                                            int t0) {
     using Scale = ScaleRow<FORM>;
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
@@ -202,7 +202,31 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
     // the last step find nothing (a branch around them would make the compiler
     // wait for everything).
     UpStage<RT, NT, LDS> g0, g1;
-    load(wave, g0);
+    if (LDS && t0 == 0) {
+        // 16 rows' scales lie one after the other, in whole vectors. From memory each
+        // step would take a line of 128 bytes for the 4 or 8 that it needs of a row.
+        constexpr int kPasses = kCols * kLdsScales / 16 / kThreads;
+        u32x4 v[2][kPasses];
+#pragma unroll
+        for (int n = 0; n < kPasses; ++n) {
+            v[0][n] = buf_load16(s_gate, tid * 16, n * kThreads * 16);
+            v[1][n] = buf_load16(s_up, tid * 16, n * kThreads * 16);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(wave, g0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kPasses; ++n) {
+            const uint32_t at = (n * kThreads + tid) * 16;
+            if (at < kCols * lds) {
+                st16(scales + at, v[0][n]);
+                st16(scales + kCols * lds + at, v[1][n]);
+            }
+        }
+        barrier_only();
+    } else {
+        load(wave, g0);
+    }
     for (int s = wave; s < steps; s += 2 * kWaves) {
         load(s + kWaves, g1);
         __builtin_amdgcn_sched_barrier(0);
@@ -267,19 +291,6 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     const Found found = find_expert<kThreads>(a, sh.find);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
-    if constexpr (LDS) {
-        // 16 rows' scales lie one after the other, in whole vectors. From memory each
-        // step would take a line of 128 bytes for the 4 or 8 that it needs of a row.
-        constexpr int kRows = RT * 8;  // gate rows, and as many up rows
-        const uint32_t lds = ScaleRow<FORM>::bytes(a.H);
-        const int f0 = blockIdx.x * kRows, n = min(kRows, a.F - f0) * lds / 16;
-        const char* from = a.s13 + ((int64_t)found.expert * 2 * a.F + f0) * lds;
-        for (int v = tid; v < n; v += kThreads) {
-            st16(scales + v * 16, ld16(from + v * 16));
-            st16(scales + kRows * lds + v * 16, ld16(from + (int64_t)a.F * lds + v * 16));
-        }
-        __syncthreads();
-    }
     for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {
         if (NT > 1 && found.tokens - t0 > 16)
             up4_tokens<FORM, RT, NT, LDS>(a, found, sh, scales, t0);
