@@ -334,7 +334,10 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     }
     const int i = lane & 15, q = lane >> 4;
     const int h0 = blockIdx.x * kCols, cols = min(kCols, a.H - h0);
-    const int spans = (a.F + kSpan - 1) / kSpan, used = a.used[0];
+    // The number of used experts and the first 63 of them, in one load (the array is
+    // padded to 256 bytes).
+    int entries = a.used[lane], entries_from = -1;
+    const int spans = (a.F + kSpan - 1) / kSpan, used = readlane(entries, 0);
     const int units = used * spans;
     float* mine = sums + wave * a.T * kLd;
     for (int n = lane; n < a.T * kLd; n += kWave) mine[n] = 0.f;
@@ -349,10 +352,9 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     const int end = (int)((int64_t)units * (run + 1) / runs);
     int rank = u / spans, span = u % spans;
 
-    // 64 experts' entries at a time (one past the last is asked for, and none behind it).
-    int entries = 0, entries_from = -64;
+    // 64 experts' entries at a time.
     auto entry_of = [&](int r) {
-        if (r >= entries_from + 64) {
+        if (r < entries_from || r >= entries_from + 64) {
             entries_from = r;
             entries = a.used[1 + min(r + lane, used - 1)];
         }
@@ -565,7 +567,7 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const uint32_t row = ScaleRow<FORM>::bytes(a.H);
     const bool lds_scales = row <= kLdsScales;
     const bool many = lds_scales && s.T > 16 && lanes > 16 * experts;
-    const bool narrow = !lds_scales || (int64_t)((a.F + 31) / 32) * experts < 512;
+    const bool narrow = !lds_scales || (int64_t)((a.F + 31) / 32) * experts < 1024;
     const int cols = !many && narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
     void (*const kernel)(Few4Args) = !lds_scales ? few4_up_kernel<FORM, 2, 1, false>
