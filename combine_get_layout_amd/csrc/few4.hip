@@ -94,32 +94,48 @@ struct ScaleRow {
     }
 };
 
+// Orders this wave's own LDS stores and loads of other lanes' values (LDS takes a
+// wave's instructions in order; the compiler must not exchange them).
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Rows of 512 bytes (256 bf16 values) in LDS, their 16-byte chunks exchanged so that
+// 16 rows read at the same chunk, as a fragment of the matrix instruction does, lie
+// in different banks.
+__device__ __forceinline__ uint32_t row_chunk(int row, int chunk) { return row * 512 + ((chunk ^ (row & 15)) << 4); }
+
 // First launch: workgroup (x, y) computes RT / 2 * 16 values of f for the tokens
-// of the y-th used expert.
+// of the y-th used expert, up to TT of them at a time (NT tiles of 16 where NT > 1).
+// Dynamic LDS: the scales (2 * 16 * GT rows, if LDS), then the waves' copies of a
+// step's tokens, kWaves * NT * TT * 512 bytes, where their parts lie at the end.
 struct Up4Shared {
     FindShared find;
-    float part[kWaves][4][16][17];
 };
+typedef float Up4Part[4][16][17];
 
 // What a wave loads for one step; the scales unless they lie in LDS.
-template <int RT, int NT, bool LDS>
+template <int RT, int XL, bool LDS>
 struct UpStage {
     u32x4 w[RT][2];
     uint32_t scale[LDS ? 1 : RT][2];
-    u32x4 x[NT][8];
+    u32x4 x[XL];
 };
 
 // Bytes of a row's scales at most for them to lie in LDS.
 constexpr int kLdsScales = 512;
 
-// Tokens [t0, t0 + 16 * NT) of the expert's list.
-template <int FORM, int RT, int NT, bool LDS>
+// Tokens [t0, t0 + TT * NT) of the expert's list.
+template <int FORM, int RT, int NT, int TT, bool LDS>
 __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, uint8_t* scales,
-                                           int t0) {
+                                           uint8_t* area) {
     using Scale = ScaleRow<FORM>;
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     const int i = lane & 15, q = lane >> 4;
-    constexpr int GT = RT / 2, kCols = GT * 16;
+    constexpr int GT = RT / 2, kCols = GT * 16, kLoads = NT * TT / 2;
+    using Stage = UpStage<RT, kLoads, LDS>;
     const int f0 = blockIdx.x * kCols, cols = min(kCols, a.F - f0);
     const uint32_t ld = (uint32_t)a.H / 2;
     const uint8_t* w = a.w13 + ((int64_t)found.expert * 2 * a.F + f0) * ld;
@@ -131,157 +147,175 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
     const char* sc = a.s13 + ((int64_t)found.expert * 2 * a.F + f0) * lds;
     const auto s_gate = buf_resource(sc, cols * lds), s_up = buf_resource(sc + (int64_t)a.F * lds, cols * lds);
     const int steps = (a.H + kSpan - 1) / kSpan;
-    uint32_t xr[NT];
-    bool has[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        has[n] = t0 + n * 16 + i < found.tokens;
-        xr[n] = has[n] ? (uint32_t)sh.find.token[t0 + n * 16 + i] * a.H * 2 + q * 64 : kBufNone;
-    }
     bf16x8 minus_eight;
 #pragma unroll
     for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
-    f32x4 acc[RT][NT] = {};
-    auto load = [&](int s, UpStage<RT, NT, LDS>& g) {
+
+    for (int t0 = 0; t0 < found.tokens; t0 += TT * NT) {
+        // A step's values of a token are 512 bytes in a row: half a wave's load. (As the
+        // fragments that the matrix instruction takes they would be eight loads of four
+        // lanes a token each, which the L1 ran out of: one token 31 us instead of 25.)
+        uint32_t xr[kLoads];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            // Columns past H: past the end, zeros.
-            const uint32_t far = s * kSpan + p * 128 + q * 32 >= a.H ? kBufFar : 0u;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                g.w[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, s * 128 + p * 64);
-                if constexpr (!LDS)
-                    g.scale[r][p] = Scale::load(r < GT ? s_gate : s_up, (i + r % GT * 16) * lds + Scale::offset(p, q) + far,
-                                                s * Scale::kStep);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) g.x[n][p * 4 + m] = buf_load16(d_x, xr[n] + far, s * 512 + p * 256 + m * 16);
+        for (int n = 0; n < kLoads; ++n) {
+            const int at = t0 + 2 * n + (lane >> 5);
+            xr[n] = at < found.tokens ? (uint32_t)sh.find.token[at] * a.H * 2 + (lane & 31) * 16 : kBufNone;
         }
-    };
-    auto multiply = [&](const UpStage<RT, NT, LDS>& g, int s) {
+        uint8_t* const xs = area + wave * (NT * TT * 512);
+        f32x4 acc[RT][NT] = {};
+        auto load = [&](int s, Stage& g) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            // Past the row's scales: those of the row's start, beside codes of 0.
-            const uint32_t at = s * kSpan + p * 128 + q * 32 >= a.H ? 0u : s * Scale::kStep + Scale::offset(p, q);
-            f32x4 base[NT] = {};
-            if constexpr (FORM == EP_W4_INT) {
+            for (int p = 0; p < 2; ++p) {
+                // Columns past H: past the end, zeros.
+                const uint32_t far = s * kSpan + p * 128 + q * 32 >= a.H ? kBufFar : 0u;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    g.w[r][p] = buf_load16(r < GT ? d_gate : d_up, row0 + r % GT * 16 * ld + far, s * 128 + p * 64);
+                    if constexpr (!LDS)
+                        g.scale[r][p] = Scale::load(r < GT ? s_gate : s_up, (i + r % GT * 16) * lds + Scale::offset(p, q) + far,
+                                                    s * Scale::kStep);
+                }
+            }
+            const uint32_t far = s * kSpan + (lane & 31) * 8 >= a.H ? kBufFar : 0u;
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) g.x[n] = buf_load16(d_x, xr[n] + far, s * 512);
+        };
+        auto multiply = [&](const Stage& g, int s) {
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) st16(xs + row_chunk(2 * n + (lane >> 5), lane & 31), g.x[n]);
+            wave_lds_order();
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                bf16x8 xf[NT][4];
+                f32x4 base[NT] = {};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) base[n] = mfma_bf16(as_bf16(g.x[n][p * 4 + m]), minus_eight, base[n]);
-            }
+                    for (int m = 0; m < 4; ++m)  // rows past TT: earlier ones again, of which nothing is kept
+                        xf[n][m] = as_bf16(ld16(xs + row_chunk(n * 16 + (i & (TT - 1)), p * 16 + q * 4 + m)));
+                if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                uint32_t bits;
-                if constexpr (LDS)
-                    bits = Scale::from_lds(scales + (r * 16 + i) * lds + at);
-                else
-                    bits = g.scale[r][p];
-                const float scale = Scale::value(bits);
-                bf16x8 wf[4];
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(g.w[r][p][m], scale);
+                        for (int m = 0; m < 4; ++m) base[n] = mfma_bf16(xf[n][m], minus_eight, base[n]);
+                }
+                const bool in = s * kSpan + p * 128 + q * 32 < a.H;  // else codes of 0, and no scale
+                const uint32_t at = in ? s * Scale::kStep + Scale::offset(p, q) : 0u;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 c = FORM == EP_W4_INT ? base[n] : acc[r][n];
+                for (int r = 0; r < RT; ++r) {
+                    uint32_t bits;
+                    if constexpr (LDS)
+                        bits = in ? Scale::from_lds(scales + (r * 16 + i) * lds + at) : 0u;
+                    else
+                        bits = g.scale[r][p];
+                    const float scale = Scale::value(bits);
+                    bf16x8 wf[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) c = mfma_bf16(as_bf16(g.x[n][p * 4 + m]), wf[m], c);
-                    if constexpr (FORM == EP_W4_INT) {
+                    for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(g.w[r][p][m], scale);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(scale, c[j], acc[r][n][j]);
-                    } else {
-                        acc[r][n] = c;
+                    for (int n = 0; n < NT; ++n) {
+                        f32x4 c = FORM == EP_W4_INT ? base[n] : acc[r][n];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[n][m], wf[m], c);
+                        if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(scale, c[j], acc[r][n][j]);
+                        } else {
+                            acc[r][n] = c;
+                        }
                     }
                 }
             }
-        }
-    };
-    // The next step's loads are in flight while this one is multiplied; those past
-    // the last step find nothing (a branch around them would make the compiler
-    // wait for everything).
-    UpStage<RT, NT, LDS> g0, g1;
-    if (LDS && t0 == 0) {
-        // 16 rows' scales lie one after the other, in whole vectors. From memory each
-        // step would take a line of 128 bytes for the 4 or 8 that it needs of a row.
-        constexpr int kPasses = kCols * kLdsScales / 16 / kThreads;
-        u32x4 v[2][kPasses];
+            wave_lds_order();
+        };
+        // The next step's loads are in flight while this one is multiplied; those past
+        // the last step find nothing (a branch around them would make the compiler
+        // wait for everything).
+        Stage g0, g1;
+        if (LDS && t0 == 0) {
+            // 16 rows' scales lie one after the other, in whole vectors. From memory each
+            // step would take a line of 128 bytes for the 4 or 8 that it needs of a row.
+            constexpr int kPasses = kCols * kLdsScales / 16 / kThreads;
+            u32x4 v[2][kPasses];
 #pragma unroll
-        for (int n = 0; n < kPasses; ++n) {
-            v[0][n] = buf_load16(s_gate, tid * 16, n * kThreads * 16);
-            v[1][n] = buf_load16(s_up, tid * 16, n * kThreads * 16);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        load(wave, g0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int n = 0; n < kPasses; ++n) {
-            const uint32_t at = (n * kThreads + tid) * 16;
-            if (at < kCols * lds) {
-                st16(scales + at, v[0][n]);
-                st16(scales + kCols * lds + at, v[1][n]);
+            for (int n = 0; n < kPasses; ++n) {
+                v[0][n] = buf_load16(s_gate, tid * 16, n * kThreads * 16);
+                v[1][n] = buf_load16(s_up, tid * 16, n * kThreads * 16);
             }
-        }
-        barrier_only();
-    } else {
-        load(wave, g0);
-    }
-    for (int s = wave; s < steps; s += 2 * kWaves) {
-        load(s + kWaves, g1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(g0, s);
-        __builtin_amdgcn_sched_barrier(0);
-        load(s + 2 * kWaves, g0);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(g1, s + kWaves);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    settle(acc);
-    // Sum the waves' parts, 32 values of f at a time.
+            __builtin_amdgcn_sched_barrier(0);
+            load(wave, g0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int g = 0; g < GT; g += 2) {
-            constexpr int kSub = GT < 2 ? 1 : 2;  // sub-tiles of 16 values in this pass
-#pragma unroll
-            for (int r = 0; r < 2 * kSub; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sh.part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][n][j];
-            __syncthreads();
-#pragma unroll
-            for (int c0 = 0; c0 < 16 * 32; c0 += kThreads) {
-                const int tk = (c0 + tid) >> 5, c = tid & 31;
-                const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
-                if (at >= found.tokens || f >= a.F || c >= 16 * kSub) continue;
-                float gate = 0.f, up = 0.f;
-#pragma unroll
-                for (int v = 0; v < kWaves; ++v) {
-                    gate += sh.part[v][c >> 4][tk][c & 15];
-                    up += sh.part[v][2 + (c >> 4)][tk][c & 15];
+            for (int n = 0; n < kPasses; ++n) {
+                const uint32_t at = (n * kThreads + tid) * 16;
+                if (at < kCols * lds) {
+                    st16(scales + at, v[0][n]);
+                    st16(scales + kCols * lds + at, v[1][n]);
                 }
-                const float r = gate / (1.0f + __expf(-gate)) * up;
-                // Two bf16 values for the second product's matrix instruction, the
-                // rounded one (of a finite value bf16's largest at most) and what it
-                // leaves (nothing of an infinity or NaN).
-                uint32_t hi = f32_to_bf16(r);
-                if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
-                const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
-                uint16_t* act = a.act + (int64_t)sh.find.row[at] * 2 * a.F + f;
-                act[0] = (uint16_t)hi;
-                act[a.F] = (uint16_t)f32_to_bf16(rest);
             }
-            __syncthreads();
+            barrier_only();
+        } else {
+            load(wave, g0);
+        }
+        for (int s = wave; s < steps; s += 2 * kWaves) {
+            load(s + kWaves, g1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(g0, s);
+            __builtin_amdgcn_sched_barrier(0);
+            load(s + 2 * kWaves, g0);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(g1, s + kWaves);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        settle(acc);
+        // Sum the waves' parts, 32 values of f at a time.
+        Up4Part* const part = reinterpret_cast<Up4Part*>(area);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int g = 0; g < GT; g += 2) {
+                constexpr int kSub = GT < 2 ? 1 : 2;  // sub-tiles of 16 values in this pass
+#pragma unroll
+                for (int r = 0; r < 2 * kSub; ++r)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][n][j];
+                __syncthreads();
+#pragma unroll
+                for (int c0 = 0; c0 < 16 * 32; c0 += kThreads) {
+                    const int tk = (c0 + tid) >> 5, c = tid & 31;
+                    const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
+                    if (tk >= TT || at >= found.tokens || f >= a.F || c >= 16 * kSub) continue;
+                    float gate = 0.f, up = 0.f;
+#pragma unroll
+                    for (int v = 0; v < kWaves; ++v) {
+                        gate += part[v][c >> 4][tk][c & 15];
+                        up += part[v][2 + (c >> 4)][tk][c & 15];
+                    }
+                    const float r = gate / (1.0f + __expf(-gate)) * up;
+                    // Two bf16 values for the second product's matrix instruction, the
+                    // rounded one (of a finite value bf16's largest at most) and what it
+                    // leaves (nothing of an infinity or NaN).
+                    uint32_t hi = f32_to_bf16(r);
+                    if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
+                    const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
+                    uint16_t* act = a.act + (int64_t)sh.find.row[at] * 2 * a.F + f;
+                    act[0] = (uint16_t)hi;
+                    act[a.F] = (uint16_t)f32_to_bf16(rest);
+                }
+                __syncthreads();
+            }
         }
     }
 }
 
-template <int FORM, int RT, int NT, bool LDS>
+template <int FORM, int RT, int NT, int TT, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     __shared__ Up4Shared sh;
     extern __shared__ u32x4 lds_vectors[];
-    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);  // [gate rows, up rows][bytes of a row's scales]
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);
+    uint8_t* const area = scales + (LDS ? RT * 16 * ScaleRow<FORM>::bytes(a.H) : 0u);
     const int tid = threadIdx.x;
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) a.err[0] = 0u;
@@ -291,12 +325,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     const Found found = find_expert<kThreads>(a, sh.find);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
-    for (int t0 = 0; t0 < found.tokens; t0 += 16 * NT) {
-        if (NT > 1 && found.tokens - t0 > 16)
-            up4_tokens<FORM, RT, NT, LDS>(a, found, sh, scales, t0);
-        else
-            up4_tokens<FORM, RT, 1, LDS>(a, found, sh, scales, t0);
-    }
+    up4_tokens<FORM, RT, NT, TT, LDS>(a, found, sh, scales, area);
 }
 
 // What a wave loads for one unit; the scales as its own run of an expert's, where
@@ -411,9 +440,15 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
         uint32_t bits[RT][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const uint32_t at = span * kSpan + p * 128 + q * 32 >= a.F ? 0u : span * Scale::kStep + Scale::offset(p, q);
+            const bool in = span * kSpan + p * 128 + q * 32 < a.F;  // else codes of 0, and no scale
+            const uint32_t at = in ? span * Scale::kStep + Scale::offset(p, q) : 0u;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) bits[r][p] = LDS ? Scale::from_lds(scales + (r * 16 + i) * lds + at) : g.scale[LDS ? 0 : r][p];
+            for (int r = 0; r < RT; ++r) {
+                if constexpr (LDS)
+                    bits[r][p] = in ? Scale::from_lds(scales + (r * 16 + i) * lds + at) : 0u;
+                else
+                    bits[r][p] = g.scale[r][p];
+            }
         }
         for (int t0 = 0; t0 < tokens; t0 += 8) {
             // The conversion stays in the loop: its results take four times the registers.
@@ -550,8 +585,9 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// 16-value tiles of h per workgroup of the second launch, as LDS holds their sums.
-int down_tiles(const ep_shape& s) { return s.T <= 64 ? 4 : 2; }
+// 16-value tiles of h per workgroup of the second launch, so that two workgroups'
+// sums fit a CU's LDS.
+int down_tiles(const ep_shape& s) { return s.T <= 32 ? 4 : 2; }
 
 // Workgroups of the second launch for the same values of h: as many as fill the
 // chip, with a unit for every wave.
@@ -559,6 +595,15 @@ int down_splits(const ep_shape& s, int F) {
     const int64_t units = std::min<int64_t>(s.E, (int64_t)s.T * s.K) * ((F + kSpan - 1) / kSpan);
     const int64_t cols = (s.H + 16 * down_tiles(s) - 1) / (16 * down_tiles(s));
     return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), units / kWaves));
+}
+
+typedef void (*Kernel)(Few4Args);
+template <int FORM, int RT>
+Kernel up_kernel(int tt) {
+    return tt == 2   ? few4_up_kernel<FORM, RT, 1, 2, true>
+           : tt == 4 ? few4_up_kernel<FORM, RT, 1, 4, true>
+           : tt == 8 ? few4_up_kernel<FORM, RT, 1, 8, true>
+                     : few4_up_kernel<FORM, RT, 1, 16, true>;
 }
 
 template <int FORM>
@@ -570,19 +615,21 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const bool narrow = !lds_scales || (int64_t)((a.F + 31) / 32) * experts < 1024;
     const int cols = !many && narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
-    void (*const kernel)(Few4Args) = !lds_scales ? few4_up_kernel<FORM, 2, 1, false>
-                                     : many      ? few4_up_kernel<FORM, 4, 2, true>
-                                     : narrow    ? few4_up_kernel<FORM, 2, 1, true>
-                                                 : few4_up_kernel<FORM, 4, 1, true>;
-    hipLaunchKernelGGL(kernel, up, dim3(kThreads), lds_scales ? 2 * cols * row : 0, st, a);
+    // Tokens at a time: those of most experts, as the weights are read again for more.
+    const int tt = s.T <= 2 ? 2 : s.T <= 4 ? 4 : s.T <= 8 || lanes <= 4 * experts ? 8 : 16;
+    const Kernel first = !lds_scales ? few4_up_kernel<FORM, 2, 1, 16, false>
+                         : many      ? few4_up_kernel<FORM, 4, 2, 16, true>
+                         : narrow    ? up_kernel<FORM, 2>(tt)
+                                     : up_kernel<FORM, 4>(tt);
+    const size_t area = std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (many ? 32 : lds_scales ? tt : 16));
+    hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);
     const int tiles = down_tiles(s);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
     const uint32_t row2 = ScaleRow<FORM>::bytes(a.F);
     const bool lds2 = row2 <= kLdsScales2;
-    // 66,560 + 16,384 bytes at most
-    const size_t lds = sizeof(float) * kWaves * (16 * tiles + 1) * s.T + (lds2 ? kWaves * 16 * tiles * row2 : 0);
-    void (*const second)(Few4Args) = tiles == 4 ? (lds2 ? few4_down_kernel<FORM, 4, true> : few4_down_kernel<FORM, 4, false>)
-                                                : (lds2 ? few4_down_kernel<FORM, 2, true> : few4_down_kernel<FORM, 2, false>);
+    const size_t lds = kWaves * (sizeof(float) * (16 * tiles + 1) * s.T + (lds2 ? 16 * tiles * row2 : 0));  // 75,776 at most
+    const Kernel second = tiles == 4 ? (lds2 ? few4_down_kernel<FORM, 4, true> : few4_down_kernel<FORM, 4, false>)
+                                     : (lds2 ? few4_down_kernel<FORM, 2, true> : few4_down_kernel<FORM, 2, false>);
     hipLaunchKernelGGL(second, down, dim3(kThreads), lds, st, a);
 }
 
