@@ -626,7 +626,7 @@ int ep_route_grad(const ep_shape* shape, const float* logits, const ep_router* r
 }
 
 size_t ep_few_w4_workspace_bytes(const ep_shape* shape, int32_t F) {
-    if (ep_few_workspace_bytes(shape, F) == 0) return 0;
+    if (ep_few_workspace_bytes(shape, F) == 0 || (int64_t)shape->T * shape->K * F >= 1 << 29) return 0;
     return ws_few_w4(*shape, F).total;
 }
 
@@ -639,6 +639,8 @@ int ep_moe_few_w4(const ep_shape* shape, const ep_tokens* tokens, const ep_exper
     const int step = x.form == EP_W4_INT ? 128 : 32;  // columns that share a scale
     if (x.F < step || x.F % step != 0 || shape->H % step != 0) return EP_ERR_ARG;
     if (shape->T > EP_FEW_MAX_TOKENS || x.F > EP_MAX_DIM || shape->H > EP_MAX_DIM) return EP_ERR_UNSUPPORTED;
+    // 32-bit offsets in the inner activations, 4 F bytes a lane.
+    if ((int64_t)shape->T * shape->K * x.F >= 1 << 29) return EP_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < ws_few_w4(*shape, x.F).total) return EP_ERR_ARG;
     if (!x.w13 || !x.w13_scales || !x.w2 || !x.w2_scales) return EP_ERR_ARG;
     if (shape->T > 0 && (!tokens->x || !tokens->topk_idx || !tokens->topk_weights || !out)) return EP_ERR_ARG;

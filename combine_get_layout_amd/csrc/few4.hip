@@ -585,16 +585,26 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// 16-value tiles of h per workgroup of the second launch, so that two workgroups'
-// sums fit a CU's LDS.
-int down_tiles(const ep_shape& s) { return s.T <= 32 ? 4 : 2; }
+// Units of the second launch, at most (the used experts are known on the GPU alone).
+int64_t down_units(const ep_shape& s, int F) {
+    return std::min<int64_t>(s.E, (int64_t)s.T * s.K) * ((F + kSpan - 1) / kSpan);
+}
+// 16-value tiles of h per workgroup of the second launch: 4, which read the activations
+// half as often, where each wave has many units (and LDS holds the sums), else 2, which
+// keep more waves busy. Both launches with 4 and with 2 tiles, us:
+//   32 tokens, top-8 of 64 experts of 7168 x 2048 (512 units)  344  359
+//   16 tokens, top-8 of 64, 7168 x 512 (128)                   91.8 90.7
+//   8 tokens, top-4 of 64, 4096 x 1024 (128)                   54.4 50.4
+//   13 tokens, top-3 of 40, 2080 x 736 (117)                   37.1 30.8
+//   1 token, top-8 of 64, 7168 x 2048 (64)                     53.2 52.1
+int down_tiles(const ep_shape& s, int F) { return s.T <= 32 && down_units(s, F) >= 256 ? 4 : 2; }
 
-// Workgroups of the second launch for the same values of h: as many as fill the
-// chip, with a unit for every wave.
+// Workgroups of the second launch for the same values of h: as many as fill the chip
+// (512; 256 and 384 were 0 to 20% slower in the cases above, 1,024 4 to 20%), with a
+// unit for every wave.
 int down_splits(const ep_shape& s, int F) {
-    const int64_t units = std::min<int64_t>(s.E, (int64_t)s.T * s.K) * ((F + kSpan - 1) / kSpan);
-    const int64_t cols = (s.H + 16 * down_tiles(s) - 1) / (16 * down_tiles(s));
-    return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), units / kWaves));
+    const int64_t width = 16 * down_tiles(s, F), cols = (s.H + width - 1) / width;
+    return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), down_units(s, F) / kWaves));
 }
 
 typedef void (*Kernel)(Few4Args);
@@ -623,7 +633,7 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
                                      : up_kernel<FORM, 4>(tt);
     const size_t area = std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (many ? 32 : lds_scales ? tt : 16));
     hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);
-    const int tiles = down_tiles(s);
+    const int tiles = down_tiles(s, a.F);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
     const uint32_t row2 = ScaleRow<FORM>::bytes(a.F);
     const bool lds2 = row2 <= kLdsScales2;

@@ -691,8 +691,9 @@ size_t ep_few_w4_workspace_bytes(const ep_shape *shape, int32_t F);
 
 /* ep_moe_few with 4-bit weights: the same result for the values that codes and
  * scales stand for (these are exact in the products, sums are held in 32
- * bits), the same tokens, errors, workspace rules and limits. Longer batches
- * go in parts of EP_FEW_MAX_TOKENS. Base pointers 16 B aligned. */
+ * bits), the same tokens, errors, workspace rules and limits, and T * K * F <
+ * 2^29. Longer batches go in parts of EP_FEW_MAX_TOKENS. Base pointers 16 B
+ * aligned. */
 int ep_moe_few_w4(const ep_shape *shape, const ep_tokens *tokens, const ep_experts_w4 *experts,
                   uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 

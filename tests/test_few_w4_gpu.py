@@ -212,6 +212,31 @@ def test_few_w4_keeps_nonfinite_values_with_their_tokens(form):
     assert torch.isnan(out[3]).all() and torch.isnan(out[4]).all() and torch.isnan(out[1]).all()
 
 
+@pytest.mark.parametrize("H,F", [(128, 128), (640, 384), (256, 1152)])
+def test_few_w4_keeps_the_sign_of_infinite_scales(H, F):
+    """An infinite scale of the second matrix makes an infinity of its block's sum's sign (sums far
+    from zero), and none of a NaN where a row's columns or the steps behind its end have no value."""
+    T = 5
+    g = torch.Generator().manual_seed(14)
+    x, w13, w2 = randn(g, T, H), four(g, 1, 2 * F, H, INT), four(g, 1, H, F, INT)
+    w2[1][0, 3, 0] = float("inf")
+    w2[1][0, 7, F // 128 - 1] = float("-inf")
+    idx, w = torch.zeros((T, 1), dtype=torch.int64), torch.full((T, 1), 0.5)
+    out, _ = few_call(x, idx, w, experts(w13, w2, F, INT), 1)
+    finite = (w2[0], torch.where(torch.isfinite(w2[1]), w2[1], torch.ones((), dtype=BF16)))
+    act = silu_parts(x.double() @ values(w13[0][0], w13[1][0], INT)[0].T, F)[3]
+    codes, mags = values(finite[0][0], torch.ones_like(finite[1][0]), INT)
+    for h, block, sign in ((3, 0, 1.0), (7, F // 128 - 1, -1.0)):
+        cut = slice(block * 128, block * 128 + 128)
+        part = act[:, cut] @ codes[h, cut]
+        sure = part.abs() > 1e-3 * (act[:, cut].abs() @ mags[h, cut])
+        assert sure.any()
+        assert torch.equal(out[sure.cuda(), h].cpu().double(), sign * torch.sign(part[sure]) * float("inf")), h
+    keep = [h for h in range(H) if h not in (3, 7)]
+    ref, bound = few_reference(x, w13, finite, idx, w, F, INT)
+    check(out[:, keep], ref[:, keep], bound[:, keep], "other outputs")
+
+
 @FORMS
 @pytest.mark.parametrize("F", [128, 2048])
 def test_few_w4_without_any_lane(form, F):

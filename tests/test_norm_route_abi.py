@@ -108,10 +108,12 @@ def test_few_w4_refusals_and_workspace(lib, shape):
     refused(call(s=ep.make_shape(129, 256, 2, 8, 1)), ep.EP_ERR_UNSUPPORTED)
     refused(call(x=X((1 << 20) + 128, 0, P, P, P, P)), ep.EP_ERR_UNSUPPORTED)
     refused(call(s=ep.make_shape(4, (1 << 20) + 128, 2, 8, 1)), ep.EP_ERR_UNSUPPORTED)
+    refused(call(s=ep.make_shape(128, 256, 4, 8, 1), x=X(1 << 20, 0, P, P, P, P)), ep.EP_ERR_UNSUPPORTED)
     n = ep.ep_few_w4_workspace_bytes(shape, 128)
     assert n >= 256 + 32 * 2 * 128 * 2 and n % 256 == 0
     refused(call(wsb=n - 1))
-    for s, F in ((ep.make_shape(129, 256, 2, 8, 1), 128), (shape, 0), (shape, (1 << 20) + 32)):
+    for s, F in ((ep.make_shape(129, 256, 2, 8, 1), 128), (shape, 0), (shape, (1 << 20) + 32),
+                 (ep.make_shape(128, 256, 4, 8, 1), 1 << 20)):
         assert ep.ep_few_w4_workspace_bytes(s, F) == 0
     with pytest.raises(RuntimeError):
         ep.alloc_few_w4_workspace(ep.make_shape(129, 256, 2, 8, 1), 128)
