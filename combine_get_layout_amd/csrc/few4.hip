@@ -330,11 +330,11 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
 
 // What a wave loads for one unit; the scales as its own run of an expert's, where
 // they lie in LDS.
-template <int RT, bool LDS>
+template <int RT, int CAP, bool LDS>
 struct DownStage {
     u32x4 w[RT][2];
     uint32_t scale[LDS ? 1 : RT][2];
-    u32x4 act[8];
+    u32x4 act[CAP ? CAP : 8];
 };
 
 // Bytes of a row's scales at most for a wave to hold those of its rows in LDS.
@@ -343,18 +343,19 @@ constexpr int kLdsScales2 = 64;
 // Second launch: workgroup x computes RT * 16 values of h for every token, or,
 // where `splits` workgroups (grid y) share them, its part. Unit u = (used expert,
 // span of 256 values of f); each wave takes a run of units. The matrix
-// instruction's 16 rows are 8 tokens of the expert, as rounded values (rows 0 to
-// 7) and as what those leave (rows 8 to 15). Sums per token lie in LDS, one set a
-// wave, and are added at the end in a fixed order.
-template <int FORM, int RT, bool LDS>
+// instruction's 16 rows are 8 tokens of the expert (CAP, where that is not 0), as
+// rounded values (rows 0 to 7) and as what those leave (rows 8 to 15). Sums per token
+// lie in LDS, one set a wave, and are added at the end in a fixed order.
+template <int FORM, int RT, int CAP, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     using Scale = ScaleRow<FORM>;
-    constexpr int kCols = RT * 16, kLd = kCols + 1;
+    constexpr int kCols = RT * 16, kLd = kCols + 1, kTokens = CAP ? CAP : 8;
     extern __shared__ u32x4 lds_vectors[];
-    // [kWaves][rows][bytes of a row's scales] and [kWaves][T][kLd]
-    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors) + (LDS ? uniform_wave() * kCols * Scale::bytes(a.F) : 0u);
-    float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds_vectors) +
-                                                 (LDS ? kWaves * kCols * Scale::bytes(a.F) : 0u));
+    // [kWaves][rows][bytes of a row's scales], [kWaves][2 * CAP][512] and [kWaves][T][kLd]
+    const uint32_t lds = Scale::bytes(a.F), lds_block = LDS ? kCols * lds : 0u;
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors) + uniform_wave() * lds_block;
+    uint8_t* const rows = reinterpret_cast<uint8_t*>(lds_vectors) + kWaves * lds_block + uniform_wave() * (CAP * 1024);
+    float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds_vectors) + kWaves * (lds_block + CAP * 1024));
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         bool bad = false;
@@ -375,7 +376,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
 
     const uint32_t ld = (uint32_t)a.F / 2;
-    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld, lds = Scale::bytes(a.F);
+    const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld;
     const int run = blockIdx.y * kWaves + wave, runs = a.splits * kWaves;
     int u = (int)((int64_t)units * run / runs);
     const int end = (int)((int64_t)units * (run + 1) / runs);
@@ -398,16 +399,30 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
         return r;
     };
     const auto d_act = buf_resource(a.act, (uint32_t)(a.T * a.K) * 4 * a.F);
-    auto load_act = [&](int id, bool has, int span, u32x4 (&v)[8]) {
-        const uint32_t off = has ? (uint32_t)((id & 0xFFFF) * 2 + (i >> 3)) * a.F * 2 + q * 64 : kBufFar;
+    auto load_act = [&](const Route& route, int t0, int tokens, int span, auto& v) {
+        if constexpr (CAP > 0) {
+            // A token's values and their rests are 512 bytes each: a wave's load.
+            const uint32_t off = (lane >> 5) * a.F * 2 + (lane & 31) * 16;
+            const bool in = span * kSpan + (lane & 31) * 8 < a.F;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const uint32_t far = span * kSpan + p * 128 + q * 32 >= a.F ? kBufFar : off;
+            for (int n = 0; n < CAP; ++n) {
+                const int row = readlane(route.id, (t0 & 15) + n) & 0xFFFF;
+                const uint32_t far = in && t0 + n < tokens ? row * 4u * a.F : kBufFar;
+                v[n] = buf_load16(d_act, off + far, span * 512);
+            }
+        } else {
+            const bool has = t0 + (i & 7) < tokens;
+            const int id = __shfl(route.id, (t0 & 8) + (i & 7));
+            const uint32_t off = has ? (uint32_t)((id & 0xFFFF) * 2 + (i >> 3)) * a.F * 2 + q * 64 : kBufFar;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) v[p * 4 + m] = buf_load16(d_act, far, span * 512 + p * 256 + m * 16);
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t far = span * kSpan + p * 128 + q * 32 >= a.F ? kBufFar : off;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) v[p * 4 + m] = buf_load16(d_act, far, span * 512 + p * 256 + m * 16);
+            }
         }
     };
-    auto load_weights = [&](int64_t e, int span, DownStage<RT, LDS>& g) {
+    auto load_weights = [&](int64_t e, int span, DownStage<RT, CAP, LDS>& g) {
         const auto d = buf_resource(a.w2 + (e * a.H + h0) * ld, w_bytes);
         const auto ds = buf_resource(a.s2 + (e * a.H + h0) * lds, cols * lds);
 #pragma unroll
@@ -436,7 +451,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 
     float acc[RT][4] = {};
     // One unit, whose loads are there.
-    auto unit = [&](DownStage<RT, LDS>& g, int tokens, Route route, bool last) {
+    auto unit = [&](DownStage<RT, CAP, LDS>& g, int tokens, Route route, bool last) {
         uint32_t bits[RT][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -450,18 +465,31 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                     bits[r][p] = g.scale[r][p];
             }
         }
-        for (int t0 = 0; t0 < tokens; t0 += 8) {
+        for (int t0 = 0; t0 < tokens; t0 += kTokens) {
             // The conversion stays in the loop: its results take four times the registers.
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) asm volatile("" : "+v"(g.w[r][p]));
+            bf16x8 v[8];
+            if constexpr (CAP > 0) {
+#pragma unroll
+                for (int n = 0; n < CAP; ++n) st16(rows + row_chunk(2 * n + (lane >> 5), lane & 31), g.act[n]);
+                wave_lds_order();
+#pragma unroll
+                for (int m = 0; m < 8; ++m)  // rows past CAP: earlier ones again, of which nothing is kept
+                    v[m] = as_bf16(ld16(rows + row_chunk((i & (CAP - 1)) * 2 + (i >> 3), (m >> 2) * 16 + q * 4 + (m & 3))));
+                wave_lds_order();
+            } else {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) v[m] = as_bf16(g.act[m]);
+            }
             f32x4 c[RT][2] = {};
             if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(as_bf16(g.act[p * 4 + m]), minus_eight, c[0][p]);
+                    for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(v[p * 4 + m], minus_eight, c[0][p]);
 #pragma unroll
                     for (int r = 1; r < RT; ++r) c[r][p] = c[0][p];
                 }
@@ -472,14 +500,13 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
-                        c[r][p] = mfma_bf16(as_bf16(g.act[p * 4 + m]),
+                        c[r][p] = mfma_bf16(v[p * 4 + m],
                                             codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(bits[r][p])), c[r][p]);
             settle(c);
             const Route now = route;
-            if (t0 + 8 < tokens) {  // more than 8 tokens: the weights stay, the tokens change
-                if (t0 & 8) route = load_route(rank, tokens, t0 + 8);
-                const int n = (~t0 & 8) + (i & 7);
-                load_act(__shfl(route.id, n), t0 + 8 + (i & 7) < tokens, span, g.act);
+            if (t0 + kTokens < tokens) {  // the weights stay, the tokens change
+                if (((t0 + kTokens) & 15) == 0) route = load_route(rank, tokens, t0 + kTokens);
+                load_act(route, t0 + kTokens, tokens, span, g.act);
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -488,10 +515,10 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                     acc[r][j] += FORM == EP_W4_INT ? fmaf(Scale::value(bits[r][1]), c[r][1][j],
                                                           Scale::value(bits[r][0]) * c[r][0][j])
                                                    : c[r][0][j] + c[r][1][j];
-            if (tokens <= 8 && !last) break;
+            if (tokens <= kTokens && !last) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int n = (t0 & 8) + (q & 1) * 4 + j;
+                const int n = (t0 & 15) + (((q & 1) * 4 + j) & (kTokens - 1));
                 const int id = __shfl(now.id, n);
                 const float weight = __shfl(now.w, n);
 #pragma unroll
@@ -501,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                     const float rest = __shfl_xor(acc[r][j], 32);
                     const float dot = __builtin_isfinite(acc[r][j]) ? acc[r][j] + rest : acc[r][j];
                     acc[r][j] = 0.f;
-                    if (q < 2 && t0 + q * 4 + j < tokens) {
+                    if (q < 2 && q * 4 + j < kTokens && t0 + q * 4 + j < tokens) {
                         float* sum = mine + (id >> 16) * kLd + r * 16 + i;
                         *sum = fmaf(weight, dot, *sum);
                     }
@@ -509,7 +536,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
             }
         }
     };
-    DownStage<RT, LDS> g0, g1;
+    DownStage<RT, CAP, LDS> g0, g1;
     int entry = 0;
     Route route = {0, 0.f}, ahead = {0, 0.f};  // the first 16 tokens of this expert and of the next
     if (u < end) {
@@ -522,13 +549,13 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
             load_scales(entry & 0xFFFF, 0u);
             keep_scales();
         }
-        load_act(__shfl(route.id, i & 7), (i & 7) < entry >> 16, span, g0.act);
+        load_act(route, 0, entry >> 16, span, g0.act);
     }
     // The next unit's loads, and the routes of the expert behind its own, are in flight
     // while this one is multiplied. All of them are made on every turn, behind the last
     // unit past the row's end: a branch around them would make the compiler wait for
     // everything.
-    auto turn = [&](DownStage<RT, LDS>& g, DownStage<RT, LDS>& gn) {
+    auto turn = [&](DownStage<RT, CAP, LDS>& g, DownStage<RT, CAP, LDS>& gn) {
         const bool more = u + 1 < end, same = !more || span + 1 < spans;
         const int next_rank = same ? rank : rank + 1, next_span = !more ? spans : same ? span + 1 : 0;
         const int next_entry = entry_of(next_rank), after = min(next_rank + 1, used - 1);
@@ -537,7 +564,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
         if (!same) next = ahead;
         load_weights(next_entry & 0xFFFF, next_span, gn);
         if constexpr (LDS) load_scales(next_entry & 0xFFFF, same ? kBufFar : 0u);
-        load_act(__shfl(next.id, i & 7), (i & 7) < next_entry >> 16, next_span, gn.act);
+        load_act(next, 0, next_entry >> 16, next_span, gn.act);
         ahead = load_route(after, after_tokens, 0);
         __builtin_amdgcn_sched_barrier(0);
         unit(g, entry >> 16, route, !more || !same);
@@ -608,6 +635,10 @@ int down_splits(const ep_shape& s, int F) {
 }
 
 typedef void (*Kernel)(Few4Args);
+template <int FORM, int RT, int CAP>
+Kernel down_kernel(bool lds) {
+    return lds ? few4_down_kernel<FORM, RT, CAP, true> : few4_down_kernel<FORM, RT, CAP, false>;
+}
 template <int FORM, int RT>
 Kernel up_kernel(int tt) {
     return tt == 2   ? few4_up_kernel<FORM, RT, 1, 2, true>
@@ -637,9 +668,14 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
     const uint32_t row2 = ScaleRow<FORM>::bytes(a.F);
     const bool lds2 = row2 <= kLdsScales2;
-    const size_t lds = kWaves * (sizeof(float) * (16 * tiles + 1) * s.T + (lds2 ? 16 * tiles * row2 : 0));  // 75,776 at most
-    const Kernel second = tiles == 4 ? (lds2 ? few4_down_kernel<FORM, 4, true> : few4_down_kernel<FORM, 4, false>)
-                                     : (lds2 ? few4_down_kernel<FORM, 2, true> : few4_down_kernel<FORM, 2, false>);
+    // One or two tokens' activations over LDS, in whole loads instead of fragments: 51.9
+    // and 42.5 us instead of 53.6 and 43.9 (1 token, top-8 of 64 experts of 7168 x 2048; 2,
+    // top-6 of 64 of 5120 x 1536), the same as fragments at 4 tokens, slower at more.
+    const int cap = s.T <= 2 ? 2 : 0;
+    const size_t lds = kWaves * (sizeof(float) * (16 * tiles + 1) * s.T + cap * 1024 + (lds2 ? 16 * tiles * row2 : 0));
+    const Kernel second = tiles == 4 ? down_kernel<FORM, 4, 0>(lds2)
+                          : cap == 2 ? down_kernel<FORM, 2, 2>(lds2)
+                                     : down_kernel<FORM, 2, 0>(lds2);
     hipLaunchKernelGGL(second, down, dim3(kThreads), lds, st, a);
 }
 
