@@ -42,14 +42,11 @@ __device__ __forceinline__ V row_sum(V v) {
     v += dpp<kDppMirror16>(v);
     return v;
 }
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
-template <class V>
-__device__ __forceinline__ V row_max(V v) {
-    v = larger(v, dpp<kDppSwap1>(v));
-    v = larger(v, dpp<kDppSwap2>(v));
-    v = larger(v, dpp<kDppMirror8>(v));
-    v = larger(v, dpp<kDppMirror16>(v));
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp<kDppSwap1>(v));
+    v = fmaxf(v, dpp<kDppSwap2>(v));
+    v = fmaxf(v, dpp<kDppMirror8>(v));
+    v = fmaxf(v, dpp<kDppMirror16>(v));
     return v;
 }
 // The same over the wave's 64 lanes.
@@ -58,10 +55,22 @@ __device__ __forceinline__ V wave_sum(V v) {
     v = row_sum(v);
     return (readlane_f(v, 0) + readlane_f(v, 16)) + (readlane_f(v, 32) + readlane_f(v, 48));
 }
-template <class V>
-__device__ __forceinline__ V wave_max(V v) {
+__device__ __forceinline__ float wave_max(float v) {
     v = row_max(v);
-    return larger(larger(readlane_f(v, 0), readlane_f(v, 16)), larger(readlane_f(v, 32), readlane_f(v, 48)));
+    return fmaxf(fmaxf(readlane_f(v, 0), readlane_f(v, 16)), fmaxf(readlane_f(v, 32), readlane_f(v, 48)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+// In a scalar register.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, dpp<kDppSwap1>(v));
+    v = max(v, dpp<kDppSwap2>(v));
+    v = max(v, dpp<kDppMirror8>(v));
+    v = max(v, dpp<kDppMirror16>(v));
+    return max(max((uint32_t)readlane((int)v, 0), (uint32_t)readlane((int)v, 16)),
+               max((uint32_t)readlane((int)v, 32), (uint32_t)readlane((int)v, 48)));
 }
 
 }  // namespace ep

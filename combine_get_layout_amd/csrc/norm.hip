@@ -452,7 +452,7 @@ int grad_groups(int T, int H, bool wide) {
 //   T x H   128 x 7168  512 x 7168   1024 x 7168  2048 x 7168
 //   one     11.1        11.6         20.0         33.2
 //   two     13.9        17.0         22.2         31.2
-bool gain_beside(int T, int H) { return T <= 1024 && (int64_t)T * H <= 1 << 23; }
+bool gain_beside(int T, int H) { return H <= kLongH && T <= 1024 && (int64_t)T * H <= 1 << 23; }
 
 template <bool WIDE>
 void launch_norm(const NormArgs& a, hipStream_t st) {

@@ -27,12 +27,44 @@ struct RouteArgs {
 // infinity, 0 for a masked expert.
 __device__ __forceinline__ float relative_exp(float l, float top) { return l == kNone ? 0.f : l == top ? 1.f : __expf(l - top); }
 
+// Keys as unsigned numbers of the same order: 0 for a masked expert (below every
+// number's), the same for both zeros.
+template <class Key>
+__device__ __forceinline__ Key ordered(std::conditional_t<sizeof(Key) == 8, double, float> v) {
+    constexpr Key kTop = (Key)1 << (8 * sizeof(Key) - 1);
+    if (!(v > kNone)) return 0;
+    const Key u = __builtin_bit_cast(Key, v + 0);
+    return u & kTop ? ~u : u | kTop;
+}
+__device__ __forceinline__ uint32_t upper(uint32_t k) { return k; }
+__device__ __forceinline__ uint32_t upper(uint64_t k) { return (uint32_t)(k >> 32); }
+__device__ __forceinline__ uint32_t readlane_u(uint32_t v, int lane) { return (uint32_t)readlane((int)v, lane); }
+__device__ __forceinline__ uint64_t readlane_u(uint64_t v, int lane) {
+    return (uint64_t)readlane_u((uint32_t)(v >> 32), lane) << 32 | readlane_u((uint32_t)v, lane);
+}
+// The lowest lane with the largest key, -1 if all are masked. The upper halves
+// decide nearly always.
+template <class Key>
+__device__ __forceinline__ int first_largest(Key key) {
+    const uint32_t most = wave_max(upper(key));
+    if (most == 0u) return -1;
+    uint64_t lanes = __ballot(upper(key) == most);
+    if constexpr (sizeof(Key) == 8) {
+        if (lanes & (lanes - 1)) {
+            const uint32_t low = upper(key) == most ? (uint32_t)key : 0u, most_low = wave_max(low);
+            lanes = __ballot(upper(key) == most && low == most_low);
+        }
+    }
+    return __ffsll((unsigned long long)lanes) - 1;
+}
+
 // One wave per token. A group's experts lie in `lanes` neighbouring lanes, PER
-// to a lane in ascending order, so that ties go to the lowest lane.
+// to a lane in ascending order, so that ties go to the lowest lane. WIDE: keys
+// are scores and biases in 64 bits, else the logits.
 template <int PER, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
-    using Key = std::conditional_t<WIDE, double, float>;
-    const Key none = kNone;
+    using Number = std::conditional_t<WIDE, double, float>;
+    using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
     const int lane = lane_id();
     const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
     if (t >= a.T) return;
@@ -41,14 +73,25 @@ __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
     const int held = group < a.groups ? min(max(size - at, 0), PER) : 0;
     const float* l = a.logits + t * a.E;
     float v[PER];
+    Number key[PER];
     bool bad = false;
     float top = kNone;
 #pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] = j < held ? l[first + j] : kNone;
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const float b = a.bias && j < held ? a.bias[first + j] : 0.f;
+            if (b != b) bad = true;
+            key[j] = b;
+        }
+    }
+#pragma unroll
     for (int j = 0; j < PER; ++j) {
-        v[j] = j < held ? l[first + j] : kNone;
         if (v[j] != v[j]) bad = true, v[j] = kNone;
         top = fmaxf(top, v[j]);
     }
+    if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_LOGIT);
     float total = 1.f;
     if (!a.sigmoid) {
         top = wave_max(top);
@@ -57,85 +100,79 @@ __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
         for (int j = 0; j < PER; ++j) total += relative_exp(v[j], top);
         total = wave_sum(total);
     }
-    Key key[PER];
     if constexpr (WIDE) {
-        double sum = 1.0;
         if (a.sigmoid) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) key[j] = 1.0 / (1.0 + exp(-(double)v[j]));
+            for (int j = 0; j < PER; ++j) key[j] += 1.0 / (1.0 + exp(-(double)v[j]));
         } else {
-            sum = 0.0;
+            double p[PER], sum = 0.0;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                key[j] = v[j] == top ? 1.0 : exp((double)v[j] - (double)top);
-                if (v[j] == kNone) key[j] = 0.0;
-                sum += key[j];
+                p[j] = v[j] == top ? 1.0 : exp((double)v[j] - (double)top);
+                if (v[j] == kNone) p[j] = 0.0;
+                sum += p[j];
             }
             sum = wave_sum(sum);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) key[j] = p[j] / sum + key[j];
         }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            if (!a.sigmoid) key[j] = key[j] / sum;
-            if (a.bias && j < held) {
-                const float b = a.bias[first + j];
-                if (b != b) bad = true;
-                key[j] += (double)b;
-            }
-            if (v[j] == kNone || !(key[j] > none)) key[j] = none;
-        }
+        for (int j = 0; j < PER; ++j)
+            if (v[j] == kNone || !(key[j] > kNone)) key[j] = kNone;
     } else {
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = v[j];
     }
-    if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_LOGIT);
 
     if (a.groups > 1) {
-        Key m1 = none, m2 = none;
+        Number m1 = kNone, m2 = kNone;  // this lane's two largest, then the group's
+        auto more = [&](Number k) {
+            const bool above = k > m1;
+            m2 = above ? m1 : k > m2 ? k : m2;
+            m1 = above ? k : m1;
+        };
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            m2 = larger(m2, key[j] < m1 ? key[j] : m1);
-            m1 = larger(m1, key[j]);
-        }
+        for (int j = 0; j < PER; ++j) more(key[j]);
         for (int d = 1; d < a.lanes; d <<= 1) {
-            const Key o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
-            m2 = larger(m1 < o1 ? m1 : o1, larger(m2, o2));
-            m1 = larger(m1, o1);
+            const Number o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+            more(o1);
+            more(o2);
         }
-        const Key mine = a.group_top == 2 && m2 > none ? m1 + m2 : m1;
+        const Key mine = ordered<Key>(a.group_top == 2 && m2 > kNone ? m1 + m2 : m1);
         int rank = 0;  // groups before this lane's
         for (int g = 0; g < a.groups; ++g) {
-            const Key other = readlane_f(mine, g * a.lanes);
+            const Key other = readlane_u(mine, g * a.lanes);
             rank += other > mine || (other == mine && g < group);
         }
         if (rank >= a.top_groups) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) key[j] = none;
+            for (int j = 0; j < PER; ++j) key[j] = kNone;
         }
     }
 
-    int mine = -1;  // lane k: the k-th chosen expert
+    Key left[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) left[j] = ordered<Key>(key[j]);
+    int mine = -1;  // lane k: the k-th chosen expert and its logit
+    float lv = 0.f;
     for (int k = 0; k < a.K; ++k) {
-        Key best = key[0];
-        int j_best = 0;
+        Key best = left[0];
+        int which = 0;
+        float logit = v[0];
 #pragma unroll
         for (int j = 1; j < PER; ++j)
-            if (key[j] > best) best = key[j], j_best = j;
-        const Key most = wave_max(best);
-        if (!(most > none)) break;
-        const int src = __ffsll((unsigned long long)__ballot(best == most)) - 1;
-        const int e = readlane(first + j_best, src);
-        if (lane == k) mine = e;
-        if (lane == src) {
+            if (left[j] > best) best = left[j], which = j, logit = v[j];
+        const int src = first_largest(best);
+        if (src < 0) break;
+        const int e = readlane(first + which, src);
+        const float chosen = readlane_f(logit, src);
+        if (lane == k) mine = e, lv = chosen;
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (j == j_best) key[j] = none;
-        }
+        for (int j = 0; j < PER; ++j)
+            if (lane == src && j == which) left[j] = 0;
     }
     float s = 0.f;
-    if (mine >= 0) {
-        const float lv = l[mine];
-        s = a.sigmoid ? 1.0f / (1.0f + __expf(-lv)) : relative_exp(lv, top) / total;
-    }
+    if (mine >= 0) s = a.sigmoid ? 1.0f / (1.0f + __expf(-lv)) : relative_exp(lv, top) / total;
     float w = a.scale * s;
     if (a.normalize) w = w / (wave_sum(s) + kTiny);
     if (lane < a.K) {
@@ -158,6 +195,7 @@ struct RouteGradArgs {
 __device__ __forceinline__ float unmasked(float l) { return l != l ? kNone : l; }
 
 // One wave per token: lane k holds lane k of the token's choice.
+template <int VEC>
 __global__ __launch_bounds__(kBlockThreads) void route_grad_kernel(RouteGradArgs a) {
     const int lane = lane_id();
     const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
@@ -200,20 +238,33 @@ __global__ __launch_bounds__(kBlockThreads) void route_grad_kernel(RouteGradArgs
         mean = mean / S * (kTiny / S);
     }
     if (a.sigmoid) ds *= s * not_s, mean = 0.f;
-    for (int e0 = 0; e0 < a.E; e0 += kWave) {
-        const int e = e0 + lane;
-        float d = 0.f;
+    // VEC experts to a lane at a time.
+    for (int e0 = 0; e0 < a.E; e0 += kWave * VEC) {
+        const int e = e0 + lane * VEC;
+        float d[VEC] = {};
         for (int k = 0; k < a.K; ++k) {
-            const int ek = readlane(id, k);
+            const int ek = readlane(id, k) - e;
             const float dk = readlane_f(ds, k);
-            if (e == ek) d += dk;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) d[j] += ek == j ? dk : 0.f;
         }
-        if (e < a.E) {
-            if (!a.sigmoid) d = relative_exp(unmasked(l[e]), top) / total * (d - mean);
-            if (a.wide)
-                static_cast<float*>(a.d_logits)[t * a.E + e] = d;
-            else
-                static_cast<uint16_t*>(a.d_logits)[t * a.E + e] = (uint16_t)f32_to_bf16(d);
+        if (e >= a.E) continue;
+        if (!a.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) d[j] = relative_exp(unmasked(l[e + j]), top) / total * (d[j] - mean);
+        }
+        if constexpr (VEC == 4) {
+            if (a.wide) {
+                st16(static_cast<float*>(a.d_logits) + t * a.E + e, u32x4{__float_as_uint(d[0]), __float_as_uint(d[1]),
+                                                                          __float_as_uint(d[2]), __float_as_uint(d[3])});
+            } else {
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.d_logits) + t * a.E + e) =
+                    u32x2{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
+            }
+        } else if (a.wide) {
+            static_cast<float*>(a.d_logits)[t * a.E + e] = d[0];
+        } else {
+            static_cast<uint16_t*>(a.d_logits)[t * a.E + e] = (uint16_t)f32_to_bf16(d[0]);
         }
     }
 }
@@ -247,7 +298,7 @@ hipError_t launch_route_grad(const ep_shape& s, const float* logits, const ep_ro
     if (s.T == 0) return hipSuccess;
     const RouteGradArgs a = {s.T, s.E, s.K, r.score == EP_SCORE_SIGMOID, r.normalize != 0, dtype == EP_GRAD_F32,
                              r.scale, logits, topk, d_w, d_logits, reinterpret_cast<uint32_t*>(ws)};
-    hipLaunchKernelGGL(route_grad_kernel, dim3((unsigned)((s.T + kWavesPerBlock - 1) / kWavesPerBlock)),
+    hipLaunchKernelGGL((s.E % 4 == 0 ? route_grad_kernel<4> : route_grad_kernel<1>), dim3((unsigned)((s.T + kWavesPerBlock - 1) / kWavesPerBlock)),
                        dim3(kBlockThreads), 0, st, a);
     return hipGetLastError();
 }
