@@ -131,13 +131,18 @@ __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
             m2 = above ? m1 : k > m2 ? k : m2;
             m1 = above ? k : m1;
         };
-#pragma unroll
-        for (int j = 0; j < PER; ++j) more(key[j]);
-        for (int d = 1; d < a.lanes; d <<= 1) {
-            const Number o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+        auto merge = [&](Number o1, Number o2) {
             more(o1);
             more(o2);
-        }
+        };
+#pragma unroll
+        for (int j = 0; j < PER; ++j) more(key[j]);
+        // Lanes whose halves of the group hold the same two change places by a mirror too.
+        if (a.lanes > 1) merge(dpp<kDppSwap1>(m1), dpp<kDppSwap1>(m2));
+        if (a.lanes > 2) merge(dpp<kDppSwap2>(m1), dpp<kDppSwap2>(m2));
+        if (a.lanes > 4) merge(dpp<kDppMirror8>(m1), dpp<kDppMirror8>(m2));
+        if (a.lanes > 8) merge(dpp<kDppMirror16>(m1), dpp<kDppMirror16>(m2));
+        if (a.lanes > 16) merge(__shfl_xor(m1, 16), __shfl_xor(m2, 16));
         const Key mine = ordered<Key>(a.group_top == 2 && m2 > kNone ? m1 + m2 : m1);
         int rank = 0;  // groups before this lane's
         for (int g = 0; g < a.groups; ++g) {
@@ -150,26 +155,56 @@ __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
         }
     }
 
-    Key left[PER];
+    struct Expert {
+        Key key;
+        int id;
+        float logit;
+    };
+    Expert left[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) left[j] = ordered<Key>(key[j]);
+    for (int j = 0; j < PER; ++j) left[j] = {ordered<Key>(key[j]), first + j, v[j]};
+    // Few to a lane: each lane's in order once, then the first of each is all that a
+    // round looks at. Else the lane's largest is looked for every time.
+    constexpr bool kSorted = PER <= 8;
+    if constexpr (kSorted) {
+#pragma unroll
+        for (int n = 1; n < PER; ++n)  // equal keys keep their order
+#pragma unroll
+            for (int j = n; j > 0; --j) {
+                const Expert x = left[j - 1], y = left[j];
+                const bool swap = y.key > x.key;
+                left[j - 1] = {swap ? y.key : x.key, swap ? y.id : x.id, swap ? y.logit : x.logit};
+                left[j] = {swap ? x.key : y.key, swap ? x.id : y.id, swap ? x.logit : y.logit};
+            }
+    }
     int mine = -1;  // lane k: the k-th chosen expert and its logit
     float lv = 0.f;
     for (int k = 0; k < a.K; ++k) {
-        Key best = left[0];
+        Expert best = left[0];
         int which = 0;
-        float logit = v[0];
+        if constexpr (!kSorted) {
 #pragma unroll
-        for (int j = 1; j < PER; ++j)
-            if (left[j] > best) best = left[j], which = j, logit = v[j];
-        const int src = first_largest(best);
+            for (int j = 1; j < PER; ++j)
+                if (left[j].key > best.key) best = left[j], which = j;
+        }
+        const int src = first_largest(best.key);
         if (src < 0) break;
-        const int e = readlane(first + which, src);
-        const float chosen = readlane_f(logit, src);
+        const int e = readlane(best.id, src);
+        const float chosen = readlane_f(best.logit, src);
         if (lane == k) mine = e, lv = chosen;
+        if (lane == src) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (lane == src && j == which) left[j] = 0;
+            for (int j = 0; j < PER; ++j) {
+                if constexpr (kSorted) {
+                    if (j + 1 < PER)
+                        left[j] = left[j + 1 < PER ? j + 1 : 0];
+                    else
+                        left[j].key = 0;
+                } else if (j == which) {
+                    left[j].key = 0;
+                }
+            }
+        }
     }
     float s = 0.f;
     if (mine >= 0) s = a.sigmoid ? 1.0f / (1.0f + __expf(-lv)) : relative_exp(lv, top) / total;
