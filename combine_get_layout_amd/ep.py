@@ -34,6 +34,7 @@ EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_W4_INT, EP_W4_E2M1 = 0, 1
 
 _P = ctypes.c_void_p
+_byref = ctypes.byref
 
 
 class ep_shape(ctypes.Structure):
@@ -228,10 +229,14 @@ def _stream_on(stream, device):
     kernel would fault on another device's memory. No stream or the NULL stream
     run on the current device; a stream given as a bare handle is the caller's to
     match."""
-    handle = _stream(stream)
-    if handle and isinstance(stream, int):
-        return handle
-    runs = torch._C._cuda_getDevice() if stream is None or not handle else stream.device_index
+    if stream is None:
+        runs = torch._C._cuda_getDevice()  # runs torch's own initialisation and its checks
+        handle = torch._C._cuda_getCurrentRawStream(runs)
+    else:
+        handle = _stream(stream)
+        if handle and isinstance(stream, int):
+            return handle
+        runs = stream.device_index if handle else torch._C._cuda_getDevice()
     if runs != device:
         raise ValueError(f"workspace: on device {device}, the call's stream on device {runs}")
     return handle
@@ -539,12 +544,13 @@ def ep_rms_norm(shape, x, residual, stream_type: int, gain, eps: float, out: dic
     dev = x.get_device() if isinstance(x, torch.Tensor) else None
     if dev is not None and dev < 0:
         raise ValueError("x: must be a GPU tensor")
-    wide = 4 if int(stream_type) == EP_STREAM_F32 else 2
-    need = dict(h=wide * T * H, y=2 * T * H, y_fp8=T * H, y_scales=4 * T * (H // 128), rstd=4 * T)
-    O = ep_norm_out(*[_ptr(out.get(n), n, need[n], dev) for n in need])
-    _check(lib().ep_rms_norm(ctypes.byref(shape), _ptr(x, "x", 2 * T * H, dev),
-                             _ptr(residual, "residual", wide * T * H, dev), int(stream_type),
-                             _ptr(gain, "gain", 2 * H, dev), float(eps), ctypes.byref(O),
+    n = T * H
+    wide = 4 * n if int(stream_type) == EP_STREAM_F32 else 2 * n
+    get = out.get
+    O = ep_norm_out(_ptr(get("h"), "h", wide, dev), _ptr(get("y"), "y", 2 * n, dev), _ptr(get("y_fp8"), "y_fp8", n, dev),
+                    _ptr(get("y_scales"), "y_scales", 4 * T * (H // 128), dev), _ptr(get("rstd"), "rstd", 4 * T, dev))
+    _check(lib().ep_rms_norm(_byref(shape), _ptr(x, "x", 2 * n, dev), _ptr(residual, "residual", wide, dev),
+                             int(stream_type), _ptr(gain, "gain", 2 * H, dev), eps, _byref(O),
                              _stream(stream) if dev is None else _stream_on(stream, dev)), "ep_rms_norm")
 
 
@@ -555,19 +561,20 @@ def ep_norm_workspace_bytes(shape: ep_shape) -> int:
 def ep_rms_norm_grad(shape, h, stream_type: int, gain, rstd, dy, d_stream, d_h, d_x, d_gain, ws, stream=None):
     dev = ws.get_device()
     T, H = shape.T, shape.H
-    n = (4 if int(stream_type) == EP_STREAM_F32 else 2) * T * H
-    _check(lib().ep_rms_norm_grad(ctypes.byref(shape), _ptr(h, "h", n, dev), int(stream_type),
+    n = T * H
+    wide = 4 * n if int(stream_type) == EP_STREAM_F32 else 2 * n
+    _check(lib().ep_rms_norm_grad(_byref(shape), _ptr(h, "h", wide, dev), int(stream_type),
                                   _ptr(gain, "gain", 2 * H, dev), _ptr(rstd, "rstd", 4 * T, dev),
-                                  _ptr(dy, "dy", 2 * T * H, dev), _ptr(d_stream, "d_stream", n, dev),
-                                  _ptr(d_h, "d_h", n, dev), _ptr(d_x, "d_x", 2 * T * H, dev),
+                                  _ptr(dy, "dy", 2 * n, dev), _ptr(d_stream, "d_stream", wide, dev),
+                                  _ptr(d_h, "d_h", wide, dev), _ptr(d_x, "d_x", 2 * n, dev),
                                   _ptr(d_gain, "d_gain", 4 * H, dev), *_ws(ws), _stream_on(stream, dev)),
            "ep_rms_norm_grad")
 
 
 def _router_struct(shape: ep_shape, router: dict, device) -> ep_router:
-    return ep_router(int(router["score"]), int(router.get("top_groups", shape.G)), int(router.get("group_top", 1)),
-                     int(router.get("normalize", 1)), float(router.get("scale", 1.0)),
-                     _ptr(router.get("bias"), "bias", 4 * shape.E, device))
+    get = router.get
+    return ep_router(router["score"], get("top_groups", shape.G), get("group_top", 1), get("normalize", 1),
+                     get("scale", 1.0), _ptr(get("bias"), "bias", 4 * shape.E, device))
 
 
 def ep_route(shape, logits, router: dict, topk_idx, topk_weights, ws, stream=None):
@@ -575,24 +582,22 @@ def ep_route(shape, logits, router: dict, topk_idx, topk_weights, ws, stream=Non
     "normalize" (True), "scale" (1.0), "bias" (None)."""
     dev = ws.get_device()
     R = _router_struct(shape, router, dev)
-    T, K = shape.T, shape.K
-    _check(lib().ep_route(ctypes.byref(shape), _ptr(logits, "logits", 4 * T * shape.E, dev), ctypes.byref(R),
-                          _ptr(topk_idx, "topk_idx", 8 * T * K, dev),
-                          _ptr(topk_weights, "topk_weights", 4 * T * K, dev), *_ws(ws), _stream_on(stream, dev)),
-           "ep_route")
+    T, lanes = shape.T, shape.T * shape.K
+    _check(lib().ep_route(_byref(shape), _ptr(logits, "logits", 4 * T * shape.E, dev), _byref(R),
+                          _ptr(topk_idx, "topk_idx", 8 * lanes, dev), _ptr(topk_weights, "topk_weights", 4 * lanes, dev),
+                          *_ws(ws), _stream_on(stream, dev)), "ep_route")
 
 
 def ep_route_grad(shape, logits, router: dict, topk_idx, d_topk_weights, d_logits, dtype: int, ws, stream=None):
     """router: as for ep_route."""
     dev = ws.get_device()
     R = _router_struct(shape, router, dev)
-    T, E, K = shape.T, shape.E, shape.K
-    size = 4 if int(dtype) == EP_GRAD_F32 else 2
-    _check(lib().ep_route_grad(ctypes.byref(shape), _ptr(logits, "logits", 4 * T * E, dev), ctypes.byref(R),
-                               _ptr(topk_idx, "topk_idx", 8 * T * K, dev),
-                               _ptr(d_topk_weights, "d_topk_weights", 4 * T * K, dev),
-                               _ptr(d_logits, "d_logits", size * T * E, dev), int(dtype), *_ws(ws),
-                               _stream_on(stream, dev)), "ep_route_grad")
+    n, lanes = shape.T * shape.E, shape.T * shape.K
+    _check(lib().ep_route_grad(_byref(shape), _ptr(logits, "logits", 4 * n, dev), _byref(R),
+                               _ptr(topk_idx, "topk_idx", 8 * lanes, dev),
+                               _ptr(d_topk_weights, "d_topk_weights", 4 * lanes, dev),
+                               _ptr(d_logits, "d_logits", (4 if int(dtype) == EP_GRAD_F32 else 2) * n, dev), int(dtype),
+                               *_ws(ws), _stream_on(stream, dev)), "ep_route_grad")
 
 
 def ep_few_w4_workspace_bytes(shape: ep_shape, F: int) -> int:
@@ -602,14 +607,17 @@ def ep_few_w4_workspace_bytes(shape: ep_shape, F: int) -> int:
 def ep_moe_few_w4(shape, tokens: dict, experts: dict, out, ws, stream=None):
     """experts: {"F", "form" (EP_W4_*), "w13", "w13_scales", "w2", "w2_scales"}."""
     dev = ws.get_device()
-    tk = _tokens_struct(shape, tokens, dev)
-    E, H, F, form = shape.E, shape.H, int(experts["F"]), int(experts["form"])
-    per = 2 / 128 if form == EP_W4_INT else 1 / 32  # bytes of scales a column
-    need = dict(w13=E * F * H, w13_scales=int(2 * E * F * H * per), w2=E * H * F // 2, w2_scales=int(E * H * F * per))
-    X = ep_experts_w4(F, form, *[_ptr(experts.get(n), n, need[n], dev) for n in need])
-    _check(lib().ep_moe_few_w4(ctypes.byref(shape), ctypes.byref(tk), ctypes.byref(X),
-                               _ptr(out, "out", 2 * shape.T * H, dev), *_ws(ws), _stream_on(stream, dev)),
-           "ep_moe_few_w4")
+    T, H, lanes, F, form = shape.T, shape.H, shape.T * shape.K, int(experts["F"]), int(experts["form"])
+    get = tokens.get
+    tk = ep_tokens(_ptr(get("x"), "x", 2 * T * H, dev), None, None, _ptr(get("topk_idx"), "topk_idx", 8 * lanes, dev),
+                   _ptr(get("topk_weights"), "topk_weights", 4 * lanes, dev))
+    n = shape.E * F * H
+    scales = n // 64 if form == EP_W4_INT else n // 32  # bytes: two for 128 values, one for 32
+    get = experts.get
+    X = ep_experts_w4(F, form, _ptr(get("w13"), "w13", n, dev), _ptr(get("w13_scales"), "w13_scales", 2 * scales, dev),
+                      _ptr(get("w2"), "w2", n // 2, dev), _ptr(get("w2_scales"), "w2_scales", scales, dev))
+    _check(lib().ep_moe_few_w4(_byref(shape), _byref(tk), _byref(X), _ptr(out, "out", 2 * T * H, dev), *_ws(ws),
+                               _stream_on(stream, dev)), "ep_moe_few_w4")
 
 
 def ep_clear_errors(ws, stream=None):
