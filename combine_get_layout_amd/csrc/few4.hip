@@ -107,6 +107,18 @@ __device__ __forceinline__ void wave_lds_order() {
 // in different banks.
 __device__ __forceinline__ uint32_t row_chunk(int row, int chunk) { return row * 512 + ((chunk ^ (row & 15)) << 4); }
 
+// silu(gate) * up as two bf16 values for the second product's matrix instruction, the
+// rounded one (of a finite value bf16's largest at most) and, F values on, what it
+// leaves (nothing of an infinity or NaN).
+__device__ __forceinline__ void store_act(uint16_t* act, int F, float gate, float up) {
+    const float r = gate / (1.0f + __expf(-gate)) * up;
+    uint32_t hi = f32_to_bf16(r);
+    if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
+    const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
+    act[0] = (uint16_t)hi;
+    act[F] = (uint16_t)f32_to_bf16(rest);
+}
+
 // First launch: workgroup (x, y) computes RT / 2 * 16 values of f for the tokens
 // of the y-th used expert, up to TT of them at a time (NT tiles of 16 where NT > 1).
 // Dynamic LDS: the scales (2 * 16 * GT rows, if LDS), then the waves' copies of a
@@ -293,16 +305,7 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                         gate += part[v][c >> 4][tk][c & 15];
                         up += part[v][2 + (c >> 4)][tk][c & 15];
                     }
-                    const float r = gate / (1.0f + __expf(-gate)) * up;
-                    // Two bf16 values for the second product's matrix instruction, the
-                    // rounded one (of a finite value bf16's largest at most) and what it
-                    // leaves (nothing of an infinity or NaN).
-                    uint32_t hi = f32_to_bf16(r);
-                    if (__builtin_isfinite(r) && (hi & 0x7FFFu) == 0x7F80u) --hi;
-                    const float rest = __builtin_isfinite(r) ? r - __uint_as_float(hi << 16) : 0.f;
-                    uint16_t* act = a.act + (int64_t)sh.find.row[at] * 2 * a.F + f;
-                    act[0] = (uint16_t)hi;
-                    act[a.F] = (uint16_t)f32_to_bf16(rest);
+                    store_act(a.act + (int64_t)sh.find.row[at] * 2 * a.F + f, a.F, gate, up);
                 }
                 __syncthreads();
             }
@@ -326,6 +329,155 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
     up4_tokens<FORM, RT, NT, TT, LDS>(a, found, sh, scales, area);
+}
+
+// The same for experts with many tokens: 64 values of f to a workgroup, 16 of them (a
+// gate and an up tile) to a wave, which goes over the whole contracted axis for all of
+// the expert's tokens; steps of 128 columns, whose tokens' rows lie in LDS for all four
+// waves, in two buffers. One barrier a step; the next step's rows and the weights of
+// three are in flight.
+constexpr int kManyCols = 64, kManySpan = 128, kManyAhead = 2;
+
+// Rows of 256 bytes in LDS; chunks exchanged as in row_chunk.
+__device__ __forceinline__ uint32_t half_chunk(int row, int chunk) { return row * 256 + ((chunk ^ (row & 15)) << 4); }
+
+template <int FORM, int NT>
+__device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& found, const FindShared& find,
+                                                const uint8_t* scales, uint8_t* rows, int t0) {
+    using Scale = ScaleRow<FORM>;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
+    const int i = lane & 15, q = lane >> 4;
+    const int f0 = blockIdx.x * kManyCols + wave * 16, cols = max(min(16, a.F - f0), 0);
+    const uint32_t ld = (uint32_t)a.H / 2, lds = Scale::bytes(a.H);
+    const uint8_t* w = a.w13 + ((int64_t)found.expert * 2 * a.F + f0) * ld;
+    const auto d_gate = buf_resource(w, cols * ld), d_up = buf_resource(w + (int64_t)a.F * ld, cols * ld);
+    const auto d_x = buf_resource(a.x, (uint32_t)a.T * a.H * 2);
+    const int steps = (a.H + kManySpan - 1) / kManySpan;
+    uint32_t xr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int at = t0 + n * 16 + (tid >> 4);
+        xr[n] = at < found.tokens ? (uint32_t)find.token[at] * a.H * 2 + (tid & 15) * 16 : kBufNone;
+    }
+    bf16x8 minus_eight;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
+    f32x4 acc[2][NT] = {};
+    u32x4 xv[NT], wv[kManyAhead][2];
+    auto load_x = [&](int s) {
+        const uint32_t far = s * kManySpan + (tid & 15) * 8 >= a.H ? kBufFar : 0u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xv[n] = buf_load16(d_x, xr[n] + far, s * 256);
+    };
+    auto load_w = [&](int s, u32x4 (&v)[2]) {
+        const uint32_t off = i * ld + q * 16 + (s * kManySpan + q * 32 >= a.H ? kBufFar : 0u);
+        v[0] = buf_load16(d_gate, off, s * 64);
+        v[1] = buf_load16(d_up, off, s * 64);
+    };
+    auto step = [&](int s, uint8_t* buf, u32x4 (&v)[2]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) st16(buf + half_chunk(n * 16 + (tid >> 4), tid & 15), xv[n]);
+        barrier_only();
+        const bool in = s * kManySpan + q * 32 < a.H;  // else codes of 0, and no scale
+        float scale[2];
+        bf16x8 wf[2][4];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const uint32_t at = (g * kManyCols + wave * 16 + i) * lds + s * (Scale::kStep / 2) + Scale::offset(0, q);
+            scale[g] = Scale::value(in ? Scale::from_lds(scales + at) : 0u);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) wf[g][m] = codes_to_bf16<FORM>(v[g][m], scale[g]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(s + 1);
+        load_w(s + kManyAhead, v);
+        __builtin_amdgcn_sched_barrier(0);
+        // One tile's fragments are read while the tile before is multiplied, and no more
+        // (all of them at once would not fit the registers).
+        bf16x8 tile[2][4];
+        auto read = [&](int n) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tile[n & 1][m] = as_bf16(ld16(buf + half_chunk(n * 16 + i, q * 4 + m)));
+        };
+        read(0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n + 1 < NT) read(n + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            const bf16x8(&xf)[4] = tile[n & 1];
+            f32x4 base = {};
+            if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) base = mfma_bf16(xf[m], minus_eight, base);
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                f32x4 c = FORM == EP_W4_INT ? base : acc[g][n];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], wf[g][m], c);
+                if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[g][n][j] = fmaf(scale[g], c[j], acc[g][n][j]);
+                } else {
+                    acc[g][n] = c;
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load_x(0);
+#pragma unroll
+    for (int k = 0; k < kManyAhead; ++k) load_w(k, wv[k]);
+    for (int s = 0; s < steps; s += kManyAhead) {
+#pragma unroll
+        for (int k = 0; k < kManyAhead; ++k) step(s + k, rows + (k & 1) * NT * 4096, wv[k]);  // past the end: nothing
+    }
+    settle(acc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = t0 + n * 16 + q * 4 + j;
+            if (at < found.tokens && i < cols)
+                store_act(a.act + (int64_t)find.row[at] * 2 * a.F + f0 + i, a.F, acc[0][n][j], acc[1][n][j]);
+        }
+    __syncthreads();  // the buffers, before the next tokens
+}
+
+template <int FORM, int NT>
+__global__ __launch_bounds__(kThreads, 2) void few4_up_many_kernel(Few4Args a) {
+    __shared__ Up4Shared sh;
+    extern __shared__ u32x4 lds_vectors[];
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);
+    const uint32_t lds = ScaleRow<FORM>::bytes(a.H);
+    uint8_t* const rows = scales + 2 * kManyCols * lds;
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        if (tid == 0) a.err[0] = 0u;
+        if (a.splits > 1)
+            for (int n = tid; n * 16 < a.H; n += kThreads) a.joined[n] = 0;
+    }
+    const Found found = find_expert<kThreads>(a, sh.find);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
+    if (found.expert < 0) return;
+    const int f0 = blockIdx.x * kManyCols, vectors = min(kManyCols, a.F - f0) * lds / 16;
+    const char* from = a.s13 + ((int64_t)found.expert * 2 * a.F + f0) * lds;
+    for (int v = tid; v < vectors; v += kThreads) {
+        st16(scales + v * 16, ld16(from + v * 16));
+        st16(scales + kManyCols * lds + v * 16, ld16(from + (int64_t)a.F * lds + v * 16));
+    }
+    __syncthreads();
+    for (int t0 = 0; t0 < found.tokens;) {
+        const int left = found.tokens - t0;
+        if (NT >= 8 && left > 64)
+            up4_many_tokens<FORM, NT >= 8 ? 8 : 1>(a, found, sh.find, scales, rows, t0), t0 += 128;
+        else if (NT >= 4 && left > 32)
+            up4_many_tokens<FORM, NT >= 4 ? 4 : 1>(a, found, sh.find, scales, rows, t0), t0 += 64;
+        else if (NT >= 2 && left > 16)
+            up4_many_tokens<FORM, NT >= 2 ? 2 : 1>(a, found, sh.find, scales, rows, t0), t0 += 32;
+        else
+            up4_many_tokens<FORM, 1>(a, found, sh.find, scales, rows, t0), t0 += 16;
+    }
 }
 
 // What a wave loads for one unit; the scales as its own run of an expert's, where
@@ -450,8 +602,8 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     };
 
     float acc[RT][4] = {};
-    // One unit, whose loads are there.
-    auto unit = [&](DownStage<RT, CAP, LDS>& g, int tokens, Route route, bool last) {
+    // kTokens tokens of one unit, whose loads are there.
+    auto unit = [&](DownStage<RT, CAP, LDS>& g, int span, int t0, int tokens, const Route& route, bool flush) {
         uint32_t bits[RT][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -465,113 +617,115 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                     bits[r][p] = g.scale[r][p];
             }
         }
-        for (int t0 = 0; t0 < tokens; t0 += kTokens) {
-            // The conversion stays in the loop: its results take four times the registers.
+        bf16x8 v[8];
+        if constexpr (CAP > 0) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int n = 0; n < CAP; ++n) st16(rows + row_chunk(2 * n + (lane >> 5), lane & 31), g.act[n]);
+            wave_lds_order();
 #pragma unroll
-                for (int p = 0; p < 2; ++p) asm volatile("" : "+v"(g.w[r][p]));
-            bf16x8 v[8];
-            if constexpr (CAP > 0) {
+            for (int m = 0; m < 8; ++m)  // rows past CAP: earlier ones again, of which nothing is kept
+                v[m] = as_bf16(ld16(rows + row_chunk((i & (CAP - 1)) * 2 + (i >> 3), (m >> 2) * 16 + q * 4 + (m & 3))));
+            wave_lds_order();
+        } else {
 #pragma unroll
-                for (int n = 0; n < CAP; ++n) st16(rows + row_chunk(2 * n + (lane >> 5), lane & 31), g.act[n]);
-                wave_lds_order();
+            for (int m = 0; m < 8; ++m) v[m] = as_bf16(g.act[m]);
+        }
+        f32x4 c[RT][2] = {};
+        if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m)  // rows past CAP: earlier ones again, of which nothing is kept
-                    v[m] = as_bf16(ld16(rows + row_chunk((i & (CAP - 1)) * 2 + (i >> 3), (m >> 2) * 16 + q * 4 + (m & 3))));
-                wave_lds_order();
-            } else {
+            for (int p = 0; p < 2; ++p) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m) v[m] = as_bf16(g.act[m]);
+                for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(v[p * 4 + m], minus_eight, c[0][p]);
+#pragma unroll
+                for (int r = 1; r < RT; ++r) c[r][p] = c[0][p];
             }
-            f32x4 c[RT][2] = {};
-            if constexpr (FORM == EP_W4_INT) {
+        }
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(v[p * 4 + m], minus_eight, c[0][p]);
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int r = 1; r < RT; ++r) c[r][p] = c[0][p];
-                }
-            }
+                for (int m = 0; m < 4; ++m)
+                    c[r][p] = mfma_bf16(v[p * 4 + m],
+                                        codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(bits[r][p])), c[r][p]);
+        settle(c);
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+            for (int j = 0; j < 4; ++j)
+                acc[r][j] += FORM == EP_W4_INT ? fmaf(Scale::value(bits[r][1]), c[r][1][j],
+                                                      Scale::value(bits[r][0]) * c[r][0][j])
+                                               : c[r][0][j] + c[r][1][j];
+        if (!flush) return;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        c[r][p] = mfma_bf16(v[p * 4 + m],
-                                            codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(bits[r][p])), c[r][p]);
-            settle(c);
-            const Route now = route;
-            if (t0 + kTokens < tokens) {  // the weights stay, the tokens change
-                if (((t0 + kTokens) & 15) == 0) route = load_route(rank, tokens, t0 + kTokens);
-                load_act(route, t0 + kTokens, tokens, span, g.act);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const int n = (t0 & 15) + (((q & 1) * 4 + j) & (kTokens - 1));
+            const int id = __shfl(route.id, n);
+            const float weight = __shfl(route.w, n);
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[r][j] += FORM == EP_W4_INT ? fmaf(Scale::value(bits[r][1]), c[r][1][j],
-                                                          Scale::value(bits[r][0]) * c[r][0][j])
-                                                   : c[r][0][j] + c[r][1][j];
-            if (tokens <= kTokens && !last) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = (t0 & 15) + (((q & 1) * 4 + j) & (kTokens - 1));
-                const int id = __shfl(now.id, n);
-                const float weight = __shfl(now.w, n);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    // Rows 8 to 15: the rests' products. Where the value's is not finite the
-                    // rest's is no part of the sum.
-                    const float rest = __shfl_xor(acc[r][j], 32);
-                    const float dot = __builtin_isfinite(acc[r][j]) ? acc[r][j] + rest : acc[r][j];
-                    acc[r][j] = 0.f;
-                    if (q < 2 && q * 4 + j < kTokens && t0 + q * 4 + j < tokens) {
-                        float* sum = mine + (id >> 16) * kLd + r * 16 + i;
-                        *sum = fmaf(weight, dot, *sum);
-                    }
+            for (int r = 0; r < RT; ++r) {
+                // Rows 8 to 15: the rests' products. Where the value's is not finite the
+                // rest's is no part of the sum.
+                const float rest = __shfl_xor(acc[r][j], 32);
+                const float dot = __builtin_isfinite(acc[r][j]) ? acc[r][j] + rest : acc[r][j];
+                acc[r][j] = 0.f;
+                if (q < 2 && q * 4 + j < kTokens && t0 + q * 4 + j < tokens) {
+                    float* sum = mine + (id >> 16) * kLd + r * 16 + i;
+                    *sum = fmaf(weight, dot, *sum);
                 }
             }
         }
     };
+    // The order of the work: the units of the run, the tokens of each in tiles of kTokens;
+    // routes are kept for 16 tokens at a time.
+    struct Tile {
+        int rank, span, t0, entry;
+    };
+    auto behind = [&](const Tile& x, int step) {
+        if (x.t0 + step < x.entry >> 16) return Tile{x.rank, x.span, x.t0 + step, x.entry};
+        if (x.span + 1 < spans) return Tile{x.rank, x.span + 1, 0, x.entry};
+        const int rank = min(x.rank + 1, used - 1);
+        return Tile{rank, 0, 0, entry_of(rank)};
+    };
     DownStage<RT, CAP, LDS> g0, g1;
-    int entry = 0;
-    Route route = {0, 0.f}, ahead = {0, 0.f};  // the first 16 tokens of this expert and of the next
+    Tile now = {rank, span, 0, 0};
+    Route route = {0, 0.f}, ahead = {0, 0.f};  // of this tile's 16 tokens, and of the 16 behind them
     if (u < end) {
-        entry = entry_of(rank);
-        route = load_route(rank, entry >> 16, 0);
-        const int after = min(rank + 1, used - 1);
-        ahead = load_route(after, entry_of(after) >> 16, 0);
-        load_weights(entry & 0xFFFF, span, g0);
+        now.entry = entry_of(rank);
+        route = load_route(rank, now.entry >> 16, 0);
+        const Tile after = behind(now, 16);
+        ahead = load_route(after.rank, after.entry >> 16, after.t0);
+        load_weights(now.entry & 0xFFFF, span, g0);
         if constexpr (LDS) {
-            load_scales(entry & 0xFFFF, 0u);
+            load_scales(now.entry & 0xFFFF, 0u);
             keep_scales();
         }
-        load_act(route, 0, entry >> 16, span, g0.act);
+        load_act(route, 0, now.entry >> 16, span, g0.act);
     }
-    // The next unit's loads, and the routes of the expert behind its own, are in flight
-    // while this one is multiplied. All of them are made on every turn, behind the last
-    // unit past the row's end: a branch around them would make the compiler wait for
+    // The next tile's loads, and the routes of the 16 tokens behind its own, are in flight
+    // while this one is multiplied; a unit's weights are asked for again with its next
+    // tokens, and then lie near. All loads are made on every turn, behind the last one
+    // past the row's end: a branch around them would make the compiler wait for
     // everything.
     auto turn = [&](DownStage<RT, CAP, LDS>& g, DownStage<RT, CAP, LDS>& gn) {
-        const bool more = u + 1 < end, same = !more || span + 1 < spans;
-        const int next_rank = same ? rank : rank + 1, next_span = !more ? spans : same ? span + 1 : 0;
-        const int next_entry = entry_of(next_rank), after = min(next_rank + 1, used - 1);
-        const int after_tokens = entry_of(after) >> 16;
-        Route next = route;
-        if (!same) next = ahead;
-        load_weights(next_entry & 0xFFFF, next_span, gn);
-        if constexpr (LDS) load_scales(next_entry & 0xFFFF, same ? kBufFar : 0u);
-        load_act(next, 0, next_entry >> 16, next_span, gn.act);
-        ahead = load_route(after, after_tokens, 0);
+        const int tokens = now.entry >> 16;
+        Tile next = behind(now, kTokens);
+        const bool new_unit = next.t0 == 0, new_expert = new_unit && now.span + 1 == spans;
+        const bool more = !new_unit || u + 1 < end;
+        if (!more) next = {now.rank, spans, 0, now.entry};
+        Route following = route;
+        if (new_unit ? now.t0 >= 16 || new_expert : (next.t0 & 15) == 0) following = ahead;
+        load_weights(next.entry & 0xFFFF, next.span, gn);
+        if constexpr (LDS) load_scales(next.entry & 0xFFFF, more && new_expert ? 0u : kBufFar);
+        load_act(following, next.t0, next.entry >> 16, next.span, gn.act);
+        const Tile after = behind({next.rank, next.span, next.t0 & ~15, next.entry}, 16);
+        ahead = load_route(after.rank, after.entry >> 16, after.t0);
         __builtin_amdgcn_sched_barrier(0);
-        unit(g, entry >> 16, route, !more || !same);
+        unit(g, now.span, now.t0, tokens, route, tokens > kTokens || !more || new_expert);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (LDS)
-            if (!same) keep_scales();
-        ++u, rank = next_rank, span = next_span, entry = next_entry, route = next;
+            if (more && new_expert) keep_scales();
+        u += new_unit, now = next, route = following;
     };
     while (u < end) {
         turn(g0, g1);
@@ -652,17 +806,21 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K), lanes = (int64_t)s.T * s.K;
     const uint32_t row = ScaleRow<FORM>::bytes(a.H);
     const bool lds_scales = row <= kLdsScales;
-    const bool many = lds_scales && s.T > 16 && lanes > 16 * experts;
+    const bool many = lds_scales && (lanes > 8 * experts || (lanes > 4 * experts && (a.F + 63) / 64 * experts >= 512));
     const bool narrow = !lds_scales || (int64_t)((a.F + 31) / 32) * experts < 1024;
-    const int cols = !many && narrow ? 16 : 32;
+    const int cols = many ? kManyCols : narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
     // Tokens at a time: those of most experts, as the weights are read again for more.
     const int tt = s.T <= 2 ? 2 : s.T <= 4 ? 4 : s.T <= 8 || lanes <= 4 * experts ? 8 : 16;
+    const int tiles1 = s.T <= 32 || lanes <= 20 * experts ? 2 : s.T <= 64 || lanes <= 48 * experts ? 4 : 8;
     const Kernel first = !lds_scales ? few4_up_kernel<FORM, 2, 1, 16, false>
-                         : many      ? few4_up_kernel<FORM, 4, 2, 16, true>
+                         : many      ? (tiles1 == 8   ? few4_up_many_kernel<FORM, 8>
+                                        : tiles1 == 4 ? few4_up_many_kernel<FORM, 4>
+                                                      : few4_up_many_kernel<FORM, 2>)
                          : narrow    ? up_kernel<FORM, 2>(tt)
                                      : up_kernel<FORM, 4>(tt);
-    const size_t area = std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (many ? 32 : lds_scales ? tt : 16));
+    const size_t area = many ? 8192 * tiles1
+                             : std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (lds_scales ? tt : 16));
     hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);
     const int tiles = down_tiles(s, a.F);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
