@@ -588,6 +588,10 @@ int ep_rms_norm_grad(const ep_shape* shape, const void* h, int stream_type, cons
     if (!aligned(h, 16) || !aligned(gain, 16) || !aligned(rstd, 4) || !aligned(dy, 16) || !aligned(d_stream, 16) ||
         !aligned(d_h, 16) || !aligned(d_x, 16) || !aligned(d_gain, 16))
         return EP_ERR_ARG;
+    // The gain's workgroups may read h and dy after the rows' have stored d_h and d_x.
+    if (shape->T > 0)
+        for (const void* out : {static_cast<const void*>(d_h), static_cast<const void*>(d_x)})
+            if (out && (out == h || out == dy || out == gain)) return EP_ERR_ARG;
     return hip_status(launch_rms_norm_grad(*shape, h, stream_type, gain, rstd, dy, d_stream, d_h, d_x, d_gain,
                                            static_cast<char*>(ws), static_cast<hipStream_t>(stream)));
 }

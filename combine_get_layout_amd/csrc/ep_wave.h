@@ -9,6 +9,10 @@
 
 namespace ep {
 
+// Workgroups of a launch with one row or token to a wave or workgroup; longer batches
+// take more launches (a grid has fewer than 2^32 threads).
+constexpr int64_t kLaunchGroups = 1 << 21;
+
 // v of the lane that CTRL names in this row of 16 lanes.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {

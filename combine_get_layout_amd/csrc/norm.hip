@@ -10,6 +10,7 @@ namespace {
 
 struct NormArgs {
     int T, H;
+    int64_t row0;  // first row of this launch
     float eps;
     const uint16_t* x;
     const char* res;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void norm_kernel(NormArg
     constexpr int kThreads = LANES < 256 ? 256 : LANES;
     __shared__ float scratch[kThreads / kWave];
     const int tid = threadIdx.x % LANES;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    const int64_t row = a.row0 + (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
     if (LANES <= kWave && row >= a.T) return;  // a workgroup with barriers has one row, which exists
     const int64_t base = row * a.H;
     // h of vector c: from memory, stored where it is asked for.
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads, 4) voi
         Eight<WIDE> h[NV], s[NV];
         float r;
     };
-    const int runs = (a.T + kRows - 1) / kRows;
+    const int runs = (int)(((int64_t)a.T + kRows - 1) / kRows);
     // Rows past the last: the last again, and nothing is made of them.
     auto load = [&](int run, Row& g) {
         const int64_t row = min((int64_t)run * kRows + sub, (int64_t)a.T - 1), base = row * a.H;
@@ -441,7 +442,7 @@ int grad_lanes(int H, bool wide) {
 int grad_groups(int T, int H, bool wide) {
     if (H > kLongH) return std::min(T, 64);
     const int rows = std::max(1, kGradThreads / grad_lanes(H, wide));
-    return std::min((T + rows - 1) / rows, kGradGroups);
+    return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, kGradGroups);
 }
 // Whether d_gain is made beside the rows in the same launch, by workgroups that
 // read dy and h once more, column by column, or from the rows' workgroups' parts in a
@@ -455,11 +456,14 @@ int grad_groups(int T, int H, bool wide) {
 bool gain_beside(int T, int H) { return H <= kLongH && T <= 1024 && (int64_t)T * H <= 1 << 23; }
 
 template <bool WIDE>
-void launch_norm(const NormArgs& a, hipStream_t st) {
+void launch_norm(NormArgs a, hipStream_t st) {
     const int vecs = (a.H + 7) / 8;
     auto go = [&](auto kernel, int lanes) {
         const int threads = std::max(lanes, 256), rows = threads / lanes;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(threads), 0, st, a);
+        for (a.row0 = 0; a.row0 < a.T; a.row0 += kLaunchGroups * rows) {
+            const int64_t groups = std::min((a.T - a.row0 + rows - 1) / rows, kLaunchGroups);
+            hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(threads), 0, st, a);
+        }
     };
     if (vecs <= 64) return go(norm_kernel<64, 1, WIDE>, 64);
     if (vecs <= 128) return go(norm_kernel<64, 2, WIDE>, 64);
@@ -512,7 +516,7 @@ size_t ws_norm(const ep_shape& s) {
 hipError_t launch_rms_norm(const ep_shape& s, const uint16_t* x, const void* res, int stream_type,
                            const uint16_t* gain, float eps, const ep_norm_out& o, hipStream_t st) {
     if (s.T == 0) return hipSuccess;
-    const NormArgs a = {s.T, s.H, eps, x, static_cast<const char*>(res), gain, static_cast<char*>(o.h), o.y, o.y_fp8,
+    const NormArgs a = {s.T, s.H, 0, eps, x, static_cast<const char*>(res), gain, static_cast<char*>(o.h), o.y, o.y_fp8,
                         o.y_scales, o.rstd};
     if (stream_type == EP_STREAM_F32)
         launch_norm<true>(a, st);

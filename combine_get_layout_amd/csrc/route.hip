@@ -13,6 +13,7 @@ constexpr float kTiny = 1e-20f;  // beside the sum of the chosen scores
 
 struct RouteArgs {
     int T, E, K;
+    int64_t token0;  // first token of this launch
     int groups, lanes, top_groups, group_top;  // groups that limit the choice (1: none), lanes that share one
     bool sigmoid, normalize;
     float scale;
@@ -66,7 +67,7 @@ __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
     using Number = std::conditional_t<WIDE, double, float>;
     using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
     const int lane = lane_id();
-    const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
+    const int64_t t = a.token0 + (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
     if (t >= a.T) return;
     const int size = a.E / a.groups, group = lane / a.lanes, at = lane % a.lanes * PER;
     const int first = group * size + at;  // this lane's first expert
@@ -218,6 +219,7 @@ __global__ __launch_bounds__(kBlockThreads) void route_kernel(RouteArgs a) {
 
 struct RouteGradArgs {
     int T, E, K;
+    int64_t token0;
     bool sigmoid, normalize, wide;
     float scale;
     const float* logits;
@@ -233,7 +235,7 @@ __device__ __forceinline__ float unmasked(float l) { return l != l ? kNone : l; 
 template <int VEC>
 __global__ __launch_bounds__(kBlockThreads) void route_grad_kernel(RouteGradArgs a) {
     const int lane = lane_id();
-    const int64_t t = (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
+    const int64_t t = a.token0 + (int64_t)blockIdx.x * kWavesPerBlock + wave_in_block();
     if (t >= a.T) return;
     const float* l = a.logits + t * a.E;
     float top = kNone, total = 1.f;
@@ -304,6 +306,16 @@ __global__ __launch_bounds__(kBlockThreads) void route_grad_kernel(RouteGradArgs
     }
 }
 
+// One wave to a token, in launches of kLaunchGroups workgroups.
+template <class Args>
+hipError_t launch_tokens(void (*kernel)(Args), Args& a, hipStream_t st) {
+    for (a.token0 = 0; a.token0 < a.T; a.token0 += kLaunchGroups * kWavesPerBlock) {
+        const int64_t groups = std::min((a.T - a.token0 + kWavesPerBlock - 1) / kWavesPerBlock, kLaunchGroups);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kBlockThreads), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_route(const ep_shape& s, const float* logits, const ep_router& r, int64_t* topk, float* w, char* ws,
@@ -312,7 +324,7 @@ hipError_t launch_route(const ep_shape& s, const float* logits, const ep_router&
     const int groups = r.top_groups < s.G ? s.G : 1;
     int lanes = kWave;
     while (lanes * groups > kWave) lanes >>= 1;
-    const RouteArgs a = {s.T, s.E, s.K, groups, lanes, r.top_groups, r.group_top, r.score == EP_SCORE_SIGMOID,
+    RouteArgs a = {s.T, s.E, s.K, 0, groups, lanes, r.top_groups, r.group_top, r.score == EP_SCORE_SIGMOID,
                          r.normalize != 0, r.scale, logits, r.bias, topk, w, reinterpret_cast<uint32_t*>(ws)};
     const bool wide = r.bias || (groups > 1 && r.group_top > 1);
     const int need = (s.E / groups + lanes - 1) / lanes;  // at most 124 (groups <= 64)
@@ -323,19 +335,15 @@ hipError_t launch_route(const ep_shape& s, const float* logits, const ep_router&
          route_kernel<16, true>, route_kernel<32, true>, route_kernel<64, true>, route_kernel<128, true>}};
     int which = 0;
     while (1 << which < need) ++which;
-    hipLaunchKernelGGL(kernels[wide][which], dim3((unsigned)((s.T + kWavesPerBlock - 1) / kWavesPerBlock)),
-                       dim3(kBlockThreads), 0, st, a);
-    return hipGetLastError();
+    return launch_tokens(kernels[wide][which], a, st);
 }
 
 hipError_t launch_route_grad(const ep_shape& s, const float* logits, const ep_router& r, const int64_t* topk,
                              const float* d_w, void* d_logits, int dtype, char* ws, hipStream_t st) {
     if (s.T == 0) return hipSuccess;
-    const RouteGradArgs a = {s.T, s.E, s.K, r.score == EP_SCORE_SIGMOID, r.normalize != 0, dtype == EP_GRAD_F32,
+    RouteGradArgs a = {s.T, s.E, s.K, 0, r.score == EP_SCORE_SIGMOID, r.normalize != 0, dtype == EP_GRAD_F32,
                              r.scale, logits, topk, d_w, d_logits, reinterpret_cast<uint32_t*>(ws)};
-    hipLaunchKernelGGL((s.E % 4 == 0 ? route_grad_kernel<4> : route_grad_kernel<1>), dim3((unsigned)((s.T + kWavesPerBlock - 1) / kWavesPerBlock)),
-                       dim3(kBlockThreads), 0, st, a);
-    return hipGetLastError();
+    return launch_tokens(s.E % 4 == 0 ? route_grad_kernel<4> : route_grad_kernel<1>, a, st);
 }
 
 }  // namespace ep

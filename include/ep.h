@@ -621,7 +621,8 @@ size_t ep_norm_workspace_bytes(const ep_shape *shape);
  * without residual); dy: [T*H] bf16; d_stream: [T*H] of stream_type, the
  * gradient that h has from the layers after, or NULL; d_h: like d_stream, may
  * be it (same address); d_x: [T*H] bf16; d_gain: [H] fp32, overwritten (0 with
- * T = 0). d_h, d_x and d_gain may be NULL, not all of them. The sum over t is
+ * T = 0). d_h, d_x and d_gain may be NULL, not all of them; apart from d_h =
+ * d_stream, outputs must not overlap inputs or each other. The sum over t is
  * made in a fixed order: calls repeat bit for bit. 16 B aligned base pointers;
  * rstd 4 B. ws: ep_norm_workspace_bytes, 256 B aligned, needs no
  * initialisation; calls on one workspace must not overlap. */

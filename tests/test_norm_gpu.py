@@ -173,6 +173,23 @@ def test_norm_of_small_blocks():
     assert (out["y_fp8"][:, 128:].view(F8).float().abs().amax(1) == 448).all()
 
 
+def test_norm_of_more_rows_than_one_launch():
+    """2^21 workgroups of four rows and a few rows more: the same as in two calls."""
+    T, H, cut = (1 << 23) + 7, 8, 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((T, H), generator=g, device="cuda").to(BF16)
+    gain = (1 + 0.3 * torch.randn(H, generator=g, device="cuda")).to(BF16)
+    out = outputs(T, H, False, ["y", "rstd"], spare=2)
+    ep.ep_rms_norm(ep.make_shape(T, H, 1, 1, 1), x, None, ep.EP_STREAM_BF16, gain, EPS, out)
+    assert (out["y"][T:] == 7).all() and (out["rstd"][T:] == 7).all()
+    for part in (slice(0, cut), slice(cut, T)):
+        alone = outputs(part.stop - part.start, H, False, ["y", "rstd"])
+        ep.ep_rms_norm(ep.make_shape(part.stop - part.start, H, 1, 1, 1), x[part], None, ep.EP_STREAM_BF16, gain, EPS, alone)
+        for n in alone:
+            assert torch.equal(alone[n], out[n][part]), n
+    check_norm(x[-9:], None, gain, {n: t[T - 9:T] for n, t in out.items()}, False)
+
+
 def test_norm_offsets_past_32_bits():
     """More than 2^32 bytes of each array; the last rows are right."""
     T, H = 300_000, 8192

@@ -34,12 +34,13 @@ def test_norm_grad_refusals_and_workspace(lib, shape):
     n = ep.ep_norm_workspace_bytes(shape)
     assert n >= 256 + 4 * shape.H and n % 256 == 0
 
-    def call(s=shape, h=P, kind=0, gain=P, r=P, dy=P, ds=P, dh=P, dx=P, dg=P, ws=P, wsb=n):
+    def call(s=shape, h=P, kind=0, gain=P, r=P, dy=P, ds=P, dh=P + 256, dx=P + 512, dg=P, ws=P, wsb=n):
         return lib.ep_rms_norm_grad(byref(s), h, kind, gain, r, dy, ds, dh, dx, dg, ws, wsb, None)
 
     for bad in (dict(h=None), dict(gain=None), dict(r=None), dict(dy=None), dict(dh=None, dx=None, dg=None), dict(kind=2),
                 dict(h=ODD), dict(gain=ODD), dict(r=P + 2), dict(dy=ODD), dict(ds=ODD), dict(dh=ODD), dict(dx=ODD),
-                dict(dg=ODD), dict(ws=None), dict(ws=P + 16), dict(wsb=n - 1), dict(s=ep.make_shape(32, 252, 2, 8, 1))):
+                dict(dg=ODD), dict(ws=None), dict(ws=P + 16), dict(wsb=n - 1), dict(s=ep.make_shape(32, 252, 2, 8, 1)),
+                dict(h=P + 256), dict(h=P + 512), dict(dy=P + 256), dict(dy=P + 512), dict(gain=P + 256), dict(gain=P + 512)):
         refused(call(**bad))
     refused(call(s=ep.make_shape(4, (1 << 20) + 8, 1, 1, 1)), ep.EP_ERR_UNSUPPORTED)
     for s in (ep.make_shape(4, 250, 1, 1, 1), ep.make_shape(4, (1 << 20) + 8, 1, 1, 1)):

@@ -240,6 +240,21 @@ def test_route_many_tokens():
     assert torch.equal(idx[-1], reference(l[-1:], K, G, router)[0][0])
 
 
+def test_route_of_more_tokens_than_one_launch():
+    """2^21 workgroups of four tokens and a few tokens more, and their gradient."""
+    T, E, cut = (1 << 23) + 5, 2, 1 << 22
+    l = torch.randn((T, E), generator=torch.Generator().manual_seed(3))
+    router = dict(score=SOFTMAX, normalize=False)
+    idx, w = route(l, 1, 1, router)
+    assert torch.equal(idx[:, 0], l.argmax(1))
+    d_w = torch.ones((T, 1))
+    d = grad(l, idx, d_w, router)
+    for part in (slice(0, cut), slice(cut, T)):
+        assert torch.equal(route(l[part], 1, 1, router)[1], w[part])
+        assert torch.equal(grad(l[part], idx[part], d_w[part], router), d[part])
+    check_there(w[-9:], reference(l[-9:], 1, 1, router)[1], weight_rel(l, SOFTMAX, E) * w[-9:], "weights")
+
+
 # --------------------------------------------------------------------------
 # Gradient
 # --------------------------------------------------------------------------
