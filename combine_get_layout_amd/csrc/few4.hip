@@ -120,12 +120,10 @@ __device__ __forceinline__ void store_act(uint16_t* act, int F, float gate, floa
 }
 
 // First launch: workgroup (x, y) computes RT / 2 * 16 values of f for the tokens
-// of the y-th used expert, up to TT of them at a time (NT tiles of 16 where NT > 1).
-// Dynamic LDS: the scales (2 * 16 * GT rows, if LDS), then the waves' copies of a
-// step's tokens, kWaves * NT * TT * 512 bytes, where their parts lie at the end.
-struct Up4Shared {
-    FindShared find;
-};
+// of the y-th used expert, up to TT of them at a time; its waves share the contracted
+// axis, a step of 256 columns each. Dynamic LDS: the scales (RT * 16 rows, if LDS),
+// then the waves' copies of a step's tokens, kWaves * TT * 512 bytes, where their
+// parts of the sums lie at the end.
 typedef float Up4Part[4][16][17];
 
 // What a wave loads for one step; the scales unless they lie in LDS.
@@ -139,14 +137,13 @@ struct UpStage {
 // Bytes of a row's scales at most for them to lie in LDS.
 constexpr int kLdsScales = 512;
 
-// Tokens [t0, t0 + TT * NT) of the expert's list.
-template <int FORM, int RT, int NT, int TT, bool LDS>
-__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, Up4Shared& sh, uint8_t* scales,
+template <int FORM, int RT, int TT, bool LDS>
+__device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found, const FindShared& find, uint8_t* scales,
                                            uint8_t* area) {
     using Scale = ScaleRow<FORM>;
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     const int i = lane & 15, q = lane >> 4;
-    constexpr int GT = RT / 2, kCols = GT * 16, kLoads = NT * TT / 2;
+    constexpr int GT = RT / 2, kCols = GT * 16, kLoads = TT / 2;
     using Stage = UpStage<RT, kLoads, LDS>;
     const int f0 = blockIdx.x * kCols, cols = min(kCols, a.F - f0);
     const uint32_t ld = (uint32_t)a.H / 2;
@@ -163,7 +160,7 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 #pragma unroll
     for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
 
-    for (int t0 = 0; t0 < found.tokens; t0 += TT * NT) {
+    for (int t0 = 0; t0 < found.tokens; t0 += TT) {
         // A step's values of a token are 512 bytes in a row: half a wave's load. (As the
         // fragments that the matrix instruction takes they would be eight loads of four
         // lanes a token each, which the L1 ran out of: one token 31 us instead of 25.)
@@ -171,10 +168,10 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
 #pragma unroll
         for (int n = 0; n < kLoads; ++n) {
             const int at = t0 + 2 * n + (lane >> 5);
-            xr[n] = at < found.tokens ? (uint32_t)sh.find.token[at] * a.H * 2 + (lane & 31) * 16 : kBufNone;
+            xr[n] = at < found.tokens ? (uint32_t)find.token[at] * a.H * 2 + (lane & 31) * 16 : kBufNone;
         }
-        uint8_t* const xs = area + wave * (NT * TT * 512);
-        f32x4 acc[RT][NT] = {};
+        uint8_t* const xs = area + wave * (TT * 512);
+        f32x4 acc[RT][1] = {};  // as `settle` takes them
         auto load = [&](int s, Stage& g) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -198,18 +195,14 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
             wave_lds_order();
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                bf16x8 xf[NT][4];
-                f32x4 base[NT] = {};
+                bf16x8 xf[4];
+                f32x4 base = {};
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)  // rows past TT: earlier ones again, of which nothing is kept
-                        xf[n][m] = as_bf16(ld16(xs + row_chunk(n * 16 + (i & (TT - 1)), p * 16 + q * 4 + m)));
+                for (int m = 0; m < 4; ++m)  // rows past TT: earlier ones again, of which nothing is kept
+                    xf[m] = as_bf16(ld16(xs + row_chunk(i & (TT - 1), p * 16 + q * 4 + m)));
                 if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) base[n] = mfma_bf16(xf[n][m], minus_eight, base[n]);
+                    for (int m = 0; m < 4; ++m) base = mfma_bf16(xf[m], minus_eight, base);
                 }
                 const bool in = s * kSpan + p * 128 + q * 32 < a.H;  // else codes of 0, and no scale
                 const uint32_t at = in ? s * Scale::kStep + Scale::offset(p, q) : 0u;
@@ -224,17 +217,14 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                     bf16x8 wf[4];
 #pragma unroll
                     for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(g.w[r][p][m], scale);
+                    f32x4 c = FORM == EP_W4_INT ? base : acc[r][0];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        f32x4 c = FORM == EP_W4_INT ? base[n] : acc[r][n];
+                    for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], wf[m], c);
+                    if constexpr (FORM == EP_W4_INT) {
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[n][m], wf[m], c);
-                        if constexpr (FORM == EP_W4_INT) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(scale, c[j], acc[r][n][j]);
-                        } else {
-                            acc[r][n] = c;
-                        }
+                        for (int j = 0; j < 4; ++j) acc[r][0][j] = fmaf(scale, c[j], acc[r][0][j]);
+                    } else {
+                        acc[r][0] = c;
                     }
                 }
             }
@@ -284,38 +274,35 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
         Up4Part* const part = reinterpret_cast<Up4Part*>(area);
         __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int g = 0; g < GT; g += 2) {
+            constexpr int kSub = GT < 2 ? 1 : 2;  // sub-tiles of 16 values in this pass
 #pragma unroll
-            for (int g = 0; g < GT; g += 2) {
-                constexpr int kSub = GT < 2 ? 1 : 2;  // sub-tiles of 16 values in this pass
+            for (int r = 0; r < 2 * kSub; ++r)
 #pragma unroll
-                for (int r = 0; r < 2 * kSub; ++r)
+                for (int j = 0; j < 4; ++j)
+                    part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][0][j];
+            __syncthreads();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        part[wave][r / kSub * 2 + r % kSub][q * 4 + j][i] = acc[r / kSub * GT + g + r % kSub][n][j];
-                __syncthreads();
+            for (int c0 = 0; c0 < 16 * 32; c0 += kThreads) {
+                const int tk = (c0 + tid) >> 5, c = tid & 31;
+                const int at = t0 + tk, f = f0 + g * 16 + c;
+                if (tk >= TT || at >= found.tokens || f >= a.F || c >= 16 * kSub) continue;
+                float gate = 0.f, up = 0.f;
 #pragma unroll
-                for (int c0 = 0; c0 < 16 * 32; c0 += kThreads) {
-                    const int tk = (c0 + tid) >> 5, c = tid & 31;
-                    const int at = t0 + n * 16 + tk, f = f0 + g * 16 + c;
-                    if (tk >= TT || at >= found.tokens || f >= a.F || c >= 16 * kSub) continue;
-                    float gate = 0.f, up = 0.f;
-#pragma unroll
-                    for (int v = 0; v < kWaves; ++v) {
-                        gate += part[v][c >> 4][tk][c & 15];
-                        up += part[v][2 + (c >> 4)][tk][c & 15];
-                    }
-                    store_act(a.act + (int64_t)sh.find.row[at] * 2 * a.F + f, a.F, gate, up);
+                for (int v = 0; v < kWaves; ++v) {
+                    gate += part[v][c >> 4][tk][c & 15];
+                    up += part[v][2 + (c >> 4)][tk][c & 15];
                 }
-                __syncthreads();
+                store_act(a.act + (int64_t)find.row[at] * 2 * a.F + f, a.F, gate, up);
             }
+            __syncthreads();
         }
     }
 }
 
-template <int FORM, int RT, int NT, int TT, bool LDS>
+template <int FORM, int RT, int TT, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
-    __shared__ Up4Shared sh;
+    __shared__ FindShared find;
     extern __shared__ u32x4 lds_vectors[];
     uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);
     uint8_t* const area = scales + (LDS ? RT * 16 * ScaleRow<FORM>::bytes(a.H) : 0u);
@@ -325,10 +312,10 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
         if (a.splits > 1)
             for (int n = tid; n * 16 < a.H; n += kThreads) a.joined[n] = 0;
     }
-    const Found found = find_expert<kThreads>(a, sh.find);
+    const Found found = find_expert<kThreads>(a, find);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
-    up4_tokens<FORM, RT, NT, TT, LDS>(a, found, sh, scales, area);
+    up4_tokens<FORM, RT, TT, LDS>(a, found, find, scales, area);
 }
 
 // The same for experts with many tokens: 64 values of f to a workgroup, 16 of them (a
@@ -446,7 +433,7 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
 
 template <int FORM, int NT>
 __global__ __launch_bounds__(kThreads, 2) void few4_up_many_kernel(Few4Args a) {
-    __shared__ Up4Shared sh;
+    __shared__ FindShared find;
     extern __shared__ u32x4 lds_vectors[];
     uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);
     const uint32_t lds = ScaleRow<FORM>::bytes(a.H);
@@ -457,7 +444,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_many_kernel(Few4Args a) {
         if (a.splits > 1)
             for (int n = tid; n * 16 < a.H; n += kThreads) a.joined[n] = 0;
     }
-    const Found found = find_expert<kThreads>(a, sh.find);
+    const Found found = find_expert<kThreads>(a, find);
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.used[0] = found.used;
     if (found.expert < 0) return;
     const int f0 = blockIdx.x * kManyCols, vectors = min(kManyCols, a.F - f0) * lds / 16;
@@ -470,13 +457,13 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_many_kernel(Few4Args a) {
     for (int t0 = 0; t0 < found.tokens;) {
         const int left = found.tokens - t0;
         if (NT >= 8 && left > 64)
-            up4_many_tokens<FORM, NT >= 8 ? 8 : 1>(a, found, sh.find, scales, rows, t0), t0 += 128;
+            up4_many_tokens<FORM, NT >= 8 ? 8 : 1>(a, found, find, scales, rows, t0), t0 += 128;
         else if (NT >= 4 && left > 32)
-            up4_many_tokens<FORM, NT >= 4 ? 4 : 1>(a, found, sh.find, scales, rows, t0), t0 += 64;
+            up4_many_tokens<FORM, NT >= 4 ? 4 : 1>(a, found, find, scales, rows, t0), t0 += 64;
         else if (NT >= 2 && left > 16)
-            up4_many_tokens<FORM, NT >= 2 ? 2 : 1>(a, found, sh.find, scales, rows, t0), t0 += 32;
+            up4_many_tokens<FORM, NT >= 2 ? 2 : 1>(a, found, find, scales, rows, t0), t0 += 32;
         else
-            up4_many_tokens<FORM, 1>(a, found, sh.find, scales, rows, t0), t0 += 16;
+            up4_many_tokens<FORM, 1>(a, found, find, scales, rows, t0), t0 += 16;
     }
 }
 
@@ -793,12 +780,13 @@ template <int FORM, int RT, int CAP>
 Kernel down_kernel(bool lds) {
     return lds ? few4_down_kernel<FORM, RT, CAP, true> : few4_down_kernel<FORM, RT, CAP, false>;
 }
-template <int FORM, int RT>
-Kernel up_kernel(int tt) {
-    return tt == 2   ? few4_up_kernel<FORM, RT, 1, 2, true>
-           : tt == 4 ? few4_up_kernel<FORM, RT, 1, 4, true>
-           : tt == 8 ? few4_up_kernel<FORM, RT, 1, 8, true>
-                     : few4_up_kernel<FORM, RT, 1, 16, true>;
+template <int FORM>
+Kernel up_kernel(int tt, bool narrow) {
+    if (!narrow) return tt == 8 ? few4_up_kernel<FORM, 4, 8, true> : few4_up_kernel<FORM, 4, 16, true>;
+    return tt == 2   ? few4_up_kernel<FORM, 2, 2, true>
+           : tt == 4 ? few4_up_kernel<FORM, 2, 4, true>
+           : tt == 8 ? few4_up_kernel<FORM, 2, 8, true>
+                     : few4_up_kernel<FORM, 2, 16, true>;
 }
 
 template <int FORM>
@@ -806,19 +794,48 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const int64_t experts = std::min<int64_t>(s.E, (int64_t)s.T * s.K), lanes = (int64_t)s.T * s.K;
     const uint32_t row = ScaleRow<FORM>::bytes(a.H);
     const bool lds_scales = row <= kLdsScales;
-    const bool many = lds_scales && (lanes > 8 * experts || (lanes > 4 * experts && (a.F + 63) / 64 * experts >= 512));
-    const bool narrow = !lds_scales || (int64_t)((a.F + 31) / 32) * experts < 1024;
+    // Experts of many tokens: few4_up_many_kernel, if there are workgroups for most CUs.
+    // Both launches without and with it, us (form; workgroups it has):
+    //   128 tokens, top-8 of 64 experts of 2048 x 768 (int, 768)   133  102
+    //   100 tokens, top-8 of 10, 512 x 1024 (e2m1, 160)            71.4 57.1
+    //   128 tokens, top-1 of 8, 2048 x 2048 (int, 256)             62.8 59.0
+    //   48 tokens, top-8 of 64, 7168 x 2048 (int, 2048)            458  424
+    //   48 tokens, top-4 of 32, 4096 x 2048 (e2m1, 1024)           141  146
+    //   64 tokens, top-2 of 8, 2048 x 1024 (int, 128)              36.2 40.2
+    //   128 tokens, top-4 of 8, 2048 x 512 (int, 64)               54.7 73.4
+    //   32 tokens, top-8 of 64, 7168 x 2048 (e2m1, 2048)           347  372
+    //   16 tokens, top-8 of 64, 7168 x 512 (e2m1, 512)             91.5 94.0
+    const int64_t groups64 = (a.F + kManyCols - 1) / kManyCols * experts;
+    const bool many = lds_scales && (lanes > 8 * experts ? groups64 >= 160 : lanes > 4 * experts && groups64 >= 512);
+    // 16 or 32 values of f to a workgroup: 32 read the tokens half as often, 16 have more
+    // waves to hide a step's latency. us with 16 and with 32 (form):
+    //   1 token, top-8 of 64 experts of 7168 x 2048 (e2m1)    48.0 49.3
+    //   2 tokens, top-6 of 64, 5120 x 1536 (int)              44.5 52.0
+    //   8 tokens, top-4 of 64, 4096 x 1024 (int)              48.0 50.7
+    //   16 tokens, top-4 of 16, 2048 x 1024 (int, e2m1)       30.2 28.3, 26.4 27.1
+    //   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1)       350 354, 338 347
+    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1)            46.5 43.3
+    //   64 tokens, top-2 of 16, 2048 x 1024 (int, e2m1)       43.2 39.9, 41.6 38.9
+    //   32 tokens, top-2 of 8, 1024 x 512 (int)               18.5 20.1
+    const bool narrow = !lds_scales || lanes <= 4 * experts || (int64_t)((a.F + 31) / 32) * experts < 512;
     const int cols = many ? kManyCols : narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
-    // Tokens at a time: those of most experts, as the weights are read again for more.
+    // Tokens at a time: those of most experts, as the weights are read again for more; no
+    // more than these, as each is a load a step. us, and with 16 always: 48.0 56.7 (1
+    // token), 31.7 38.8 (4 tokens, top-4 of 64 experts of 4096 x 1024), 347 370 (32
+    // tokens, top-8 of 64, 7168 x 2048).
     const int tt = s.T <= 2 ? 2 : s.T <= 4 ? 4 : s.T <= 8 || lanes <= 4 * experts ? 8 : 16;
+    // Tiles of 16 tokens that few4_up_many_kernel multiplies at a time, at most: what fits
+    // the registers decides how many waves there are. us with 2, this and 8: 102 102 138
+    // (128 tokens, top-8 of 64, 2048 x 768), 424 424 609 (48 tokens, top-8 of 64, 7168 x
+    // 2048), 61.1 57.1 57.1 (100 tokens, top-8 of 10), 88.2 74.3 74.3 (128 tokens, top-4
+    // of 8, 2048 x 1024).
     const int tiles1 = s.T <= 32 || lanes <= 20 * experts ? 2 : s.T <= 64 || lanes <= 48 * experts ? 4 : 8;
-    const Kernel first = !lds_scales ? few4_up_kernel<FORM, 2, 1, 16, false>
+    const Kernel first = !lds_scales ? few4_up_kernel<FORM, 2, 16, false>
                          : many      ? (tiles1 == 8   ? few4_up_many_kernel<FORM, 8>
                                         : tiles1 == 4 ? few4_up_many_kernel<FORM, 4>
                                                       : few4_up_many_kernel<FORM, 2>)
-                         : narrow    ? up_kernel<FORM, 2>(tt)
-                                     : up_kernel<FORM, 4>(tt);
+                                     : up_kernel<FORM>(tt, narrow);  // wide: more than 4 tokens
     const size_t area = many ? 8192 * tiles1
                              : std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (lds_scales ? tt : 16));
     hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);

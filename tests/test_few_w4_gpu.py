@@ -267,6 +267,31 @@ def test_few_w4_with_most_lanes_and_experts(form):
 
 
 @FORMS
+@pytest.mark.parametrize("case", [(64, 256, 896, 12, 8, {}), (36, 384, 480, 20, 16, dict(skip=0.1)),
+                                  (40, 128, 672, 48, 10, {}), (128, 1024, 2080, 5, 5, {})], ids=str)
+def test_few_w4_many_tokens_an_expert(case, form):
+    """16, 32, 64 and 128 tokens of an expert at a time, and what is left of them."""
+    test_few_w4(case, form)
+
+
+@FORMS
+def test_few_w4_many_tokens_of_the_longest_rows_in_lds(form):
+    """Scales of 512 bytes a row in LDS, beside 128 tokens' rows."""
+    T, H, F, E, K = 128, 16384 if form == E2M1 else 32768, 128, 80, 40
+    g = torch.Generator().manual_seed(19)
+    some = [four(g, 4, n, k, form) for n, k in ((2 * F, H), (H, F))]
+    w13, w2 = [tuple(t.repeat(E // 4, 1, 1) for t in m) for m in some]
+    x = randn(g, T, H)
+    idx, w = routing(T, K, E, 18)
+    out, ws = few_call(x, idx, w, experts(w13, w2, F, form), E)
+    assert ep.ep_check_errors(ws) == 0
+    # A sample of the tokens: each is a sum of its own.
+    at = torch.arange(0, T, 17)
+    ref, bound = few_reference(x[at], w13, w2, idx[at], w[at], F, form)
+    check(out.cpu()[at], ref, bound, "out")
+
+
+@FORMS
 @pytest.mark.parametrize("wide", ["H", "F"])
 def test_few_w4_at_the_largest_dimensions(form, wide):
     small = 128 if form == INT else 32
