@@ -1,4 +1,14 @@
 // norm.hip -- ep_rms_norm and ep_rms_norm_grad on gfx950.
+//
+// Bound by memory: a row is read once, held in registers over the sum of its squares
+// (its dot product in the gradient) and written once, so 4,096 rows of 7,168 move
+//   forward (x, residual; h, y, the 8-bit rows)  265 MB in 43.2 us, 6.1 TB/s
+//   gradient (h, dy, d_stream; d_h, d_gain)      235 MB in 45.2 us, 5.2 TB/s, and 4.7 us
+//     to add the workgroups' parts of d_gain (14.7 MB, still in the caches)
+// and one row of 7,168 takes 2.5 us, a launch's latency and two dependent loads.
+// 201 rows of 2,056 with a 32-bit stream, gradient: 4.9 us in one launch.
+// Vectors of eight values, as bf16 loads of 16 bytes; past 32,768 values a row does not
+// fit the registers and is read twice.
 #include <algorithm>
 
 #include "ep_internal.h"
@@ -429,20 +439,25 @@ __global__ __launch_bounds__(1024) void norm_gain_kernel(const float* part, int 
     }
 }
 
-constexpr int kGradGroups = 512;  // workgroups of norm_grad_kernel that take rows, two per CU
 constexpr int kLongH = 32768;     // longest row held in registers
 
 // Threads to a row: with one vector of eight to a thread (a stream in 32 bits, whose
 // rows take more registers) or two.
+// In bf16 one, and two, us: 4,096 rows of 2,056 23.7 22.4, of 4,096 31.5 32.3, of 7,168
+// 50.2 50.5.
 int grad_lanes(int H, bool wide) {
     int lanes = 64;
     while (lanes < 1024 && lanes * 8 * (wide ? 1 : 2) < H) lanes *= 2;
     return lanes;
 }
+// Workgroups of norm_grad_kernel that take rows: what the chip holds at once, 512 of 512
+// threads or 256 of 1,024. us with 256 and 512: bf16, 4,096 rows of 2,056 (512 threads)
+// 25.0 22.4, of 7,168 52.7 50.5; 2,048 of 16,384 (1,024 threads) 57.6 68.7; 32-bit
+// stream, 4,096 of 7,168 (1,024) 95.4 101.
 int grad_groups(int T, int H, bool wide) {
     if (H > kLongH) return std::min(T, 64);
-    const int rows = std::max(1, kGradThreads / grad_lanes(H, wide));
-    return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, kGradGroups);
+    const int lanes = grad_lanes(H, wide), rows = std::max(1, kGradThreads / lanes);
+    return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, lanes > kGradThreads ? 256 : 512);
 }
 // Whether d_gain is made beside the rows in the same launch, by workgroups that
 // read dy and h once more, column by column, or from the rows' workgroups' parts in a
@@ -455,6 +470,11 @@ int grad_groups(int T, int H, bool wide) {
 //   two     13.9        17.0         22.2         31.2
 bool gain_beside(int T, int H) { return H <= kLongH && T <= 1024 && (int64_t)T * H <= 1 << 23; }
 
+// Threads to a row: a wave up to 2,048 values (256 threads, with a barrier, are the same
+// within 1%), then one vector to a thread, as far as a workgroup goes. us, 4,096 rows of
+// 4,096, 5,120 and 7,168 with all outputs: 26.3 31.6 43.4; with 256 threads of two or
+// four vectors 27.2 34.8 47.5; with a 32-bit stream of 7,168 69.6, 75.3. 2,048 rows of
+// 16,384: 53.2, with 256 threads of eight vectors 61.4.
 template <bool WIDE>
 void launch_norm(NormArgs a, hipStream_t st) {
     const int vecs = (a.H + 7) / 8;
@@ -468,8 +488,12 @@ void launch_norm(NormArgs a, hipStream_t st) {
     if (vecs <= 64) return go(norm_kernel<64, 1, WIDE>, 64);
     if (vecs <= 128) return go(norm_kernel<64, 2, WIDE>, 64);
     if (vecs <= 256) return go(norm_kernel<64, 4, WIDE>, 64);
-    if (vecs <= 512) return go(norm_kernel<256, 2, WIDE>, 256);
-    if (vecs <= 1024) return go(norm_kernel<256, 4, WIDE>, 256);
+    if (vecs <= 384) return go(norm_kernel<384, 1, WIDE>, 384);
+    if (vecs <= 512) return go(norm_kernel<512, 1, WIDE>, 512);
+    if (vecs <= 640) return go(norm_kernel<640, 1, WIDE>, 640);
+    if (vecs <= 768) return go(norm_kernel<768, 1, WIDE>, 768);
+    if (vecs <= 896) return go(norm_kernel<896, 1, WIDE>, 896);
+    if (vecs <= 1024) return go(norm_kernel<1024, 1, WIDE>, 1024);
     if (vecs <= 2048) return go(norm_kernel<1024, 2, WIDE>, 1024);
     if (vecs <= 4096) return go(norm_kernel<1024, 4, WIDE>, 1024);
     go(norm_kernel<1024, 0, WIDE>, 1024);

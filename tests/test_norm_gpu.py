@@ -87,9 +87,9 @@ def outputs(T, H, wide, names, spare=0):
     return {n: make[n]() for n in names}
 
 
-# Row lengths on both sides of every change of kernel: 64, 256 and 1,024 threads to a row, one
-# to four vectors of eight to a thread, and rows in two passes.
-LENGTHS = [8, 72, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 7168, 8192, 8200, 16384, 16392, 32768, 32776, 40960]
+# Row lengths on both sides of every change of kernel: 64 to 1,024 threads to a row, one to
+# four vectors of eight to a thread, and rows in two passes.
+LENGTHS = [8, 72, 512, 520, 1024, 1032, 2048, 2056, 3080, 4096, 4104, 5120, 5128, 6144, 6152, 7168, 7176, 8192, 8200, 16384, 16392, 32768, 32776, 40960]
 
 
 @pytest.mark.parametrize("residual", [True, False], ids=["residual", "alone"])
