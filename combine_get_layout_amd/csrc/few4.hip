@@ -1,5 +1,24 @@
 // few4.hip -- ep_moe_few_w4 on gfx950: the expert layer for a few tokens with
 // 4-bit weights, in the two launches of ep_moe_few.
+//
+// For token t and each used expert e, over the values w that codes and scales stand for:
+//   gate, up = x[t] . w13[e],  act = gate / (1 + exp(-gate)) * up          (first launch)
+//   out[t] = bf16(sum over e of (sum of t's weights for e) * act . w2[e])  (second launch)
+// A code becomes bf16 exactly (four bits of magnitude at most), so the matrix
+// instructions' products are those of the formula, summed in 32 bits. act goes to the
+// second product as two bf16 values, the rounded one and the rest: 16 bits of it.
+//
+// What has to move is the used experts' weights once, 1.5 F H bytes each and a 32nd (int)
+// or 16th (e2m1) of that in scales; products are few (32 tokens, top-8 of 64 experts
+// of 7168 x 2048: 22 GFLOP for 1.48 GB). Medians on inputs that the caches do not hold:
+//   1 token, top-8 of 64 experts of 7168 x 2048, int   28.5 + 21.0 us, 182 MB: 3.7 TB/s
+//   32 tokens, the same, e2m1                          202 + 131 us, 1.48 GB: 4.4 TB/s
+//   13 tokens, top-3 of 40, 2080 x 736, e2m1           15.4 + 13.7 us, 60 MB: 2.1 TB/s
+//   1 token, top-2 of 16, 256 x 512, int               5.5 + 5.1 us: two launches' latency
+// The first launch of 32 tokens reads at 4.9 TB/s, as a copy does; the second is bound by
+// latency: a wave waits for one unit of 256 values' fragments behind another, with the
+// activations' (as many loads as the weights') between them. One token's launches end
+// before the memory has come up to its rate.
 #include <algorithm>
 
 #include "ep_internal.h"
@@ -321,8 +340,8 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_kernel(Few4Args a) {
 // The same for experts with many tokens: 64 values of f to a workgroup, 16 of them (a
 // gate and an up tile) to a wave, which goes over the whole contracted axis for all of
 // the expert's tokens; steps of 128 columns, whose tokens' rows lie in LDS for all four
-// waves, in two buffers. One barrier a step; the next step's rows and the weights of
-// three are in flight.
+// waves, in two buffers. One barrier a step; the next step's rows and the next two's
+// weights are in flight.
 constexpr int kManyCols = 64, kManySpan = 128, kManyAhead = 2;
 
 // Rows of 256 bytes in LDS; chunks exchanged as in row_chunk.
@@ -516,6 +535,9 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 
     const uint32_t ld = (uint32_t)a.F / 2;
     const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld;
+    // A run of neighbouring units to each wave; dealt to a workgroup's waves in turn, which
+    // then read 512 bytes of a row together, they took 348 us instead of 338 (32 tokens,
+    // top-8 of 64 experts of 7168 x 2048), as each wave has every expert's scales to load.
     const int run = blockIdx.y * kWaves + wave, runs = a.splits * kWaves;
     int u = (int)((int64_t)units * run / runs);
     const int end = (int)((int64_t)units * (run + 1) / runs);

