@@ -353,7 +353,9 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
     using Scale = ScaleRow<FORM>;
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
     const int i = lane & 15, q = lane >> 4;
-    const int f0 = blockIdx.x * kManyCols + wave * 16, cols = max(min(16, a.F - f0), 0);
+    const int f0 = blockIdx.x * kManyCols + wave * 16;
+    // Into a scalar register: it would be found in a vector one, and each load be a loop.
+    const int cols = __builtin_amdgcn_readfirstlane(max(min(16, a.F - f0), 0));
     const uint32_t ld = (uint32_t)a.H / 2, lds = Scale::bytes(a.H);
     const uint8_t* w = a.w13 + ((int64_t)found.expert * 2 * a.F + f0) * ld;
     const auto d_gate = buf_resource(w, cols * ld), d_up = buf_resource(w + (int64_t)a.F * ld, cols * ld);
@@ -389,8 +391,10 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
         bf16x8 wf[2][4];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const uint32_t at = (g * kManyCols + wave * 16 + i) * lds + s * (Scale::kStep / 2) + Scale::offset(0, q);
-            scale[g] = Scale::value(in ? Scale::from_lds(scales + at) : 0u);
+            const uint32_t at = (g * kManyCols + wave * 16 + i) * lds + (in ? s * (Scale::kStep / 2) + Scale::offset(0, q) : 0u);
+            uint32_t bits = Scale::from_lds(scales + at);
+            asm volatile("" : "+v"(bits));  // read in any case, without a branch
+            scale[g] = Scale::value(in ? bits : 0u);
 #pragma unroll
             for (int m = 0; m < 4; ++m) wf[g][m] = codes_to_bf16<FORM>(v[g][m], scale[g]);
         }
@@ -432,6 +436,7 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
         __builtin_amdgcn_sched_barrier(0);
     };
     load_x(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < kManyAhead; ++k) load_w(k, wv[k]);
     for (int s = 0; s < steps; s += kManyAhead) {
@@ -486,6 +491,85 @@ __global__ __launch_bounds__(kThreads, 2) void few4_up_many_kernel(Few4Args a) {
     }
 }
 
+__device__ __forceinline__ void look_over_ids(const Few4Args& a) {
+    if (blockIdx.x != 0 || blockIdx.y != 0) return;
+    bool bad = false;
+    for (int n = threadIdx.x; n < a.T * a.K; n += kThreads) bad |= expert_bad(a.topk[n], a.E);
+    if (__ballot(bad) && lane_id() == 0) report(a.err, EP_DEVERR_EXPERT_ID);
+}
+
+// The end of the second launch: COLS values of h for every token from the workgroup's
+// SETS sums in LDS, [SETS][T][COLS + 1], and, where workgroups share outputs, from all
+// of theirs by the last one to finish; in a fixed order.
+template <int COLS, int SETS>
+__device__ __forceinline__ void join(const Few4Args& a, const float* sums) {
+    constexpr int kPairs = COLS / 2;  // two columns to a thread
+    const int tid = threadIdx.x, h0 = blockIdx.x * COLS, cols = min(COLS, a.H - h0), pairs = a.T * kPairs;
+    uint64_t* const part = reinterpret_cast<uint64_t*>(a.part);
+    const int64_t set = (int64_t)a.T * a.H / 2;  // one workgroup's part, in pairs
+    auto at = [&](int n) { return ((int64_t)(n / kPairs) * a.H + h0) / 2 + n % kPairs; };
+    auto put = [&](int n, float v0, float v1) {
+        *reinterpret_cast<uint32_t*>(a.out + 2 * at(n)) = pack_bf16(v0, v1);
+    };
+    __syncthreads();
+    for (int n = tid; n < pairs; n += kThreads) {
+        const int t = n / kPairs, c = n % kPairs * 2;
+        if (c >= cols) continue;
+        float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < SETS; ++w) {
+            const float* s = sums + (w * a.T + t) * (COLS + 1) + c;
+            v0 += s[0], v1 += s[1];
+        }
+        if (a.splits == 1)
+            put(n, v0, v1);
+        else
+            __hip_atomic_store(part + blockIdx.y * set + at(n), (uint64_t)__float_as_uint(v1) << 32 | __float_as_uint(v0),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (a.splits == 1) return;
+    __shared__ int before;
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are acknowledged
+    __syncthreads();
+    if (tid == 0)
+        before = __hip_atomic_fetch_add(a.joined + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before != a.splits - 1) return;
+    // Eight parts of two pairs in flight: with four loads of one value, 128 tokens' sixteen
+    // parts took 40 us.
+    constexpr int kAtOnce = 8;
+    for (int n0 = tid; n0 < pairs; n0 += 2 * kThreads) {
+        float v[2][2] = {};
+        int64_t from[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int n = min(n0 + g * kThreads, pairs - 1), c = n % kPairs * 2;
+            from[g] = ((int64_t)(n / kPairs) * a.H + h0 + min(c, cols - 2)) / 2;
+        }
+        for (int p = 0; p < a.splits; p += kAtOnce) {
+            uint64_t w[2][kAtOnce];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    w[g][k] = __hip_atomic_load(part + min(p + k, a.splits - 1) * set + from[g], __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    v[g][0] += p + k < a.splits ? __uint_as_float((uint32_t)w[g][k]) : 0.f;
+                    v[g][1] += p + k < a.splits ? __uint_as_float((uint32_t)(w[g][k] >> 32)) : 0.f;
+                }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int n = n0 + g * kThreads;
+            if (n < pairs && n % kPairs * 2 < cols) put(n, v[g][0], v[g][1]);
+        }
+    }
+}
+
 // What a wave loads for one unit; the scales as its own run of an expert's, where
 // they lie in LDS.
 template <int RT, int CAP, bool LDS>
@@ -515,11 +599,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     uint8_t* const rows = reinterpret_cast<uint8_t*>(lds_vectors) + kWaves * lds_block + uniform_wave() * (CAP * 1024);
     float* const sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(lds_vectors) + kWaves * (lds_block + CAP * 1024));
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-        bool bad = false;
-        for (int n = tid; n < a.T * a.K; n += kThreads) bad |= expert_bad(a.topk[n], a.E);
-        if (__ballot(bad) && lane == 0) report(a.err, EP_DEVERR_EXPERT_ID);
-    }
+    look_over_ids(a);
     const int i = lane & 15, q = lane >> 4;
     const int h0 = blockIdx.x * kCols, cols = min(kCols, a.H - h0);
     // The number of used experts and the first 63 of them, in one load (the array is
@@ -740,37 +820,168 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
         turn(g0, g1);
         if (u < end) turn(g1, g0);
     }
-    __syncthreads();
-    for (int n = tid; n < a.T * kCols; n += kThreads) {
-        const int t = n / kCols, h = h0 + n % kCols;
-        if (n % kCols >= cols) continue;
-        float v = 0.f;
+    join<kCols, kWaves>(a, sums);
+}
+
+// The same for experts with many tokens: 64 values of h to a workgroup, 16 of them to a
+// wave, for up to NT tiles of 16 tokens at a time, whose rows of act (rounded values, then
+// rests) lie in LDS for all four waves, as in few4_up_many_kernel. The work of the
+// workgroups that share outputs is cut into steps of 128 columns, over the used experts in
+// order. A wave's sums are those of its own columns: one set of [T][65] in LDS.
+struct DownManyShared {
+    Route routes[EP_FEW_MAX_TOKENS];  // of the expert at hand
+};
+
+template <int FORM, int NT>
+__device__ __forceinline__ void down4_many_tokens(const Few4Args& a, const DownManyShared& sh, const uint8_t* scales,
+                                                  uint8_t* rows, float* sums, int expert, int tokens, int t0, int begin,
+                                                  int end) {
+    using Scale = ScaleRow<FORM>;
+    const int tid = threadIdx.x, lane = lane_id(), wave = uniform_wave();
+    const int i = lane & 15, q = lane >> 4;
+    const int h0 = blockIdx.x * kManyCols + wave * 16;
+    const int cols = __builtin_amdgcn_readfirstlane(max(min(16, a.H - h0), 0));
+    const uint32_t ld = (uint32_t)a.F / 2, lds = Scale::bytes(a.F);
+    const auto d_w = buf_resource(a.w2 + ((int64_t)expert * a.H + h0) * ld, cols * ld);
+    const auto d_act = buf_resource(a.act, (uint32_t)(a.T * a.K) * 4 * a.F);
+    uint32_t xr[2 * NT];  // tiles 0 to NT - 1: values, NT and on: rests
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += sums[(w * a.T + t) * kLd + n % kCols];
-        if (a.splits == 1)
-            a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
-        else
-            __hip_atomic_store(a.part + ((int64_t)blockIdx.y * a.T + t) * a.H + h, v, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
+    for (int n = 0; n < NT; ++n) {
+        const int at = t0 + n * 16 + (tid >> 4);
+        const uint32_t row = sh.routes[min(at, EP_FEW_MAX_TOKENS - 1)].id & 0xFFFF;
+        xr[n] = at < tokens ? row * 4u * a.F + (tid & 15) * 16 : kBufFar;
+        xr[NT + n] = at < tokens ? row * 4u * a.F + 2u * a.F + (tid & 15) * 16 : kBufFar;
     }
-    if (a.splits == 1) return;
-    __shared__ int before;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are acknowledged
-    __syncthreads();
-    if (tid == 0)
-        before = __hip_atomic_fetch_add(a.joined + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (before != a.splits - 1) return;
-    for (int n = tid; n < a.T * kCols; n += kThreads) {
-        const int t = n / kCols, h = h0 + n % kCols;
-        if (n % kCols >= cols) continue;
-        float v = 0.f;
-#pragma unroll 4
-        for (int p = 0; p < a.splits; ++p)
-            v += __hip_atomic_load(a.part + ((int64_t)p * a.T + t) * a.H + h, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
-        a.out[(int64_t)t * a.H + h] = (uint16_t)f32_to_bf16(v);
+    bf16x8 minus_eight;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
+    f32x4 acc[1][2 * NT] = {};
+    u32x4 xv[2 * NT], wv[kManyAhead];
+    auto load_x = [&](int s) {
+        const bool in = s < end && s * kManySpan + (tid & 15) * 8 < a.F;
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n) xv[n] = buf_load16(d_act, in ? xr[n] : kBufFar, s * 256);
+    };
+    auto load_w = [&](int s, u32x4& v) {
+        const bool in = s < end && s * kManySpan + q * 32 < a.F;
+        v = buf_load16(d_w, in ? i * ld + q * 16 : kBufFar, s * 64);
+    };
+    auto step = [&](int s, uint8_t* buf, u32x4& v) {
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n) st16(buf + half_chunk(n * 16 + (tid >> 4), tid & 15), xv[n]);
+        barrier_only();
+        const bool in = s < end && s * kManySpan + q * 32 < a.F;  // else codes of 0, and no scale
+        const uint32_t at = (wave * 16 + i) * lds + (in ? s * (Scale::kStep / 2) + Scale::offset(0, q) : 0u);
+        uint32_t bits = Scale::from_lds(scales + at);
+        asm volatile("" : "+v"(bits));  // read in any case, without a branch
+        const float scale = Scale::value(in ? bits : 0u);
+        bf16x8 wf[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(v[m], scale);
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(s + 1);
+        load_w(s + kManyAhead, v);
+        __builtin_amdgcn_sched_barrier(0);
+        bf16x8 tile[2][4];
+        auto read = [&](int n) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tile[n & 1][m] = as_bf16(ld16(buf + half_chunk(n * 16 + i, q * 4 + m)));
+        };
+        read(0);
+#pragma unroll
+        for (int n = 0; n < 2 * NT; ++n) {
+            if (n + 1 < 2 * NT) read(n + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            const bf16x8(&xf)[4] = tile[n & 1];
+            f32x4 c = {};
+            if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], minus_eight, c);
+            } else {
+                c = acc[0][n];
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], wf[m], c);
+            if constexpr (FORM == EP_W4_INT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[0][n][j] = fmaf(scale, c[j], acc[0][n][j]);
+            } else {
+                acc[0][n] = c;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load_x(begin);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < kManyAhead; ++k) load_w(begin + k, wv[k]);
+    for (int s = begin; s < end; s += kManyAhead) {
+#pragma unroll
+        for (int k = 0; k < kManyAhead; ++k) step(s + k, rows + (k & 1) * NT * 8192, wv[k]);  // past the end: nothing
     }
+    settle(acc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = t0 + n * 16 + q * 4 + j;
+            if (at >= tokens) continue;
+            // The rests count where the values' product is finite.
+            const float v = acc[0][n][j], dot = __builtin_isfinite(v) ? v + acc[0][NT + n][j] : v;
+            const Route r = sh.routes[at];
+            float* sum = sums + (r.id >> 16) * (kManyCols + 1) + wave * 16 + i;
+            *sum = fmaf(r.w, dot, *sum);
+        }
+    __syncthreads();  // the buffers, before the next tokens
+}
+
+template <int FORM, int NT>
+__global__ __launch_bounds__(kThreads, 2) void few4_down_many_kernel(Few4Args a) {
+    __shared__ DownManyShared sh;
+    extern __shared__ u32x4 lds_vectors[];
+    // [64][bytes of a row's scales], two buffers of [2 * NT * 16][256] and [T][65]
+    using Scale = ScaleRow<FORM>;
+    const uint32_t lds = Scale::bytes(a.F);
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(lds_vectors);
+    uint8_t* const rows = scales + kManyCols * kLdsScales2;
+    float* const sums = reinterpret_cast<float*>(rows + NT * 16384);
+    const int tid = threadIdx.x;
+    look_over_ids(a);
+    for (int n = tid; n < a.T * (kManyCols + 1); n += kThreads) sums[n] = 0.f;
+    const int steps = (a.F + kManySpan - 1) / kManySpan, used = a.used[0];
+    const int from = (int)((int64_t)used * steps * blockIdx.y / a.splits);
+    const int to = (int)((int64_t)used * steps * (blockIdx.y + 1) / a.splits);
+    const int h0 = blockIdx.x * kManyCols, vectors = min(kManyCols, a.H - h0) * (int)lds / 16;
+    // An expert's scales and routes, in registers while the one before is worked on.
+    u32x4 scale = {};
+    Route route = {0, 0.f};
+    auto load = [&](int rank) {
+        if (rank * steps >= to) return;
+        const int entry = __builtin_amdgcn_readfirstlane(a.used[1 + rank]);
+        if (tid < vectors)
+            scale = ld16(reinterpret_cast<const uint8_t*>(a.s2) + ((int64_t)(entry & 0xFFFF) * a.H + h0) * lds + tid * 16);
+        if (tid < entry >> 16) route = a.routes[(int64_t)rank * a.T + tid];
+    };
+    int rank = from / steps;
+    load(rank);
+    for (int s = from; s < to; s = ++rank * steps) {
+        const int entry = __builtin_amdgcn_readfirstlane(a.used[1 + rank]), expert = entry & 0xFFFF, tokens = entry >> 16;
+        if (tid < vectors) st16(scales + tid * 16, scale);
+        if (tid < tokens) sh.routes[tid] = route;
+        __syncthreads();
+        load(rank + 1);
+        const int begin = s - rank * steps, end = min(to - rank * steps, steps);
+        for (int t0 = 0; t0 < tokens;) {
+            const int left = tokens - t0;
+            if (NT >= 4 && left > 32)
+                down4_many_tokens<FORM, NT >= 4 ? 4 : 1>(a, sh, scales, rows, sums, expert, tokens, t0, begin, end), t0 += 64;
+            else if (NT >= 2 && left > 16)
+                down4_many_tokens<FORM, NT >= 2 ? 2 : 1>(a, sh, scales, rows, sums, expert, tokens, t0, begin, end), t0 += 32;
+            else
+                down4_many_tokens<FORM, 1>(a, sh, scales, rows, sums, expert, tokens, t0, begin, end), t0 += 16;
+        }
+    }
+    join<kManyCols, 1>(a, sums);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -789,10 +1000,35 @@ int64_t down_units(const ep_shape& s, int F) {
 //   1 token, top-8 of 64, 7168 x 2048 (64)                     53.2 52.1
 int down_tiles(const ep_shape& s, int F) { return s.T <= 32 && down_units(s, F) >= 256 ? 4 : 2; }
 
+// few4_down_many_kernel where an expert has more than four tokens on the average. Both
+// launches without and with it, us:
+//   128 tokens, top-8 of 64 experts of 7168 x 2048 (int)    674  493
+//   128 tokens, top-4 of 32, 4096 x 1536 (e2m1)             154  111
+//   128 tokens, top-8 of 64, 2048 x 768 (int)               92.8 83.2
+//   64 tokens, top-6 of 13, 384 x 512 (int)                 34.5 29.0
+//   48 tokens, top-4 of 32, 4096 x 2048 (e2m1)              143  138
+//   100 tokens, top-8 of 10, 512 x 1024 (e2m1)              46.0 46.4
+//   64 tokens, top-2 of 16, 2048 x 1024 (e2m1)              34.7 35.1
+//   32 tokens, top-8 of 64, 7168 x 2048 (e2m1)              337  402
+//   16 tokens, top-4 of 16, 2048 x 1024 (int)               29.6 30.7
+bool down_many(const ep_shape& s, int F, int form) {
+    const uint32_t row = form == EP_W4_INT ? ScaleRow<EP_W4_INT>::bytes(F) : ScaleRow<EP_W4_E2M1>::bytes(F);
+    return row <= kLdsScales2 && (int64_t)s.T * s.K > 4 * std::min<int64_t>(s.E, (int64_t)s.T * s.K);
+}
+
 // Workgroups of the second launch for the same values of h: as many as fill the chip
-// (512; 256 and 384 were 0 to 20% slower in the cases above, 1,024 4 to 20%), with a
-// unit for every wave.
-int down_splits(const ep_shape& s, int F) {
+// (512; 256 were 0 to 20% slower, 1,024 4 to 20%), with a unit for every wave. Of
+// few4_down_many_kernel: eight steps to each, or four while there are fewer than 256.
+// us with four always, and with eight: 70.1 57.4 (128 tokens, top-4 of 8 experts of 2048 x
+// 1024), 47.9 43.2 (128, top-2 of 8, 4096 x 512); 44.7 51.3 (128, top-2 of 4, 1024 x 1024),
+// 33.0 38.9 (64, top-6 of 13, 384 x 512).
+int down_splits(const ep_shape& s, int F, int form) {
+    if (down_many(s, F, form)) {
+        const int64_t cols = (s.H + kManyCols - 1) / kManyCols;
+        const int64_t steps = std::min<int64_t>(s.E, (int64_t)s.T * s.K) * ((F + kManySpan - 1) / kManySpan);
+        const int64_t eight = std::min(kDownGroups / cols, steps / 8), four = std::min(kDownGroups / 2 / cols, steps / 4);
+        return (int)std::max<int64_t>({1, eight, four});
+    }
     const int64_t width = 16 * down_tiles(s, F), cols = (s.H + width - 1) / width;
     return (int)std::max<int64_t>(1, std::min(kDownGroups / std::max<int64_t>(cols, 1), down_units(s, F) / kWaves));
 }
@@ -818,27 +1054,33 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const bool lds_scales = row <= kLdsScales;
     // Experts of many tokens: few4_up_many_kernel, if there are workgroups for most CUs.
     // Both launches without and with it, us (form; workgroups it has):
-    //   128 tokens, top-8 of 64 experts of 2048 x 768 (int, 768)   133  102
-    //   100 tokens, top-8 of 10, 512 x 1024 (e2m1, 160)            71.4 57.1
-    //   128 tokens, top-1 of 8, 2048 x 2048 (int, 256)             62.8 59.0
-    //   48 tokens, top-8 of 64, 7168 x 2048 (int, 2048)            458  424
-    //   48 tokens, top-4 of 32, 4096 x 2048 (e2m1, 1024)           141  146
-    //   64 tokens, top-2 of 8, 2048 x 1024 (int, 128)              36.2 40.2
-    //   128 tokens, top-4 of 8, 2048 x 512 (int, 64)               54.7 73.4
-    //   32 tokens, top-8 of 64, 7168 x 2048 (e2m1, 2048)           347  372
-    //   16 tokens, top-8 of 64, 7168 x 512 (e2m1, 512)             91.5 94.0
+    //   128 tokens, top-8 of 64 experts of 7168 x 2048 (int, 2048) 633  495
+    //   128 tokens, top-8 of 64, 2048 x 768 (int, 768)             114  83.2
+    //   48 tokens, top-8 of 64, 7168 x 2048 (int, 2048)            455  416
+    //   48 tokens, top-4 of 32, 4096 x 2048 (e2m1, 1024)           136  138
+    //   100 tokens, top-8 of 10, 512 x 1024 (e2m1, 160)            61.2 46.4
+    //   128 tokens, top-1 of 8, 2048 x 2048 (int, 256)             50.9 49.2
+    //   64 tokens, top-6 of 13, 384 x 512 (int, 104)               33.0 29.0
+    //   128 tokens, top-4 of 8, 2048 x 1024 (e2m1, 128)            57.3 54.2
+    //   64 tokens, top-2 of 8, 2048 x 1024 (int, 128)              30.3 33.2
+    //   128 tokens, top-4 of 8, 2048 x 512 (int, 64)               46.5 58.4
+    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1, 256)            43.3 49.8
+    //   24 tokens, top-8 of 64, 2048 x 768 (int, 768)              60.7 51.1
+    //   32 tokens, top-8 of 64, 7168 x 2048 (e2m1, 2048)           337  355
     const int64_t groups64 = (a.F + kManyCols - 1) / kManyCols * experts;
-    const bool many = lds_scales && (lanes > 8 * experts ? groups64 >= 160 : lanes > 4 * experts && groups64 >= 512);
+    const bool many = lds_scales && (lanes > 20 * experts  ? groups64 >= 96
+                                     : lanes > 8 * experts ? groups64 >= 160
+                                                           : lanes > 4 * experts && groups64 >= 512);
     // 16 or 32 values of f to a workgroup: 32 read the tokens half as often, 16 have more
     // waves to hide a step's latency. us with 16 and with 32 (form):
     //   1 token, top-8 of 64 experts of 7168 x 2048 (e2m1)    48.0 49.3
     //   2 tokens, top-6 of 64, 5120 x 1536 (int)              44.5 52.0
-    //   8 tokens, top-4 of 64, 4096 x 1024 (int)              48.0 50.7
-    //   16 tokens, top-4 of 16, 2048 x 1024 (int, e2m1)       30.2 28.3, 26.4 27.1
-    //   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1)       350 354, 338 347
-    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1)            46.5 43.3
-    //   64 tokens, top-2 of 16, 2048 x 1024 (int, e2m1)       43.2 39.9, 41.6 38.9
-    //   32 tokens, top-2 of 8, 1024 x 512 (int)               18.5 20.1
+    //   8 tokens, top-4 of 64, 4096 x 1024 (int)              48.2 51.1
+    //   16 tokens, top-4 of 16, 2048 x 1024 (int, e2m1)       29.4 27.5, 25.8 26.5
+    //   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1)       351 353, 337 346
+    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1)            46.2 43.2
+    //   64 tokens, top-2 of 16, 2048 x 1024 (int, e2m1)       39.1 35.8, 37.9 35.1
+    //   32 tokens, top-2 of 8, 1024 x 512 (int)               17.5 19.1
     const bool narrow = !lds_scales || lanes <= 4 * experts || (int64_t)((a.F + 31) / 32) * experts < 512;
     const int cols = many ? kManyCols : narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
@@ -848,9 +1090,9 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     // tokens, top-8 of 64, 7168 x 2048).
     const int tt = s.T <= 2 ? 2 : s.T <= 4 ? 4 : s.T <= 8 || lanes <= 4 * experts ? 8 : 16;
     // Tiles of 16 tokens that few4_up_many_kernel multiplies at a time, at most: what fits
-    // the registers decides how many waves there are. us with 2, this and 8: 102 102 138
-    // (128 tokens, top-8 of 64, 2048 x 768), 424 424 609 (48 tokens, top-8 of 64, 7168 x
-    // 2048), 61.1 57.1 57.1 (100 tokens, top-8 of 10), 88.2 74.3 74.3 (128 tokens, top-4
+    // the registers decides how many waves there are. us with 2, this and 8: 83.2 83.2 106
+    // (128 tokens, top-8 of 64, 2048 x 768), 417 416 532 (48 tokens, top-8 of 64, 7168 x
+    // 2048), 49.0 46.4 46.4 (100 tokens, top-8 of 10), 63.2 54.2 54.2 (128 tokens, top-4
     // of 8, 2048 x 1024).
     const int tiles1 = s.T <= 32 || lanes <= 20 * experts ? 2 : s.T <= 64 || lanes <= 48 * experts ? 4 : 8;
     const Kernel first = !lds_scales ? few4_up_kernel<FORM, 2, 16, false>
@@ -861,6 +1103,16 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const size_t area = many ? 8192 * tiles1
                              : std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (lds_scales ? tt : 16));
     hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);
+    if (down_many(s, a.F, FORM)) {
+        // As tiles1. us with 2, this and 4: 83.1 83.2 103, 417 416 576, 47.9 46.4 46.4 and
+        // 56.9 54.2 54.2 in the cases above.
+        const int most = s.T <= 32 || lanes <= 20 * experts ? 2 : 4;
+        const dim3 grid((s.H + kManyCols - 1) / kManyCols, (unsigned)a.splits);
+        const size_t lds = kManyCols * kLdsScales2 + 16384 * most + sizeof(float) * (kManyCols + 1) * s.T;
+        hipLaunchKernelGGL((most == 4 ? few4_down_many_kernel<FORM, 4> : few4_down_many_kernel<FORM, 2>), grid,
+                           dim3(kThreads), lds, st, a);
+        return;
+    }
     const int tiles = down_tiles(s, a.F);
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
     const uint32_t row2 = ScaleRow<FORM>::bytes(a.F);
@@ -886,7 +1138,7 @@ WsFew ws_few_w4(const ep_shape& s, int F) {
     w.act = w.routes + align256(sizeof(Route) * used * s.T);
     w.joined = w.act + align256(4 * lanes * F);
     w.part = w.joined + align256(4 * (((size_t)s.H + 15) / 16));
-    const size_t splits = down_splits(s, F);
+    const size_t splits = std::max(down_splits(s, F, EP_W4_INT), down_splits(s, F, EP_W4_E2M1));
     w.total = w.part + (splits > 1 ? align256(4 * splits * s.T * s.H) : 0);
     return w;
 }
@@ -903,7 +1155,7 @@ hipError_t launch_moe_few_w4(const ep_shape& s, const ep_tokens& tk, const ep_ex
                         static_cast<const char*>(x.w13_scales), x.w2, static_cast<const char*>(x.w2_scales), out, err,
                         reinterpret_cast<int*>(ws + l.used), reinterpret_cast<Route*>(ws + l.routes),
                         reinterpret_cast<uint16_t*>(ws + l.act), reinterpret_cast<int*>(ws + l.joined),
-                        reinterpret_cast<float*>(ws + l.part), down_splits(s, x.F)};
+                        reinterpret_cast<float*>(ws + l.part), down_splits(s, x.F, x.form)};
     if (x.form == EP_W4_INT)
         launch<EP_W4_INT>(a, s, st);
     else

@@ -212,6 +212,31 @@ def test_few_w4_keeps_nonfinite_values_with_their_tokens(form):
     assert torch.isnan(out[3]).all() and torch.isnan(out[4]).all() and torch.isnan(out[1]).all()
 
 
+@FORMS
+@pytest.mark.parametrize("F", [256, 2560])
+def test_few_w4_keeps_nonfinite_values_among_many_tokens(form, F):
+    """The same where an expert's tokens are multiplied in tiles of 16 and more."""
+    copies, H, E, K = 16, 128, 4, 2
+    g = torch.Generator().manual_seed(22)
+    T = 6 * copies
+    x, w13, w2 = randn(g, T, H), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    idx = torch.tensor([[0, 1], [1, 2], [-1, -1], [3, 0], [0, 99], [-7, 1]]).repeat(copies, 1)
+    w = torch.full((T, K), 0.5)
+    clean = torch.where((idx < 0) | (idx >= E), -1, idx)
+    ref, bound = few_reference(x, w13, w2, clean, w, F, form)
+    bad13, bad2, badx = (w13[0], w13[1].clone()), (w2[0], w2[1].clone()), x.clone()
+    bad13[1][2, 3, 0] = float("nan") if form == INT else 255
+    bad2[1][3] = float("nan") if form == INT else 255
+    badx[4::6] = float("nan")
+    out, ws = few_call(badx, idx, w, experts(bad13, bad2, F, form), E)
+    assert ep.ep_check_errors(ws) == ep.EP_DEVERR_EXPERT_ID
+    for t in (0, 2, 5):
+        check(out[t::6], ref[t::6], bound[t::6], f"tokens {t}, {t + 6}, ...")
+    assert (out[2::6] == 0).all()
+    for t in (1, 3, 4):
+        assert torch.isnan(out[t::6]).all()
+
+
 @pytest.mark.parametrize("H,F", [(128, 128), (640, 384), (256, 1152)])
 def test_few_w4_keeps_the_sign_of_infinite_scales(H, F):
     """An infinite scale of the second matrix makes an infinity of its block's sum's sign (sums far
