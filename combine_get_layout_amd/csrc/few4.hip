@@ -11,14 +11,16 @@
 // What has to move is the used experts' weights once, 1.5 F H bytes each and a 32nd (int)
 // or 16th (e2m1) of that in scales; products are few (32 tokens, top-8 of 64 experts
 // of 7168 x 2048: 22 GFLOP for 1.48 GB). Medians on inputs that the caches do not hold:
-//   1 token, top-8 of 64 experts of 7168 x 2048, int   28.5 + 21.0 us, 182 MB: 3.7 TB/s
-//   32 tokens, the same, e2m1                          202 + 131 us, 1.48 GB: 4.4 TB/s
-//   13 tokens, top-3 of 40, 2080 x 736, e2m1           15.4 + 13.7 us, 60 MB: 2.1 TB/s
-//   1 token, top-2 of 16, 256 x 512, int               5.5 + 5.1 us: two launches' latency
+//   1 token, top-8 of 64 experts of 7168 x 2048, int   28.5 + 21.1 us, 182 MB: 3.7 TB/s
+//   32 tokens, the same, e2m1                          203 + 131 us, 1.48 GB: 4.4 TB/s
+//   13 tokens, top-3 of 40, 2080 x 736, e2m1           14.9 + 12.1 us, 58 MB: 2.2 TB/s
+//   1 token, top-2 of 16, 256 x 512, int               5.6 + 5.1 us: two launches' latency
 // The first launch of 32 tokens reads at 4.9 TB/s, as a copy does; the second is bound by
 // latency: a wave waits for one unit of 256 values' fragments behind another, with the
 // activations' (as many loads as the weights') between them. One token's launches end
-// before the memory has come up to its rate.
+// before the memory has come up to its rate. With many tokens to an expert both launches
+// have a form whose workgroups hold the tokens' rows in LDS for four waves of different
+// weights: 128 tokens, top-8 of 64 experts of 7168 x 2048, int, 493 us a call.
 #include <algorithm>
 
 #include "ep_internal.h"
