@@ -1019,7 +1019,9 @@ bool down_many(const ep_shape& s, int F, int form) {
 }
 
 // Workgroups of the second launch for the same values of h: as many as fill the chip
-// (512; 256 were 0 to 20% slower, 1,024 4 to 20%), with a unit for every wave. Of
+// (512; with 384, 768 and 1,024 49.9 us became 54.7, 49.6, 52.0 for 1 token, top-8 of 64
+// experts of 7168 x 2048, int; 337 368, 346, 333 for 32 tokens, e2m1; 82.8 95.1, 85.0, 88.1
+// for 16 tokens, 7168 x 512), with a unit for every wave. Of
 // few4_down_many_kernel: eight steps to each, or four while there are fewer than 256.
 // us with four always, and with eight: 70.1 57.4 (128 tokens, top-4 of 8 experts of 2048 x
 // 1024), 47.9 43.2 (128, top-2 of 8, 4096 x 512); 44.7 51.3 (128, top-2 of 4, 1024 x 1024),
