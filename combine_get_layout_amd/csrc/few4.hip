@@ -1042,13 +1042,26 @@ template <int FORM, int RT, int CAP>
 Kernel down_kernel(bool lds) {
     return lds ? few4_down_kernel<FORM, RT, CAP, true> : few4_down_kernel<FORM, RT, CAP, false>;
 }
+// An instance of few4_up_kernel and the tokens (TT) that it takes at a time, by which the
+// launch sizes its LDS.
+struct UpForm {
+    Kernel kernel;
+    int tokens;
+};
+template <int FORM, int RT, int TT, bool LDS>
+UpForm up_form() {
+    return {few4_up_kernel<FORM, RT, TT, LDS>, TT};
+}
+// The smallest instance for `tokens` at a time. Few tokens take the wide form too, where
+// their lanes repeat experts.
 template <int FORM>
-Kernel up_kernel(int tt, bool narrow) {
-    if (!narrow) return tt == 8 ? few4_up_kernel<FORM, 4, 8, true> : few4_up_kernel<FORM, 4, 16, true>;
-    return tt == 2   ? few4_up_kernel<FORM, 2, 2, true>
-           : tt == 4 ? few4_up_kernel<FORM, 2, 4, true>
-           : tt == 8 ? few4_up_kernel<FORM, 2, 8, true>
-                     : few4_up_kernel<FORM, 2, 16, true>;
+UpForm up_form(int tokens, bool narrow, bool lds_scales) {
+    if (!lds_scales) return up_form<FORM, 2, 16, false>();
+    if (!narrow) return tokens <= 8 ? up_form<FORM, 4, 8, true>() : up_form<FORM, 4, 16, true>();
+    return tokens <= 2   ? up_form<FORM, 2, 2, true>()
+           : tokens <= 4 ? up_form<FORM, 2, 4, true>()
+           : tokens <= 8 ? up_form<FORM, 2, 8, true>()
+                         : up_form<FORM, 2, 16, true>();
 }
 
 template <int FORM>
@@ -1099,13 +1112,12 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     // 2048), 49.0 46.4 46.4 (100 tokens, top-8 of 10), 63.2 54.2 54.2 (128 tokens, top-4
     // of 8, 2048 x 1024).
     const int tiles1 = s.T <= 32 || lanes <= 20 * experts ? 2 : s.T <= 64 || lanes <= 48 * experts ? 4 : 8;
-    const Kernel first = !lds_scales ? few4_up_kernel<FORM, 2, 16, false>
-                         : many      ? (tiles1 == 8   ? few4_up_many_kernel<FORM, 8>
-                                        : tiles1 == 4 ? few4_up_many_kernel<FORM, 4>
-                                                      : few4_up_many_kernel<FORM, 2>)
-                                     : up_kernel<FORM>(tt, narrow);  // wide: more than 4 tokens
-    const size_t area = many ? 8192 * tiles1
-                             : std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * (lds_scales ? tt : 16));
+    const UpForm form = up_form<FORM>(tt, narrow, lds_scales);
+    const Kernel first = !many         ? form.kernel
+                         : tiles1 == 8 ? few4_up_many_kernel<FORM, 8>
+                         : tiles1 == 4 ? few4_up_many_kernel<FORM, 4>
+                                       : few4_up_many_kernel<FORM, 2>;
+    const size_t area = many ? 8192 * tiles1 : std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * form.tokens);
     hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);
     if (down_many(s, a.F, FORM)) {
         // As tiles1. us with 2, this and 4: 83.1 83.2 103, 417 416 576, 47.9 46.4 46.4 and

@@ -300,6 +300,16 @@ def test_few_w4_many_tokens_an_expert(case, form):
 
 
 @FORMS
+@pytest.mark.parametrize("case", [(1, 512, 16384, 1, 5, dict(repeat=True)), (2, 1056, 8224, 2, 5, dict(repeat=True)),
+                                  (3, 1312, 5472, 3, 6, dict(repeat=True)), (4, 1024, 4096, 4, 8, dict(repeat=True)),
+                                  (4, 512, 8192, 4, 8, dict(repeat=True)), (1, 256, 6144, 1, 64, dict(repeat=True))], ids=str)
+def test_few_w4_of_few_tokens_whose_lanes_repeat_experts(case, form):
+    """One to four tokens with more than four lanes an expert, which take the first launch's forms of 32 and
+    64 values of f to a workgroup; rows of one to three steps a wave, F that fills no tile of 32."""
+    test_few_w4(case, form)
+
+
+@FORMS
 def test_few_w4_many_tokens_of_the_longest_rows_in_lds(form):
     """Scales of 512 bytes a row in LDS, beside 128 tokens' rows."""
     T, H, F, E, K = 128, 16384 if form == E2M1 else 32768, 128, 80, 40
