@@ -310,6 +310,26 @@ def test_few_w4_of_few_tokens_whose_lanes_repeat_experts(case, form):
 
 
 @FORMS
+@pytest.mark.parametrize("case", [(8, 256, 2080, 8, 5, {}), (7, 2336, 3296, 5, 4, {}), (64, 256, 1024, 16, 2, {}),
+                                  (20, 256, 1056, 16, 4, {}), (24, 1312, 864, 20, 6, dict(skip=0.1)),
+                                  (24, 1312, 864, 20, 7, {}), (40, 544, 672, 25, 5, dict(repeat=True))], ids=str)
+def test_few_w4_32_columns_a_workgroup(case, form):
+    """Four to eight lanes an expert, for 8 and for 16 tokens at a time: the first launch's form of 32 values
+    of f to a workgroup, tiles that F fills in part, rows of one to three steps a wave; and, with the last but
+    one, the form for many tokens beside it."""
+    test_few_w4(case, form)
+
+
+@FORMS
+@pytest.mark.parametrize("case", [(32, 160, 2048, 33, 4, {}), (32, 160, 4192, 16, 4, {}), (9, 224, 2336, 30, 4, dict(skip=0.1)),
+                                  (2, 96, 2048, 128, 64, {}), (1, 544, 4192, 40, 16, {})], ids=str)
+def test_few_w4_64_columns_of_the_second_launch(case, form):
+    """256 units of 256 values of f and more: the second launch's form of 64 outputs to a workgroup, which H
+    fills in part, with scales in LDS and from memory."""
+    test_few_w4(case, form)
+
+
+@FORMS
 def test_few_w4_many_tokens_of_the_longest_rows_in_lds(form):
     """Scales of 512 bytes a row in LDS, beside 128 tokens' rows."""
     T, H, F, E, K = 128, 16384 if form == E2M1 else 32768, 128, 80, 40
