@@ -60,12 +60,24 @@ struct Few4Args {
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
+// What sums of products with codes are in units of: of EP_W4_INT, whose scales come after
+// the sums of 128 columns, 2^-10, so that 128 products of |code - 8| <= 8 with the largest
+// finite values stay finite whatever the scale makes of them.
+template <int FORM>
+constexpr float kUnit = FORM == EP_W4_INT ? 1024.0f : 1.0f;
+
 // Eight codes (a byte holds two, the first in its low half) to bf16, exactly.
 // EP_W4_E2M1: the instruction's own conversion, times a power of two.
-// EP_W4_INT: code c as the e4m3 byte c, which stands for c * 2^-9 (codes below 8
-// as e4m3's denormals, the others as its first binade), times 2^9; the 8 that
-// codes stand above their values is taken off the products (`minus_eight`).
-template <int FORM>
+// EP_W4_INT: code - 8 as the e4m3 byte of its sign and magnitude m, which stands for
+// m * 2^-9 (below 8 as e4m3's denormals, 8 as the first number above them), times 2^-1.
+// Signs and magnitudes of all eight at once: where bit 3 is clear (`less`, one in each
+// four bits) the magnitude is 8 - code = ((code & 7) ^ 7) + 1, else code & 7. With SPLIT
+// the even columns come first, then the odd ones, as the other operand then lies too
+// (`split8`): two instructions less of 15. Codes as they are, in nine, and 8 times the
+// other operand taken off the products by one more matrix instruction for every four, made
+// infinities of finite values and NaN of infinite ones, and took (us, that and this) 50.1
+// 50.0 (1 token, top-8 of 64 experts of 7168 x 2048), 351 359 (32 tokens), 495 476 (128).
+template <int FORM, bool SPLIT>
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, float scale) {
     bf16x2 a, b, c, d;
     if constexpr (FORM == EP_W4_E2M1) {
@@ -74,17 +86,37 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, float scale) {
         c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
         d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
     } else {
-        const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
-        const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
-        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+        uint32_t sign = ~w & 0x88888888u;
+        asm("" : "+v"(sign));  // knowing its bits the compiler makes 17 instructions of 13
+        const uint32_t less = sign >> 3, seven = sign - less;
+        uint32_t mag = ((w & 0x77777777u) ^ seven) + less;
+        asm("" : "+v"(mag));
+        const uint32_t even = (mag & 0x0F0F0F0Fu) | ((sign << 4) & 0xF0F0F0F0u);
+        const uint32_t odd = ((mag >> 4) & 0x0F0F0F0Fu) | (sign & 0xF0F0F0F0u);
+        const uint32_t lo = SPLIT ? even : __builtin_amdgcn_perm(odd, even, 0x05010400u);
+        const uint32_t hi = SPLIT ? odd : __builtin_amdgcn_perm(odd, even, 0x07030602u);
+        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 0.5f, false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 0.5f, true);
+        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 0.5f, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 0.5f, true);
     }
     bf16x8 r;
     r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1];
     r[4] = c[0], r[5] = c[1], r[6] = d[0], r[7] = d[1];
     return r;
+}
+
+// Eight bf16 values of an operand beside codes in SPLIT order; where column c of a row lies
+// in that order.
+template <int FORM>
+__device__ __forceinline__ u32x4 split8(u32x4 v) {
+    if constexpr (FORM != EP_W4_INT) return v;
+    return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
+                 __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
+}
+template <int FORM>
+__device__ __forceinline__ int split_place(int c) {
+    return FORM == EP_W4_INT ? (c & ~7) | (c & 1) << 2 | (c & 7) >> 1 : c;
 }
 
 // Scales: of a row's blocks of 128 columns a bf16 each, or a byte for 32 of them.
@@ -177,9 +209,6 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
     const char* sc = a.s13 + ((int64_t)found.expert * 2 * a.F + f0) * lds;
     const auto s_gate = buf_resource(sc, cols * lds), s_up = buf_resource(sc + (int64_t)a.F * lds, cols * lds);
     const int steps = (a.H + kSpan - 1) / kSpan;
-    bf16x8 minus_eight;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
 
     for (int t0 = 0; t0 < found.tokens; t0 += TT) {
         // A step's values of a token are 512 bytes in a row: half a wave's load. (As the
@@ -212,19 +241,14 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
         };
         auto multiply = [&](const Stage& g, int s) {
 #pragma unroll
-            for (int n = 0; n < kLoads; ++n) st16(xs + row_chunk(2 * n + (lane >> 5), lane & 31), g.x[n]);
+            for (int n = 0; n < kLoads; ++n) st16(xs + row_chunk(2 * n + (lane >> 5), lane & 31), split8<FORM>(g.x[n]));
             wave_lds_order();
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 bf16x8 xf[4];
-                f32x4 base = {};
 #pragma unroll
                 for (int m = 0; m < 4; ++m)  // rows past TT: earlier ones again, of which nothing is kept
                     xf[m] = as_bf16(ld16(xs + row_chunk(i & (TT - 1), p * 16 + q * 4 + m)));
-                if constexpr (FORM == EP_W4_INT) {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) base = mfma_bf16(xf[m], minus_eight, base);
-                }
                 const bool in = s * kSpan + p * 128 + q * 32 < a.H;  // else codes of 0, and no scale
                 const uint32_t at = in ? s * Scale::kStep + Scale::offset(p, q) : 0u;
 #pragma unroll
@@ -237,8 +261,9 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                     const float scale = Scale::value(bits);
                     bf16x8 wf[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(g.w[r][p][m], scale);
-                    f32x4 c = FORM == EP_W4_INT ? base : acc[r][0];
+                    for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM, true>(g.w[r][p][m], scale);
+                    f32x4 c = {};
+                    if constexpr (FORM != EP_W4_INT) c = acc[r][0];
 #pragma unroll
                     for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], wf[m], c);
                     if constexpr (FORM == EP_W4_INT) {
@@ -314,7 +339,8 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
                     gate += part[v][c >> 4][tk][c & 15];
                     up += part[v][2 + (c >> 4)][tk][c & 15];
                 }
-                store_act(a.act + (int64_t)find.row[at] * 2 * a.F + f, a.F, gate, up);
+                store_act(a.act + (int64_t)find.row[at] * 2 * a.F + split_place<FORM>(f), a.F, gate * kUnit<FORM>,
+                          up * kUnit<FORM>);
             }
             __syncthreads();
         }
@@ -369,9 +395,6 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
         const int at = t0 + n * 16 + (tid >> 4);
         xr[n] = at < found.tokens ? (uint32_t)find.token[at] * a.H * 2 + (tid & 15) * 16 : kBufNone;
     }
-    bf16x8 minus_eight;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
     f32x4 acc[2][NT] = {};
     u32x4 xv[NT], wv[kManyAhead][2];
     auto load_x = [&](int s) {
@@ -398,7 +421,7 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
             asm volatile("" : "+v"(bits));  // read in any case, without a branch
             scale[g] = Scale::value(in ? bits : 0u);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) wf[g][m] = codes_to_bf16<FORM>(v[g][m], scale[g]);
+            for (int m = 0; m < 4; ++m) wf[g][m] = codes_to_bf16<FORM, false>(v[g][m], scale[g]);
         }
         __builtin_amdgcn_sched_barrier(0);
         load_x(s + 1);
@@ -417,14 +440,10 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
             if (n + 1 < NT) read(n + 1);
             __builtin_amdgcn_sched_barrier(0);
             const bf16x8(&xf)[4] = tile[n & 1];
-            f32x4 base = {};
-            if constexpr (FORM == EP_W4_INT) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) base = mfma_bf16(xf[m], minus_eight, base);
-            }
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                f32x4 c = FORM == EP_W4_INT ? base : acc[g][n];
+                f32x4 c = {};
+                if constexpr (FORM != EP_W4_INT) c = acc[g][n];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], wf[g][m], c);
                 if constexpr (FORM == EP_W4_INT) {
@@ -452,7 +471,8 @@ __device__ __forceinline__ void up4_many_tokens(const Few4Args& a, const Found& 
         for (int j = 0; j < 4; ++j) {
             const int at = t0 + n * 16 + q * 4 + j;
             if (at < found.tokens && i < cols)
-                store_act(a.act + (int64_t)find.row[at] * 2 * a.F + f0 + i, a.F, acc[0][n][j], acc[1][n][j]);
+                store_act(a.act + (int64_t)find.row[at] * 2 * a.F + split_place<FORM>(f0 + i), a.F,
+                          acc[0][n][j] * kUnit<FORM>, acc[1][n][j] * kUnit<FORM>);
         }
     __syncthreads();  // the buffers, before the next tokens
 }
@@ -611,9 +631,6 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     const int units = used * spans;
     float* mine = sums + wave * a.T * kLd;
     for (int n = lane; n < a.T * kLd; n += kWave) mine[n] = 0.f;
-    bf16x8 minus_eight;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
 
     const uint32_t ld = (uint32_t)a.F / 2;
     const uint32_t w_off = i * ld + q * 16, w_bytes = (uint32_t)cols * ld;
@@ -722,15 +739,6 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
             for (int m = 0; m < 8; ++m) v[m] = as_bf16(g.act[m]);
         }
         f32x4 c[RT][2] = {};
-        if constexpr (FORM == EP_W4_INT) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) c[0][p] = mfma_bf16(v[p * 4 + m], minus_eight, c[0][p]);
-#pragma unroll
-                for (int r = 1; r < RT; ++r) c[r][p] = c[0][p];
-            }
-        }
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -738,7 +746,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     c[r][p] = mfma_bf16(v[p * 4 + m],
-                                        codes_to_bf16<FORM>(g.w[r][p][m], Scale::value(bits[r][p])), c[r][p]);
+                                        codes_to_bf16<FORM, true>(g.w[r][p][m], Scale::value(bits[r][p])), c[r][p]);
         settle(c);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -762,7 +770,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
                 acc[r][j] = 0.f;
                 if (q < 2 && q * 4 + j < kTokens && t0 + q * 4 + j < tokens) {
                     float* sum = mine + (id >> 16) * kLd + r * 16 + i;
-                    *sum = fmaf(weight, dot, *sum);
+                    *sum = fmaf(weight, dot * kUnit<FORM>, *sum);
                 }
             }
         }
@@ -854,9 +862,6 @@ __device__ __forceinline__ void down4_many_tokens(const Few4Args& a, const DownM
         xr[n] = at < tokens ? row * 4u * a.F + (tid & 15) * 16 : kBufFar;
         xr[NT + n] = at < tokens ? row * 4u * a.F + 2u * a.F + (tid & 15) * 16 : kBufFar;
     }
-    bf16x8 minus_eight;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) minus_eight[j] = (__bf16)-8.0f;
     f32x4 acc[1][2 * NT] = {};
     u32x4 xv[2 * NT], wv[kManyAhead];
     auto load_x = [&](int s) {
@@ -879,7 +884,7 @@ __device__ __forceinline__ void down4_many_tokens(const Few4Args& a, const DownM
         const float scale = Scale::value(in ? bits : 0u);
         bf16x8 wf[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM>(v[m], scale);
+        for (int m = 0; m < 4; ++m) wf[m] = codes_to_bf16<FORM, true>(v[m], scale);
         __builtin_amdgcn_sched_barrier(0);
         load_x(s + 1);
         load_w(s + kManyAhead, v);
@@ -896,12 +901,7 @@ __device__ __forceinline__ void down4_many_tokens(const Few4Args& a, const DownM
             __builtin_amdgcn_sched_barrier(0);
             const bf16x8(&xf)[4] = tile[n & 1];
             f32x4 c = {};
-            if constexpr (FORM == EP_W4_INT) {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], minus_eight, c);
-            } else {
-                c = acc[0][n];
-            }
+            if constexpr (FORM != EP_W4_INT) c = acc[0][n];
 #pragma unroll
             for (int m = 0; m < 4; ++m) c = mfma_bf16(xf[m], wf[m], c);
             if constexpr (FORM == EP_W4_INT) {
@@ -932,7 +932,7 @@ __device__ __forceinline__ void down4_many_tokens(const Few4Args& a, const DownM
             const float v = acc[0][n][j], dot = __builtin_isfinite(v) ? v + acc[0][NT + n][j] : v;
             const Route r = sh.routes[at];
             float* sum = sums + (r.id >> 16) * (kManyCols + 1) + wave * 16 + i;
-            *sum = fmaf(r.w, dot, *sum);
+            *sum = fmaf(r.w, dot * kUnit<FORM>, *sum);
         }
     __syncthreads();  // the buffers, before the next tokens
 }

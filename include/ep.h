@@ -694,9 +694,8 @@ size_t ep_few_w4_workspace_bytes(const ep_shape *shape, int32_t F);
  * scales stand for (these are exact in the products, sums are held in 32
  * bits), the same tokens, errors, workspace rules and limits, and T * K * F <
  * 2^29. Longer batches go in parts of EP_FEW_MAX_TOKENS. Base pointers 16 B
- * aligned. EP_W4_INT sums x * code and takes 8 * x off before the scale: an
- * infinite x makes NaN of its token's outputs. EP_W4_E2M1 values past bf16's
- * range (scale bytes of 253 and 254) are infinite. */
+ * aligned. EP_W4_E2M1 values past bf16's range (scale bytes of 253 and 254)
+ * are infinite. */
 int ep_moe_few_w4(const ep_shape *shape, const ep_tokens *tokens, const ep_experts_w4 *experts,
                   uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 

@@ -3,8 +3,8 @@ arithmetic on the values that codes and scales stand for, and the layers that
 the norm, the router and the expert operators make together.
 
 Tolerances as in test_experts_gpu.py: a sum of n products in 32 bits is off by
-at most n * 2^-23 of the sum of their magnitudes. EP_W4_INT sums x * code and
-takes 8 * x off, so the magnitudes there are x * (code + 8) * scale.
+at most n * 2^-23 of the sum of their magnitudes. EP_W4_INT's magnitudes are taken
+as x * (code + 8) * scale, which is more than the x * |code - 8| * scale that it sums.
 """
 import pytest
 import torch
@@ -260,6 +260,108 @@ def test_few_w4_keeps_the_sign_of_infinite_scales(H, F):
     keep = [h for h in range(H) if h not in (3, 7)]
     ref, bound = few_reference(x, w13, finite, idx, w, F, INT)
     check(out[:, keep], ref[:, keep], bound[:, keep], "other outputs")
+
+
+def by_power(m, form, rows=slice(None), power=0):
+    """(codes, scales) with the scales of some rows times 2^power, exactly."""
+    sc = m[1].clone()
+    sc[:, rows] = (sc[:, rows].double() * 2.0 ** power).to(BF16) if form == INT else (sc[:, rows].int() + power).to(U8)
+    return m[0], sc
+
+
+def set_codes(code, e, rows, cols, values):
+    """The codes of some rows and columns of expert e."""
+    full = torch.stack([code[e] & 15, code[e] >> 4], -1).flatten(-2)
+    full[rows, cols] = torch.as_tensor(values, dtype=U8)
+    code[e] = full[:, 0::2] | full[:, 1::2] << 4
+
+
+# (T, F, E, K): each launch's forms for one token, for few and for many tokens an expert.
+EXTREME = [(1, 256, 1, 1), (5, 384, 2, 1), (64, 1024, 16, 2), (96, 256, 1, 1), (128, 256, 24, 5)]
+
+
+def extreme_values(case, form):
+    T, F, E, K = case
+    H = 256
+    g = torch.Generator().manual_seed(31)
+    x, w13, w2 = randn(g, T, H), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    idx, w = routing(T, K, E, 17)
+    up, most = slice(F, None), 122 if form == INT else 119
+    return idx, w, dict(inputs=(x * 2.0 ** 124, by_power(w13, form, power=-116), w2),
+                        inner=(x, by_power(w13, form, up, most), by_power(w2, form, power=-114)),
+                        small=(x * 2.0 ** -104, by_power(w13, form, power=100), w2))
+
+
+@FORMS
+@pytest.mark.parametrize("case", EXTREME, ids=str)
+def test_few_w4_of_large_and_small_finite_values(case, form):
+    """Inputs, then inner values, close to bf16's largest (sums of eight of them pass 32 bits), and inputs of
+    2^-104, whose scales bring the results back to common sizes: the same bounds as for common inputs."""
+    F, E = case[1:3]
+    idx, w, cases = extreme_values(case, form)
+    for name, (x, w13, w2) in cases.items():
+        assert torch.isfinite(x).all()
+        ref, bound = few_reference(x, w13, w2, idx, w, F, form)
+        out, ws = few_call(x, idx, w, experts(w13, w2, F, form), E)
+        assert ep.ep_check_errors(ws) == 0
+        check(out, ref, bound, name)
+
+
+@FORMS
+@pytest.mark.parametrize("case", EXTREME, ids=str)
+def test_few_w4_keeps_the_sign_of_infinite_inputs(case, form):
+    """An infinite input makes infinite inner values, and outputs of the sign that the values give; tokens
+    of finite inputs keep theirs."""
+    T, F, E, K = case
+    H = 256
+    g = torch.Generator().manual_seed(32)
+    x, w13, w2 = randn(g, T, H), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    idx, w = routing(T, K, E, 17)
+    w = w.abs() + 0.1
+    plus, minus = (11, 2) if form == INT else (3, 12)
+    w13, w2 = (w13[0], w13[1].abs()), (w2[0], w2[1].abs())
+    x[0::2, 77] = float("inf")
+    sign = torch.where(torch.arange(H) % 2 == 0, 1.0, -1.0)
+    for e in range(E):  # each gate and up is +infinity, each output's weights have one sign
+        set_codes(w13[0], e, slice(None), 77, plus)
+        set_codes(w2[0], e, slice(None), slice(None), torch.where(sign > 0, plus, minus).unsqueeze(1).expand(H, F))
+    out, _ = few_call(x, idx, w, experts(w13, w2, F, form), E)
+    assert torch.equal(out[0::2].float().cpu(), (sign * float("inf")).expand(len(out[0::2]), H))
+    ref, bound = few_reference(x[1::2], w13, w2, idx[1::2], w[1::2], F, form)
+    check(out[1::2], ref, bound, "tokens of finite inputs")
+
+
+@FORMS
+@pytest.mark.parametrize("case", EXTREME, ids=str)
+def test_few_w4_keeps_the_sign_of_infinite_inner_values(case, form):
+    """Finite inputs and weights whose inner value 77 passes 32 bits, to +infinity in even experts and
+    -infinity in odd ones: outputs of its sign times the weight's, NaN where the weight is 0 or the token
+    has experts of both kinds."""
+    T, F, E, K = case
+    H, at = 256, 77
+    g = torch.Generator().manual_seed(33)
+    x, w13, w2 = randn(g, T, H).abs(), four(g, E, 2 * F, H, form), four(g, E, H, F, form)
+    idx, w = routing(T, K, E, 17)
+    w = w.abs() + 0.1
+    zero, plus, minus = (8, 11, 2) if form == INT else (0, 3, 12)
+    w13, w2 = (w13[0], w13[1].abs()), (w2[0], w2[1].abs())
+    w13 = by_power(w13, form, slice(F + at, F + at + 1), 130 if form == INT else 127)
+    pick = torch.arange(H) % 3
+    for e in range(E):
+        set_codes(w13[0], e, at, slice(None), plus)
+        set_codes(w13[0], e, F + at, slice(None), plus if e % 2 == 0 else minus)
+        set_codes(w2[0], e, slice(None), at, torch.tensor([plus, minus, zero])[pick])
+        for m in (w13, w2):
+            assert torch.isfinite(values(m[0][e], m[1][e], form)[0].to(BF16)).all()
+    out = few_call(x, idx, w, experts(w13, w2, F, form), E)[0].float().cpu()
+    for t in range(T):
+        kinds = {e % 2 for e in idx[t].tolist()}
+        if len(kinds) == 2:
+            assert torch.isnan(out[t]).all(), t
+            continue
+        inf = -float("inf") if kinds == {1} else float("inf")
+        assert (out[t, pick == 0] == inf).all() and (out[t, pick == 1] == -inf).all(), t
+        assert torch.isnan(out[t, pick == 2]).all(), t
 
 
 @FORMS
