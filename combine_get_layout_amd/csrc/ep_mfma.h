@@ -43,7 +43,9 @@ __device__ __forceinline__ u32x4 buf_desc(const void* p, uint32_t bytes) {
     return r;
 }
 
-// 16 bytes per lane into registers: descriptor, per-lane and scalar byte offset.
+// 16 bytes per lane into registers: descriptor, per-lane and scalar byte offset. The
+// descriptor's end is certain to be held against the per-lane offset alone, so a lane that
+// has nothing to load says so there (kBufFar, a row past the last).
 __device__ __forceinline__ u32x4 buf_load16(__amdgpu_buffer_rsrc_t d, uint32_t off, uint32_t scalar_off) {
     return __builtin_amdgcn_raw_buffer_load_b128(d, (int)off, (int)scalar_off, 0);
 }

@@ -287,8 +287,8 @@ __device__ __forceinline__ void up4_tokens(const Few4Args& a, const Found& found
             u32x4 v[2][kPasses];
 #pragma unroll
             for (int n = 0; n < kPasses; ++n) {
-                v[0][n] = buf_load16(s_gate, tid * 16, n * kThreads * 16);
-                v[1][n] = buf_load16(s_up, tid * 16, n * kThreads * 16);
+                v[0][n] = buf_load16(s_gate, (n * kThreads + tid) * 16, 0);
+                v[1][n] = buf_load16(s_up, (n * kThreads + tid) * 16, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
             load(wave, g0);
@@ -701,7 +701,7 @@ __global__ __launch_bounds__(kThreads, 2) void few4_down_kernel(Few4Args a) {
     auto load_scales = [&](int64_t e, uint32_t far) {
         const auto ds = buf_resource(a.s2 + (e * a.H + h0) * lds, cols * lds);
 #pragma unroll
-        for (int v = 0; v < RT; ++v) block[v] = buf_load16(ds, lane * 16 + far, v * 1024);
+        for (int v = 0; v < RT; ++v) block[v] = buf_load16(ds, (v * 64 + lane) * 16 + far, 0);
     };
     auto keep_scales = [&] {
 #pragma unroll

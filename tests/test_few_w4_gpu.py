@@ -365,6 +365,25 @@ def test_few_w4_keeps_the_sign_of_infinite_inner_values(case, form):
 
 
 @FORMS
+@pytest.mark.parametrize("case", [(1, 32, 32, 1, 1, {}), (1, 288, 160, 2, 2, {}), (3, 96, 416, 4, 1, {})], ids=str)
+def test_few_w4_scales_at_the_end_of_their_memory(case, form):
+    """The shortest rows of scales, which end where their memory does: a workgroup asks for whole vectors of
+    more rows than there are, and takes none of what lies behind the array. The same results as with each
+    array in the middle of other values."""
+    H, F, x, idx, w, w13, w2 = few_case(case, form)
+    X = experts(w13, w2, F, form)
+    out, _ = few_call(x, idx, w, X, case[3])
+    for name in ("w13_scales", "w2_scales"):
+        around = torch.full((1 << 16,), 0x7F, dtype=U8, device="cuda")
+        raw = X[name].view(U8).flatten()
+        last, middle = around.clone(), around.clone()
+        last[len(last) - len(raw):], middle[4096:4096 + len(raw)] = raw, raw
+        for t, at in ((last, len(last) - len(raw)), (middle, 4096)):
+            again, _ = few_call(x, idx, w, dict(X, **{name: t[at:at + len(raw)]}), case[3])
+            assert torch.equal(again.view(torch.int16), out.view(torch.int16)), name
+
+
+@FORMS
 @pytest.mark.parametrize("F", [128, 2048])
 def test_few_w4_without_any_lane(form, F):
     """All lanes skipped, or of ids that 32 bits would take for valid ones: zeros, and for the latter
