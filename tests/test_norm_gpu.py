@@ -162,6 +162,44 @@ def test_norm_of_zero_and_nonfinite_rows(H):
         check_norm(clean[t:t + 1], None, gain, {n: v[t:t + 1] for n, v in out.items()}, False)
 
 
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [8, 512, 1032, 2048, 2056, 4096, 5120, 6144, 7168, 8192, 16384, 32768, 40960, MOST])
+def test_norm_of_rows_whose_squares_add_up_past_32_bits(H, wide):
+    """Values of about 1e19: the mean of their squares is a number of 32 bits, the sum is not. One value of
+    2^63.5 sqrt(H) alone; a row of 3e19, whose mean passes too, has rstd 0. Neighbours keep theirs."""
+    x, res, gain = norm_case(6, H, wide, True)
+    x[1], res[1] = 0.5e19 * (1 + torch.rand(H, device="cuda")), 0.5e19
+    x[2], res[2] = 0, 0
+    x[2, H // 2] = 2.0 ** 63.5 * H ** 0.5
+    x[4], res[4] = 3e19, 0
+    h = x.double() + res.double()
+    assert h[1].pow(2).mean() < 3e38 and (h[1].pow(2).sum() > 4e38 or H < 8) and h[2].pow(2).mean() < 3e38
+    assert h[4].pow(2).mean() > 4e38
+    names = ["h", "y", "rstd"] + (["y_fp8", "y_scales"] if H % 128 == 0 else [])
+    out = outputs(6, H, wide, names)
+    shape = ep.make_shape(6, H, 1, 1, 1)
+    ep.ep_rms_norm(shape, x, res, kind(wide), gain, EPS, out)
+    assert out["rstd"][4] == 0 and (out["y"][4] == 0).all()
+    keep = [0, 1, 3, 5]
+    check_norm(x[keep], res[keep], gain, {n: t[keep] for n, t in out.items()}, wide)
+    check_norm(x[2:3], res[2:3], gain, {n: out[n][2:3] for n in ("h", "y", "rstd")}, wide)
+    if H % 128 == 0:  # its other blocks are zeros
+        v = h[2] * out["rstd"][2].double() * gain.double()
+        block = H // 2 // 128
+        scale = torch.ones(H // 128, dtype=F64, device="cuda")
+        scale[block] = v.abs().max() / 448
+        check_there(out["y_scales"][2], scale, 4 * U24 * scale, "y_scales of one value")
+        got = out["y_fp8"][2].view(F8).float()
+        assert (got != 0).sum() == 1 and got[H // 2] == 448 * torch.sign(v[H // 2])
+    # Without the stored stream, and in place of the residual.
+    y = outputs(6, H, wide, ["y"])
+    ep.ep_rms_norm(shape, x, res, kind(wide), gain, EPS, y)
+    assert torch.equal(y["y"], out["y"])
+    y, same = outputs(6, H, wide, ["y"]), res.clone()
+    ep.ep_rms_norm(shape, x, same, kind(wide), gain, EPS, dict(y, h=same))
+    assert torch.equal(y["y"], out["y"]) and torch.equal(same, out["h"])
+
+
 def test_norm_of_small_blocks():
     """A block whose largest magnitude is below 1e-33 has a scale of 1 and zeros."""
     H = 256
