@@ -278,6 +278,8 @@ __device__ __forceinline__ void gain_columns(const NormGradArgs& a, int c0, floa
     }
 }
 
+// With v = h r, whose mean square is 1 at most, d = d_stream + r (a - v mean(a v)): each term
+// is a number of 32 bits where d is (r^2 is none for a row of zeros with eps below 2^-128).
 // LANES threads to a row, NV vectors of eight values to a thread. A workgroup takes
 // every a.groups-th run of rows and keeps its part of d_gain in registers. The next
 // rows' loads are in flight while these are summed and stored. Workgroups behind
@@ -326,15 +328,16 @@ __global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads, 4) voi
                 unpack8(ld16(a.gain + c), w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    dot = fmaf(dy[j] * w[j], h[j], dot);
-                    dg[n][j] = fmaf(dy[j], h[j] * g.r, dg[n][j]);
+                    const float v = h[j] * g.r;
+                    dot = fmaf(dy[j] * w[j], v, dot);
+                    dg[n][j] = fmaf(dy[j], v, dg[n][j]);
                 }
             }
         }
         if (!a.dh && !a.dx) return;
         // The other half of scratch next time: a wave may still read this one.
         dot = share_sum<LANES>(dot, scratch[turn]);
-        const float k = g.r * g.r * (dot * inv_h);
+        const float k = dot * inv_h;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c = (n * LANES + tid) * 8;
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(kGradThreads < LANES ? LANES : kGradThreads, 4) voi
                 if (a.ds) floats8<WIDE>(g.s[n], s);
                 unpack8(ld16(a.gain + c), w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[j] = fmaf(g.r, fmaf(-k, h[j], dy[j] * w[j]), s[j]);
+                for (int j = 0; j < 8; ++j) s[j] = fmaf(g.r, fmaf(-k, h[j] * g.r, dy[j] * w[j]), s[j]);
                 if (a.dh) store8<WIDE>(a.dh, base + c, s);
                 if (a.dx) st16(a.dx + base + c, pack8(s));
             }
@@ -405,10 +408,10 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
         floats8<WIDE>(load8<WIDE>(a.h, base + c), h);
         unpack8(ld16(a.gain + c), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dot = fmaf(dy[j] * g[j], h[j], dot);
+        for (int j = 0; j < 8; ++j) dot = fmaf(dy[j] * g[j], h[j] * r, dot);
     }
     dot = share_sum<1024>(dot, scratch);
-    const float k = r * r * (dot / (float)a.H);
+    const float k = dot / (float)a.H;
     for (int c = threadIdx.x * 8; c < a.H; c += 8192) {
         float dy[8], h[8], g[8], s[8] = {};
         floats8<false>(load8<false>(a.dy, base + c), dy);
@@ -416,7 +419,7 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs a) {
         unpack8(ld16(a.gain + c), g);
         if (a.ds) floats8<WIDE>(load8<WIDE>(a.ds, base + c), s);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = fmaf(r, fmaf(-k, h[j], dy[j] * g[j]), s[j]);
+        for (int j = 0; j < 8; ++j) s[j] = fmaf(r, fmaf(-k, h[j] * r, dy[j] * g[j]), s[j]);
         if (a.dh) store8<WIDE>(a.dh, base + c, s);
         if (a.dx) st16(a.dx + base + c, pack8(s));
     }

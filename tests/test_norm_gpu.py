@@ -342,6 +342,32 @@ def test_norm_grad_in_place(H, wide):
     assert torch.equal(same, ref["d_h"])
 
 
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [8, 512, 1024, 1032, 2056, 4104, 7168, 8192, 16384, 32768, 40960])
+def test_norm_grad_of_small_and_large_rows(H, wide):
+    """With eps of 1e-40: a row of zeros, whose 1 / sqrt(eps) squared passes 32 bits, one of about 1e-21, an
+    ordinary one, and rows of about 1e19, with gradients of 1e19 too, whose products pass 32 bits."""
+    eps = 1e-40
+    h, gain, _, dy, ds = grad_case(5, H, wide, True, seed=9)
+    h = h / h.double().pow(2).mean(1, keepdim=True).sqrt().to(h.dtype)
+    h[0], h[1] = 0, h[1] * 1e-21
+    h[3:] *= 1e19
+    dy[4] *= 1e19
+    shape = ep.make_shape(5, H, 1, 1, 1)
+    rstd = torch.empty(5, device="cuda")
+    # The forward's rstd, of the 32-bit stream's rows by the definition (x has 16 bits).
+    r = (1 / torch.sqrt(h.double().pow(2).mean(1) + torch.tensor(eps, dtype=F32).double().item())).float()
+    if not wide:
+        ep.ep_rms_norm(shape, h, None, ep.EP_STREAM_BF16, gain, eps, dict(rstd=rstd))
+        check_there(rstd, r.double(), (row_steps(H) / 2 + 2 * U23) * r.double() + 2.0 ** -149 * r.double() / (2 * eps), "rstd")
+    ws = ep.alloc_norm_workspace(shape).fill_(0xAB)
+    for rows in ([0, 1, 2, 3, 4], [0], [3, 4]):
+        case = [t[rows].contiguous() for t in (h, r, dy, ds)]
+        case.insert(1, gain)
+        out = grad_call(ep.make_shape(len(rows), H, 1, 1, 1), case, wide, ws)
+        check_grad(*case, out, wide)
+
+
 def test_norm_grad_against_differences():
     """The gradient against central differences, in 64 bits, of sum dy * y + sum ds * h as ep_rms_norm
     defines y. With steps of 1e-4 and third derivatives of at most about 6 r^3 |a| sqrt(H) the
