@@ -1071,23 +1071,35 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const bool lds_scales = row <= kLdsScales;
     // Experts of many tokens: few4_up_many_kernel, if there are workgroups for most CUs.
     // Both launches without and with it, us (form; workgroups it has):
-    //   128 tokens, top-8 of 64 experts of 7168 x 2048 (int, 2048) 633  495
-    //   128 tokens, top-8 of 64, 2048 x 768 (int, 768)             114  83.2
-    //   48 tokens, top-8 of 64, 7168 x 2048 (int, 2048)            455  416
-    //   48 tokens, top-4 of 32, 4096 x 2048 (e2m1, 1024)           136  138
-    //   100 tokens, top-8 of 10, 512 x 1024 (e2m1, 160)            61.2 46.4
-    //   128 tokens, top-1 of 8, 2048 x 2048 (int, 256)             50.9 49.2
-    //   64 tokens, top-6 of 13, 384 x 512 (int, 104)               33.0 29.0
-    //   128 tokens, top-4 of 8, 2048 x 1024 (e2m1, 128)            57.3 54.2
-    //   64 tokens, top-2 of 8, 2048 x 1024 (int, 128)              30.3 33.2
-    //   128 tokens, top-4 of 8, 2048 x 512 (int, 64)               46.5 58.4
-    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1, 256)            43.3 49.8
-    //   24 tokens, top-8 of 64, 2048 x 768 (int, 768)              60.7 51.1
-    //   32 tokens, top-8 of 64, 7168 x 2048 (e2m1, 2048)           337  355
+    //   128 tokens, top-8 of 64 experts of 7168 x 2048 (int, 2048) 631  475
+    //   128 tokens, top-8 of 64, 2048 x 768 (int, 768)             116  82.7
+    //   48 tokens, top-8 of 64, 7168 x 2048 (int, 2048)            463  417
+    //   48 tokens, top-4 of 32, 4096 x 2048 (int, e2m1, 1024)      141 135, 135 138
+    //   100 tokens, top-8 of 10, 512 x 1024 (e2m1, 160)            61.1 46.5
+    //   128 tokens, top-1 of 8, 2048 x 2048 (int, 256)             51.1 49.3
+    //   64 tokens, top-6 of 13, 384 x 512 (int, 104)               32.9 28.2
+    //   128 tokens, top-4 of 8, 2048 x 1024 (e2m1, 128)            57.2 54.4
+    //   64 tokens, top-2 of 8, 2048 x 1024 (int, 128)              29.9 32.4
+    //   128 tokens, top-4 of 8, 2048 x 512 (int, 64)               47.4 55.7
+    //   20 tokens, top-4 of 16, 4096 x 1024 (int, e2m1, 256)       45.5 52.2, 43.1 49.4
+    //   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1, 2048)      360 351, 336 353
+    //   32 tokens, top-4 of 32, 4096 x 2048 (int, e2m1, 1024)      128 132, 117 129
+    // And of few tokens where rows are short, as a wave of the other form then has a step or
+    // two, less than its workgroup's way to them (int, e2m1):
+    //   24 tokens, top-8 of 64, 256 x 1024 (1024)                  57.5 36.8, 47.9 35.6
+    //   1 token, top-4 of 16, 1024 x 8192 (512)                    31.2 26.4, 27.9 24.6
+    //   20 tokens, top-4 of 64, 1024 x 1024 (1024)                 57.4 42.3, 50.0 39.9
+    //   2 tokens, top-8 of 64, 2048 x 2048 (512)                   35.3 37.2, 33.1 33.4
+    //   8 tokens, top-8 of 64, 2048 x 768 (768)                    43.7 41.6, 39.6 37.6
+    //   24 tokens, top-8 of 64, 2048 x 768 (768)                   61.9 52.8, 55.7 49.3
+    //   16 tokens, top-4 of 32, 2048 x 2048 (1024)                 67.9 65.9, 61.5 66.4
+    //   24 tokens, top-8 of 64, 2816 x 1024 (1024)                 99.7 88.1, 87.8 92.8
+    //   24 tokens, top-8 of 64, 4096 x 1024 (1024)                 113  116,  101  118
     const int64_t groups64 = (a.F + kManyCols - 1) / kManyCols * experts;
     const bool many = lds_scales && (lanes > 20 * experts  ? groups64 >= 96
                                      : lanes > 8 * experts ? groups64 >= 160
-                                                           : lanes > 4 * experts && groups64 >= 512);
+                                                           : groups64 >= 512 && (lanes > 4 * experts ||
+                                                                                 a.H <= (s.T <= 4 ? 1024 : 2048)));
     // 16 or 32 values of f to a workgroup: 32 read the tokens half as often, 16 have more
     // waves to hide a step's latency. us with 16 and with 32 (form):
     //   1 token, top-8 of 64 experts of 7168 x 2048 (e2m1)    48.0 49.3

@@ -442,6 +442,16 @@ def test_few_w4_32_columns_a_workgroup(case, form):
 
 
 @FORMS
+@pytest.mark.parametrize("case", [(1, 1024, 8192, 4, 4, {}), (3, 256, 2080, 16, 6, {}), (4, 1056, 1024, 32, 8, {}),
+                                  (5, 2048, 1056, 32, 8, {}), (12, 2080, 1056, 32, 3, dict(skip=0.1)),
+                                  (17, 96, 1056, 40, 2, {})], ids=str)
+def test_few_w4_short_rows(case, form):
+    """One to a few tokens an expert in the first launch's form for many, on both sides of the row lengths
+    that take it."""
+    test_few_w4(case, form)
+
+
+@FORMS
 @pytest.mark.parametrize("case", [(32, 160, 2048, 33, 4, {}), (32, 160, 4192, 16, 4, {}), (9, 224, 2336, 30, 4, dict(skip=0.1)),
                                   (2, 96, 2048, 128, 64, {}), (1, 544, 4192, 40, 16, {})], ids=str)
 def test_few_w4_64_columns_of_the_second_launch(case, form):
