@@ -467,12 +467,18 @@ __global__ __launch_bounds__(1024) void norm_gain_kernel(const float* part, int 
     }
 }
 
-constexpr int kLongH = 32768;     // longest row held in registers
+// Longest row held in registers. Up to it kernels of more than 8,192 values of a 32-bit
+// stream and 16,384 of a bf16 one spill (52 and 80 bytes a lane: two vectors and more to
+// each of 1,024 threads, at 128 registers); past it rows are read twice, d_gain in a launch of
+// its own. us held and read twice: 32-bit stream, 2,048 rows of 16,384 127 148, 1,024 of
+// 20,480 136 96.4, of 32,768 (208 bytes spilt) 194 158, 8 of 32,768 23.6 19.0; bf16, 1,024
+// rows of 20,480 58.9 55.0, of 32,768 89.8 86.1, 8 of 32,768 11.4 17.2.
+constexpr int long_h(bool wide) { return wide ? 16384 : 32768; }
 
 // Threads to a row: with one vector of eight to a thread (a stream in 32 bits, whose
 // rows take more registers) or two.
 // In bf16 one, and two, us: 4,096 rows of 2,056 23.7 22.4, of 4,096 31.5 32.3, of 7,168
-// 50.2 50.5.
+// 50.2 50.5; two for every length, within 3% of the better.
 int grad_lanes(int H, bool wide) {
     int lanes = 64;
     while (lanes < 1024 && lanes * 8 * (wide ? 1 : 2) < H) lanes *= 2;
@@ -483,20 +489,29 @@ int grad_lanes(int H, bool wide) {
 // 25.0 22.4, of 7,168 52.7 50.5; 2,048 of 16,384 (1,024 threads) 57.6 68.7; 32-bit
 // stream, 4,096 of 7,168 (1,024) 95.4 101.
 int grad_groups(int T, int H, bool wide) {
-    if (H > kLongH) return std::min(T, 64);
+    if (H > long_h(wide)) return std::min(T, 64);
     const int lanes = grad_lanes(H, wide), rows = std::max(1, kGradThreads / lanes);
     return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, lanes > kGradThreads ? 256 : 512);
 }
 // Whether d_gain is made beside the rows in the same launch, by workgroups that
 // read dy and h once more, column by column, or from the rows' workgroups' parts in a
-// second one. us a call, in one launch and in two, bf16 stream:
-//   T x H   128 x 512   1024 x 512   4096 x 512   512 x 2056   1024 x 2056   2048 x 2056
-//   one     11.1        11.3         20.7         11.4         12.0          19.4
-//   two     13.9        13.9         14.0         14.0         14.1          15.3
-//   T x H   128 x 7168  512 x 7168   1024 x 7168  2048 x 7168
-//   one     11.1        11.6         20.0         33.2
-//   two     13.9        17.0         22.2         31.2
-bool gain_beside(int T, int H) { return H <= kLongH && T <= 1024 && (int64_t)T * H <= 1 << 23; }
+// second one. us a call, in one launch and in two:
+//   bf16     128 x 512   1024 x 512   2048 x 512   4096 x 512   512 x 2056   1024 x 2056
+//   one      11.1        11.2         11.5         20.7         11.3         12.1
+//   two      14.1        13.9         14.4         14.1         14.1         14.1
+//   bf16     1500 x 2056   128 x 7168   512 x 7168   1024 x 7168  2048 x 7168
+//   one      16.3          10.9         11.7         19.9         33.2
+//   two      14.0          13.8         17.0         22.2         31.4
+//   32-bit   128 x 512   1024 x 512   2048 x 512   4096 x 512   512 x 2056   1024 x 2056
+//   one      12.6        12.7         14.0         24.7         13.4         15.2
+//   two      15.1        15.1         15.0         15.0         16.2         16.1
+//   32-bit   1500 x 2056   128 x 7168   512 x 7168   1024 x 7168  512 x 16384
+//   one      21.2          13.1         18.8         30.5         40.4
+//   two      17.5          16.0         19.6         28.3         39.8
+bool gain_beside(int T, int H, bool wide) {
+    const int64_t values = (int64_t)T * H;
+    return H <= long_h(wide) && (T <= 1024 ? values <= (wide ? 1 << 22 : 1 << 23) : T <= 2048 && values <= 1 << 20);
+}
 
 // Threads to a row: a wave up to 2,048 values (256 threads, with a barrier, are the same
 // within 1%), then one vector to a thread, as far as a workgroup goes. us, 4,096 rows of
@@ -530,7 +545,7 @@ void launch_norm(NormArgs a, hipStream_t st) {
 template <bool WIDE>
 void launch_norm_grad(const NormGradArgs& a, int parts, hipStream_t st) {
     const int vecs = (a.H + 7) / 8;
-    if (a.H > kLongH) {
+    if (a.H > long_h(WIDE)) {
         if (a.dh || a.dx) hipLaunchKernelGGL(norm_grad_long_kernel<WIDE>, dim3((unsigned)a.T), dim3(1024), 0, st, a);
         if (a.part)
             hipLaunchKernelGGL(norm_gain_long_kernel<WIDE>, dim3((unsigned)((vecs + 255) / 256), (unsigned)parts),
@@ -554,8 +569,8 @@ void launch_norm_grad(const NormGradArgs& a, int parts, hipStream_t st) {
         if (lanes == 256) return go(norm_grad_kernel<256, 2, WIDE>, lanes);
         if (lanes == 512) return go(norm_grad_kernel<512, 2, WIDE>, lanes);
     }
-    if (vecs <= 2048) return go(norm_grad_kernel<1024, 2, WIDE>, lanes);
-    go(norm_grad_kernel<1024, 4, WIDE>, lanes);
+    if (WIDE || vecs <= 2048) return go(norm_grad_kernel<1024, 2, WIDE>, lanes);
+    if constexpr (!WIDE) go(norm_grad_kernel<1024, 4, WIDE>, lanes);
 }
 
 }  // namespace
@@ -580,14 +595,15 @@ hipError_t launch_rms_norm(const ep_shape& s, const uint16_t* x, const void* res
 hipError_t launch_rms_norm_grad(const ep_shape& s, const void* h, int stream_type, const uint16_t* gain,
                                 const float* rstd, const uint16_t* dy, const void* d_stream, void* d_h, uint16_t* d_x,
                                 float* d_gain, char* ws, hipStream_t st) {
-    const int parts = grad_groups(s.T, s.H, stream_type == EP_STREAM_F32);
+    const bool rows = s.T > 0 && (d_h || d_x), wide = stream_type == EP_STREAM_F32,
+               beside = d_gain && s.T > 0 && gain_beside(s.T, s.H, wide);
+    const int parts = grad_groups(s.T, s.H, wide);
     float* part = reinterpret_cast<float*>(ws + 256);
-    const bool rows = s.T > 0 && (d_h || d_x), beside = d_gain && s.T > 0 && gain_beside(s.T, s.H);
     const NormGradArgs a = {s.T, s.H, static_cast<const char*>(h), gain, rstd, dy, static_cast<const char*>(d_stream),
                             static_cast<char*>(d_h), d_x, d_gain && !beside ? part : nullptr, beside ? d_gain : nullptr,
                             beside && !rows ? 0 : parts};
     if (s.T > 0) {
-        if (stream_type == EP_STREAM_F32)
+        if (wide)
             launch_norm_grad<true>(a, parts, st);
         else
             launch_norm_grad<false>(a, parts, st);

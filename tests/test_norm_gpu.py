@@ -330,6 +330,21 @@ def test_norm_grad_rows(T, H):
 
 
 @pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(1500, 512), (2049, 512), (512, 8192), (513, 8192), (1024, 8192), (300, 16384), (70, 20480),
+                                 (1, 32768), (300, 32768)])
+def test_norm_grad_in_one_launch_and_in_two(T, H, wide):
+    """The gain's gradient beside the rows and behind them, and rows held and read twice, in both streams."""
+    case = grad_case(T, H, wide, True, seed=T)
+    shape = ep.make_shape(T, H, 1, 1, 1)
+    ws = ep.alloc_norm_workspace(shape).fill_(0xAB)
+    out = grad_call(shape, case, wide, ws)
+    check_grad(*case, out, wide)
+    for only in ("d_h", "d_gain"):
+        alone = grad_call(shape, case, wide, ws, **{n: n == only for n in ("d_h", "d_x", "d_gain")})
+        assert torch.equal(alone[only], out[only]), only
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "f32"])
 @pytest.mark.parametrize("H", [264, 4096, 32776])
 def test_norm_grad_in_place(H, wide):
     T = 9
