@@ -11,16 +11,18 @@
 // What has to move is the used experts' weights once, 1.5 F H bytes each and a 32nd (int)
 // or 16th (e2m1) of that in scales; products are few (32 tokens, top-8 of 64 experts
 // of 7168 x 2048: 22 GFLOP for 1.48 GB). Medians on inputs that the caches do not hold:
-//   1 token, top-8 of 64 experts of 7168 x 2048, int   28.5 + 21.1 us, 182 MB: 3.7 TB/s
-//   32 tokens, the same, e2m1                          203 + 131 us, 1.48 GB: 4.4 TB/s
-//   13 tokens, top-3 of 40, 2080 x 736, e2m1           14.9 + 12.1 us, 58 MB: 2.2 TB/s
-//   1 token, top-2 of 16, 256 x 512, int               5.6 + 5.1 us: two launches' latency
+//   1 token, top-8 of 64 experts of 7168 x 2048, int   27.3 + 22.0 us, 182 MB: 3.7 TB/s
+//     e2m1                                             27.3 + 20.4 us, 187 MB: 3.9 TB/s
+//   32 tokens, the same, e2m1                          202 + 131 us, 1.48 GB: 4.4 TB/s
+//     int                                              219 + 136 us, 1.43 GB: 4.0 TB/s
+//   13 tokens, top-3 of 40, 2080 x 736, e2m1           15.2 + 11.9 us, 58 MB: 2.2 TB/s
+//   1 token, top-2 of 16, 256 x 512, int               5.6 + 5.2 us: two launches' latency
 // The first launch of 32 tokens reads at 4.9 TB/s, as a copy does; the second is bound by
 // latency: a wave waits for one unit of 256 values' fragments behind another, with the
 // activations' (as many loads as the weights') between them. One token's launches end
 // before the memory has come up to its rate. With many tokens to an expert both launches
 // have a form whose workgroups hold the tokens' rows in LDS for four waves of different
-// weights: 128 tokens, top-8 of 64 experts of 7168 x 2048, int, 493 us a call.
+// weights: 128 tokens, top-8 of 64 experts of 7168 x 2048, int, 233 + 243 us.
 #include <algorithm>
 
 #include "ep_internal.h"
@@ -160,7 +162,8 @@ __device__ __forceinline__ void wave_lds_order() {
 // in different banks.
 __device__ __forceinline__ uint32_t row_chunk(int row, int chunk) { return row * 512 + ((chunk ^ (row & 15)) << 4); }
 
-// silu(gate) * up as two bf16 values for the second product's matrix instruction, the
+// silu(gate) * up (__expf: |gate| 2^-24 of it, beside the 2^-16 that two bf16 values keep) as
+// two bf16 values for the second product's matrix instruction, the
 // rounded one (of a finite value bf16's largest at most) and, F values on, what it
 // leaves (nothing of an infinity or NaN).
 __device__ __forceinline__ void store_act(uint16_t* act, int F, float gate, float up) {
@@ -995,37 +998,37 @@ int64_t down_units(const ep_shape& s, int F) {
 // 16-value tiles of h per workgroup of the second launch: 4, which read the activations
 // half as often, where each wave has many units (and LDS holds the sums), else 2, which
 // keep more waves busy. Both launches with 4 and with 2 tiles, us:
-//   32 tokens, top-8 of 64 experts of 7168 x 2048 (512 units)  344  359
-//   16 tokens, top-8 of 64, 7168 x 512 (128)                   91.8 90.7
-//   8 tokens, top-4 of 64, 4096 x 1024 (128)                   54.4 50.4
-//   13 tokens, top-3 of 40, 2080 x 736 (117)                   37.1 30.8
-//   1 token, top-8 of 64, 7168 x 2048 (64)                     53.2 52.1
+//   32 tokens, top-8 of 64 experts of 7168 x 2048 (int, e2m1; 512 units)  360 372, 337 351
+//   16 tokens, top-8 of 64, 7168 x 512 (int, e2m1; 128)      89.3 89.9, 82.7 82.8
+//   8 tokens, top-4 of 64, 4096 x 1024 (int; 128)            51.6 49.3
+//   13 tokens, top-3 of 40, 2080 x 736 (e2m1; 117)           32.6 30.6
+//   1 token, top-8 of 64, 7168 x 2048 (int; 64)              52.9 49.8
 int down_tiles(const ep_shape& s, int F) { return s.T <= 32 && down_units(s, F) >= 256 ? 4 : 2; }
 
 // few4_down_many_kernel where an expert has more than four tokens on the average. Both
 // launches without and with it, us:
-//   128 tokens, top-8 of 64 experts of 7168 x 2048 (int)    674  493
+//   128 tokens, top-8 of 64 experts of 7168 x 2048 (int)    676  476
 //   128 tokens, top-4 of 32, 4096 x 1536 (e2m1)             154  111
-//   128 tokens, top-8 of 64, 2048 x 768 (int)               92.8 83.2
-//   64 tokens, top-6 of 13, 384 x 512 (int)                 34.5 29.0
-//   48 tokens, top-4 of 32, 4096 x 2048 (e2m1)              143  138
-//   100 tokens, top-8 of 10, 512 x 1024 (e2m1)              46.0 46.4
-//   64 tokens, top-2 of 16, 2048 x 1024 (e2m1)              34.7 35.1
-//   32 tokens, top-8 of 64, 7168 x 2048 (e2m1)              337  402
-//   16 tokens, top-4 of 16, 2048 x 1024 (int)               29.6 30.7
+//   128 tokens, top-8 of 64, 2048 x 768 (int)               94.4 82.6
+//   64 tokens, top-6 of 13, 384 x 512 (int)                 34.9 28.2
+//   48 tokens, top-4 of 32, 4096 x 2048 (int, e2m1)         146 135, 143 138
+//   100 tokens, top-8 of 10, 512 x 1024 (e2m1)              46.0 46.5
+//   64 tokens, top-2 of 16, 2048 x 1024 (int, e2m1)         37.0 36.6, 34.4 35.4
+//   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1)         360 411, 337 401
+//   16 tokens, top-4 of 16, 2048 x 1024 (int)               30.1 30.8
 bool down_many(const ep_shape& s, int F, int form) {
     const uint32_t row = form == EP_W4_INT ? ScaleRow<EP_W4_INT>::bytes(F) : ScaleRow<EP_W4_E2M1>::bytes(F);
     return row <= kLdsScales2 && (int64_t)s.T * s.K > 4 * std::min<int64_t>(s.E, (int64_t)s.T * s.K);
 }
 
 // Workgroups of the second launch for the same values of h: as many as fill the chip
-// (512; with 384, 768 and 1,024 49.9 us became 54.7, 49.6, 52.0 for 1 token, top-8 of 64
-// experts of 7168 x 2048, int; 337 368, 346, 333 for 32 tokens, e2m1; 82.8 95.1, 85.0, 88.1
-// for 16 tokens, 7168 x 512), with a unit for every wave. Of
+// (512; with 384, 768 and 1,024 50.0 us became 54.6, 49.2, 51.5 for 1 token, top-8 of 64
+// experts of 7168 x 2048, int; 337 369, 347, 334 for 32 tokens, e2m1; 90.0 105, 90.7, 94.0
+// for 16 tokens, 7168 x 512, int), with a unit for every wave. Of
 // few4_down_many_kernel: eight steps to each, or four while there are fewer than 256.
-// us with four always, and with eight: 70.1 57.4 (128 tokens, top-4 of 8 experts of 2048 x
-// 1024), 47.9 43.2 (128, top-2 of 8, 4096 x 512); 44.7 51.3 (128, top-2 of 4, 1024 x 1024),
-// 33.0 38.9 (64, top-6 of 13, 384 x 512).
+// us with four always, and with eight (int): 74.6 61.8 (128 tokens, top-4 of 8 experts of 2048
+// x 1024), 52.6 47.7 (128, top-2 of 8, 4096 x 512); 45.3 51.2 (128, top-2 of 4, 1024 x 1024),
+// 28.1 33.2 (64, top-6 of 13, 384 x 512).
 int down_splits(const ep_shape& s, int F, int form) {
     if (down_many(s, F, form)) {
         const int64_t cols = (s.H + kManyCols - 1) / kManyCols;
@@ -1102,26 +1105,26 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
                                                                                  a.H <= (s.T <= 4 ? 1024 : 2048)));
     // 16 or 32 values of f to a workgroup: 32 read the tokens half as often, 16 have more
     // waves to hide a step's latency. us with 16 and with 32 (form):
-    //   1 token, top-8 of 64 experts of 7168 x 2048 (e2m1)    48.0 49.3
-    //   2 tokens, top-6 of 64, 5120 x 1536 (int)              44.5 52.0
-    //   8 tokens, top-4 of 64, 4096 x 1024 (int)              48.2 51.1
-    //   16 tokens, top-4 of 16, 2048 x 1024 (int, e2m1)       29.4 27.5, 25.8 26.5
-    //   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1)       351 353, 337 346
-    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1)            46.2 43.2
-    //   64 tokens, top-2 of 16, 2048 x 1024 (int, e2m1)       39.1 35.8, 37.9 35.1
-    //   32 tokens, top-2 of 8, 1024 x 512 (int)               17.5 19.1
+    //   1 token, top-8 of 64 experts of 7168 x 2048 (e2m1)    48.4 53.6
+    //   2 tokens, top-6 of 64, 5120 x 1536 (int)              44.4 56.6
+    //   8 tokens, top-4 of 64, 4096 x 1024 (int)              49.5 52.3
+    //   16 tokens, top-4 of 16, 2048 x 1024 (int, e2m1)       30.1 28.5, 26.0 26.6
+    //   32 tokens, top-8 of 64, 7168 x 2048 (int, e2m1)       359 364, 336 346
+    //   20 tokens, top-4 of 16, 4096 x 1024 (e2m1)            46.3 43.1
+    //   64 tokens, top-2 of 16, 2048 x 1024 (int, e2m1)       39.6 36.3, 38.2 35.2
+    //   32 tokens, top-2 of 8, 1024 x 512 (int)               17.7 19.5
     const bool narrow = !lds_scales || lanes <= 4 * experts || (int64_t)((a.F + 31) / 32) * experts < 512;
     const int cols = many ? kManyCols : narrow ? 16 : 32;
     const dim3 up((a.F + cols - 1) / cols, (unsigned)experts);
     // Tokens at a time: those of most experts, as the weights are read again for more; no
-    // more than these, as each is a load a step. us, and with 16 always: 48.0 56.7 (1
-    // token), 31.7 38.8 (4 tokens, top-4 of 64 experts of 4096 x 1024), 347 370 (32
-    // tokens, top-8 of 64, 7168 x 2048).
+    // more than these, as each is a load a step. us, and with 16 always (int): 49.9 64.5 (1
+    // token, top-8 of 64 experts of 7168 x 2048), 35.9 41.5 (4 tokens, top-4 of 64, 4096 x
+    // 1024), 360 426 (32 tokens, top-8 of 64, 7168 x 2048; e2m1 337 390).
     const int tt = s.T <= 2 ? 2 : s.T <= 4 ? 4 : s.T <= 8 || lanes <= 4 * experts ? 8 : 16;
     // Tiles of 16 tokens that few4_up_many_kernel multiplies at a time, at most: what fits
-    // the registers decides how many waves there are. us with 2, this and 8: 83.2 83.2 106
-    // (128 tokens, top-8 of 64, 2048 x 768), 417 416 532 (48 tokens, top-8 of 64, 7168 x
-    // 2048), 49.0 46.4 46.4 (100 tokens, top-8 of 10), 63.2 54.2 54.2 (128 tokens, top-4
+    // the registers decides how many waves there are. us with 2, this and 8: 82.6 82.8 107
+    // (128 tokens, top-8 of 64, 2048 x 768), 417 417 561 (48 tokens, top-8 of 64, 7168 x
+    // 2048), 49.0 46.4 46.4 (100 tokens, top-8 of 10), 63.3 54.4 54.4 (128 tokens, top-4
     // of 8, 2048 x 1024).
     const int tiles1 = s.T <= 32 || lanes <= 20 * experts ? 2 : s.T <= 64 || lanes <= 48 * experts ? 4 : 8;
     const UpForm form = up_form<FORM>(tt, narrow, lds_scales);
@@ -1132,8 +1135,8 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const size_t area = many ? 8192 * tiles1 : std::max<size_t>(sizeof(Up4Part) * kWaves, kWaves * 512 * form.tokens);
     hipLaunchKernelGGL(first, up, dim3(kThreads), area + (lds_scales ? 2 * cols * row : 0), st, a);
     if (down_many(s, a.F, FORM)) {
-        // As tiles1. us with 2, this and 4: 83.1 83.2 103, 417 416 576, 47.9 46.4 46.4 and
-        // 56.9 54.2 54.2 in the cases above.
+        // As tiles1. us with 2, this and 4: 82.4 82.4 101, 417 417 578, 47.9 46.4 46.4 and
+        // 57.1 54.4 54.4 in the cases above.
         const int most = s.T <= 32 || lanes <= 20 * experts ? 2 : 4;
         const dim3 grid((s.H + kManyCols - 1) / kManyCols, (unsigned)a.splits);
         const size_t lds = kManyCols * kLdsScales2 + 16384 * most + sizeof(float) * (kManyCols + 1) * s.T;
@@ -1145,9 +1148,9 @@ void launch(const Few4Args& a, const ep_shape& s, hipStream_t st) {
     const dim3 down((s.H + 16 * tiles - 1) / (16 * tiles), (unsigned)a.splits);
     const uint32_t row2 = ScaleRow<FORM>::bytes(a.F);
     const bool lds2 = row2 <= kLdsScales2;
-    // One or two tokens' activations over LDS, in whole loads instead of fragments: 51.9
-    // and 42.5 us instead of 53.6 and 43.9 (1 token, top-8 of 64 experts of 7168 x 2048; 2,
-    // top-6 of 64 of 5120 x 1536), the same as fragments at 4 tokens, slower at more.
+    // One or two tokens' activations over LDS, in whole loads instead of fragments: 49.8
+    // and 44.3 us instead of 52.0 and 46.1 (1 token, top-8 of 64 experts of 7168 x 2048; 2,
+    // top-6 of 64 of 5120 x 1536; int), the same as fragments at 4 tokens, slower at more.
     const int cap = s.T <= 2 ? 2 : 0;
     const size_t lds = kWaves * (sizeof(float) * (16 * tiles + 1) * s.T + cap * 1024 + (lds2 ? 16 * tiles * row2 : 0));
     const Kernel second = tiles == 4 ? down_kernel<FORM, 4, 0>(lds2)

@@ -2,13 +2,15 @@
 //
 // Bound by memory: a row is read once, held in registers over the sum of its squares
 // (its dot product in the gradient) and written once, so 4,096 rows of 7,168 move
-//   forward (x, residual; h, y, the 8-bit rows)  265 MB in 43.2 us, 6.1 TB/s
-//   gradient (h, dy, d_stream; d_h, d_gain)      235 MB in 45.2 us, 5.2 TB/s, and 4.7 us
+//   forward (x, residual; h, y, the 8-bit rows)  265 MB in 42.4 us, 6.2 TB/s
+//     with a 32-bit stream                       382 MB in 68.6 us, 5.6 TB/s
+//   gradient (h, dy, d_stream; d_h, d_gain)      235 MB in 45.1 us, 5.2 TB/s, and 4.9 us
 //     to add the workgroups' parts of d_gain (14.7 MB, still in the caches)
-// and one row of 7,168 takes 2.5 us, a launch's latency and two dependent loads.
-// 201 rows of 2,056 with a 32-bit stream, gradient: 4.9 us in one launch.
-// Vectors of eight values, as bf16 loads of 16 bytes; past 32,768 values a row does not
-// fit the registers and is read twice.
+//     with a 32-bit stream (and d_x)             470 MB in 90.0 us, 5.2 TB/s, and 4.8 us
+// and one row of 7,168 takes 2.4 us, a launch's latency and two dependent loads.
+// 201 rows of 2,056 with a 32-bit stream, gradient: 4.8 us in one launch.
+// Vectors of eight values, as bf16 loads of 16 bytes; past 32,768 values (in the gradient of
+// a 32-bit stream 16,384) a row does not fit the registers and is read twice.
 #include <algorithm>
 #include <cfloat>
 
@@ -123,7 +125,7 @@ __device__ __forceinline__ void put_normed(const NormArgs& a, int64_t t, int c, 
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
         m = row_max(m);  // 16 lanes hold 128 channels
         const float s = m < 1e-33f ? 1.0f : m * (1.0f / 448.0f);
-        const float inv = __builtin_amdgcn_rcpf(s);
+        const float inv = __builtin_amdgcn_rcpf(s);  // to 2^-23, beside e4m3's rounding of 2^-4
         u32x2 q;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -517,7 +519,7 @@ bool gain_beside(int T, int H, bool wide) {
 // within 1%), then one vector to a thread, as far as a workgroup goes. us, 4,096 rows of
 // 4,096, 5,120 and 7,168 with all outputs: 26.3 31.6 43.4; with 256 threads of two or
 // four vectors 27.2 34.8 47.5; with a 32-bit stream of 7,168 69.6, 75.3. 2,048 rows of
-// 16,384: 53.2, with 256 threads of eight vectors 61.4.
+// 16,384: 52.3, with 256 threads of eight vectors 61.4.
 template <bool WIDE>
 void launch_norm(NormArgs a, hipStream_t st) {
     const int vecs = (a.H + 7) / 8;

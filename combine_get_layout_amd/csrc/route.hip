@@ -5,9 +5,14 @@
 // Bytes are few (4,096 tokens of 256 experts: 4.5 MB, 0.9 us at the memory's rate); what
 // bounds it is the chain of K rounds, each a maximum over the wave that the next waits for,
 // and the keys' arithmetic:
-//   4,096 tokens, top-8 of 256, 4 of 8 groups by sums of two, bias (64-bit keys)  10.2 us
-//   13 tokens, top-6 of 72, softmax (keys are the logits)                          3.5 us
-//   gradients: 4,096 tokens of 256 experts 5.0 us, 333 tokens of 48 experts        4.0 us
+//   4,096 tokens, top-8 of 256, 4 of 8 groups by sums of two, bias (64-bit keys)  10.1 us
+//   the same without groups, softmax                                              10.1 us
+//   the same without bias (keys are the logits): softmax, sigmoid             6.8, 6.2 us
+//   13 tokens, top-6 of 72, softmax (keys are the logits)                          3.4 us
+//   1,024 tokens, top-8 of 4,092 in 33 groups: 124 experts in a lane's registers, of which
+//     944 bytes spill (where more than 64 fall to a lane, with bias alone)         140 us
+//   gradients: 4,096 tokens of 256 experts, sigmoid, softmax                  5.0, 7.3 us
+//              333 tokens of 48 experts, softmax                                   4.2 us
 // Choices are made by keys in 64 bits
 // where scores and biases are added: rounded to 32 bits, sums that differ would tie.
 #include <algorithm>
@@ -36,7 +41,9 @@ struct RouteArgs {
 };
 
 // exp(l - top) for a token's largest logit `top`: 1 where both are the same
-// infinity, 0 for a masked expert.
+// infinity, 0 for a masked expert. __expf scales its argument to base 2 in 32 bits, which
+// puts |l - top| 2^-24 on the value, as much as the difference itself has lost: 5e-6 of a
+// score of e^-80, nothing that counts in a sum with the largest's 1. No id depends on it.
 __device__ __forceinline__ float relative_exp(float l, float top) { return l == kNone ? 0.f : l == top ? 1.f : __expf(l - top); }
 
 // Keys as unsigned numbers of the same order: 0 for a masked expert (below every
