@@ -10,7 +10,7 @@
 //   the same without bias (keys are the logits): softmax, sigmoid             6.8, 6.2 us
 //   13 tokens, top-6 of 72, softmax (keys are the logits)                          3.4 us
 //   1,024 tokens, top-8 of 4,092 in 33 groups: 124 experts in a lane's registers, of which
-//     944 bytes spill (where more than 64 fall to a lane, with bias alone)         140 us
+//     944 bytes spill (64-bit keys, where more than 64 fall to a lane)             140 us
 //   gradients: 4,096 tokens of 256 experts, sigmoid, softmax                  5.0, 7.3 us
 //              333 tokens of 48 experts, softmax                                   4.2 us
 // Choices are made by keys in 64 bits
